@@ -1,0 +1,535 @@
+"""The gated feed-forward block, the cross entropy of a quantized head and the backward
+passes through quantized weights (libhqq_layers.so) against their definitions in 64 bits.
+
+Bounds.  W_hat is the dtype's rounding of an fp32 quotient, the same on both sides.
+Products of 16-bit values are exact in fp32, so a kernel's fp32 sum of R products is within
+R 2^-24 times the sum of their magnitudes (any order; 1.01 covers the higher orders).  An
+output's rounding adds half a step, eps / 2 of its size (fp16 2^-11, bf16 2^-8), and below
+fp16's normal range 2^-25.  The elementary functions (exp2, reciprocal and erfc of an
+fp32 argument z) are within (8 + 2 |z|) 2^-24, at most 2^-16 for |z| <= 120 where their
+values still count.  What a call rounds in between is said at its bound.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+FN = 2.0 ** -16
+DTYPES = [torch.float16, torch.bfloat16]
+PER_WORD = {8: 4, 4: 8, 2: 16, 1: 32}
+
+
+@pytest.fixture(scope="module")
+def hq():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import weight_quantization_group_amd as w
+
+    w.load_layers_library()
+    return w
+
+
+def make_weight(seed, N, K, nbits, gs, dtype, std=None):
+    """((packed, scale, zero) on the GPU, W_hat in 64 bits on the GPU) of random codes."""
+    rng = np.random.RandomState(seed)
+    qmax = (1 << nbits) - 1
+    q = rng.randint(0, qmax + 1, size=(N, K)).astype(np.uint32)
+    std = std or 1.0 / math.sqrt(K)
+    lo = -np.abs(rng.normal(2, 0.5, (N, K // gs))) * std
+    hi = np.abs(rng.normal(2, 0.5, (N, K // gs))) * std + 1e-3 * std
+    scale = (qmax / (hi - lo)).astype(np.float32)
+    zero = (-lo * scale).astype(np.float32)
+    C = PER_WORD[nbits]
+    shifts = (np.arange(C) * nbits).astype(np.uint32)
+    words = np.bitwise_or.reduce(q.reshape(N, K // C, C) << shifts, axis=2).astype(np.uint32)
+    w32 = (q.astype(np.float32) - np.repeat(zero, gs, 1)) / np.repeat(scale, gs, 1)
+    what = torch.from_numpy(w32).to(dtype).double().cuda()
+    return (torch.from_numpy(words.view(np.int32)).cuda(), torch.from_numpy(scale).cuda(),
+            torch.from_numpy(zero).cuda()), what
+
+
+def normal(seed, shape, dtype, std=1.0):
+    return (torch.from_numpy(np.random.RandomState(seed).randn(*shape)) * std).to(dtype).cuda()
+
+
+def within(got, ref, bound, tag=""):
+    got, ref = got.double(), ref.double()
+    assert got.shape == ref.shape, tag
+    assert torch.isfinite(got).all(), f"{tag}: not finite"
+    worst = ((got - ref).abs() / bound).max().item()
+    assert worst <= 1.0, f"{tag}: worst error / bound {worst:.3g}"
+
+
+def act64(act, g):
+    g = g.detach().requires_grad_(True)
+    f = {"silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu,
+         "gelu_tanh": lambda x: torch.nn.functional.gelu(x, approximate="tanh")}[act](g)
+    d, = torch.autograd.grad(f.sum(), g)
+    return f.detach(), d
+
+
+def gated_terms(X, Wg, Wu, act):
+    """G, U, act(G), act'(G) and the bounds of the fp32 sums G and U."""
+    x = X.double()
+    e = 1.01 * X.shape[1] * 2.0 ** -24
+    G, Up = x @ Wg.T, x @ Wu.T
+    f, d = act64(act, G)
+    return G, Up, f, d, e * (x.abs() @ Wg.abs().T), e * (x.abs() @ Wu.abs().T)
+
+
+def check_gated(Y, X, Wg, Wu, act, tag=""):
+    G, Up, f, d, eG, eU = gated_terms(X, Wg, Wu, act)
+    ref = f * Up
+    # |act'| <= 1.2
+    bound = (U[X.dtype] + FN) * ref.abs() + 1.01 * (1.2 * eG * (Up.abs() + eU) + f.abs() * eU) + TINY[X.dtype]
+    within(Y, ref, bound, tag)
+
+
+def grad_bound(terms, errors, weights, dtype):
+    """(sum_i T_i W_i, bound) where the kernel multiplies T_i' with |T_i' - T_i| <= errors_i."""
+    ref = sum(t @ w for t, w in zip(terms, weights))
+    R = sum(t.shape[1] for t in terms)
+    off = sum(e @ w.abs() for e, w in zip(errors, weights))
+    size = sum((t.abs() + e) @ w.abs() for t, e, w in zip(terms, errors, weights))
+    return ref, U[dtype] * ref.abs() + 1.01 * off + 1.01 * (R + 64) * 2.0 ** -24 * size + TINY[dtype]
+
+
+def check_gated_backward(dX, dY, X, Wg, Wu, act, tag=""):
+    G, Up, f, d, eG, eU = gated_terms(X, Wg, Wu, act)
+    y = dY.double()
+    dG, dU = y * Up * d, y * f
+    # |act''| <= 1.2; dG and dU are rounded once, in fp16 relative to a row scaled to [2^-7, 2^-6)
+    u = U[X.dtype]
+    floor = 2.0 ** -25 * 2.0 ** 7 * y.abs().amax(1, keepdim=True) if X.dtype == torch.float16 else 1e-38
+    act_off = FN * (d.abs() + G.abs())      # act' is a sum of two terms of at most these sizes
+    errG = 1.01 * y.abs() * ((Up.abs() + eU) * (1.2 * eG + act_off) + d.abs() * eU) + u * dG.abs() + floor
+    errU = 1.01 * y.abs() * (1.2 * eG + FN * f.abs()) + u * dU.abs() + floor
+    ref, bound = grad_bound([dG, dU], [errG * 1.01, errU * 1.01], [Wg, Wu], X.dtype)
+    within(dX, ref, bound, tag)
+
+
+def loss_terms(X, W):
+    x = X.double()
+    return x @ W.T, 1.01 * X.shape[1] * 2.0 ** -24 * (x.abs() @ W.abs().T)
+
+
+def check_loss(loss, lse, X, W, targets, tag=""):
+    L, eL = loss_terms(X, W)
+    N = W.shape[0]
+    keep = (targets >= 0) & (targets < N)
+    ref = torch.logsumexp(L, 1)
+    # each exponential is within FN (and its logit's error); up to 2^10 joins of fp32 sums in the
+    # longest chain; the logarithm and the final sums round at the size of lse
+    e = eL.amax(1) + 2 * FN + 2.0 ** -14 + 2.0 ** -22 * (1 + ref.abs() + L.abs().amax(1))
+    within(lse, ref, e, tag + " lse")
+    assert (loss[~keep] == 0).all(), tag
+    if keep.any():
+        at = targets.clamp(0, N - 1)[:, None]
+        lr = (ref - L.gather(1, at)[:, 0])[keep]
+        if N > 1:
+            rest = torch.logsumexp(L.scatter(1, at, -math.inf), 1)[keep]
+            lr = torch.nn.functional.softplus(rest - L.gather(1, at)[keep, 0])
+        # loss = log(1 + exp(d)) with |d - d_ref| <= 2 e: relative to a small loss
+        within(loss[keep], lr, torch.clamp(lr, max=1.0) * 2 * e[keep] * 1.01 + 2.0 ** -21 * lr + 1e-37, tag + " loss")
+
+
+def check_loss_backward(dX, dloss, X, W, targets, lse, tag=""):
+    L, eL = loss_terms(X, W)
+    N = W.shape[0]
+    keep = (targets >= 0) & (targets < N)
+    P = torch.exp(torch.where(keep[:, None], L - lse.double()[:, None], torch.zeros_like(L)))
+    P = torch.where(keep[:, None], P, torch.zeros_like(P))
+    S = P.clone()
+    rows = torch.arange(len(targets), device=S.device)[keep]
+    S[rows, targets[keep]] -= 1.0
+    dl = torch.where(keep, dloss.double(), torch.zeros_like(lse.double()))[:, None]
+    floor = 2.0 ** -40 if X.dtype == torch.float16 else 1e-38
+    # p from a logit off by eL and rounded sums of it and lse, the difference rounded once
+    off = P * 1.01 * (eL + FN + 2.0 ** -23 * (L.abs() + lse.double().abs()[:, None])) + U[X.dtype] * S.abs() + floor
+    off = torch.where(keep[:, None], off, torch.zeros_like(off))
+    ref, bound = grad_bound([S], [off * 1.01], [W], X.dtype)
+    u = U[X.dtype]
+    bound = dl.abs() * bound + u * (dl * ref).abs() + 2.0 ** -23 * (dl * ref).abs() + TINY[X.dtype]
+    within(dX, dl * ref, bound, tag)
+    assert (dX[~keep] == 0).all(), tag
+
+
+# (M, K, N, nbits, gs): one row, few rows, many; depths that end inside a step; widths of one,
+# odd, and across tiles; every code width and group size
+SIZES = [
+    (1, 32, 1, 4, 8),
+    (1, 64, 5, 4, 32),
+    (1, 4096, 200, 4, 64),
+    (2, 96, 33, 4, 32),
+    (3, 256, 64, 8, 256),
+    (5, 160, 100, 2, 16),
+    (8, 128, 257, 1, 32),
+    (16, 512, 130, 4, 128),
+    (17, 320, 66, 4, 64),
+    (31, 1056, 129, 2, 32),
+    (32, 256, 48, 1, 64),
+    (33, 192, 71, 8, 8),
+    (64, 64, 64, 4, 16),
+    (100, 544, 301, 4, 32),
+    (129, 128, 127, 2, 8),
+    (200, 768, 520, 4, 64),
+    (257, 96, 255, 8, 32),
+    (300, 1024, 1000, 4, 256),
+    (513, 256, 640, 1, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M,K,N,nbits,gs", SIZES)
+def test_gated(hq, M, K, N, nbits, gs, dtype):
+    act = ("silu", "gelu", "gelu_tanh")[(M + N) % 3]
+    gate, Wg = make_weight(M + N, N, K, nbits, gs, dtype)
+    up, Wu = make_weight(M + N + 1, N, K, nbits, gs, dtype)
+    X, dY = normal(K, (M, K), dtype, 1.5), normal(K + 1, (M, N), dtype)
+    Y = hq.hqq_linear_gated(X, gate, up, N, nbits, gs, activation=act)
+    check_gated(Y, X, Wg, Wu, act, f"{act}")
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, nbits, gs, activation=act)
+    check_gated_backward(dX, dY, X, Wg, Wu, act, f"{act}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M,K,N,nbits,gs", SIZES)
+def test_linear_backward(hq, M, K, N, nbits, gs, dtype):
+    w, W = make_weight(3 * M + N, N, K, nbits, gs, dtype)
+    dY = normal(N, (M, N), dtype)
+    dX = hq.hqq_linear_backward(dY, *w, K, nbits, gs)
+    y = dY.double()
+    within(dX, *grad_bound([y], [torch.zeros_like(y)], [W], dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M,K,nbits,gs,Ns", [
+    (1, 256, 4, 64, [64, 17, 300]),
+    (7, 128, 2, 32, [8, 16, 24, 7]),
+    (40, 512, 8, 64, [512, 128, 128]),
+    (150, 96, 4, 32, [1, 63, 65, 64]),
+    (260, 320, 1, 64, list(range(1, 17))),
+])
+def test_linear_batch_backward(hq, M, K, nbits, gs, Ns, dtype):
+    """One sum over all weights; each alone in the other rows' place."""
+    ws = [make_weight(50 + i, N, K, nbits, gs, dtype) for i, N in enumerate(Ns)]
+    dYs = [normal(90 + i, (M, N), dtype) for i, N in enumerate(Ns)]
+    dX = hq.hqq_linear_batch_backward(dYs, [w[0] + (N,) for w, N in zip(ws, Ns)], K, nbits, gs)
+    y = [d.double() for d in dYs]
+    within(dX, *grad_bound(y, [torch.zeros_like(d) for d in y], [w[1] for w in ws], dtype))
+
+
+def some_targets(seed, M, N):
+    """Random classes, the first and the last among them, some ignored."""
+    rng = np.random.RandomState(seed)
+    t = rng.randint(0, N, M)
+    t[rng.rand(M) < 0.2] = -100
+    t[0] = N - 1
+    if M > 2:
+        t[1], t[2] = 0, N                   # N itself is no class
+    return torch.from_numpy(t.astype(np.int64)).cuda()
+
+
+def loss_case(hq, M, K, N, nbits, gs, dtype, spread=1.0, targets=None):
+    head, W = make_weight(7 * M + N, N, K, nbits, gs, dtype)
+    X = normal(M + K, (M, K), dtype, spread)
+    t = some_targets(M, M, N) if targets is None else targets
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, nbits, gs)
+    check_loss(loss, lse, X, W, t)
+    dloss = normal(M + 3, (M,), torch.float32, 0.1)
+    dX = hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *head, N, nbits, gs)
+    check_loss_backward(dX, dloss, X, W, t, lse)
+    return loss, lse, dX
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M,K,N,nbits,gs", SIZES)
+def test_cross_entropy(hq, M, K, N, nbits, gs, dtype):
+    loss_case(hq, M, K, N, nbits, gs, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M,K,N", [(1, 4096, 20001), (9, 8192, 9001), (70, 4096, 17000), (300, 8192, 8300)])
+def test_cross_entropy_in_pieces(hq, M, K, N, dtype):
+    """More classes than a piece: targets in every piece, and at its first and last class."""
+    t = torch.randint(0, N, (M,), generator=torch.Generator().manual_seed(M))
+    for i, edge in enumerate((8191, 8192, 16383, 16384, N - 1, 4095, 4096)):
+        if i < M and edge < N:
+            t[i] = edge
+    loss_case(hq, M, K, N, 4, 64, dtype, targets=t.cuda())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+def test_cross_entropy_peaked_rows(hq, dtype):
+    """Logits far apart: one class holds nearly everything, as the target and as another."""
+    M, K, N = 24, 256, 500
+    head, W = make_weight(5, N, K, 4, 64, dtype)
+    t = torch.arange(M).cuda() * 7
+    lead = t.clone()
+    lead[::2] += 1
+    X = (W[lead] * torch.linspace(2, 30, M, device="cuda", dtype=torch.float64)[:, None]).to(dtype)
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 4, 64)
+    check_loss(loss, lse, X, W, t)
+    assert loss.max() > 20 and 0 < loss.min() < 1e-4
+    dloss = torch.ones(M, device="cuda")
+    dX = hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *head, N, 4, 64)
+    check_loss_backward(dX, dloss, X, W, t, lse)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M", [3, 70])
+def test_cross_entropy_ignored_rows(hq, dtype, M):
+    """Rows without a target give 0, whatever their inputs hold; all rows may be such."""
+    K, N = 128, 300
+    head, W = make_weight(5, N, K, 4, 64, dtype)
+    X = normal(1, (M, K), dtype)
+    t = torch.full((M,), -100, dtype=torch.int64, device="cuda")
+    X[1], t[1] = math.nan, N
+    X[2], t[2] = math.inf, 1 << 40
+    t[0] = 5
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 4, 64)
+    dloss = torch.full((M,), 2.0, device="cuda")
+    dloss[1] = math.nan
+    dX = hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *head, N, 4, 64)
+    assert (loss[1:] == 0).all() and (dX[1:] == 0).all()
+    check_loss(loss[:1], lse[:1], X[:1], W, t[:1])
+    check_loss_backward(dX[:1], dloss[:1], X[:1], W, t[:1], lse[:1])
+    t[0] = -1
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 4, 64)
+    dX = hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *head, N, 4, 64)
+    assert (loss == 0).all() and (dX == 0).all()
+
+
+def test_fp16_small_gradients_keep_their_precision(hq):
+    """Gradients near fp16's smallest normal number (a loss scale too low): dG and dU are formed
+    relative to the row."""
+    dtype = torch.float16
+    M, K, N = 40, 256, 200
+    gate, Wg = make_weight(1, N, K, 4, 64, dtype, std=1.0)
+    up, Wu = make_weight(2, N, K, 4, 64, dtype, std=1.0)
+    X = normal(3, (M, K), dtype, 2.0 ** -5)
+    dY = normal(4, (M, N), dtype, 2.0 ** -13)
+    dY[7] = 0
+    dY[8] = 2.0 ** -24
+    check_gated_backward(hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 64), dY, X, Wg, Wu, "silu")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [4, 96])
+def test_gated_saturated_activations(hq, act, M):
+    """Projections up to several hundred: the activation's flat and linear ends."""
+    dtype, K, N = torch.bfloat16, 64, 96
+    gate, Wg = make_weight(1, N, K, 8, 64, dtype, std=4.0)
+    up, Wu = make_weight(2, N, K, 8, 64, dtype, std=0.2)
+    X, dY = normal(3, (M, K), dtype, 4.0), normal(4, (M, N), dtype)
+    Y = hq.hqq_linear_gated(X, gate, up, N, 8, 64, activation=act)
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, 8, 64, activation=act)
+    assert torch.isfinite(Y).all() and torch.isfinite(dX).all()
+    G, Up, f, d, eG, eU = gated_terms(X, Wg, Wu, act)
+    assert G.abs().max() > 100
+    # the exponent's own rounding grows with it: at most 2^-24 |z| for the exponents |z| < 10^7
+    # that occur, times |act| <= |G| where the activation has not reached its end
+    live = (G.abs() < 30).double()
+    ref = f * Up
+    bound = (U[dtype] + FN) * ref.abs() + 1.01 * (1.2 * eG * (Up.abs() + eU) + f.abs() * eU) + 2.0 ** -12 * live * ref.abs() + 1e-9
+    within(Y, ref, bound)
+    check_gated_backward(dX, dY, X, Wg, Wu, act)
+
+
+def chain(hq, dtype, M=37, K=128, F=192, V=400, nbits=4, gs=64):
+    """A small block and head: h = down(gated(x)), loss(h)."""
+    gate, Wg = make_weight(1, F, K, nbits, gs, dtype)
+    up, Wu = make_weight(2, F, K, nbits, gs, dtype)
+    down, Wd = make_weight(3, K, F, nbits, gs, dtype)
+    head, Wh = make_weight(4, V, K, nbits, gs, dtype, std=1.0)
+    t = some_targets(9, M, V)
+
+    def forward(x):
+        y = hq.hqq_linear_gated(x, gate, up, F, nbits, gs)
+        h = hq.hqq_linear(y, *down, K, nbits, gs)
+        loss, lse = hq.hqq_linear_cross_entropy(h, t, *head, V, nbits, gs)
+        return y, h, loss, lse
+
+    def backward(x, h, lse, dloss):
+        dh = hq.hqq_linear_cross_entropy_backward(dloss, h, t, lse, *head, V, nbits, gs)
+        dy = hq.hqq_linear_backward(dh, *down, F, nbits, gs)
+        return hq.hqq_linear_gated_backward(dy, x, gate, up, F, nbits, gs)
+
+    def total64(x):
+        y = torch.nn.functional.silu(x @ Wg.T) * (x @ Wu.T)
+        L = (y @ Wd.T) @ Wh.T
+        keep = (t >= 0) & (t < V)
+        return torch.nn.functional.cross_entropy(L[keep], t[keep], reduction="sum")
+
+    return forward, backward, total64, normal(7, (M, K), dtype, 2.0), t
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+def test_operators_together(hq, dtype):
+    """A block and a head as a fine-tuning step runs them: loss and gradient against autograd and
+    against differences in 64 bits.  Three 16-bit intermediates on the way forward and three on the
+    way back, each off by u of its size: as independent errors well within 16 u of the norm."""
+    forward, backward, total64, X, t = chain(hq, dtype)
+    _, h, loss, lse = forward(X)
+    dX = backward(X, h, lse, torch.ones(len(t), device="cuda")).double()
+    x = X.double().requires_grad_(True)
+    ref = total64(x)
+    g, = torch.autograd.grad(ref, x)
+    u = U[dtype]
+    assert abs(loss.double().sum() - ref).item() <= 16 * u * abs(ref.item())
+    assert (dX - g).norm() <= 16 * u * g.norm()
+    v = normal(21, tuple(X.shape), torch.float64)
+    step = 1e-5
+    diff = (total64(x.detach() + step * v) - total64(x.detach() - step * v)) / (2 * step)
+    # the step's own error is of order step^2; the gradient's along v is that of its norm
+    assert abs((dX * v).sum() - diff).item() <= 16 * u * (g.norm() * v.norm()).item() + 1e-6
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M", [1, 20, 150])
+def test_captured_and_replayed(hq, dtype, M):
+    """The whole step in a HIP graph, replayed with new inputs between eager calls: the same bits."""
+    forward, backward, _, X, t = chain(hq, dtype, M=M)
+    dloss = torch.ones(M, device="cuda")
+
+    def step(x):
+        y, h, loss, lse = forward(x)
+        return y, loss, lse, backward(x, h, lse, dloss)
+
+    buf = X.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(buf)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(buf)
+    for i in range(4):
+        new = normal(100 + i, tuple(X.shape), dtype)
+        buf.copy_(new)
+        graph.replay()
+        got = [o.clone() for o in out]
+        torch.cuda.synchronize()
+        for a, b in zip(got, step(new)):
+            assert torch.equal(a, b), i
+
+
+def everything(hq, dtype, M, K, N, nbits, gs, ws=None):
+    """Every operator once, with workspaces from ws(bytes)."""
+    a, _ = make_weight(1, N, K, nbits, gs, dtype)
+    b, _ = make_weight(2, N, K, nbits, gs, dtype)
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+    t = some_targets(5, M, N)
+    dl = torch.ones(M, device="cuda")
+    ws = ws or (lambda n: None)
+    s = (M, K, N, nbits, gs)
+    f = (N, nbits, gs)
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *a, *f, workspace=ws(hq.hqq_linear_cross_entropy_workspace(*s)))
+    return [hq.hqq_linear_gated(X, a, b, *f, workspace=ws(hq.hqq_linear_gated_workspace(*s))),
+            hq.hqq_linear_gated_backward(dY, X, a, b, *f, workspace=ws(hq.hqq_linear_gated_backward_workspace(*s))),
+            hq.hqq_linear_batch_backward([dY, dY], [a + (N,), b + (N,)], K, nbits, gs,
+                                         workspace=ws(hq.hqq_linear_batch_backward_workspace(M, K, [N, N], nbits, gs))),
+            loss, lse,
+            hq.hqq_linear_cross_entropy_backward(dl, X, t, lse, *a, *f,
+                                                 workspace=ws(hq.hqq_linear_cross_entropy_backward_workspace(*s)))]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M,K,N", [(1, 160, 77), (13, 256, 300), (200, 352, 515)])
+def test_workspace_contents_and_repeats(hq, dtype, M, K, N):
+    """A caller's workspace of the stated size, full of NaN (bytes 0xff) with a guard behind it:
+    the same bits as without, twice, and the guard untouched."""
+    plain = everything(hq, dtype, M, K, N, 4, 32)
+    guards = []
+
+    def ws(n):
+        t = torch.full((n + 4096,), 0xff, dtype=torch.uint8, device="cuda")
+        guards.append(t[n:])
+        return t[:n]
+
+    for _ in range(2):
+        for a, b in zip(everything(hq, dtype, M, K, N, 4, 32, ws), plain):
+            assert torch.equal(a, b)
+    for g in guards:
+        assert (g == 0xff).all()
+
+
+def test_outputs_in_larger_buffers(hq):
+    """Nothing is written outside the outputs (odd widths end inside vector stores)."""
+    dtype, M, K, N = torch.float16, 45, 96, 67
+    a, _ = make_weight(1, N, K, 4, 32, dtype)
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+
+    def guarded(n, dt):
+        whole = torch.full((n + 512,), 7.0, dtype=dt, device="cuda")
+        return whole, whole[256:256 + n]
+
+    for shape, call in [((M, N), lambda o: hq.hqq_linear_gated(X, a, a, N, 4, 32, out=o)),
+                        ((M, K), lambda o: hq.hqq_linear_gated_backward(dY, X, a, a, N, 4, 32, out=o)),
+                        ((M, K), lambda o: hq.hqq_linear_backward(dY, *a, K, 4, 32, out=o))]:
+        whole, part = guarded(shape[0] * shape[1], dtype)
+        call(part.view(shape))
+        assert (whole[:256] == 7).all() and (whole[256 + part.numel():] == 7).all()
+        assert (part != 7).any()
+
+
+def test_two_streams_with_their_own_workspaces(hq):
+    """The same calls on two streams at once give what they give alone."""
+    want = everything(hq, torch.bfloat16, 150, 256, 333, 4, 64)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(everything(hq, torch.bfloat16, 150, 256, 333, 4, 64))
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
+
+
+def test_same_weight_and_gradient_twice(hq):
+    """One weight given as both projections, and one gradient for two weights."""
+    dtype, M, K, N = torch.bfloat16, 19, 128, 80
+    w, W = make_weight(1, N, K, 4, 64, dtype)
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+    check_gated(hq.hqq_linear_gated(X, w, w, N, 4, 64), X, W, W, "silu")
+    y = dY.double()
+    dX = hq.hqq_linear_batch_backward([dY, dY], [w + (N,), w + (N,)], K, 4, 64)
+    z = torch.zeros_like(y)
+    within(dX, *grad_bound([y, y], [z, z], [W, W], dtype))
+
+
+def test_shapes_are_checked(hq):
+    """The binding refuses what does not fit, before anything runs."""
+    dtype, M, K, N = torch.float16, 4, 128, 80
+    w, _ = make_weight(1, N, K, 4, 64, dtype)
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+    t = torch.zeros(M, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        hq.hqq_linear_gated(X, w, w, N + 1, 4, 64)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_gated(X, w, w, N, 8, 64)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_gated(X, w, w, N, 4, 64, activation="relu")
+    with pytest.raises(ValueError):
+        hq.hqq_linear_gated(X.t().contiguous().t(), w, w, N, 4, 64)
+    with pytest.raises(TypeError):
+        hq.hqq_linear_gated_backward(dY.bfloat16(), X, w, w, N, 4, 64)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_backward(dY[:, :-1].contiguous(), *w, K, 4, 64)
+    with pytest.raises(TypeError):
+        hq.hqq_linear_cross_entropy(X, t.int(), *w, N, 4, 64)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_cross_entropy(X, t[:3], *w, N, 4, 64)
+    with pytest.raises(hq.LayersError):
+        hq.hqq_linear_gated(X[:0], w, w, N, 4, 64)
+    need = hq.hqq_linear_gated_backward_workspace(M, K, N, 4, 64)
+    with pytest.raises(hq.LayersError) as e:
+        hq.hqq_linear_gated_backward(dY, X, w, w, N, 4, 64, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == -11

@@ -1,0 +1,186 @@
+"""CPU-side checks of libhqq_layers.so: it exports exactly what include/hqq_layers.h declares,
+the header compiles as C and C++, workspace sizes, and every invalid argument is refused on the
+host before any HIP call (no GPU is needed; no compute call is made here)."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "hqq_layers.h")
+
+NBITS, GROUP, SHAPE, PTR, DTYPE, ACT, WORKSPACE = -1, -3, -4, -5, -8, -10, -11
+# fake, 16-byte aligned, never dereferenced: every call below fails validation first
+A, MIS, MIS4 = 0x1000, 0x1008, 0x1002
+
+
+@pytest.fixture(scope="module")
+def w():
+    import weight_quantization_group_amd as w
+
+    if not os.path.exists(w.LAYERS_LIB_PATH):
+        pytest.fail(f"{w.LAYERS_LIB_PATH} is not built (run __graft_entry__.build())")
+    w.load_layers_library()
+    return w
+
+
+@pytest.fixture(scope="module")
+def lib(w):
+    return w.load_layers_library()
+
+
+def test_exports_exactly_the_header(w):
+    text = open(HEADER).read()
+    declared = sorted(set(re.findall(r"^HQQ_API (?:int|int64_t|const char \*)\s*(hqq_\w+)\s*\(", text, re.M)))
+    assert declared == sorted(w.LAYERS_EXPORTS)
+    out = subprocess.run(["nm", "-D", "--defined-only", w.LAYERS_LIB_PATH], capture_output=True, text=True).stdout
+    assert sorted(line.split()[-1] for line in out.splitlines() if " T " in line) == declared
+
+
+@pytest.mark.parametrize("lang,compiler", [("c", "gcc"), ("c++", "g++")])
+def test_header_compiles_cleanly(lang, compiler, tmp_path):
+    if shutil.which(compiler) is None:
+        pytest.skip(f"{compiler} not installed")
+    src = tmp_path / ("use." + ("c" if lang == "c" else "cpp"))
+    src.write_text('#include "hqq_layers.h"\nint main(void) { return hqq_linear_gated_workspace(1, 32, 1, 4, 32) < 0; }\n')
+    r = subprocess.run([compiler, "-fsyntax-only", "-Wall", "-Wextra", "-Werror", "-I",
+                        os.path.join(ROOT, "include"), str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_strerror(w):
+    text = open(HEADER).read()
+    for name, code in (("HQQ_EINVAL_ACT", ACT), ("HQQ_EWORKSPACE", WORKSPACE)):
+        assert int(re.search(rf"#define {name} \((-\d+)\)", text).group(1)) == code
+    for code in (0, NBITS, GROUP, SHAPE, PTR, -7, DTYPE, ACT, WORKSPACE):
+        assert w.hqq_layers_strerror(code) != "unknown status"
+    assert w.hqq_layers_strerror(12345) == "unknown status"
+
+
+SIZES = [
+    (dict(nbits=3), NBITS), (dict(nbits=16), NBITS),
+    (dict(M=0), SHAPE), (dict(M=(1 << 20) + 1), SHAPE), (dict(K=0), SHAPE), (dict(K=48), SHAPE),
+    (dict(K=1 << 18), SHAPE), (dict(N=0), SHAPE), (dict(N=-3), SHAPE), (dict(N=1 << 40), SHAPE),
+    (dict(N=1 << 26, K=64, gs=8), SHAPE),                   # the codes take 2^31 bytes
+    (dict(N=1 << 26, K=64, gs=8, nbits=1), SHAPE),          # the meta does
+    (dict(gs=48), GROUP), (dict(gs=4), GROUP), (dict(gs=512, K=512), GROUP), (dict(K=96, gs=64), GROUP),
+]
+
+
+def weight(w, packed=A, scale=A, zero=A):
+    from weight_quantization_group_amd.layers import HqqWeight
+    return HqqWeight(packed, scale, zero)
+
+
+def gated(w, lib, X=A, gate=A, up=A, Y=A, M=4, K=128, N=40, nbits=4, gs=64, dtype=0, act=0, ws=A, size=1 << 40):
+    g = ctypes.byref(weight(w, gate)) if gate else None
+    u = ctypes.byref(weight(w, up)) if up else None
+    return lib.hqq_linear_gated(X, M, K, g, u, N, nbits, gs, dtype, act, Y, ws, size, None)
+
+
+def gated_backward(w, lib, dY=A, X=A, gate=A, up=A, dX=A, M=4, K=128, N=40, nbits=4, gs=64, dtype=0, act=0, ws=A,
+                   size=1 << 40):
+    g = ctypes.byref(weight(w, gate)) if gate else None
+    u = ctypes.byref(weight(w, scale=up)) if up else None
+    return lib.hqq_linear_gated_backward(dY, X, M, K, g, u, N, nbits, gs, dtype, act, dX, ws, size, None)
+
+
+def batch_backward(w, lib, dY=A, packed=A, scale=A, zero=A, dX=A, count=2, M=4, K=128, N=40, nbits=4, gs=64, dtype=0,
+                   ws=A, size=1 << 40, array=True):
+    from weight_quantization_group_amd.layers import HqqLinearGrad
+    arr = (HqqLinearGrad * 32)(*[HqqLinearGrad(A, A, A, 40, A)] * 32)
+    arr[1] = HqqLinearGrad(packed, scale, zero, N, dY)      # the second one is the bad one
+    return lib.hqq_linear_batch_backward(arr if array else None, count, M, K, nbits, gs, dtype, dX, ws, size, None)
+
+
+def loss(w, lib, X=A, head=A, targets=A, loss=A, lse=A, M=4, K=128, N=40, nbits=4, gs=64, dtype=0, ws=A,
+         size=1 << 40):
+    h = ctypes.byref(weight(w, zero=head)) if head else None
+    return lib.hqq_linear_cross_entropy(X, M, K, h, N, nbits, gs, dtype, targets, loss, lse, ws, size, None)
+
+
+def loss_backward(w, lib, dloss=A, X=A, head=A, targets=A, lse=A, dX=A, M=4, K=128, N=40, nbits=4, gs=64, dtype=0,
+                  ws=A, size=1 << 40):
+    h = ctypes.byref(weight(w, head)) if head else None
+    return lib.hqq_linear_cross_entropy_backward(dloss, X, M, K, h, N, nbits, gs, dtype, targets, lse, dX, ws, size, None)
+
+
+CALLS = [gated, gated_backward, batch_backward, loss, loss_backward]
+
+
+@pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
+@pytest.mark.parametrize("kw,code", SIZES + [(dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE),
+                                             (dict(ws=MIS), PTR), (dict(ws=None), PTR), (dict(size=-1), PTR),
+                                             (dict(size=0), WORKSPACE), (dict(ws=None, size=0), WORKSPACE)])
+def test_rejects(w, lib, call, kw, code):
+    assert call(w, lib, **kw) == code
+
+
+@pytest.mark.parametrize("call,names", [
+    (gated, ["X", "gate", "up", "Y"]), (gated_backward, ["dY", "X", "gate", "up", "dX"]),
+    (batch_backward, ["dY", "packed", "scale", "zero", "dX"]), (loss, ["X", "head"]),
+    (loss_backward, ["X", "head", "dX"])], ids=lambda v: getattr(v, "__name__", ""))
+def test_rejects_pointers(w, lib, call, names):
+    for name in names:
+        assert call(w, lib, **{name: None}) == PTR, name
+        assert call(w, lib, **{name: MIS}) == PTR, name
+
+
+def test_rejects_row_arrays(w, lib):
+    """targets need 8-byte alignment, the fp32 rows 4."""
+    for call, names in ((loss, ["targets", "loss", "lse"]), (loss_backward, ["targets", "lse", "dloss"])):
+        for name in names:
+            assert call(w, lib, **{name: None}) == PTR
+            assert call(w, lib, **{name: MIS4}) == PTR
+        assert call(w, lib, targets=0x1004) == PTR
+
+
+def test_rejects_activation_and_counts(w, lib):
+    for call in (gated, gated_backward):
+        assert call(w, lib, act=3) == ACT and call(w, lib, act=-1) == ACT
+    assert batch_backward(w, lib, count=0) == SHAPE
+    assert batch_backward(w, lib, count=17) == SHAPE
+    assert batch_backward(w, lib, count=-1) == SHAPE
+    assert batch_backward(w, lib, array=False) == PTR
+
+
+def test_workspace_sizes(w):
+    """One byte less than stated is refused; invalid sizes raise; sizes stay far below the logits'
+    for long batches over large vocabularies."""
+    sizes = (37, 1056, 2753, 2, 32)
+    for call, fn in ((gated, w.hqq_linear_gated_workspace), (gated_backward, w.hqq_linear_gated_backward_workspace),
+                     (loss, w.hqq_linear_cross_entropy_workspace),
+                     (loss_backward, w.hqq_linear_cross_entropy_backward_workspace)):
+        need = fn(*sizes)
+        if need:
+            assert call(w, w.load_layers_library(), M=37, K=1056, N=2753, nbits=2, gs=32, size=need - 1) == WORKSPACE
+        with pytest.raises(w.LayersError):
+            fn(37, 1056, 2753, 3, 32)
+    assert w.hqq_linear_batch_backward_workspace(5, 128, [40, 7], 4, 64) > 0
+    with pytest.raises(w.LayersError):
+        w.hqq_linear_batch_backward_workspace(5, 128, [], 4, 64)
+    with pytest.raises(w.LayersError):
+        w.hqq_linear_batch_backward_workspace(5, 128, [40] * 17, 4, 64)
+    M, K, N = 65536, 4096, 128000
+    logits = 2 * M * N
+    assert w.hqq_linear_cross_entropy_workspace(M, K, N, 4, 64) < logits / 16
+    assert w.hqq_linear_cross_entropy_backward_workspace(M, K, N, 4, 64) < logits / 16
+
+
+def test_binding_refuses_host_tensors(w):
+    import torch
+
+    X = torch.zeros(4, 128, dtype=torch.float16)
+    q = (torch.zeros(40, 16, dtype=torch.int32), torch.zeros(40, 2), torch.zeros(40, 2))
+    t = torch.zeros(4, dtype=torch.int64)
+    for call in (lambda: w.hqq_linear_gated(X, q, q, 40, 4, 64), lambda: w.hqq_linear_gated_backward(X, X, q, q, 40, 4, 64),
+                 lambda: w.hqq_linear_backward(X, *q, 128, 4, 64),
+                 lambda: w.hqq_linear_cross_entropy(X, t, *q, 40, 4, 64),
+                 lambda: w.hqq_linear_cross_entropy_backward(t.float(), X, t, t.float(), *q, 40, 4, 64)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        w.hqq_linear_batch_backward([], [], 128, 4, 64)

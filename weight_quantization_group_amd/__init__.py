@@ -582,3 +582,12 @@ def hqq_dequantize_meta_batch(quantized, group_size: int = 128):
     outs = [torch.empty(c.numel(), dtype=torch.float32, device=c.device) for c, _, _ in quantized]
     MetaBatch([(o, c, ms, mz) for o, (c, ms, mz) in zip(outs, quantized)], group_size).dequantize()
     return outs
+
+
+from .layers import (  # noqa: E402,F401  (needs the names above)
+    ACT_CODES, LAYERS_EXPORTS, LAYERS_LIB_PATH, LayersError, MAX_GRADS, hqq_layers_strerror,
+    hqq_linear_backward, hqq_linear_batch_backward, hqq_linear_batch_backward_workspace,
+    hqq_linear_cross_entropy, hqq_linear_cross_entropy_backward,
+    hqq_linear_cross_entropy_backward_workspace, hqq_linear_cross_entropy_workspace, hqq_linear_gated,
+    hqq_linear_gated_backward, hqq_linear_gated_backward_workspace, hqq_linear_gated_workspace,
+    load_layers_library)

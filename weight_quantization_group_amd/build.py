@@ -1,9 +1,9 @@
-"""Build the HIP library ``libhqq.so`` for gfx950, in-tree.
+"""Build the HIP libraries ``libhqq.so`` and ``libhqq_layers.so`` for gfx950, in-tree.
 
     python -m weight_quantization_group_amd.build
 
 The translation units are compiled in parallel (one hipcc process each) and
-linked into one shared library.  Flags that matter for exactness:
+linked into one shared library per header of include/.  Flags that matter for exactness:
   -ffp-contract=off                  no fma contraction beyond the explicit ones
   -fno-gpu-flush-denormals-to-zero   fp32 denormals kept (IEEE)
   (HIP's default fp32 division is correctly rounded; no unsafe-math flags)
@@ -28,6 +28,9 @@ SOURCES = ["hqq_abi.cpp", "hqq_stream.cpp", "hqq_solve.hip", "hqq_solve_b1.hip",
            "hqq_solve_b4_bf16.hip", "hqq_solve_b8_bf16.hip", "hqq_codec.hip",
            "hqq_linear.hip", "hqq_gemm.cpp"]
 
+LAYERS_LIB = os.path.join(PKG, "libhqq_layers.so")
+LAYERS_SOURCES = ["hqq_layers_abi.cpp", "hqq_layers_unpack.hip", "hqq_layers_gemm.hip", "hqq_layers_rows.hip"]
+
 FLAGS = ["-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-fvisibility=hidden",
          "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -44,18 +47,25 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = ["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs, "-lhipblaslt"]
+def _link(lib: str, objs, libs=()) -> None:
+    tmp = lib + ".tmp"
+    cmd = ["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs, *libs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
+    os.replace(tmp, lib)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    todo = SOURCES + LAYERS_SOURCES
+    with cf.ThreadPoolExecutor(max_workers=len(todo)) as ex:
+        objs = dict(zip(todo, ex.map(_compile, todo)))
+    _link(LIB, [objs[s] for s in SOURCES], ["-lhipblaslt"])
+    _link(LAYERS_LIB, [objs[s] for s in LAYERS_SOURCES])
     if verbose:
         print("built", LIB)
+        print("built", LAYERS_LIB)
     return LIB
 
 

@@ -1,0 +1,587 @@
+// hqq_layers_abi.cpp -- the C ABI of include/hqq_layers.h: argument checks, the
+// workspace layouts, and the order of the launches.  No allocation, no state.
+#include "hqq_layers_internal.h"
+
+#include <stdint.h>
+
+namespace {
+
+using namespace hqq;
+
+constexpr int64_t kMaxRows = int64_t(1) << 20;
+constexpr int64_t kMaxDepth32 = int64_t(1) << 17;
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+constexpr int64_t kMaxBytes = int64_t(1) << 31;
+// The backward passes keep 16-bit gradients of this many rows at a time.
+constexpr int64_t kRowChunk = 8192;
+
+bool aligned(const void *p, unsigned to) { return p && ((uintptr_t)p & (to - 1)) == 0; }
+
+int log2_group(int gs)
+{
+    for (int b = 3; b <= 8; ++b)
+        if (gs == (1 << b))
+            return b;
+    return -1;
+}
+
+int check_sizes(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
+{
+    if (!valid_nbits(nbits) || nbits == 3)
+        return HQQ_EINVAL_NBITS;
+    if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > kMaxRows || K > kMaxDepth32 || N > kMaxBytes ||
+        M * N > kMaxElems || N * (K * nbits / 32) * 4 >= kMaxBytes)
+        return HQQ_EINVAL_SHAPE;
+    if (log2_group(group_size) < 0 || K % group_size != 0)
+        return HQQ_EINVAL_GROUP;
+    if (N * (K / group_size) * 4 >= kMaxBytes)
+        return HQQ_EINVAL_SHAPE;
+    return HQQ_OK;
+}
+
+int check_dtype(int dtype)
+{
+    return dtype == HQQ_DTYPE_FP16 || dtype == HQQ_DTYPE_BF16 ? HQQ_OK : HQQ_EINVAL_DTYPE;
+}
+
+bool weight_ok(const uint32_t *packed, const float *scale, const float *zero)
+{
+    return aligned(packed, 16) && aligned(scale, 16) && aligned(zero, 16);
+}
+
+int check_workspace(const void *ws, int64_t have, int64_t need)
+{
+    if (have < 0 || (!ws && have > 0) || (ws && !aligned(ws, 16)))
+        return HQQ_EINVAL_PTR;
+    return have < need ? HQQ_EWORKSPACE : HQQ_OK;
+}
+
+// The workspace as a run of 256-byte aligned arrays; with a null base only
+// their sizes count.
+struct Carve {
+    char *base;
+    int64_t at = 0;
+    explicit Carve(void *p) : base((char *)p) {}
+    template <typename T>
+    T *take(int64_t n)
+    {
+        T *p = base ? reinterpret_cast<T *>(base + at) : nullptr;
+        at += round_up(n * (int64_t)sizeof(T), 256);
+        return p;
+    }
+};
+
+UnpackArgs unpack_args(const uint32_t *packed, const float *scale, const float *zero, int64_t row0, int64_t n, int64_t K,
+                       int nbits, int group_size)
+{
+    UnpackArgs a{};
+    a.wpr = K * nbits / 32;
+    a.gpl = K / group_size;
+    a.packed = packed + row0 * a.wpr;
+    a.scale = scale + row0 * a.gpl;
+    a.zero = zero + row0 * a.gpl;
+    a.n = n;
+    a.K = K;
+    a.gshift = log2_group(group_size);
+    a.ldw = round_up(K, kStep);
+    return a;
+}
+
+// floats of split sums that a product of up to M rows by N columns may need
+// (the largest over the row chunks: whole ones and the last)
+int64_t part_floats(int64_t M, int64_t N, int64_t steps)
+{
+    int64_t most = 0;
+    for (const int64_t m : {M < kRowChunk ? M : kRowChunk, M % kRowChunk})
+        if (m > 0) {
+            const int64_t f = (int64_t)gemm_splits(m, N, steps) * m * N;
+            most = f > most ? f : most;
+        }
+    return most;
+}
+
+void single_segment(GemmArgs &g, const uint16_t *A, int64_t lda, int64_t depth)
+{
+    g.A[0] = A;
+    g.lda[0] = lda;
+    g.rlen[0] = (int32_t)depth;
+    g.step0[0] = 0;
+    g.step0[1] = (int32_t)((depth + kStep - 1) / kStep);
+    g.segs = 1;
+    g.splits = 1;
+}
+
+// dX [M, K] = rowf * (A . WT^T): in one launch, or by split sums and a second;
+// acc: fp32 sums carried between pieces (null: one piece)
+hipError_t gradient_product(GemmArgs &g, bool bf16, float *part, float *acc, bool first, bool last, uint16_t *dX,
+                            const float *rowf, hipStream_t s)
+{
+    const int64_t M = g.M, K = g.N;
+    g.splits = gemm_splits(M, K, g.step0[g.segs]);
+    if (g.splits == 1 && first && last) {
+        g.out = dX;
+        g.ldo = K;
+        g.rowf = rowf;
+        return launch_gemm(kOutStore, bf16, g, s);
+    }
+    g.part = part;
+    if (const hipError_t e = launch_gemm(kOutPart, bf16, g, s))
+        return e;
+    ReduceArgs r{};
+    r.part = part;
+    r.splits = g.splits;
+    r.M = M;
+    r.N = K;
+    r.acc_in = first ? nullptr : acc;
+    r.acc_out = last ? nullptr : acc;
+    r.out = dX;
+    r.rowf = rowf;
+    return launch_reduce(bf16, r, s);
+}
+
+// ---------------------------------------------------------------------------
+// layouts
+// ---------------------------------------------------------------------------
+
+struct GatedLayout {
+    uint16_t *W;
+    int64_t bytes;
+    GatedLayout(void *p, int64_t, int64_t K, int64_t N)
+    {
+        Carve c(p);
+        W = c.take<uint16_t>(2 * N * round_up(K, kStep));
+        bytes = c.at;
+    }
+};
+
+struct GatedGradLayout {
+    uint16_t *W, *WT, *dGU;
+    float *scale, *inv, *part;
+    int64_t bytes;
+    GatedGradLayout(void *p, int64_t M, int64_t K, int64_t N)
+    {
+        const int64_t Np = round_up(N, kStep), mc = M < kRowChunk ? M : kRowChunk;
+        Carve c(p);
+        W = c.take<uint16_t>(2 * N * round_up(K, kStep));
+        WT = c.take<uint16_t>(K * 2 * Np);
+        dGU = c.take<uint16_t>(mc * 2 * Np);
+        scale = c.take<float>(mc);
+        inv = c.take<float>(mc);
+        part = c.take<float>(part_floats(M, K, 2 * Np / kStep));
+        bytes = c.at;
+    }
+};
+
+struct BatchGradLayout {
+    uint16_t *WT, *pad[HQQ_MAX_GRADS];
+    float *part;
+    int64_t bytes, ldt;
+    BatchGradLayout(void *p, int64_t M, int64_t K, const int64_t *n, int count)
+    {
+        const int64_t mc = M < kRowChunk ? M : kRowChunk;
+        Carve c(p);
+        ldt = 0;
+        for (int i = 0; i < count; ++i)
+            ldt += round_up(n[i], kStep);
+        WT = c.take<uint16_t>(K * ldt);
+        for (int i = 0; i < count; ++i)
+            pad[i] = n[i] % 8 ? c.take<uint16_t>(mc * round_up(n[i], 8)) : nullptr;
+        part = c.take<float>(part_floats(M, K, ldt / kStep));
+        bytes = c.at;
+    }
+};
+
+// classes per piece: W_hat of a piece takes about 128 MiB
+int64_t loss_piece(int64_t K, int64_t N)
+{
+    int64_t p = (int64_t(64) << 20) / round_up(K, kStep) / 256 * 256;
+    p = p < 4096 ? 4096 : p;
+    return p < N ? p : N;
+}
+
+struct LossLayout {
+    uint16_t *W;
+    float2 *stats, *state;
+    float *tlogit;
+    int64_t bytes, piece, blocks;
+    LossLayout(void *p, int64_t M, int64_t K, int64_t N)
+    {
+        piece = loss_piece(K, N);
+        blocks = (piece + 63) / 64;
+        Carve c(p);
+        W = c.take<uint16_t>(piece * round_up(K, kStep));
+        stats = c.take<float2>(M * blocks);
+        state = c.take<float2>(M);
+        tlogit = c.take<float>(M);
+        bytes = c.at;
+    }
+};
+
+// classes per piece of the backward pass: the 16-bit gradients of a piece's
+// logits take at most about 64 MiB, W_hat 128 MiB
+int64_t loss_grad_piece(int64_t M, int64_t K, int64_t N)
+{
+    const int64_t mc = M < kRowChunk ? M : kRowChunk;
+    int64_t p = (int64_t(32) << 20) / mc / 256 * 256;
+    const int64_t q = loss_piece(K, N);
+    p = p < 4096 ? 4096 : p;
+    p = p < q ? p : q;
+    return p < N ? p : N;
+}
+
+struct LossGradLayout {
+    uint16_t *W, *WT, *dL;
+    float *rowf, *part, *acc;
+    int64_t bytes, piece, ldl;
+    LossGradLayout(void *p, int64_t M, int64_t K, int64_t N)
+    {
+        const int64_t mc = M < kRowChunk ? M : kRowChunk;
+        piece = loss_grad_piece(M, K, N);
+        ldl = round_up(piece, kStep);
+        Carve c(p);
+        W = c.take<uint16_t>(piece * round_up(K, kStep));
+        WT = c.take<uint16_t>(K * ldl);
+        dL = c.take<uint16_t>(mc * ldl);
+        rowf = c.take<float>(mc);
+        int64_t f = part_floats(M, K, ldl / kStep);
+        const int64_t rest = N % piece;
+        if (rest) {
+            const int64_t f2 = part_floats(M, K, (rest + kStep - 1) / kStep);
+            f = f2 > f ? f2 : f;
+        }
+        part = c.take<float>(f);
+        acc = c.take<float>(piece < N ? mc * K : 0);
+        bytes = c.at;
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+const char *hqq_layers_strerror(int status)
+{
+    switch (status) {
+    case HQQ_OK: return "ok";
+    case HQQ_EINVAL_NBITS: return "nbits must be 1, 2, 4 or 8";
+    case HQQ_EINVAL_GROUP: return "group_size must be 8, 16, 32, 64, 128 or 256 and divide K";
+    case HQQ_EINVAL_SHAPE: return "a size is out of range (K a multiple of 32; M, N, count >= 1 and within their limits)";
+    case HQQ_EINVAL_PTR: return "a pointer is NULL or misaligned";
+    case HQQ_EHIP: return "a HIP kernel launch failed";
+    case HQQ_EINVAL_DTYPE: return "dtype must be HQQ_DTYPE_FP16 or HQQ_DTYPE_BF16";
+    case HQQ_EINVAL_ACT: return "act must be HQQ_ACT_SILU, HQQ_ACT_GELU or HQQ_ACT_GELU_TANH";
+    case HQQ_EWORKSPACE: return "the workspace is smaller than this call needs";
+    default: return "unknown status";
+    }
+}
+
+int64_t hqq_linear_gated_workspace(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    return GatedLayout(nullptr, M, K, N).bytes;
+}
+
+int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate, const hqq_weight *up, int64_t N,
+                     int nbits, int group_size, int dtype, int act, uint16_t *Y, void *workspace,
+                     int64_t workspace_bytes, void *stream)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    if (const int st = check_dtype(dtype))
+        return st;
+    if (act < HQQ_ACT_SILU || act > HQQ_ACT_GELU_TANH)
+        return HQQ_EINVAL_ACT;
+    if (!gate || !up || !weight_ok(gate->packed, gate->scale, gate->zero) || !weight_ok(up->packed, up->scale, up->zero) ||
+        !aligned(X, 16) || !aligned(Y, 16))
+        return HQQ_EINVAL_PTR;
+    const GatedLayout l(workspace, M, K, N);
+    if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
+        return st;
+    const bool bf16 = dtype == HQQ_DTYPE_BF16;
+    const hipStream_t s = (hipStream_t)stream;
+    const int64_t ldw = round_up(K, kStep);
+    for (int i = 0; i < 2; ++i) {
+        const hqq_weight &w = i ? *up : *gate;
+        UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
+        a.W = l.W + i * N * ldw;
+        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
+            return HQQ_EHIP;
+    }
+    GemmArgs g{};
+    single_segment(g, X, K, K);
+    g.B = l.W;
+    g.ldb = ldw;
+    g.B_up = N;
+    g.M = (int32_t)M;
+    g.N = (int32_t)N;
+    g.out = Y;
+    g.ldo = N;
+    g.act = act;
+    return launch_gemm(kOutGated, bf16, g, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
+}
+
+int64_t hqq_linear_gated_backward_workspace(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    return GatedGradLayout(nullptr, M, K, N).bytes;
+}
+
+int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate,
+                              const hqq_weight *up, int64_t N, int nbits, int group_size, int dtype, int act,
+                              uint16_t *dX, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    if (const int st = check_dtype(dtype))
+        return st;
+    if (act < HQQ_ACT_SILU || act > HQQ_ACT_GELU_TANH)
+        return HQQ_EINVAL_ACT;
+    if (!gate || !up || !weight_ok(gate->packed, gate->scale, gate->zero) || !weight_ok(up->packed, up->scale, up->zero) ||
+        !aligned(X, 16) || !aligned(dY, 16) || !aligned(dX, 16))
+        return HQQ_EINVAL_PTR;
+    const GatedGradLayout l(workspace, M, K, N);
+    if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
+        return st;
+    const bool bf16 = dtype == HQQ_DTYPE_BF16;
+    const hipStream_t s = (hipStream_t)stream;
+    const int64_t ldw = round_up(K, kStep), Np = round_up(N, kStep);
+    for (int i = 0; i < 2; ++i) {
+        const hqq_weight &w = i ? *up : *gate;
+        UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
+        a.W = l.W + i * N * ldw;
+        a.WT = l.WT + i * Np;
+        a.ldt = 2 * Np;
+        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
+            return HQQ_EHIP;
+    }
+    for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
+        const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
+        // fp16: dG and dU relative to the row's largest |dY| (bf16 has fp32's range)
+        if (!bf16 && launch_row_scale(dY + m0 * N, m, N, l.scale, l.inv, s) != hipSuccess)
+            return HQQ_EHIP;
+        GemmArgs g{};
+        single_segment(g, X + m0 * K, K, K);
+        g.B = l.W;
+        g.ldb = ldw;
+        g.B_up = N;
+        g.M = (int32_t)m;
+        g.N = (int32_t)N;
+        g.act = act;
+        g.dY = dY + m0 * N;
+        g.rscale = bf16 ? nullptr : l.scale;
+        g.out = l.dGU;
+        g.ldo = 2 * Np;
+        g.up_off = Np;
+        if (launch_gemm(kOutGatedGrad, bf16, g, s) != hipSuccess)
+            return HQQ_EHIP;
+        GemmArgs p{};
+        single_segment(p, l.dGU, 2 * Np, 2 * Np);
+        p.B = l.WT;
+        p.ldb = 2 * Np;
+        p.M = (int32_t)m;
+        p.N = (int32_t)K;
+        if (gradient_product(p, bf16, l.part, nullptr, true, true, dX + m0 * K, bf16 ? nullptr : l.inv, s) != hipSuccess)
+            return HQQ_EHIP;
+    }
+    return HQQ_OK;
+}
+
+int64_t hqq_linear_batch_backward_workspace(int64_t M, int64_t K, const int64_t *n, int count, int nbits, int group_size)
+{
+    if (count < 1 || count > HQQ_MAX_GRADS)
+        return HQQ_EINVAL_SHAPE;
+    if (!n)
+        return HQQ_EINVAL_PTR;
+    for (int i = 0; i < count; ++i)
+        if (const int st = check_sizes(M, K, n[i], nbits, group_size))
+            return st;
+    return BatchGradLayout(nullptr, M, K, n, count).bytes;
+}
+
+int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, int64_t K, int nbits, int group_size,
+                              int dtype, uint16_t *dX, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (count < 1 || count > HQQ_MAX_GRADS)
+        return HQQ_EINVAL_SHAPE;
+    if (!ws)
+        return HQQ_EINVAL_PTR;
+    int64_t n[HQQ_MAX_GRADS];
+    for (int i = 0; i < count; ++i) {
+        n[i] = ws[i].N;
+        if (const int st = check_sizes(M, K, n[i], nbits, group_size))
+            return st;
+    }
+    if (const int st = check_dtype(dtype))
+        return st;
+    if (!aligned(dX, 16))
+        return HQQ_EINVAL_PTR;
+    for (int i = 0; i < count; ++i)
+        if (!weight_ok(ws[i].packed, ws[i].scale, ws[i].zero) || !aligned(ws[i].dY, 16))
+            return HQQ_EINVAL_PTR;
+    const BatchGradLayout l(workspace, M, K, n, count);
+    if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
+        return st;
+    const bool bf16 = dtype == HQQ_DTYPE_BF16;
+    const hipStream_t s = (hipStream_t)stream;
+    int64_t col = 0;
+    for (int i = 0; i < count; ++i) {
+        UnpackArgs a = unpack_args(ws[i].packed, ws[i].scale, ws[i].zero, 0, n[i], K, nbits, group_size);
+        a.WT = l.WT + col;
+        a.ldt = l.ldt;
+        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
+            return HQQ_EHIP;
+        col += round_up(n[i], kStep);
+    }
+    for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
+        const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
+        GemmArgs g{};
+        g.segs = count;
+        for (int i = 0; i < count; ++i) {
+            g.A[i] = ws[i].dY + m0 * n[i];
+            g.lda[i] = n[i];
+            g.rlen[i] = (int32_t)n[i];
+            if (l.pad[i]) {
+                // rows that do not start at 16 bytes: a padded copy
+                const int64_t ld = round_up(n[i], 8);
+                if (launch_pad_rows(g.A[i], m, n[i], l.pad[i], ld, s) != hipSuccess)
+                    return HQQ_EHIP;
+                g.A[i] = l.pad[i];
+                g.lda[i] = ld;
+                g.rlen[i] = (int32_t)ld;
+            }
+            g.step0[i + 1] = g.step0[i] + (int32_t)((n[i] + kStep - 1) / kStep);
+        }
+        g.B = l.WT;
+        g.ldb = l.ldt;
+        g.M = (int32_t)m;
+        g.N = (int32_t)K;
+        if (gradient_product(g, bf16, l.part, nullptr, true, true, dX + m0 * K, nullptr, s) != hipSuccess)
+            return HQQ_EHIP;
+    }
+    return HQQ_OK;
+}
+
+int64_t hqq_linear_cross_entropy_workspace(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    return LossLayout(nullptr, M, K, N).bytes;
+}
+
+int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *head, int64_t N, int nbits,
+                             int group_size, int dtype, const int64_t *targets, float *loss, float *lse, void *workspace,
+                             int64_t workspace_bytes, void *stream)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    if (const int st = check_dtype(dtype))
+        return st;
+    if (!head || !weight_ok(head->packed, head->scale, head->zero) || !aligned(X, 16) || !aligned(targets, 8) ||
+        !aligned(loss, 4) || !aligned(lse, 4))
+        return HQQ_EINVAL_PTR;
+    const LossLayout l(workspace, M, K, N);
+    if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
+        return st;
+    const bool bf16 = dtype == HQQ_DTYPE_BF16;
+    const hipStream_t s = (hipStream_t)stream;
+    const int64_t ldw = round_up(K, kStep);
+    for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
+        const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
+        UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
+        a.W = l.W;
+        GemmArgs g{};
+        single_segment(g, X, K, K);
+        g.B = l.W;
+        g.ldb = ldw;
+        g.M = (int32_t)M;
+        g.N = (int32_t)n;
+        g.stats = l.stats;
+        g.blocks = (n + 63) / 64;
+        g.tlogit = l.tlogit;
+        g.targets = targets;
+        g.n0 = n0;
+        g.Nall = N;
+        LossArgs e{};
+        e.stats = l.stats;
+        e.blocks = g.blocks;
+        e.M = M;
+        e.N = N;
+        e.state = l.state;
+        e.tlogit = l.tlogit;
+        e.targets = targets;
+        e.loss = loss;
+        e.lse = lse;
+        e.first = n0 == 0;
+        e.last = n0 + n == N;
+        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess || launch_gemm(kOutStats, bf16, g, s) != hipSuccess ||
+            launch_loss(e, s) != hipSuccess)
+            return HQQ_EHIP;
+    }
+    return HQQ_OK;
+}
+
+int64_t hqq_linear_cross_entropy_backward_workspace(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    return LossGradLayout(nullptr, M, K, N).bytes;
+}
+
+int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *head,
+                                      int64_t N, int nbits, int group_size, int dtype, const int64_t *targets,
+                                      const float *lse, uint16_t *dX, void *workspace, int64_t workspace_bytes,
+                                      void *stream)
+{
+    if (const int st = check_sizes(M, K, N, nbits, group_size))
+        return st;
+    if (const int st = check_dtype(dtype))
+        return st;
+    if (!head || !weight_ok(head->packed, head->scale, head->zero) || !aligned(X, 16) || !aligned(dX, 16) ||
+        !aligned(targets, 8) || !aligned(dloss, 4) || !aligned(lse, 4))
+        return HQQ_EINVAL_PTR;
+    const LossGradLayout l(workspace, M, K, N);
+    if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
+        return st;
+    const bool bf16 = dtype == HQQ_DTYPE_BF16;
+    const hipStream_t s = (hipStream_t)stream;
+    const int64_t ldw = round_up(K, kStep);
+    for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
+        const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
+        if (launch_loss_factor(dloss + m0, targets + m0, m, N, bf16 ? 1.0f : 1.0f / 32768.0f, l.rowf, s) != hipSuccess)
+            return HQQ_EHIP;
+        for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
+            const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
+            UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
+            a.W = l.W;
+            a.WT = l.WT;
+            a.ldt = round_up(n, kStep);
+            GemmArgs g{};
+            single_segment(g, X + m0 * K, K, K);
+            g.B = l.W;
+            g.ldb = ldw;
+            g.M = (int32_t)m;
+            g.N = (int32_t)n;
+            g.targets = targets + m0;
+            g.lse = lse + m0;
+            g.n0 = n0;
+            g.Nall = N;
+            g.out = l.dL;
+            g.ldo = a.ldt;
+            GemmArgs p{};
+            single_segment(p, l.dL, a.ldt, a.ldt);
+            p.B = l.WT;
+            p.ldb = a.ldt;
+            p.M = (int32_t)m;
+            p.N = (int32_t)K;
+            if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess ||
+                launch_gemm(kOutSoftGrad, bf16, g, s) != hipSuccess ||
+                gradient_product(p, bf16, l.part, l.acc, n0 == 0, n0 + n == N, dX + m0 * K, l.rowf, s) != hipSuccess)
+                return HQQ_EHIP;
+        }
+    }
+    return HQQ_OK;
+}
+
+}  // extern "C"

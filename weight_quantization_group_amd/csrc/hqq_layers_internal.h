@@ -1,0 +1,111 @@
+// hqq_layers_internal.h -- declarations shared by libhqq_layers.so's own
+// translation units.
+#pragma once
+
+#include "hqq_internal.h"
+#include "hqq_layers.h"
+
+namespace hqq {
+
+constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Dequantization of n rows of a weight into the workspace (either output may
+// be null): W [n, ldw] row-major with columns K .. ldw - 1 zeroed, and its
+// transpose WT [K, ldt] with columns n .. round_up(n, 64) - 1 zeroed.
+struct UnpackArgs {
+    const uint32_t *packed;   // of the first row
+    const float *scale, *zero;
+    int64_t n, K;
+    int64_t wpr, gpl;         // words and groups per row
+    int gshift;               // log2 of the group size
+    uint16_t *W;
+    int64_t ldw;
+    uint16_t *WT;
+    int64_t ldt;
+};
+hipError_t launch_unpack_weight(int nbits, bool bf16, const UnpackArgs &a, hipStream_t s);
+
+// The matrix product C [M, N] = A [M, R] . B [N, R]^T of 16-bit matrices with
+// fp32 sums, and what becomes of C.  A comes in segments along R (each a
+// matrix of its own, its columns padded to whole 64-wide steps by the reader
+// with zeros); B is one matrix in the workspace whose columns are zero
+// wherever A's are padding.
+constexpr int kStep = 64;            // depth of a step
+constexpr int kMaxSegs = HQQ_MAX_GRADS;
+
+enum GemmOut {
+    kOutStore,      // out16 = round(rowf * C)
+    kOutPart,       // part[z] = C over this split's steps (fp32)
+    kOutGated,      // out16 = act(C_gate) * C_up
+    kOutGatedGrad,  // dG, dU from C_gate, C_up and dY
+    kOutStats,      // per row and 64 columns: max and sum of exp of the logits
+    kOutSoftGrad    // exp(C - lse) - onehot(target)
+};
+
+struct GemmArgs {
+    const uint16_t *A[kMaxSegs];     // segment i: [M, rlen[i]], row pitch lda[i]
+    int64_t lda[kMaxSegs];
+    int32_t rlen[kMaxSegs];          // a multiple of 8
+    int32_t step0[kMaxSegs + 1];     // first step of each segment; step0[segs]: their number
+    int segs;
+    const uint16_t *B;               // [N, ldb]; gated: gate rows, then (at row B_up) up rows
+    int64_t ldb, B_up;
+    int32_t M, N;
+    int splits;                      // kOutPart: parts of the steps
+    int tiles_m, tiles_n;            // filled by the launcher
+    // outputs
+    uint16_t *out;                   // [M, ldo]
+    int64_t ldo;
+    float *part;                     // kOutPart: [splits, M, N]
+    const float *rowf;               // kOutStore: per-row factor or null
+    int act;
+    const uint16_t *dY;              // kOutGatedGrad: [M, N]
+    const float *rscale;             // per-row scale of dG and dU, or null
+    int64_t up_off;                  // kOutGatedGrad: dU's first column in out; columns N .. up_off - 1 zeroed
+    float2 *stats;                   // kOutStats: [M, blocks] (max, sum)
+    int64_t blocks;
+    float *tlogit;                   // kOutStats: the target's logit, where it is in this piece
+    const int64_t *targets;
+    const float *lse;
+    int64_t n0, Nall;                // first class of this piece, and all classes
+};
+hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s);
+// Splits of the steps for a kOutPart product (none of them empty).
+int gemm_splits(int64_t M, int64_t N, int64_t steps);
+
+// Sum of the parts: v = sum_z part[z] (+ acc_in), then out = round(rowf * v),
+// or acc_out = v.  M x N values, N a multiple of 4.
+struct ReduceArgs {
+    const float *part;
+    int splits;
+    int64_t M, N;
+    const float *acc_in;
+    float *acc_out;
+    uint16_t *out;
+    const float *rowf;
+};
+hipError_t launch_reduce(bool bf16, const ReduceArgs &a, hipStream_t s);
+
+// Cross entropy, the end of a piece: the blocks' (max, sum) of each row join
+// the row's state; last: loss and lse.
+struct LossArgs {
+    const float2 *stats;
+    int64_t blocks, M, N;
+    float2 *state;
+    const float *tlogit;
+    const int64_t *targets;
+    float *loss, *lse;
+    int first, last;
+};
+hipError_t launch_loss(const LossArgs &a, hipStream_t s);
+
+// rowf[m] = dloss[m] * mul, 0 for ignored rows
+hipError_t launch_loss_factor(const float *dloss, const int64_t *targets, int64_t M, int64_t N, float mul,
+                              float *rowf, hipStream_t s);
+// fp16 rows [M, N]: scale[m] = the power of two that brings max |row| to
+// [2^-7, 2^-6), inv[m] = 1 / scale[m] (1 for rows that are zero or not finite)
+hipError_t launch_row_scale(const uint16_t *rows, int64_t M, int64_t N, float *scale, float *inv, hipStream_t s);
+// dst [M, ldd] = src [M, N], columns N .. ldd - 1 zeroed
+hipError_t launch_pad_rows(const uint16_t *src, int64_t M, int64_t N, uint16_t *dst, int64_t ldd, hipStream_t s);
+
+}  // namespace hqq

@@ -1,0 +1,180 @@
+// hqq_layers_rows.hip -- the small row-wise kernels around the layers' products:
+// joining split sums and the softmax blocks, row factors, padded copies.
+#include "hqq_layers_internal.h"
+#include "hqq_linear_dev.h"
+
+namespace hqq {
+namespace {
+
+constexpr int kRowsBlock = 256;
+
+// parts of a split product added in split order in fp32; 4 values per lane
+template <bool BF>
+__global__ __launch_bounds__(kRowsBlock) void reduce_kernel(ReduceArgs a)
+{
+    const int64_t i = ((int64_t)blockIdx.x * kRowsBlock + threadIdx.x) * 4;
+    const int64_t total = a.M * a.N;
+    if (i >= total)
+        return;
+    float4v v = *reinterpret_cast<const float4v *>(a.part + i);
+    for (int z = 1; z < a.splits; ++z)
+        v += *reinterpret_cast<const float4v *>(a.part + z * total + i);
+    if (a.acc_in)
+        v += *reinterpret_cast<const float4v *>(a.acc_in + i);
+    if (a.acc_out) {
+        *reinterpret_cast<float4v *>(a.acc_out + i) = v;
+        return;
+    }
+    const float f = a.rowf ? a.rowf[i / a.N] : 1.0f;
+    *reinterpret_cast<uint2 *>(a.out + i) = uint2{out2<BF>(v[0] * f, v[1] * f), out2<BF>(v[2] * f, v[3] * f)};
+}
+
+// (max, sum) pairs of sums of exponentials; an empty one is (-inf, 0)
+__device__ __forceinline__ float2 join(float2 a, float2 b)
+{
+    const float m = fmaxf(a.x, b.x);
+    if (!(m > -INFINITY))
+        return float2{m, a.y + b.y};     // both empty (or a NaN, which stays)
+    return float2{m, a.y * expf(a.x - m) + b.y * expf(b.x - m)};
+}
+
+// one wave per row
+__global__ __launch_bounds__(kRowsBlock) void loss_kernel(LossArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * (kRowsBlock / 64) + (threadIdx.x >> 6);
+    if (m >= a.M)
+        return;
+    float2 s{-INFINITY, 0.0f};
+    for (int64_t b = lane; b < a.blocks; b += 64)
+        s = join(s, a.stats[m * a.blocks + b]);
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2)
+        s = join(s, float2{__shfl_xor(s.x, o), __shfl_xor(s.y, o)});
+    if (lane != 0)
+        return;
+    if (!a.first)
+        s = join(a.state[m], s);
+    if (!a.last) {
+        a.state[m] = s;
+        return;
+    }
+    // lse of the others, then the target joins: with d = lse_others - l_t,
+    // loss = log(1 + exp(d)), lse = l_t + loss
+    const float others = s.x + logf(s.y);
+    const int64_t t = a.targets[m];
+    if (t < 0 || t >= a.N) {
+        a.loss[m] = 0.0f;
+        a.lse[m] = others;
+        return;
+    }
+    const float lt = a.tlogit[m];
+    const float d = a.N > 1 ? others - lt : -INFINITY;
+    const float tail = log1pf(expf(-fabsf(d)));
+    a.loss[m] = fmaxf(d, 0.0f) + tail;
+    a.lse[m] = (d > 0.0f ? others : lt) + tail;
+}
+
+__global__ __launch_bounds__(kRowsBlock) void loss_factor_kernel(const float *dloss, const int64_t *targets, int64_t M,
+                                                                 int64_t N, float mul, float *rowf)
+{
+    const int64_t m = (int64_t)blockIdx.x * kRowsBlock + threadIdx.x;
+    if (m < M)
+        rowf[m] = targets[m] >= 0 && targets[m] < N ? dloss[m] * mul : 0.0f;
+}
+
+// one workgroup per row; fp16 magnitudes compare as their bits
+__global__ __launch_bounds__(kRowsBlock) void row_scale_kernel(const uint16_t *rows, int64_t N, float *scale, float *inv)
+{
+    __shared__ uint32_t top[kRowsBlock / 64];
+    const uint16_t *r = rows + (int64_t)blockIdx.x * N;
+    uint32_t mx = 0;
+    for (int64_t i = threadIdx.x; i < N; i += kRowsBlock) {
+        const uint32_t b = r[i] & 0x7fffu;
+        mx = b > mx ? b : mx;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        const uint32_t b = (uint32_t)__shfl_xor((int)mx, o);
+        mx = b > mx ? b : mx;
+    }
+    if ((threadIdx.x & 63) == 0)
+        top[threadIdx.x >> 6] = mx;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kRowsBlock / 64; ++w)
+            mx = top[w] > mx ? top[w] : mx;
+        float f = 1.0f;
+        if (mx > 0 && mx < 0x7c00u) {
+            _Float16 h;
+            const uint16_t b = (uint16_t)mx;
+            __builtin_memcpy(&h, &b, 2);
+            int e;
+            frexpf((float)h, &e);          // max = f * 2^e, f in [1/2, 1)
+            f = ldexpf(1.0f, -6 - e);
+        }
+        scale[blockIdx.x] = f;
+        inv[blockIdx.x] = 1.0f / f;
+    }
+}
+
+__global__ __launch_bounds__(kRowsBlock) void pad_rows_kernel(const uint16_t *src, int64_t M, int64_t N, uint16_t *dst,
+                                                              int64_t ldd)
+{
+    const int64_t i = ((int64_t)blockIdx.x * kRowsBlock + threadIdx.x) * 8;
+    if (i >= M * ldd)
+        return;
+    const int64_t m = i / ldd, n = i - m * ldd;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = n + 2 * j < N ? src[m * N + n + 2 * j] : 0u;
+        const uint32_t hi = n + 2 * j + 1 < N ? src[m * N + n + 2 * j + 1] : 0u;
+        w[j] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint4 *>(dst + i) = uint4{w[0], w[1], w[2], w[3]};
+}
+
+unsigned blocks_for(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+
+}  // namespace
+
+hipError_t launch_reduce(bool bf16, const ReduceArgs &a, hipStream_t s)
+{
+    const dim3 grid(blocks_for(a.M * a.N, 4 * kRowsBlock));
+    if (bf16)
+        hipLaunchKernelGGL((reduce_kernel<true>), grid, dim3(kRowsBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((reduce_kernel<false>), grid, dim3(kRowsBlock), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss(const LossArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL(loss_kernel, dim3(blocks_for(a.M, kRowsBlock / 64)), dim3(kRowsBlock), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_factor(const float *dloss, const int64_t *targets, int64_t M, int64_t N, float mul, float *rowf,
+                              hipStream_t s)
+{
+    hipLaunchKernelGGL(loss_factor_kernel, dim3(blocks_for(M, kRowsBlock)), dim3(kRowsBlock), 0, s, dloss, targets, M, N,
+                       mul, rowf);
+    return hipGetLastError();
+}
+
+hipError_t launch_row_scale(const uint16_t *rows, int64_t M, int64_t N, float *scale, float *inv, hipStream_t s)
+{
+    hipLaunchKernelGGL(row_scale_kernel, dim3((unsigned)M), dim3(kRowsBlock), 0, s, rows, N, scale, inv);
+    return hipGetLastError();
+}
+
+hipError_t launch_pad_rows(const uint16_t *src, int64_t M, int64_t N, uint16_t *dst, int64_t ldd, hipStream_t s)
+{
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks_for(M * ldd, 8 * kRowsBlock)), dim3(kRowsBlock), 0, s, src, M, N, dst,
+                       ldd);
+    return hipGetLastError();
+}
+
+}  // namespace hqq

@@ -1,0 +1,119 @@
+// hqq_layers_unpack.hip -- a weight's W_hat and its transpose, written to the
+// workspace for the products of many rows.
+//
+// W_hat is bit for bit what the dequantize kernel writes (the fp64 product of
+// hqq_linear_dev.h in place of the division).  A lane takes 8 rows n by one run
+// of 8 consecutive k: 64 values in registers are both the 8 row runs of W
+// (16 bytes each) and, after one byte permutation per pair (the other steps of
+// the 8 x 8 transposition only rename registers), the 8 column runs of W^T.  The
+// 64 lanes of a wave are 8 x 8 such squares, so that each row of codes is read,
+// and each row of W and of W^T written, in whole 128-byte (codes: 8 to 64 byte)
+// stretches.  Bound by the bytes written.
+#include "hqq_layers_internal.h"
+#include "hqq_linear_dev.h"
+
+namespace hqq {
+namespace {
+
+constexpr int kUnpackWaves = 4;
+
+template <int NB, bool BF, bool WANT_W, bool WANT_T>
+__global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
+{
+    constexpr uint32_t MASK = (1u << NB) - 1u;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int kl = lane & 7, nl = lane >> 3;
+    const uint32_t kblocks = (uint32_t)((a.K + 63) / 64), nb = blockIdx.x / kblocks;
+    const int64_t run = (int64_t)(blockIdx.x - nb * kblocks) * 8 + kl;      // 8-k run of the row
+    const int64_t n0 = ((int64_t)nb * kUnpackWaves + wave) * 64 + 8 * nl;
+    const int64_t runs = a.K / 8;
+    const bool k_in = run < runs;
+    if (n0 >= round_up(a.n, 64) || run * 8 >= a.ldw)
+        return;
+
+    uint32_t v[8][4];     // row i: 8 values of the run
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t n = n0 + i < a.n ? n0 + i : a.n - 1;
+        const int64_t r = k_in ? run : runs - 1;
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(a.packed + n * a.wpr) + r * NB;
+        uint32_t w[2] = {0, 0};
+        if constexpr (NB == 8) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x;
+            w[1] = u.y;
+        } else if constexpr (NB == 4) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else if constexpr (NB == 2) {
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
+        } else {
+            w[0] = *p;
+        }
+        const int64_t g = n * a.gpl + ((8 * r) >> a.gshift);
+        const float z = a.zero[g];
+        const double R = 1.0 / (double)a.scale[g];
+        const bool in = k_in && n0 + i < a.n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int b0 = 2 * j * NB, b1 = (2 * j + 1) * NB;
+            const float x = wq((float)((w[b0 / 32] >> (b0 % 32)) & MASK), z, R);
+            const float y = wq((float)((w[b1 / 32] >> (b1 % 32)) & MASK), z, R);
+            v[i][j] = in ? out2<BF>(x, y) : 0u;
+        }
+    }
+    if constexpr (WANT_W) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n0 + i < a.n)
+                *reinterpret_cast<uint4 *>(a.W + (n0 + i) * a.ldw + run * 8) = uint4{v[i][0], v[i][1], v[i][2], v[i][3]};
+    }
+    if constexpr (WANT_T) {
+        if (k_in) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t sel = k & 1 ? 0x07060302u : 0x05040100u;
+                uint4 o;
+                o.x = perm(v[1][k / 2], v[0][k / 2], sel);
+                o.y = perm(v[3][k / 2], v[2][k / 2], sel);
+                o.z = perm(v[5][k / 2], v[4][k / 2], sel);
+                o.w = perm(v[7][k / 2], v[6][k / 2], sel);
+                *reinterpret_cast<uint4 *>(a.WT + (run * 8 + k) * a.ldt + n0) = o;
+            }
+        }
+    }
+}
+
+template <int NB, bool BF>
+hipError_t launch_nb(const UnpackArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.K + 63) / 64 * ((a.n + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves))));
+    const dim3 block(kUnpackWaves * 64);
+    if (a.W && a.WT)
+        hipLaunchKernelGGL((unpack_kernel<NB, BF, true, true>), grid, block, 0, s, a);
+    else if (a.W)
+        hipLaunchKernelGGL((unpack_kernel<NB, BF, true, false>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((unpack_kernel<NB, BF, false, true>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_bits(int nbits, const UnpackArgs &a, hipStream_t s)
+{
+    switch (nbits) {
+    case 1: return launch_nb<1, BF>(a, s);
+    case 2: return launch_nb<2, BF>(a, s);
+    case 4: return launch_nb<4, BF>(a, s);
+    case 8: return launch_nb<8, BF>(a, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_unpack_weight(int nbits, bool bf16, const UnpackArgs &a, hipStream_t s)
+{
+    return bf16 ? launch_bits<true>(nbits, a, s) : launch_bits<false>(nbits, a, s);
+}
+
+}  // namespace hqq
