@@ -56,8 +56,9 @@ typedef struct hqq_weight {
 /* Gated feed-forward block: Y = act(X . Wg_hat^T) * (X . Wu_hat^T).
  *   X     [M, K], gate and up: weights [N, K] of one format, Y [M, N]
  * Both projections stay in fp32; each output is rounded once.
- * Limits (HQQ_EINVAL_SHAPE): M, N >= 1; M <= 2^20; K <= 2^17; X and Y below
- * 2^40 values; the codes and the meta of a weight each below 2^31 bytes. */
+ * Limits of all calls (HQQ_EINVAL_SHAPE): M, N >= 1; M <= 2^20; K <= 2^17;
+ * N <= 2^22; M * N <= 2^40; the codes and the meta of a weight each below 2^31
+ * bytes. */
 HQQ_API int64_t hqq_linear_gated_workspace(int64_t M, int64_t K, int64_t N, int nbits, int group_size);
 HQQ_API int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate,
                              const hqq_weight *up, int64_t N, int nbits, int group_size, int dtype,
@@ -92,7 +93,8 @@ typedef struct hqq_linear_grad {
  * weights [N_i, K] of one format that read the same X [M, K] (count = 1: the
  * backward pass of hqq_linear).  The sum over all weights and outputs is one
  * fp32 sum, rounded once.
- *   ws  HOST array of count descriptors, 1 <= count <= HQQ_MAX_GRADS
+ *   ws  HOST array of count descriptors, 1 <= count <= HQQ_MAX_GRADS; their N,
+ *       each rounded up to 64, add up to at most 2^23
  *   n   (workspace function) HOST array of the count widths N_i */
 #define HQQ_MAX_GRADS 16
 HQQ_API int64_t hqq_linear_batch_backward_workspace(int64_t M, int64_t K, const int64_t *n, int count,

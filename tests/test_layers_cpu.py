@@ -64,8 +64,9 @@ SIZES = [
     (dict(nbits=3), NBITS), (dict(nbits=16), NBITS),
     (dict(M=0), SHAPE), (dict(M=(1 << 20) + 1), SHAPE), (dict(K=0), SHAPE), (dict(K=48), SHAPE),
     (dict(K=1 << 18), SHAPE), (dict(N=0), SHAPE), (dict(N=-3), SHAPE), (dict(N=1 << 40), SHAPE),
-    (dict(N=1 << 26, K=64, gs=8), SHAPE),                   # the codes take 2^31 bytes
-    (dict(N=1 << 26, K=64, gs=8, nbits=1), SHAPE),          # the meta does
+    (dict(N=(1 << 22) + 1), SHAPE),
+    (dict(N=1 << 20, K=4096, gs=256), SHAPE),               # the codes take 2^31 bytes
+    (dict(N=1 << 20, K=4096, gs=8, nbits=1), SHAPE),        # the meta does
     (dict(gs=48), GROUP), (dict(gs=4), GROUP), (dict(gs=512, K=512), GROUP), (dict(K=96, gs=64), GROUP),
 ]
 
@@ -184,3 +185,12 @@ def test_binding_refuses_host_tensors(w):
             call()
     with pytest.raises(ValueError):
         w.hqq_linear_batch_backward([], [], 128, 4, 64)
+
+
+def test_batch_width_limit(w, lib):
+    """Every width may be within its limit and their sum beyond the batch's."""
+    from weight_quantization_group_amd.layers import HqqLinearGrad
+    N = 1 << 22
+    arr = (HqqLinearGrad * 3)(*[HqqLinearGrad(A, A, A, N, A)] * 3)
+    assert lib.hqq_linear_batch_backward(arr, 3, 1, 32, 1, 32, 0, A, A, 1 << 40, None) == SHAPE
+    assert lib.hqq_linear_batch_backward(arr, 2, 1, 32, 1, 32, 0, A, A, 0, None) == WORKSPACE

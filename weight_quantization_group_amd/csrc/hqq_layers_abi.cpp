@@ -9,7 +9,8 @@ namespace {
 using namespace hqq;
 
 constexpr int64_t kMaxRows = int64_t(1) << 20;
-constexpr int64_t kMaxDepth32 = int64_t(1) << 17;
+constexpr int64_t kMaxDepth = int64_t(1) << 17;
+constexpr int64_t kMaxWidth = int64_t(1) << 22;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxBytes = int64_t(1) << 31;
 // The backward passes keep 16-bit gradients of this many rows at a time.
@@ -29,7 +30,7 @@ int check_sizes(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
 {
     if (!valid_nbits(nbits) || nbits == 3)
         return HQQ_EINVAL_NBITS;
-    if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > kMaxRows || K > kMaxDepth32 || N > kMaxBytes ||
+    if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > kMaxRows || K > kMaxDepth || N > kMaxWidth ||
         M * N > kMaxElems || N * (K * nbits / 32) * 4 >= kMaxBytes)
         return HQQ_EINVAL_SHAPE;
     if (log2_group(group_size) < 0 || K % group_size != 0)
@@ -37,6 +38,17 @@ int check_sizes(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
     if (N * (K / group_size) * 4 >= kMaxBytes)
         return HQQ_EINVAL_SHAPE;
     return HQQ_OK;
+}
+
+int check_batch(int64_t M, int64_t K, const int64_t *n, int count, int nbits, int group_size)
+{
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) {
+        if (const int st = check_sizes(M, K, n[i], nbits, group_size))
+            return st;
+        total += round_up(n[i], kStep);
+    }
+    return total > 2 * kMaxWidth ? HQQ_EINVAL_SHAPE : HQQ_OK;
 }
 
 int check_dtype(int dtype)
@@ -69,6 +81,11 @@ struct Carve {
         at += round_up(n * (int64_t)sizeof(T), 256);
         return p;
     }
+    template <typename T>
+    T *take_some(int64_t n)        // null for none
+    {
+        return n ? take<T>(n) : nullptr;
+    }
 };
 
 UnpackArgs unpack_args(const uint32_t *packed, const float *scale, const float *zero, int64_t row0, int64_t n, int64_t K,
@@ -100,13 +117,26 @@ int64_t part_floats(int64_t M, int64_t N, int64_t steps)
     return most;
 }
 
-void single_segment(GemmArgs &g, const uint16_t *A, int64_t lda, int64_t depth)
+// A [m, depth] whose rows end inside a step, copied with zeros up to its end (pad:
+// room for that, or null where they end with one)
+hipError_t whole_steps(const uint16_t *&A, int64_t m, int64_t depth, uint16_t *pad, hipStream_t s)
+{
+    if (!pad)
+        return hipSuccess;
+    const uint16_t *src = A;
+    A = pad;
+    return launch_pad_rows(src, m, depth, pad, round_up(depth, kStep), s);
+}
+
+int64_t pad_values(int64_t m, int64_t depth) { return depth % kStep ? m * round_up(depth, kStep) : 0; }
+
+// one segment of whole steps, contiguous
+void single_segment(GemmArgs &g, const uint16_t *A, int64_t depth)
 {
     g.A[0] = A;
-    g.lda[0] = lda;
-    g.rlen[0] = (int32_t)depth;
+    g.lda[0] = depth;
     g.step0[0] = 0;
-    g.step0[1] = (int32_t)((depth + kStep - 1) / kStep);
+    g.step0[1] = (int32_t)(depth / kStep);
     g.segs = 1;
     g.splits = 1;
 }
@@ -144,25 +174,27 @@ hipError_t gradient_product(GemmArgs &g, bool bf16, float *part, float *acc, boo
 // ---------------------------------------------------------------------------
 
 struct GatedLayout {
-    uint16_t *W;
+    uint16_t *W, *X;
     int64_t bytes;
-    GatedLayout(void *p, int64_t, int64_t K, int64_t N)
+    GatedLayout(void *p, int64_t M, int64_t K, int64_t N)
     {
         Carve c(p);
-        W = c.take<uint16_t>(2 * N * round_up(K, kStep));
+        W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
+        X = c.take_some<uint16_t>(pad_values(M, K));
         bytes = c.at;
     }
 };
 
 struct GatedGradLayout {
-    uint16_t *W, *WT, *dGU;
+    uint16_t *W, *WT, *dGU, *X;
     float *scale, *inv, *part;
     int64_t bytes;
     GatedGradLayout(void *p, int64_t M, int64_t K, int64_t N)
     {
         const int64_t Np = round_up(N, kStep), mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
-        W = c.take<uint16_t>(2 * N * round_up(K, kStep));
+        W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
+        X = c.take_some<uint16_t>(pad_values(mc, K));
         WT = c.take<uint16_t>(K * 2 * Np);
         dGU = c.take<uint16_t>(mc * 2 * Np);
         scale = c.take<float>(mc);
@@ -185,7 +217,7 @@ struct BatchGradLayout {
             ldt += round_up(n[i], kStep);
         WT = c.take<uint16_t>(K * ldt);
         for (int i = 0; i < count; ++i)
-            pad[i] = n[i] % 8 ? c.take<uint16_t>(mc * round_up(n[i], 8)) : nullptr;
+            pad[i] = c.take_some<uint16_t>(pad_values(mc, n[i]));
         part = c.take<float>(part_floats(M, K, ldt / kStep));
         bytes = c.at;
     }
@@ -200,7 +232,7 @@ int64_t loss_piece(int64_t K, int64_t N)
 }
 
 struct LossLayout {
-    uint16_t *W;
+    uint16_t *W, *X;
     float2 *stats, *state;
     float *tlogit;
     int64_t bytes, piece, blocks;
@@ -210,6 +242,7 @@ struct LossLayout {
         blocks = (piece + 63) / 64;
         Carve c(p);
         W = c.take<uint16_t>(piece * round_up(K, kStep));
+        X = c.take_some<uint16_t>(pad_values(M, K));
         stats = c.take<float2>(M * blocks);
         state = c.take<float2>(M);
         tlogit = c.take<float>(M);
@@ -230,7 +263,7 @@ int64_t loss_grad_piece(int64_t M, int64_t K, int64_t N)
 }
 
 struct LossGradLayout {
-    uint16_t *W, *WT, *dL;
+    uint16_t *W, *WT, *dL, *X;
     float *rowf, *part, *acc;
     int64_t bytes, piece, ldl;
     LossGradLayout(void *p, int64_t M, int64_t K, int64_t N)
@@ -242,6 +275,7 @@ struct LossGradLayout {
         W = c.take<uint16_t>(piece * round_up(K, kStep));
         WT = c.take<uint16_t>(K * ldl);
         dL = c.take<uint16_t>(mc * ldl);
+        X = c.take_some<uint16_t>(pad_values(mc, K));
         rowf = c.take<float>(mc);
         int64_t f = part_floats(M, K, ldl / kStep);
         const int64_t rest = N % piece;
@@ -304,15 +338,17 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
     for (int i = 0; i < 2; ++i) {
         const hqq_weight &w = i ? *up : *gate;
         UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
-        a.W = l.W + i * N * ldw;
+        a.W = l.W;
+        a.interleave = 1 + i;
         if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
             return HQQ_EHIP;
     }
+    if (whole_steps(X, M, K, l.X, s) != hipSuccess)
+        return HQQ_EHIP;
     GemmArgs g{};
-    single_segment(g, X, K, K);
+    single_segment(g, X, ldw);
     g.B = l.W;
     g.ldb = ldw;
-    g.B_up = N;
     g.M = (int32_t)M;
     g.N = (int32_t)N;
     g.out = Y;
@@ -350,7 +386,8 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     for (int i = 0; i < 2; ++i) {
         const hqq_weight &w = i ? *up : *gate;
         UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
-        a.W = l.W + i * N * ldw;
+        a.W = l.W;
+        a.interleave = 1 + i;
         a.WT = l.WT + i * Np;
         a.ldt = 2 * Np;
         if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
@@ -361,11 +398,13 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         // fp16: dG and dU relative to the row's largest |dY| (bf16 has fp32's range)
         if (!bf16 && launch_row_scale(dY + m0 * N, m, N, l.scale, l.inv, s) != hipSuccess)
             return HQQ_EHIP;
+        const uint16_t *x = X + m0 * K;
+        if (whole_steps(x, m, K, l.X, s) != hipSuccess)
+            return HQQ_EHIP;
         GemmArgs g{};
-        single_segment(g, X + m0 * K, K, K);
+        single_segment(g, x, ldw);
         g.B = l.W;
         g.ldb = ldw;
-        g.B_up = N;
         g.M = (int32_t)m;
         g.N = (int32_t)N;
         g.act = act;
@@ -377,7 +416,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         if (launch_gemm(kOutGatedGrad, bf16, g, s) != hipSuccess)
             return HQQ_EHIP;
         GemmArgs p{};
-        single_segment(p, l.dGU, 2 * Np, 2 * Np);
+        single_segment(p, l.dGU, 2 * Np);
         p.B = l.WT;
         p.ldb = 2 * Np;
         p.M = (int32_t)m;
@@ -394,9 +433,8 @@ int64_t hqq_linear_batch_backward_workspace(int64_t M, int64_t K, const int64_t 
         return HQQ_EINVAL_SHAPE;
     if (!n)
         return HQQ_EINVAL_PTR;
-    for (int i = 0; i < count; ++i)
-        if (const int st = check_sizes(M, K, n[i], nbits, group_size))
-            return st;
+    if (const int st = check_batch(M, K, n, count, nbits, group_size))
+        return st;
     return BatchGradLayout(nullptr, M, K, n, count).bytes;
 }
 
@@ -408,11 +446,10 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
     if (!ws)
         return HQQ_EINVAL_PTR;
     int64_t n[HQQ_MAX_GRADS];
-    for (int i = 0; i < count; ++i) {
+    for (int i = 0; i < count; ++i)
         n[i] = ws[i].N;
-        if (const int st = check_sizes(M, K, n[i], nbits, group_size))
-            return st;
-    }
+    if (const int st = check_batch(M, K, n, count, nbits, group_size))
+        return st;
     if (const int st = check_dtype(dtype))
         return st;
     if (!aligned(dX, 16))
@@ -440,17 +477,9 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
         g.segs = count;
         for (int i = 0; i < count; ++i) {
             g.A[i] = ws[i].dY + m0 * n[i];
-            g.lda[i] = n[i];
-            g.rlen[i] = (int32_t)n[i];
-            if (l.pad[i]) {
-                // rows that do not start at 16 bytes: a padded copy
-                const int64_t ld = round_up(n[i], 8);
-                if (launch_pad_rows(g.A[i], m, n[i], l.pad[i], ld, s) != hipSuccess)
-                    return HQQ_EHIP;
-                g.A[i] = l.pad[i];
-                g.lda[i] = ld;
-                g.rlen[i] = (int32_t)ld;
-            }
+            g.lda[i] = round_up(n[i], kStep);
+            if (whole_steps(g.A[i], m, n[i], l.pad[i], s) != hipSuccess)
+                return HQQ_EHIP;
             g.step0[i + 1] = g.step0[i] + (int32_t)((n[i] + kStep - 1) / kStep);
         }
         g.B = l.WT;
@@ -487,12 +516,14 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const int64_t ldw = round_up(K, kStep);
+    if (whole_steps(X, M, K, l.X, s) != hipSuccess)
+        return HQQ_EHIP;
     for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
         const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
         UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
         a.W = l.W;
         GemmArgs g{};
-        single_segment(g, X, K, K);
+        single_segment(g, X, ldw);
         g.B = l.W;
         g.ldb = ldw;
         g.M = (int32_t)M;
@@ -551,6 +582,9 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
         if (launch_loss_factor(dloss + m0, targets + m0, m, N, bf16 ? 1.0f : 1.0f / 32768.0f, l.rowf, s) != hipSuccess)
             return HQQ_EHIP;
+        const uint16_t *x = X + m0 * K;
+        if (whole_steps(x, m, K, l.X, s) != hipSuccess)
+            return HQQ_EHIP;
         for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
             const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
             UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
@@ -558,7 +592,7 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             a.WT = l.WT;
             a.ldt = round_up(n, kStep);
             GemmArgs g{};
-            single_segment(g, X + m0 * K, K, K);
+            single_segment(g, x, ldw);
             g.B = l.W;
             g.ldb = ldw;
             g.M = (int32_t)m;
@@ -570,7 +604,7 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             g.out = l.dL;
             g.ldo = a.ldt;
             GemmArgs p{};
-            single_segment(p, l.dL, a.ldt, a.ldt);
+            single_segment(p, l.dL, a.ldt);
             p.B = l.WT;
             p.ldb = a.ldt;
             p.M = (int32_t)m;

@@ -3,8 +3,8 @@
 // cores, and the operators' arithmetic on C while it is in registers.
 //
 // A workgroup computes a BM x BN tile of C with WM x WN waves.  Each 64-wide step
-// of A and B goes from memory to LDS by DMA (no registers) into one of two
-// buffers while the other is multiplied; a row's eight 16-byte runs are stored
+// of A and B goes from memory to LDS by DMA (no registers), into two buffers in
+// turn; a row's eight 16-byte runs are stored
 // XOR-swizzled by the row's low bits, so that the 16 rows of an operand read
 // spread over the banks.  The product is formed transposed (the rows of B are
 // the instruction's rows): a lane then holds 4 consecutive columns n of one row
@@ -16,15 +16,12 @@ namespace hqq {
 namespace {
 
 // 16 bytes per lane from p into LDS at lds + 16 lane (lds the same in all lanes)
-__device__ __forceinline__ void dma16(const uint16_t *p, uint4 *lds)
+__device__ __forceinline__ void dma16(const void *p, uint4 *lds)
 {
 #ifdef __HIP_DEVICE_COMPILE__
     __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 #endif
 }
-
-// what a run past the end of a segment of A reads
-__device__ const uint4 zero_run = {0, 0, 0, 0};
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -36,16 +33,17 @@ __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcp
 // act(g) and, for the backward pass, act'(g).  Each activation is g * p with p in
 // (0, 1) formed without cancellation (erfc, and (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))),
 // so that its far negative tail keeps its relative precision.
-__device__ __forceinline__ float act_value(int act, float g, float &d)
+template <int ACT>
+__device__ __forceinline__ float act_value(float g, float &d)
 {
-    if (act == HQQ_ACT_GELU) {
+    if constexpr (ACT == HQQ_ACT_GELU) {
         const float p = 0.5f * erfcf(g * -0.70710678118654752440f);
         d = p + g * 0.39894228040143267794f * exp2_fast(-0.5f * kLog2e * g * g);
         return g * p;
-    }
+    } else {
     // exponent y2 of p = 1 / (1 + exp(-y2)), and its derivative
     float y2 = g, dy2 = 1.0f;
-    if (act == HQQ_ACT_GELU_TANH) {
+    if constexpr (ACT == HQQ_ACT_GELU_TANH) {
         const float a = 1.59576912160573071176f, b = 0.044715f;   // 2 sqrt(2 / pi)
         y2 = a * (g + b * g * g * g);
         dy2 = a * (1.0f + 3.0f * b * g * g);
@@ -55,6 +53,7 @@ __device__ __forceinline__ float act_value(int act, float g, float &d)
     // p (1 - p) = p^2 e; where e overflows p is 0 and so is the product
     d = p + (e < INFINITY ? g * dy2 * (p * (p * e)) : 0.0f);
     return g * p;
+    }
 }
 
 __device__ __forceinline__ float from16(uint16_t b, bool bf)
@@ -108,11 +107,41 @@ __device__ __forceinline__ void tile_barrier()
     asm volatile("" ::: "memory");
 }
 
+// c += B . A (one 16x16x32 step) with c in accumulation registers, in place.  Written as
+// an instruction: from the builtin the compiler gives results registers of their own
+// and moves them about, which with 128 sums per lane costs spills in the loop.  It does
+// not see an instruction here that needs waiting for: see settle().
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+
+template <bool BF>
+__device__ __forceinline__ void mfma_into(float4v &c, uint4v B, uint4v A)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    if constexpr (BF)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(B), "v"(A));
+    else
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(B), "v"(A));
+#endif
+}
+
+// The sums may be read after this: the last matrix instruction's result takes at most
+// 18 wait states, and every sum's uses are ordered behind them.
+template <int N>
+__device__ __forceinline__ void settle(float4v (&c)[N])
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_nop 15\n\ts_nop 3");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+a"(c[i]));
+#endif
+}
+
 // What becomes of a wave's part of C: TM x TN blocks of 16 x 16; acc[u][t][r] of
 // lane l is C[m][n] with m = mw + 16 u + l % 16 and n = nw + 16 t + 4 (l / 16) + r.
 // Gated kinds: blocks t < TN / 2 are gate columns and t >= TN / 2 the up columns
 // of the same n = nw + 16 (t mod TN / 2) + ...
-template <int OUT, bool BF, int TM, int TN>
+template <int OUT, int ACT, bool BF, int TM, int TN>
 __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)[TM][TN], int mw, int nw, int lane,
                                          int z)
 {
@@ -143,7 +172,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                     float v[4], d;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        v[r] = act_value(g.act, acc[u][t][r], d) * acc[u][t + TN / 2][r];
+                        v[r] = act_value<ACT>(acc[u][t][r], d) * acc[u][t + TN / 2][r];
                     store4<BF>(g.out + (int64_t)m * g.ldo + n, v, g.N - n);
                 }
             }
@@ -159,7 +188,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         float d;
-                        const float f = act_value(g.act, acc[u][t][r], d);
+                        const float f = act_value<ACT>(acc[u][t][r], d);
                         const float ys = y[r] * sc;
                         vg[r] = n + r < g.N ? ys * acc[u][t + TN / 2][r] * d : 0.0f;
                         vu[r] = n + r < g.N ? ys * f : 0.0f;
@@ -223,11 +252,35 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
     }
 }
 
-template <int OUT, bool BF, int BM, int BN, int WM, int WN>
+// The tile of a workgroup.  Workgroups go to the 8 XCDs in turn: each XCD gets a
+// contiguous part of the tiles, in bands of kBand tile rows walked column by column,
+// so that the tiles that run on it at one time share rows of A and of B in its L2.
+constexpr int kBand = 4;
+
+__device__ __forceinline__ void tile_of(const GemmArgs &g, int &tm, int &tn)
+{
+    const uint32_t T = (uint32_t)(g.tiles_m * g.tiles_n), id = blockIdx.x;
+    const uint32_t q = T / 8, r = T % 8, x = id % 8;
+    const uint32_t t = x * q + (x < r ? x : r) + id / 8;
+    const uint32_t band = t / (uint32_t)(kBand * g.tiles_n), first = band * kBand;
+    const uint32_t rows = (uint32_t)g.tiles_m - first < kBand ? (uint32_t)g.tiles_m - first : kBand;
+    const uint32_t l = t - first * (uint32_t)g.tiles_n;
+    tm = (int)(first + l % rows);
+    tn = (int)(l / rows);
+}
+
+// A step is two halves of 32 k.  A wave's operands of one half are in registers
+// while those of the next are read from LDS under its matrix instructions: the
+// second half's from this step's buffers, then, behind the step's one barrier, the
+// next step's first half from the other buffers.  That barrier also frees this
+// step's buffers, and the DMA of the step after next goes into them under the
+// second half, a whole step ahead of its use.
+template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
 {
     constexpr int NW = WM * WN;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+    static_assert(TN == 4, "64 columns per wave: the softmax blocks and the gate / up halves");
     constexpr bool GATED = OUT == kOutGated || OUT == kOutGatedGrad;
     constexpr int BNC = GATED ? BN / 2 : BN;         // columns of the output per tile
     constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW;
@@ -235,60 +288,48 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int tile_n = (int)blockIdx.x / g.tiles_m, tile_m = (int)blockIdx.x - tile_n * g.tiles_m;
+    int tile_m, tile_n;
+    tile_of(g, tile_m, tile_n);
     const int m0 = tile_m * BM, n0 = tile_n * BNC;
 
     // DMA: wave w moves rows IA * 8 w ..., 8 rows per instruction; lane l fills
-    // slot (row 8 i + l / 8, column l % 8), which holds run (l % 8) ^ (row % 8)
-    const int run = (lane & 7) ^ (lane >> 3);
-    int arow[IA];
-#pragma unroll
-    for (int i = 0; i < IA; ++i) {
-        const int m = m0 + (IA * wave + i) * 8 + (lane >> 3);
-        arow[i] = m < g.M ? m : g.M - 1;
-    }
-    const uint16_t *bp[IB], *ap[IA];
-#pragma unroll
-    for (int i = 0; i < IB; ++i) {
-        const int r = (IB * wave + i) * 8 + (lane >> 3);
-        int64_t row;
-        if constexpr (GATED) {
-            // a wave's BN / WN rows: half of them gate, half up, of the same n
-            constexpr int PW = BN / WN, H = PW / 2;
-            const int n = n0 + (r / PW) * H + r % H;
-            row = (n < g.N ? n : g.N - 1) + (r % PW >= H ? g.B_up : 0);
-        } else {
-            const int n = n0 + r;
-            row = n < g.N ? n : g.N - 1;
-        }
-        bp[i] = g.B + row * g.ldb + run * 8;
-    }
+    // slot (row 8 i + l / 8, column l % 8), which holds run (l % 8) ^ (row % 8).
+    // Rows past the end repeat the last.  The lanes' byte offsets from the tile's
+    // first row are formed at each use: kept, they would cost registers.
+    const uint32_t run16 = 16 * ((lane & 7) ^ (lane >> 3));
+    int row_a = IA * 8 * wave + (lane >> 3), row_b = IB * 8 * wave + (lane >> 3);
+    const int b0 = tile_n * BN, last_b = (GATED ? 2 * ((g.N + 31) / 32 * 32) : g.N) - b0 - 1;
+    const int last_a = g.M - m0 - 1;
+    const char *bb = reinterpret_cast<const char *>(g.B + (int64_t)b0 * g.ldb);
+    uint32_t ldb2 = (uint32_t)(g.ldb * 2);
     const int steps = g.step0[g.segs];
     const int per = (steps + g.splits - 1) / g.splits;
     const int s0 = (int)blockIdx.y * per;
     const int s1 = s0 + per < steps ? s0 + per : steps;
-    int seg = 0;
-    auto enter = [&](int sg) {
-        seg = sg;
-#pragma unroll
-        for (int i = 0; i < IA; ++i)
-            ap[i] = g.A[sg] + (int64_t)arow[i] * g.lda[sg] + run * 8;
+    int seg = -1, seg_end = 0;
+    const char *ab = nullptr;          // of the segment's (virtual) step 0
+    uint32_t lda2 = 0;
+    auto enter = [&](int s) {          // the segment of step s (not before the current one)
+        while (s >= seg_end)
+            seg_end = g.step0[++seg + 1];
+        ab = reinterpret_cast<const char *>(g.A[seg] + (int64_t)m0 * g.lda[seg] - (int64_t)g.step0[seg] * kStep);
+        lda2 = (uint32_t)(g.lda[seg] * 2);
+    };
+    auto dma_a = [&](int i, int s, uint4 *as) {
+        const int r = row_a + 8 * i < last_a ? row_a + 8 * i : last_a;
+        dma16(ab + (int64_t)s * (2 * kStep) + ((uint32_t)r * lda2 + run16), as + (IA * wave + i) * 64);
+    };
+    auto dma_b = [&](int i, int s, uint4 *bs) {
+        const int r = row_b + 8 * i < last_b ? row_b + 8 * i : last_b;
+        dma16(bb + (int64_t)s * (2 * kStep) + ((uint32_t)r * ldb2 + run16), bs + (IB * wave + i) * 64);
     };
     auto dma = [&](int s, uint4 *as, uint4 *bs) {
-        while (s >= g.step0[seg + 1])
-            enter(seg + 1);
-        const int c = (s - g.step0[seg]) * kStep;
-        const bool whole = c + kStep <= g.rlen[seg];
 #pragma unroll
-        for (int i = 0; i < IA; ++i) {
-            const uint16_t *p = ap[i] + c;
-            if (!whole)
-                p = c + 8 * run < g.rlen[seg] ? p : reinterpret_cast<const uint16_t *>(&zero_run);
-            dma16(p, &as[(IA * wave + i) * 64]);
-        }
+        for (int i = 0; i < IA; ++i)
+            dma_a(i, s, as);
 #pragma unroll
         for (int i = 0; i < IB; ++i)
-            dma16(bp[i] + (int64_t)s * kStep, &bs[(IB * wave + i) * 64]);
+            dma_b(i, s, bs);
     };
     float4v acc[TM][TN];
 #pragma unroll
@@ -296,66 +337,187 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
 #pragma unroll
         for (int t = 0; t < TN; ++t)
             acc[u][t] = float4v{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const uint4 *as, const uint4 *bs) {
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            uint4 a[TM], b[TN];
-#pragma unroll
-            for (int u = 0; u < TM; ++u) {
-                const int r = wm * (BM / WM) + 16 * u + (lane & 15);
-                a[u] = as[r * 8 + ((4 * ks + (lane >> 4)) ^ (r & 7))];
-            }
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const int r = wn * (BN / WN) + 16 * t + (lane & 15);
-                b[t] = bs[r * 8 + ((4 * ks + (lane >> 4)) ^ (r & 7))];
-            }
-#pragma unroll
-            for (int u = 0; u < TM; ++u)
-#pragma unroll
-                for (int t = 0; t < TN; ++t)
-                    acc[u][t] = mfma<BF>(b[t], a[u], acc[u][t]);
-        }
+    uint4v a[TM], b[TN];
+    const int l16 = lane & 15, l4 = lane >> 4, sw = lane & 7;
+    auto read_a = [&](int ks, int u, const uint4 *as) {
+        return reinterpret_cast<const uint4v *>(as)[(wm * (BM / WM) + 16 * u + l16) * 8 + ((4 * ks + l4) ^ sw)];
     };
-    enter(0);
-    dma(s0, as0, bs0);
-    for (int s = s0; s < s1; s += 2) {
-        tile_barrier();                       // step s has landed; buffer 1 is free
-        if (s + 1 < s1)
-            dma(s + 1, as1, bs1);
-        multiply(as0, bs0);
-        if (s + 1 < s1) {
-            tile_barrier();
-            if (s + 2 < s1)
-                dma(s + 2, as0, bs0);
-            multiply(as1, bs1);
+    auto read_b = [&](int ks, int t, const uint4 *bs) {
+        return reinterpret_cast<const uint4v *>(bs)[(wn * (BN / WN) + 16 * t + l16) * 8 + ((4 * ks + l4) ^ sw)];
+    };
+    // One half: TM groups of TN matrix instructions; the reads of the next half's
+    // operands (half ks of the given buffers) are spread over all but the last of
+    // them, in the order of their use, so that most of them take the registers of
+    // operands already used; `more(i)` goes beside group i.
+    constexpr int RP = (TM + TN + TM - 2) / (TM - 1);
+    auto half = [&](int ks, const uint4 *as, const uint4 *bs, auto &&more) {
+        uint4v an[TM], bn[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int r = RP * i; r < RP * (i + 1); ++r) {
+                if (r < TN)
+                    bn[r] = read_b(ks, r, bs);
+                else if (r < TN + TM)
+                    an[r - TN] = read_a(ks, r - TN, as);
+            }
+            more(i);
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+                mfma_into<BF>(acc[i][t], b[t], a[i]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int u = 0; u < TM; ++u)
+            a[u] = an[u];
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+            b[t] = bn[t];
+    };
+    constexpr int DP = (IA + IB + TM - 1) / TM;
+    auto step = [&](int s, uint4 *asc, uint4 *bsc, const uint4 *asn, const uint4 *bsn) {
+        // past the end the DMA repeats the last step (in bounds, never used)
+        const int sn = s + 2 < s1 ? s + 2 : s1 - 1;
+        if (sn >= seg_end)
+            enter(sn);
+        // (hides that the pitches do not change: the offsets are not to be kept)
+        asm volatile("" : "+s"(lda2), "+s"(ldb2), "+v"(row_a), "+v"(row_b));
+        __builtin_amdgcn_sched_barrier(0);
+        half(1, asc, bsc, [](int) {});
+        tile_barrier();        // this step's reads are done, the next step has landed
+        half(0, asn, bsn, [&](int i) {
+#pragma unroll
+            for (int j = DP * i; j < DP * (i + 1); ++j) {
+                if (j < IA)
+                    dma_a(j, sn, asc);
+                else if (j < IA + IB)
+                    dma_b(j - IA, sn, bsc);
+            }
+        });
+    };
+    enter(s0);
+    dma(s0, as0, bs0);
+    const int sn = s0 + 1 < s1 ? s0 + 1 : s0;
+    if (sn >= seg_end)
+        enter(sn);
+    dma(sn, as1, bs1);
+    tile_barrier();
+#pragma unroll
+    for (int t = 0; t < TN; ++t)
+        b[t] = read_b(0, t, bs0);
+#pragma unroll
+    for (int u = 0; u < TM; ++u)
+        a[u] = read_a(0, u, as0);
+    int s = s0;
+    for (; s + 1 < s1; s += 2) {
+        step(s, as0, bs0, as1, bs1);
+        step(s + 1, as1, bs1, as0, bs0);
     }
-    epilogue<OUT, BF, TM, TN>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, (int)blockIdx.y);
+    if (s < s1)
+        step(s, as0, bs0, as1, bs1);
+    __builtin_amdgcn_s_waitcnt(0x0070);       // no DMA outlives the workgroup
+#pragma unroll
+    for (int u = 0; u < TM; ++u)
+        settle(acc[u]);
+    epilogue<OUT, ACT, BF, TM, TN>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, (int)blockIdx.y);
+}
+
+// Tiles: 256 x 256 and 256 x 128 with 8 waves, one workgroup per CU, and 128 x 128
+// with 4 waves, two per CU.  Their times per 64-wide step with the chip full, in
+// bf16 on MI355X: 1.54, 0.92 and 0.98 us (42, 36 and 34 thousand outputs per CU
+// and us).  The fewest-time tile by rounds of workgroups over the CUs; where that
+// leaves CUs idle, the steps are split and a second pass adds the parts (about
+// 4 us and the parts' bytes at 4 TB/s).
+struct Tile {
+    int bm, bn, per_cu;
+    double us;
+};
+constexpr Tile kTiles[3] = {{256, 256, 1, 1.54}, {256, 128, 1, 0.92}, {128, 128, 2, 0.98}};
+constexpr int kCus = 256;
+constexpr int kMaxSplits = 16;
+
+double product_us(int tile, int64_t M, int64_t N, int64_t steps, int splits, bool gated, bool parts)
+{
+    const Tile &t = kTiles[tile];
+    const int64_t bn = gated ? t.bn / 2 : t.bn;
+    const int64_t wgs = (M + t.bm - 1) / t.bm * ((N + bn - 1) / bn) * splits;
+    const int64_t slots = kCus * t.per_cu;
+    double us = (double)((wgs + slots - 1) / slots) * (2.0 + (double)((steps + splits - 1) / splits) * t.us);
+    if (splits > 1 || parts)
+        us += 4.0 + (double)M * (double)N * 4.0 * splits * 2.0 / 4.0e6;
+    return us;
+}
+
+void pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool parts, int &tile, int &splits, bool may_split)
+{
+    double best = 0.0;
+    tile = 0;
+    splits = 1;
+    for (int t = 0; t < 3; ++t)
+        for (int sp = 1; sp <= (may_split ? kMaxSplits : 1); ++sp) {
+            if (sp > 1 && (steps / sp < 4 || (sp - 1) * ((steps + sp - 1) / sp) >= steps))
+                continue;       // a part has a few steps at least, and none is empty
+            const double us = product_us(t, M, N, steps, sp, gated, parts);
+            if (best == 0.0 || us < best) {
+                best = us;
+                tile = t;
+                splits = sp;
+            }
+        }
+}
+
+template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN>
+hipError_t launch_tile(GemmArgs &g, hipStream_t s)
+{
+    constexpr bool GATED = OUT == kOutGated || OUT == kOutGatedGrad;
+    constexpr int BNC = GATED ? BN / 2 : BN;
+    g.tiles_m = (g.M + BM - 1) / BM;
+    g.tiles_n = (g.N + BNC - 1) / BNC;
+    hipLaunchKernelGGL((gemm_kernel<OUT, ACT, BF, BM, BN, WM, WN>),
+                       dim3((unsigned)(g.tiles_m * g.tiles_n), (unsigned)g.splits), dim3(WM * WN * 64), 0, s, g);
+    return hipGetLastError();
+}
+
+void gradient_tile(int64_t M, int64_t N, int64_t steps, int &tile, int &splits)
+{
+    pick_tile(M, N, steps, false, false, tile, splits, true);
+}
+
+template <int OUT, int ACT, bool BF>
+hipError_t launch_out(GemmArgs &g, hipStream_t s)
+{
+    int tile, sp;
+    if (OUT == kOutStore || OUT == kOutPart)
+        gradient_tile(g.M, g.N, g.step0[g.segs], tile, sp);
+    else
+        pick_tile(g.M, g.N, g.step0[g.segs], OUT == kOutGated || OUT == kOutGatedGrad, false, tile, sp, false);
+    switch (tile) {
+    case 0: return launch_tile<OUT, ACT, BF, 256, 256, 2, 4>(g, s);
+    case 1: return launch_tile<OUT, ACT, BF, 256, 128, 4, 2>(g, s);
+    default: return launch_tile<OUT, ACT, BF, 128, 128, 2, 2>(g, s);
+    }
 }
 
 template <int OUT, bool BF>
-hipError_t launch_out(GemmArgs &g, hipStream_t s)
+hipError_t launch_act(GemmArgs &g, hipStream_t s)
 {
-    constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
-    constexpr bool GATED = OUT == kOutGated || OUT == kOutGatedGrad;
-    g.tiles_m = (g.M + BM - 1) / BM;
-    g.tiles_n = (g.N + (GATED ? BN / 2 : BN) - 1) / (GATED ? BN / 2 : BN);
-    hipLaunchKernelGGL((gemm_kernel<OUT, BF, BM, BN, WM, WN>), dim3((unsigned)(g.tiles_m * g.tiles_n), (unsigned)g.splits),
-                       dim3(WM * WN * 64), 0, s, g);
-    return hipGetLastError();
+    switch (g.act) {
+    case HQQ_ACT_SILU: return launch_out<OUT, HQQ_ACT_SILU, BF>(g, s);
+    case HQQ_ACT_GELU: return launch_out<OUT, HQQ_ACT_GELU, BF>(g, s);
+    default: return launch_out<OUT, HQQ_ACT_GELU_TANH, BF>(g, s);
+    }
 }
 
 template <bool BF>
 hipError_t launch_dtype(GemmOut out, GemmArgs &g, hipStream_t s)
 {
     switch (out) {
-    case kOutStore: return launch_out<kOutStore, BF>(g, s);
-    case kOutPart: return launch_out<kOutPart, BF>(g, s);
-    case kOutGated: return launch_out<kOutGated, BF>(g, s);
-    case kOutGatedGrad: return launch_out<kOutGatedGrad, BF>(g, s);
-    case kOutStats: return launch_out<kOutStats, BF>(g, s);
-    default: return launch_out<kOutSoftGrad, BF>(g, s);
+    case kOutStore: return launch_out<kOutStore, 0, BF>(g, s);
+    case kOutPart: return launch_out<kOutPart, 0, BF>(g, s);
+    case kOutGated: return launch_act<kOutGated, BF>(g, s);
+    case kOutGatedGrad: return launch_act<kOutGatedGrad, BF>(g, s);
+    case kOutStats: return launch_out<kOutStats, 0, BF>(g, s);
+    default: return launch_out<kOutSoftGrad, 0, BF>(g, s);
     }
 }
 
@@ -368,13 +530,9 @@ hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s)
 
 int gemm_splits(int64_t M, int64_t N, int64_t steps)
 {
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-    int sp = 1;
-    while (sp < 32 && tiles * sp < 512 && steps / (2 * sp) >= 8)
-        sp *= 2;
-    while ((sp - 1) * ((steps + sp - 1) / sp) >= steps)
-        --sp;
-    return sp;
+    int tile, splits;
+    gradient_tile(M, N, steps, tile, splits);
+    return splits;
 }
 
 }  // namespace hqq

@@ -20,16 +20,17 @@ struct UnpackArgs {
     int gshift;               // log2 of the group size
     uint16_t *W;
     int64_t ldw;
+    int interleave;           // 0: row n at row n of W; a gated pair shares W, 32 rows of the one and
+                              // 32 of the other in turn: 1 its first (gate), 2 its second (up)
     uint16_t *WT;
     int64_t ldt;
 };
 hipError_t launch_unpack_weight(int nbits, bool bf16, const UnpackArgs &a, hipStream_t s);
 
 // The matrix product C [M, N] = A [M, R] . B [N, R]^T of 16-bit matrices with
-// fp32 sums, and what becomes of C.  A comes in segments along R (each a
-// matrix of its own, its columns padded to whole 64-wide steps by the reader
-// with zeros); B is one matrix in the workspace whose columns are zero
-// wherever A's are padding.
+// fp32 sums, and what becomes of C.  A comes in segments along R, each a matrix
+// of its own of whole 64-wide steps; B is one matrix in the workspace.  Columns
+// that pad the last step of a segment are finite in A and zero in B.
 constexpr int kStep = 64;            // depth of a step
 constexpr int kMaxSegs = HQQ_MAX_GRADS;
 
@@ -43,13 +44,12 @@ enum GemmOut {
 };
 
 struct GemmArgs {
-    const uint16_t *A[kMaxSegs];     // segment i: [M, rlen[i]], row pitch lda[i]
+    const uint16_t *A[kMaxSegs];     // segment i: [M, 64 steps], row pitch lda[i] (below 2^23)
     int64_t lda[kMaxSegs];
-    int32_t rlen[kMaxSegs];          // a multiple of 8
     int32_t step0[kMaxSegs + 1];     // first step of each segment; step0[segs]: their number
     int segs;
-    const uint16_t *B;               // [N, ldb]; gated: gate rows, then (at row B_up) up rows
-    int64_t ldb, B_up;
+    const uint16_t *B;               // [N, ldb]; gated: [2 round_up(N, 32), ldb], see UnpackArgs
+    int64_t ldb;                     // below 2^23
     int32_t M, N;
     int splits;                      // kOutPart: parts of the steps
     int tiles_m, tiles_n;            // filled by the launcher

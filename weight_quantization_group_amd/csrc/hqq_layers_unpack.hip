@@ -64,8 +64,10 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
     if constexpr (WANT_W) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (n0 + i < a.n)
-                *reinterpret_cast<uint4 *>(a.W + (n0 + i) * a.ldw + run * 8) = uint4{v[i][0], v[i][1], v[i][2], v[i][3]};
+            if (n0 + i < a.n) {
+                const int64_t n = n0 + i, row = a.interleave ? (n >> 5) * 64 + (n & 31) + 32 * (a.interleave - 1) : n;
+                *reinterpret_cast<uint4 *>(a.W + row * a.ldw + run * 8) = uint4{v[i][0], v[i][1], v[i][2], v[i][3]};
+            }
     }
     if constexpr (WANT_T) {
         if (k_in) {
