@@ -6,9 +6,12 @@
 // of 8 consecutive k: 64 values in registers are both the 8 row runs of W
 // (16 bytes each) and, after one byte permutation per pair (the other steps of
 // the 8 x 8 transposition only rename registers), the 8 column runs of W^T.  The
-// 64 lanes of a wave are 8 x 8 such squares, so that each row of codes is read,
-// and each row of W and of W^T written, in whole 128-byte (codes: 8 to 64 byte)
-// stretches.  Bound by the bytes written.
+// 64 lanes of a wave are 8 x 8 such squares, and the four waves of a workgroup lie
+// side by side along k: each row of codes is read, and each row of W and of W^T
+// written, in stretches of 128 bytes or more.  Workgroups go to the 8 XCDs in turn;
+// each XCD gets a contiguous part of them, so that the lines of codes, scales and
+// zeros that neighbours along k share are fetched into one L2 only.  Bound by the
+// bytes written.
 #include "hqq_layers_internal.h"
 #include "hqq_linear_dev.h"
 
@@ -17,15 +20,29 @@ namespace {
 
 constexpr int kUnpackWaves = 4;
 
+// 1 / s in fp64 by two Newton steps from v_rcp_f64 (2^-24 or better): within 2^-51.5
+// relative, which the exactness of wq needs no more than (a quotient is nowhere nearer
+// than 2^-49 to where fp32 rounds the other way); a third of the division's steps.
+__device__ __forceinline__ double reciprocal(float s)
+{
+    const double d = (double)s;
+    double r = __builtin_amdgcn_rcp(d);
+    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+    return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+
 template <int NB, bool BF, bool WANT_W, bool WANT_T>
 __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
 {
     constexpr uint32_t MASK = (1u << NB) - 1u;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int kl = lane & 7, nl = lane >> 3;
-    const uint32_t kblocks = (uint32_t)((a.K + 63) / 64), nb = blockIdx.x / kblocks;
-    const int64_t run = (int64_t)(blockIdx.x - nb * kblocks) * 8 + kl;      // 8-k run of the row
-    const int64_t n0 = ((int64_t)nb * kUnpackWaves + wave) * 64 + 8 * nl;
+    // this workgroup's place in the order of its XCD
+    const uint32_t T = gridDim.x, q = T / 8, rest = T % 8, x = blockIdx.x % 8;
+    const uint32_t id = x * q + (x < rest ? x : rest) + blockIdx.x / 8;
+    const uint32_t kblocks = (uint32_t)((a.K + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves)), nb = id / kblocks;
+    const int64_t run = (int64_t)((id - nb * kblocks) * kUnpackWaves + wave) * 8 + kl;   // 8-k run of the row
+    const int64_t n0 = (int64_t)nb * 64 + 8 * nl;
     const int64_t runs = a.K / 8;
     const bool k_in = run < runs;
     if (n0 >= round_up(a.n, 64) || run * 8 >= a.ldw)
@@ -51,7 +68,7 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
         }
         const int64_t g = n * a.gpl + ((8 * r) >> a.gshift);
         const float z = a.zero[g];
-        const double R = 1.0 / (double)a.scale[g];
+        const double R = reciprocal(a.scale[g]);
         const bool in = k_in && n0 + i < a.n;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -88,7 +105,7 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
 template <int NB, bool BF>
 hipError_t launch_nb(const UnpackArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.K + 63) / 64 * ((a.n + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves))));
+    const dim3 grid((unsigned)((a.K + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves) * ((a.n + 63) / 64)));
     const dim3 block(kUnpackWaves * 64);
     if (a.W && a.WT)
         hipLaunchKernelGGL((unpack_kernel<NB, BF, true, true>), grid, block, 0, s, a);
