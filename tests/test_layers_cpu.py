@@ -115,7 +115,7 @@ CALLS = [gated, gated_backward, batch_backward, loss, loss_backward]
 @pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
 @pytest.mark.parametrize("kw,code", SIZES + [(dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE),
                                              (dict(ws=MIS), PTR), (dict(ws=None), PTR), (dict(size=-1), PTR),
-                                             (dict(size=0), WORKSPACE), (dict(ws=None, size=0), WORKSPACE)])
+                                             (dict(M=40, size=0), WORKSPACE), (dict(M=40, ws=None, size=0), WORKSPACE)])
 def test_rejects(w, lib, call, kw, code):
     assert call(w, lib, **kw) == code
 
@@ -152,6 +152,7 @@ def test_workspace_sizes(w):
     """One byte less than stated is refused; invalid sizes raise; sizes stay far below the logits'
     for long batches over large vocabularies."""
     sizes = (37, 1056, 2753, 2, 32)
+    assert w.hqq_linear_gated_workspace(1, 1056, 2753, 2, 32) == 0       # straight from the codes
     for call, fn in ((gated, w.hqq_linear_gated_workspace), (gated_backward, w.hqq_linear_gated_backward_workspace),
                      (loss, w.hqq_linear_cross_entropy_workspace),
                      (loss_backward, w.hqq_linear_cross_entropy_backward_workspace)):
@@ -160,7 +161,7 @@ def test_workspace_sizes(w):
             assert call(w, w.load_layers_library(), M=37, K=1056, N=2753, nbits=2, gs=32, size=need - 1) == WORKSPACE
         with pytest.raises(w.LayersError):
             fn(37, 1056, 2753, 3, 32)
-    assert w.hqq_linear_batch_backward_workspace(5, 128, [40, 7], 4, 64) > 0
+    assert w.hqq_linear_batch_backward_workspace(50, 128, [40, 7], 4, 64) > 0
     with pytest.raises(w.LayersError):
         w.hqq_linear_batch_backward_workspace(5, 128, [], 4, 64)
     with pytest.raises(w.LayersError):
@@ -193,4 +194,4 @@ def test_batch_width_limit(w, lib):
     N = 1 << 22
     arr = (HqqLinearGrad * 3)(*[HqqLinearGrad(A, A, A, N, A)] * 3)
     assert lib.hqq_linear_batch_backward(arr, 3, 1, 32, 1, 32, 0, A, A, 1 << 40, None) == SHAPE
-    assert lib.hqq_linear_batch_backward(arr, 2, 1, 32, 1, 32, 0, A, A, 0, None) == WORKSPACE
+    assert lib.hqq_linear_batch_backward(arr, 2, 40, 32, 1, 32, 0, A, A, 0, None) == WORKSPACE

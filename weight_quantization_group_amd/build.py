@@ -29,7 +29,8 @@ SOURCES = ["hqq_abi.cpp", "hqq_stream.cpp", "hqq_solve.hip", "hqq_solve_b1.hip",
            "hqq_linear.hip", "hqq_gemm.cpp"]
 
 LAYERS_LIB = os.path.join(PKG, "libhqq_layers.so")
-LAYERS_SOURCES = ["hqq_layers_abi.cpp", "hqq_layers_unpack.hip", "hqq_layers_gemm.hip", "hqq_layers_rows.hip"]
+LAYERS_SOURCES = ["hqq_layers_abi.cpp", "hqq_layers_unpack.hip", "hqq_layers_gemm.hip", "hqq_layers_rows.hip",
+                  "hqq_layers_skinny_one.hip", "hqq_layers_skinny_pair.hip", "hqq_layers_skinny_grad.hip"]
 
 FLAGS = ["-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-fvisibility=hidden",
          "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",

@@ -13,6 +13,9 @@ constexpr int64_t kMaxDepth = int64_t(1) << 17;
 constexpr int64_t kMaxWidth = int64_t(1) << 22;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxBytes = int64_t(1) << 31;
+// Up to this many rows the kernels that work straight from the codes run; from
+// the next on, W_hat is unpacked and the tiled product runs.
+constexpr int64_t kFewRows = 32;
 // The backward passes keep 16-bit gradients of this many rows at a time.
 constexpr int64_t kRowChunk = 8192;
 
@@ -169,6 +172,78 @@ hipError_t gradient_product(GemmArgs &g, bool bf16, float *part, float *acc, boo
     return launch_reduce(bf16, r, s);
 }
 
+LinearArgs linear_args(const uint16_t *X, const hqq_weight &w, int64_t M, int64_t K, int64_t N, int nbits, int group_size)
+{
+    LinearArgs a{};
+    a.X = X;
+    a.packed = w.packed;
+    a.scale = w.scale;
+    a.zero = w.zero;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.wpr = K * nbits / 32;
+    a.gpl = K / group_size;
+    a.gs = group_size;
+    a.gshift = log2_group(group_size);
+    return a;
+}
+
+// the weights and gradients of a few-rows backward product
+void add_grad(SkinnyGradArgs &a, const uint32_t *packed, const float *scale, const float *zero, const uint16_t *A,
+              int64_t lda, int64_t n)
+{
+    const int i = a.count++;
+    a.packed[i] = packed;
+    a.scale[i] = scale;
+    a.zero[i] = zero;
+    a.A[i] = A;
+    a.lda[i] = lda;
+    a.n[i] = (int32_t)n;
+    a.step0[i + 1] = a.step0[i] + (int32_t)((n + 31) / 32);
+}
+
+// 32-row steps of the widths n
+int64_t grad_steps(const int64_t *n, int count)
+{
+    int64_t t = 0;
+    for (int i = 0; i < count; ++i)
+        t += (n[i] + 31) / 32;
+    return t;
+}
+
+int64_t few_part_floats(int64_t M, int64_t K, int64_t steps)
+{
+    const int sp = skinny_grad_splits(M, K, steps);
+    return sp > 1 ? sp * M * K : 0;
+}
+
+hipError_t few_rows_gradient(SkinnyGradArgs &a, bool bf16, int nbits, int group_size, int64_t M, int64_t K, float *part,
+                             uint16_t *dX, const float *rowf, hipStream_t s)
+{
+    a.M = M;
+    a.K = K;
+    a.wpr = K * nbits / 32;
+    a.gpl = K / group_size;
+    a.gshift = log2_group(group_size);
+    a.splits = skinny_grad_splits(M, K, a.step0[a.count]);
+    a.out = dX;
+    a.rowf = rowf;
+    a.part = a.splits > 1 ? part : nullptr;
+    if (const hipError_t e = launch_skinny_grad(nbits, bf16, a, s))
+        return e;
+    if (a.splits == 1)
+        return hipSuccess;
+    ReduceArgs r{};
+    r.part = part;
+    r.splits = a.splits;
+    r.M = M;
+    r.N = K;
+    r.out = dX;
+    r.rowf = rowf;
+    return launch_reduce(bf16, r, s);
+}
+
 // ---------------------------------------------------------------------------
 // layouts
 // ---------------------------------------------------------------------------
@@ -179,8 +254,11 @@ struct GatedLayout {
     GatedLayout(void *p, int64_t M, int64_t K, int64_t N)
     {
         Carve c(p);
-        W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
-        X = c.take_some<uint16_t>(pad_values(M, K));
+        W = X = nullptr;
+        if (M > kFewRows) {
+            W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
+            X = c.take_some<uint16_t>(pad_values(M, K));
+        }
         bytes = c.at;
     }
 };
@@ -193,13 +271,18 @@ struct GatedGradLayout {
     {
         const int64_t Np = round_up(N, kStep), mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
-        W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
-        X = c.take_some<uint16_t>(pad_values(mc, K));
-        WT = c.take<uint16_t>(K * 2 * Np);
+        W = WT = X = nullptr;
+        if (M > kFewRows) {
+            W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
+            X = c.take_some<uint16_t>(pad_values(mc, K));
+            WT = c.take<uint16_t>(K * 2 * Np);
+        }
         dGU = c.take<uint16_t>(mc * 2 * Np);
         scale = c.take<float>(mc);
         inv = c.take<float>(mc);
-        part = c.take<float>(part_floats(M, K, 2 * Np / kStep));
+        const int64_t n[2] = {N, N};
+        part = c.take_some<float>(M > kFewRows ? part_floats(M, K, 2 * Np / kStep)
+                                               : few_part_floats(M, K, grad_steps(n, 2)));
         bytes = c.at;
     }
 };
@@ -213,6 +296,12 @@ struct BatchGradLayout {
         const int64_t mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
         ldt = 0;
+        WT = nullptr;
+        if (M <= kFewRows) {
+            part = c.take_some<float>(few_part_floats(M, K, grad_steps(n, count)));
+            bytes = c.at;
+            return;
+        }
         for (int i = 0; i < count; ++i)
             ldt += round_up(n[i], kStep);
         WT = c.take<uint16_t>(K * ldt);
@@ -238,11 +327,17 @@ struct LossLayout {
     int64_t bytes, piece, blocks;
     LossLayout(void *p, int64_t M, int64_t K, int64_t N)
     {
-        piece = loss_piece(K, N);
-        blocks = (piece + 63) / 64;
         Carve c(p);
-        W = c.take<uint16_t>(piece * round_up(K, kStep));
-        X = c.take_some<uint16_t>(pad_values(M, K));
+        W = X = nullptr;
+        if (M > kFewRows) {
+            piece = loss_piece(K, N);
+            blocks = (piece + 63) / 64;
+            W = c.take<uint16_t>(piece * round_up(K, kStep));
+            X = c.take_some<uint16_t>(pad_values(M, K));
+        } else {
+            piece = N;
+            blocks = (N + 15) / 16;
+        }
         stats = c.take<float2>(M * blocks);
         state = c.take<float2>(M);
         tlogit = c.take<float>(M);
@@ -269,9 +364,20 @@ struct LossGradLayout {
     LossGradLayout(void *p, int64_t M, int64_t K, int64_t N)
     {
         const int64_t mc = M < kRowChunk ? M : kRowChunk;
+        Carve c(p);
+        W = WT = X = nullptr;
+        acc = nullptr;
+        if (M <= kFewRows) {
+            piece = N;
+            ldl = round_up(N, kStep);
+            dL = c.take<uint16_t>(M * ldl);
+            rowf = c.take<float>(M);
+            part = c.take_some<float>(few_part_floats(M, K, grad_steps(&N, 1)));
+            bytes = c.at;
+            return;
+        }
         piece = loss_grad_piece(M, K, N);
         ldl = round_up(piece, kStep);
-        Carve c(p);
         W = c.take<uint16_t>(piece * round_up(K, kStep));
         WT = c.take<uint16_t>(K * ldl);
         dL = c.take<uint16_t>(mc * ldl);
@@ -334,6 +440,19 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
+    if (M <= kFewRows) {
+        SkinnyArgs f{};
+        f.w[0] = linear_args(X, *gate, M, K, N, nbits, group_size);
+        f.w[1] = linear_args(X, *up, M, K, N, nbits, group_size);
+        f.out = kOutGated;
+        f.cols = N;
+        f.g.M = (int32_t)M;
+        f.g.N = (int32_t)N;
+        f.g.out = Y;
+        f.g.ldo = N;
+        f.g.act = act;
+        return launch_skinny(nbits, bf16, f, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
+    }
     const int64_t ldw = round_up(K, kStep);
     for (int i = 0; i < 2; ++i) {
         const hqq_weight &w = i ? *up : *gate;
@@ -383,6 +502,31 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const int64_t ldw = round_up(K, kStep), Np = round_up(N, kStep);
+    if (M <= kFewRows) {
+        if (!bf16 && launch_row_scale(dY, M, N, l.scale, l.inv, s) != hipSuccess)
+            return HQQ_EHIP;
+        SkinnyArgs f{};
+        f.w[0] = linear_args(X, *gate, M, K, N, nbits, group_size);
+        f.w[1] = linear_args(X, *up, M, K, N, nbits, group_size);
+        f.out = kOutGatedGrad;
+        f.cols = Np;
+        f.g.M = (int32_t)M;
+        f.g.N = (int32_t)N;
+        f.g.out = l.dGU;
+        f.g.ldo = 2 * Np;
+        f.g.up_off = Np;
+        f.g.act = act;
+        f.g.dY = dY;
+        f.g.rscale = bf16 ? nullptr : l.scale;
+        SkinnyGradArgs b{};
+        add_grad(b, gate->packed, gate->scale, gate->zero, l.dGU, 2 * Np, N);
+        add_grad(b, up->packed, up->scale, up->zero, l.dGU + Np, 2 * Np, N);
+        return launch_skinny(nbits, bf16, f, s) == hipSuccess &&
+                       few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, bf16 ? nullptr : l.inv, s) ==
+                           hipSuccess
+                   ? HQQ_OK
+                   : HQQ_EHIP;
+    }
     for (int i = 0; i < 2; ++i) {
         const hqq_weight &w = i ? *up : *gate;
         UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
@@ -462,6 +606,13 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
+    if (M <= kFewRows) {
+        SkinnyGradArgs b{};
+        for (int i = 0; i < count; ++i)
+            add_grad(b, ws[i].packed, ws[i].scale, ws[i].zero, ws[i].dY, n[i], n[i]);
+        return few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, nullptr, s) == hipSuccess ? HQQ_OK
+                                                                                                        : HQQ_EHIP;
+    }
     int64_t col = 0;
     for (int i = 0; i < count; ++i) {
         UnpackArgs a = unpack_args(ws[i].packed, ws[i].scale, ws[i].zero, 0, n[i], K, nbits, group_size);
@@ -516,6 +667,21 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const int64_t ldw = round_up(K, kStep);
+    if (M <= kFewRows) {
+        SkinnyArgs f{};
+        f.w[0] = linear_args(X, *head, M, K, N, nbits, group_size);
+        f.out = kOutStats;
+        f.cols = N;
+        f.g.M = (int32_t)M;
+        f.g.N = (int32_t)N;
+        f.g.Nall = N;
+        f.g.targets = targets;
+        f.g.stats = l.stats;
+        f.g.blocks = l.blocks;
+        f.g.tlogit = l.tlogit;
+        const LossArgs e{l.stats, l.blocks, M, N, l.state, l.tlogit, targets, loss, lse, 1, 1};
+        return launch_skinny(nbits, bf16, f, s) == hipSuccess && launch_loss(e, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
+    }
     if (whole_steps(X, M, K, l.X, s) != hipSuccess)
         return HQQ_EHIP;
     for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
@@ -534,18 +700,7 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
         g.targets = targets;
         g.n0 = n0;
         g.Nall = N;
-        LossArgs e{};
-        e.stats = l.stats;
-        e.blocks = g.blocks;
-        e.M = M;
-        e.N = N;
-        e.state = l.state;
-        e.tlogit = l.tlogit;
-        e.targets = targets;
-        e.loss = loss;
-        e.lse = lse;
-        e.first = n0 == 0;
-        e.last = n0 + n == N;
+        const LossArgs e{l.stats, g.blocks, M, N, l.state, l.tlogit, targets, loss, lse, n0 == 0, n0 + n == N};
         if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess || launch_gemm(kOutStats, bf16, g, s) != hipSuccess ||
             launch_loss(e, s) != hipSuccess)
             return HQQ_EHIP;
@@ -578,9 +733,30 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const int64_t ldw = round_up(K, kStep);
+    const float unit = bf16 ? 1.0f : 1.0f / 32768.0f;     // of the rounded differences
+    if (M <= kFewRows) {
+        SkinnyArgs f{};
+        f.w[0] = linear_args(X, *head, M, K, N, nbits, group_size);
+        f.out = kOutSoftGrad;
+        f.cols = l.ldl;
+        f.g.M = (int32_t)M;
+        f.g.N = (int32_t)N;
+        f.g.Nall = N;
+        f.g.targets = targets;
+        f.g.lse = lse;
+        f.g.out = l.dL;
+        f.g.ldo = l.ldl;
+        SkinnyGradArgs b{};
+        add_grad(b, head->packed, head->scale, head->zero, l.dL, l.ldl, N);
+        return launch_loss_factor(dloss, targets, M, N, unit, l.rowf, s) == hipSuccess &&
+                       launch_skinny(nbits, bf16, f, s) == hipSuccess &&
+                       few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, l.rowf, s) == hipSuccess
+                   ? HQQ_OK
+                   : HQQ_EHIP;
+    }
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
-        if (launch_loss_factor(dloss + m0, targets + m0, m, N, bf16 ? 1.0f : 1.0f / 32768.0f, l.rowf, s) != hipSuccess)
+        if (launch_loss_factor(dloss + m0, targets + m0, m, N, unit, l.rowf, s) != hipSuccess)
             return HQQ_EHIP;
         const uint16_t *x = X + m0 * K;
         if (whole_steps(x, m, K, l.X, s) != hipSuccess)

@@ -9,8 +9,7 @@
 // spread over the banks.  The product is formed transposed (the rows of B are
 // the instruction's rows): a lane then holds 4 consecutive columns n of one row
 // m, which is what the row-wise softmax and the 16-bit stores want.
-#include "hqq_layers_internal.h"
-#include "hqq_linear_dev.h"
+#include "hqq_layers_epilogue.h"
 
 namespace hqq {
 namespace {
@@ -21,82 +20,6 @@ __device__ __forceinline__ void dma16(const void *p, uint4 *lds)
 #ifdef __HIP_DEVICE_COMPILE__
     __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 #endif
-}
-
-constexpr float kLog2e = 1.44269504088896340736f;
-
-// 2^x and 1 / x to about an ulp of fp32 (v_exp_f32, v_rcp_f32): the results are
-// rounded to 16 bits, or summed over many terms
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
-
-// act(g) and, for the backward pass, act'(g).  Each activation is g * p with p in
-// (0, 1) formed without cancellation (erfc, and (1 + tanh y) / 2 = 1 / (1 + exp(-2 y))),
-// so that its far negative tail keeps its relative precision.
-template <int ACT>
-__device__ __forceinline__ float act_value(float g, float &d)
-{
-    if constexpr (ACT == HQQ_ACT_GELU) {
-        const float p = 0.5f * erfcf(g * -0.70710678118654752440f);
-        d = p + g * 0.39894228040143267794f * exp2_fast(-0.5f * kLog2e * g * g);
-        return g * p;
-    } else {
-    // exponent y2 of p = 1 / (1 + exp(-y2)), and its derivative
-    float y2 = g, dy2 = 1.0f;
-    if constexpr (ACT == HQQ_ACT_GELU_TANH) {
-        const float a = 1.59576912160573071176f, b = 0.044715f;   // 2 sqrt(2 / pi)
-        y2 = a * (g + b * g * g * g);
-        dy2 = a * (1.0f + 3.0f * b * g * g);
-    }
-    const float e = exp2_fast(-kLog2e * y2);
-    const float p = rcp_fast(1.0f + e);
-    // p (1 - p) = p^2 e; where e overflows p is 0 and so is the product
-    d = p + (e < INFINITY ? g * dy2 * (p * (p * e)) : 0.0f);
-    return g * p;
-    }
-}
-
-__device__ __forceinline__ float from16(uint16_t b, bool bf)
-{
-    if (bf)
-        return __uint_as_float((uint32_t)b << 16);
-    _Float16 h;
-    __builtin_memcpy(&h, &b, 2);
-    return (float)h;
-}
-
-// four consecutive 16-bit values at p, of which the first cnt exist
-template <bool BF>
-__device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4], int cnt)
-{
-    const uint32_t lo = out2<BF>(v[0], v[1]), hi = out2<BF>(v[2], v[3]);
-    if (cnt >= 4 && ((uintptr_t)p & 7u) == 0) {
-        *reinterpret_cast<uint2 *>(p) = uint2{lo, hi};
-    } else {
-        const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < cnt)
-                p[r] = h[r];
-    }
-}
-
-template <bool BF>
-__device__ __forceinline__ void load4(const uint16_t *p, float (&v)[4], int cnt)
-{
-    uint16_t h[4] = {0, 0, 0, 0};
-    if (cnt >= 4 && ((uintptr_t)p & 7u) == 0) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        h[0] = (uint16_t)u.x; h[1] = (uint16_t)(u.x >> 16); h[2] = (uint16_t)u.y; h[3] = (uint16_t)(u.y >> 16);
-    } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < cnt)
-                h[r] = p[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        v[r] = from16(h[r], BF);
 }
 
 __device__ __forceinline__ void tile_barrier()

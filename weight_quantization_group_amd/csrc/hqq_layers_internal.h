@@ -73,6 +73,37 @@ hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s);
 // Splits of the steps for a kOutPart product (none of them empty).
 int gemm_splits(int64_t M, int64_t N, int64_t steps);
 
+// Few rows, straight from the packed codes (hqq_layers_skinny.h): C [M, N] =
+// X . W_hat^T with g's fields for what becomes of it (kOutStats: 16 columns per
+// block).  Gated kinds take two weights.
+struct SkinnyArgs {
+    LinearArgs w[2];      // the weight, or gate and up (X, M, K, wpr, gpl, gs, gshift the same)
+    GemmOut out;
+    int64_t cols;         // columns to cover: N, or the padded width that out is given
+    GemmArgs g;
+};
+hipError_t launch_skinny(int nbits, bool bf16, const SkinnyArgs &s, hipStream_t st);
+hipError_t launch_skinny_pair(int nbits, bool bf16, const SkinnyArgs &s, hipStream_t st);
+
+// Few rows: C [M, K] = sum_i A_i . W_hat_i (hqq_layers_skinny_grad.hip), as
+// round(rowf * C) in out, or as the splits' parts [splits, M, K].
+struct SkinnyGradArgs {
+    int count;
+    const uint32_t *packed[kMaxSegs];
+    const float *scale[kMaxSegs], *zero[kMaxSegs];
+    const uint16_t *A[kMaxSegs];     // [M, n[i]], row pitch lda[i]
+    int64_t lda[kMaxSegs];
+    int32_t n[kMaxSegs];
+    int32_t step0[kMaxSegs + 1];     // first 32-row step of each weight
+    int64_t M, K, wpr, gpl;
+    int gshift, splits;
+    float *part;
+    uint16_t *out;
+    const float *rowf;
+};
+hipError_t launch_skinny_grad(int nbits, bool bf16, const SkinnyGradArgs &a, hipStream_t s);
+int skinny_grad_splits(int64_t M, int64_t K, int64_t steps);
+
 // Sum of the parts: v = sum_z part[z] (+ acc_in), then out = round(rowf * v),
 // or acc_out = v.  M x N values, N a multiple of 4.
 struct ReduceArgs {

@@ -1,0 +1,240 @@
+// hqq_layers_skinny.h -- the layers' products for few rows, straight from the
+// packed codes: decoding, small batches and short prompts, where the weights'
+// bytes and the latency of a launch count and nothing is unpacked to memory.
+//
+// Forward (skinny_kernel), C [M, N] = X . W_hat^T: a workgroup owns 16 columns
+// n (of the gated block: the same 16 of gate and of up, which share the rows
+// of X) and its waves split K.  Lane l works on row n = l % 16 and, in each
+// 256-wide step, on the 64 consecutive k at 64 (l / 16): the codes of one
+// group (or a few), dequantized in registers to the eight operands of eight
+// 16x16x32 MFMAs.  The next step's codes load under the current one's
+// arithmetic.  The waves add their sums through LDS, and the operator's
+// arithmetic follows there.
+#pragma once
+
+#include "hqq_layers_epilogue.h"
+
+namespace hqq {
+namespace {
+
+constexpr int kSkinnyWaves = 8;      // waves per workgroup, at most
+
+// X in LDS: a row is K / 8 + 1 runs, so that 16 rows fall in different banks
+inline int64_t skinny_x_bytes(int64_t rows, int64_t K) { return rows * (K / 8 + 1) * 16; }
+
+// Activations chosen at run time (one element at a time: the code is small).
+__device__ __forceinline__ float act_any(int act, float g, float &d)
+{
+    return act == HQQ_ACT_SILU   ? act_value<HQQ_ACT_SILU>(g, d)
+           : act == HQQ_ACT_GELU ? act_value<HQQ_ACT_GELU>(g, d)
+                                 : act_value<HQQ_ACT_GELU_TANH>(g, d);
+}
+
+// One element C[m][n] (gated: of gate and of up).  For kOutStats the 16 lanes of a
+// row hold its 16 columns; all lanes of the wave call.
+template <bool BF>
+__device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0, float c1, int m, int n)
+{
+    const bool m_in = m < g.M;
+    if (out == kOutGated) {
+        float d;
+        if (m_in && n < g.N)
+            g.out[(int64_t)m * g.ldo + n] = out1<BF>(act_any(g.act, c0, d) * c1);
+    } else if (out == kOutGatedGrad) {
+        if (m_in && n < g.up_off) {
+            float vg = 0.0f, vu = 0.0f;
+            if (n < g.N) {
+                float d;
+                const float f = act_any(g.act, c0, d);
+                const float y = from16(g.dY[(int64_t)m * g.N + n], BF) * (g.rscale ? g.rscale[m] : 1.0f);
+                vg = y * c1 * d;
+                vu = y * f;
+            }
+            uint16_t *o = g.out + (int64_t)m * g.ldo + n;
+            o[0] = out1<BF>(vg);
+            o[g.up_off] = out1<BF>(vu);
+        }
+    } else if (out == kOutStats) {
+        const int64_t at = m_in ? g.targets[m] : -1;
+        if (n == at && n < g.N && m_in)
+            g.tlogit[m] = c0;
+        const bool in = n < g.N && n != at;
+        float mx = in ? c0 : -INFINITY;
+#pragma unroll
+        for (int o = 1; o < 16; o *= 2)
+            mx = fmaxf(mx, __shfl_xor(mx, o));
+        const float ref = mx > -INFINITY ? mx * kLog2e : 0.0f;
+        float sum = in ? exp2_fast(__builtin_fmaf(c0, kLog2e, -ref)) : 0.0f;
+#pragma unroll
+        for (int o = 1; o < 16; o *= 2)
+            sum += __shfl_xor(sum, o);
+        if (m_in && (n & 15) == 0)
+            g.stats[(int64_t)m * g.blocks + n / 16] = float2{mx, sum};
+    } else {
+        const int64_t at = m_in ? g.targets[m] : -1;
+        if (m_in && n < g.ldo) {
+            float v = 0.0f;
+            if (at >= 0 && at < g.Nall && n < g.N) {
+                const float p = exp2_fast((c0 - g.lse[m]) * kLog2e) - (n == at ? 1.0f : 0.0f);
+                v = BF ? p : p * 32768.0f;
+            }
+            g.out[(int64_t)m * g.ldo + n] = out1<BF>(v);
+        }
+    }
+}
+
+// NM: matrices (2: gate and up).  The workgroup's waves split K.
+template <int NM, bool KT, int NB, int MT, int GPC, bool XL, bool BF>
+__global__ __launch_bounds__(kSkinnyWaves * 64) __attribute__((amdgpu_waves_per_eu(MT * NM > 2 || !XL ? 3 : 4))) void
+skinny_kernel(SkinnyArgs s)
+{
+    const int WPB = blockDim.x >> 6;
+    extern __shared__ uint4 lds[];
+    const LinearArgs &a = s.w[0];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane16 = lane & 15, grp = lane >> 4;
+    const uint32_t K = (uint32_t)a.K;
+    const int64_t n_raw = (int64_t)blockIdx.x * 16 + lane16;
+    const uint32_t n = (uint32_t)(n_raw < a.N ? n_raw : a.N - 1);
+    const uint32_t nw = n * (uint32_t)a.wpr, ng = n * (uint32_t)a.gpl;
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int mrows = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT);
+    const uint32_t xrow = K / 8 + 1;
+    uint32_t xr[MT];      // rows past M repeat the last; their outputs are not stored
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+        const int r = 16 * u + lane16 < mrows ? 16 * u + lane16 : mrows - 1;
+        xr[u] = XL ? (uint32_t)r * xrow : (uint32_t)((m0 + r) * a.K);
+    }
+
+    const int n_steps = (int)((K + kStepK - 1) / kStepK);
+    const int my = n_steps > wave ? (n_steps - wave + WPB - 1) / WPB : 0;
+    auto kbase = [&](int i) { return (uint32_t)(wave + i * WPB) * kStepK; };
+    StepBuf<NB, GPC> buf[NM];
+    auto load = [&](int i) {
+        const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
+#pragma unroll
+        for (int j = 0; j < NM; ++j)
+            load_step(buf[j], s.w[j], c, nw, ng);
+    };
+    // the first codes are on their way before X is staged
+    if (my > 0)
+        load(0);
+    if constexpr (XL) {
+        const uint32_t runs = K / 8;
+        const uint4 *xg = reinterpret_cast<const uint4 *>(a.X + m0 * a.K);
+        for (uint32_t c = threadIdx.x; c < (uint32_t)mrows * runs; c += WPB * 64) {
+            const uint32_t m = c / runs, r = c - m * runs;
+            lds[m * xrow + r] = run_order(xg[c]);
+        }
+        __syncthreads();
+    }
+    float4v acc[NM][MT];
+#pragma unroll
+    for (int j = 0; j < NM; ++j)
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+            acc[j][u] = float4v{0.f, 0.f, 0.f, 0.f};
+    XRuns<XL ? 1 : MT> xg;
+    for (int i = 0; i < my; ++i) {
+        const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
+        const uint32_t k0 = kbase(i) + kLaneK * grp;
+        const uint32_t km0 = k0 < K ? 0xffffffffu : 0u;
+        const uint32_t km1 = k0 + 32 < K ? 0xffffffffu : 0u;
+        if constexpr (!XL)
+            load_x(xg, a, c, xr);
+        StepBuf<NB, GPC> cur[NM];
+#pragma unroll
+        for (int j = 0; j < NM; ++j)
+            cur[j] = buf[j];
+        if (i + 1 < my)
+            load(i + 1);
+#pragma unroll
+        for (int j = 0; j < NM; ++j)
+            compute_step<KT, NB, MT, GPC, XL, BF>(cur[j], xg, km0, km1, lds, xr, c, acc[j]);
+    }
+
+    // the waves' sums: red[wave][matrix][4 u + r][lane]
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int j = 0; j < NM; ++j)
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                red[((wave * NM + j) * MT * 4 + u * 4 + r) * 64 + lane] = acc[j][u][r];
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < MT * 4 * 64; idx += WPB * 64) {
+        const int v = idx >> 6, l = idx & 63;      // one v per wave
+        float c[NM];
+#pragma unroll
+        for (int j = 0; j < NM; ++j) {
+            c[j] = 0.0f;
+            for (int w = 0; w < WPB; ++w)
+                c[j] += red[((w * NM + j) * MT * 4 + v) * 64 + l];
+        }
+        // sum r of lane l is C[4 (l / 16) + r][l % 16] of m tile u
+        const int m = (int)m0 + 16 * (v >> 2) + 4 * (l >> 4) + (v & 3);
+        const int nn = (int)blockIdx.x * 16 + (l & 15);
+        element<BF>(s.out, s.g, c[0], c[NM - 1], m, nn);
+    }
+}
+
+template <int NM, int NB, int MT, int GPC, bool XL, bool BF>
+hipError_t launch_xl(const SkinnyArgs &s, dim3 grid, int waves, hipStream_t st)
+{
+    const LinearArgs &a = s.w[0];
+    size_t lds = (size_t)waves * NM * MT * 4 * 64 * sizeof(float);
+    if (XL) {
+        const size_t x = (size_t)skinny_x_bytes(a.M < 16 * MT ? a.M : 16 * MT, a.K);
+        lds = x > lds ? x : lds;
+    }
+    if (a.K % kStepK != 0)
+        hipLaunchKernelGGL((skinny_kernel<NM, true, NB, MT, GPC, XL, BF>), grid, dim3(waves * 64), lds, st, s);
+    else
+        hipLaunchKernelGGL((skinny_kernel<NM, false, NB, MT, GPC, XL, BF>), grid, dim3(waves * 64), lds, st, s);
+    return hipGetLastError();
+}
+
+template <int NM, int NB, int MT, int GPC, bool BF>
+hipError_t launch_gpc(const SkinnyArgs &s, hipStream_t st)
+{
+    const LinearArgs &a = s.w[0];
+    const dim3 grid((unsigned)((s.cols + 15) / 16), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+    const int64_t blocks = (int64_t)grid.x * grid.y, steps = (a.K + kStepK - 1) / kStepK;
+    const int waves = blocks < 512 && steps > 4 ? 8 : 4;
+    // X in LDS where that leaves the CU 16 waves
+    const int64_t x = skinny_x_bytes(a.M < 16 * MT ? a.M : 16 * MT, a.K);
+    return x <= (waves == 8 ? 64 : 40) * 1024 ? launch_xl<NM, NB, MT, GPC, true, BF>(s, grid, waves, st)
+                                              : launch_xl<NM, NB, MT, GPC, false, BF>(s, grid, waves, st);
+}
+
+template <int NM, int NB, bool BF>
+hipError_t launch_mt(const SkinnyArgs &s, hipStream_t st)
+{
+    const int gpc = groups_per_chunk(s.w[0].gs);
+    if (s.w[0].M <= 16)
+        return gpc == 1   ? launch_gpc<NM, NB, 1, 1, BF>(s, st)
+               : gpc == 2 ? launch_gpc<NM, NB, 1, 2, BF>(s, st)
+                          : launch_gpc<NM, NB, 1, 8, BF>(s, st);
+    return gpc == 1   ? launch_gpc<NM, NB, 2, 1, BF>(s, st)
+           : gpc == 2 ? launch_gpc<NM, NB, 2, 2, BF>(s, st)
+                      : launch_gpc<NM, NB, 2, 8, BF>(s, st);
+}
+
+template <int NM>
+hipError_t launch_skinny_nm(int nbits, bool bf16, const SkinnyArgs &s, hipStream_t st)
+{
+    switch (nbits) {
+    case 1: return bf16 ? launch_mt<NM, 1, true>(s, st) : launch_mt<NM, 1, false>(s, st);
+    case 2: return bf16 ? launch_mt<NM, 2, true>(s, st) : launch_mt<NM, 2, false>(s, st);
+    case 4: return bf16 ? launch_mt<NM, 4, true>(s, st) : launch_mt<NM, 4, false>(s, st);
+    case 8: return bf16 ? launch_mt<NM, 8, true>(s, st) : launch_mt<NM, 8, false>(s, st);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+}  // namespace hqq

@@ -12,24 +12,12 @@
 // each XCD gets a contiguous part of them, so that the lines of codes, scales and
 // zeros that neighbours along k share are fetched into one L2 only.  Bound by the
 // bytes written.
-#include "hqq_layers_internal.h"
-#include "hqq_linear_dev.h"
+#include "hqq_layers_epilogue.h"
 
 namespace hqq {
 namespace {
 
 constexpr int kUnpackWaves = 4;
-
-// 1 / s in fp64 by two Newton steps from v_rcp_f64 (2^-24 or better): within 2^-51.5
-// relative, which the exactness of wq needs no more than (a quotient is nowhere nearer
-// than 2^-49 to where fp32 rounds the other way); a third of the division's steps.
-__device__ __forceinline__ double reciprocal(float s)
-{
-    const double d = (double)s;
-    double r = __builtin_amdgcn_rcp(d);
-    r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-    return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-}
 
 template <int NB, bool BF, bool WANT_W, bool WANT_T>
 __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)

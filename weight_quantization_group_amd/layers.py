@@ -16,7 +16,7 @@ import os
 
 import torch
 
-from . import _U32, DTYPE_BF16, DTYPE_FP16, HQQError, _dev_ptr, _stream
+from . import _U32, DTYPE_BF16, DTYPE_FP16, HQQError
 
 LAYERS_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhqq_layers.so")
 
@@ -84,7 +84,7 @@ def hqq_layers_strerror(status: int) -> str:
 
 
 def _bytes(name: str, *args) -> int:
-    n = getattr(load_layers_library(), name)(*args)
+    n = getattr(_lib or load_layers_library(), name)(*args)
     if n < 0:
         raise LayersError(name, n)
     return int(n)
@@ -117,42 +117,50 @@ def hqq_linear_cross_entropy_backward_workspace(M: int, K: int, N: int, nbits: i
 
 
 _DT = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
+_F32, _I64 = (torch.float32,), (torch.int64,)
 
 
-def _matrix(t, name: str, rows: int | None = None, cols: int | None = None, like=None):
-    """Check a 16-bit [rows, cols] CUDA tensor (of like's dtype and device)."""
+def _array(t, name: str, dtypes, n: int, device) -> int:
+    """The address of a contiguous CUDA tensor of n values on device, checked."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DT or (like is not None and t.dtype != like.dtype):
-        raise TypeError(f"{name} must be float16 or bfloat16, the same in all arguments, got {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be [{'M' if rows is None else rows}, {'K' if cols is None else cols}], "
-                         f"got {tuple(t.shape)}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, the other arguments are on {like.device}")
-    return _dev_ptr(t, name, (t.dtype,))
-
-
-def _array(t, name: str, dtypes, n: int, device):
-    """Check a CUDA tensor of n values on device."""
-    p = _dev_ptr(t, name, dtypes)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other arguments are on {device}")
-    return p
+    return t.data_ptr()
+
+
+def _first(t, name: str):
+    """(rows, columns, device) of the 16-bit matrix that sets a call's dtype and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DT:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
+    return t.shape[0], t.shape[1], t.device
+
+
+def _matrix(t, name: str, rows: int, cols: int, like) -> int:
+    """The address of a [rows, cols] CUDA tensor of like's dtype and device, checked."""
+    if isinstance(t, torch.Tensor) and t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    return _array(t, name, (like.dtype,), rows * cols, like.device)
 
 
 def _weight(w, name: str, N: int, K: int, nbits: int, group_size: int, device):
-    """The checked pointers (packed, scale, zero) of a weight [N, K]."""
+    """The addresses (packed, scale, zero) of a weight [N, K], checked."""
     packed, scale, zero = w
-    f32 = (torch.float32,)
     # sizes the library refuses are left to it
     words = N * K * nbits // 32 if nbits in (1, 2, 4, 8) else packed.numel()
     groups = N * (K // group_size) if group_size > 0 else scale.numel()
-    return (_array(packed, f"{name} packed", _U32, words, device).value,
-            _array(scale, f"{name} scale", f32, groups, device).value,
-            _array(zero, f"{name} zero", f32, groups, device).value)
+    return (_array(packed, name, _U32, words, device), _array(scale, name, _F32, groups, device),
+            _array(zero, name, _F32, groups, device))
 
 
 def _act(activation: str) -> int:
@@ -161,18 +169,26 @@ def _act(activation: str) -> int:
     return ACT_CODES[activation]
 
 
-def _call(name: str, device, workspace, need: int, *args):
-    """Run the library's call `name` on device's current stream with a workspace."""
+def _call(name: str, device, workspace, sizes, *args):
+    """Run the library's call `name` on device's current stream, with a workspace of
+    the size for `sizes` where none is given."""
     if workspace is None:
+        need = _bytes(name + "_workspace", *sizes)
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor")
-    elif workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, the other arguments are on {device}")
-    ptr = ctypes.c_void_p(workspace.data_ptr() if workspace is not None and workspace.numel() else None)
-    size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    with torch.cuda.device(device):
-        st = getattr(load_layers_library(), name)(*args, ptr, size, _stream(device))
+        ptr = workspace.data_ptr() if need else None
+    else:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous CUDA tensor")
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, the other arguments are on {device}")
+        need = workspace.numel() * workspace.element_size()
+        ptr = workspace.data_ptr() if need else None
+    f = getattr(_lib or load_layers_library(), name)
+    if torch.cuda.current_device() == device.index:
+        st = f(*args, ptr, need, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, ptr, need, torch._C._cuda_getCurrentRawStream(device.index))
     if st != 0:
         raise LayersError(name, st)
 
@@ -182,16 +198,15 @@ def hqq_linear_gated(X: torch.Tensor, gate, up, N: int, nbits: int, group_size: 
     """Y = act(X . Wg_hat^T) * (X . Wu_hat^T) as a tensor [M, N]: the first half of a
     gated feed-forward block, for X [M, K] and the weights gate and up [N, K], each
     (packed, scale, zero).  activation: "silu", "gelu" or "gelu_tanh"."""
-    px = _matrix(X, "X")
-    M, K = X.shape
+    M, K, dev = _first(X, "X")
     act = _act(activation)
-    g = HqqWeight(*_weight(gate, "gate", N, K, nbits, group_size, X.device))
-    u = HqqWeight(*_weight(up, "up", N, K, nbits, group_size, X.device))
-    need = hqq_linear_gated_workspace(M, K, N, nbits, group_size)
+    px = _matrix(X, "X", M, K, X)
+    g = HqqWeight(*_weight(gate, "gate", N, K, nbits, group_size, dev))
+    u = HqqWeight(*_weight(up, "up", N, K, nbits, group_size, dev))
     if out is None:
-        out = torch.empty((M, N), dtype=X.dtype, device=X.device)
-    _call("hqq_linear_gated", X.device, workspace, need, px, M, K, ctypes.byref(g), ctypes.byref(u), N, nbits,
-          group_size, _DT[X.dtype], act, _matrix(out, "out", M, N, X))
+        out = X.new_empty((M, N))
+    _call("hqq_linear_gated", dev, workspace, (M, K, N, nbits, group_size), px, M, K, ctypes.byref(g), ctypes.byref(u),
+          N, nbits, group_size, _DT[X.dtype], act, _matrix(out, "out", M, N, X))
     return out
 
 
@@ -200,17 +215,15 @@ def hqq_linear_gated_backward(dY: torch.Tensor, X: torch.Tensor, gate, up, N: in
                               workspace=None) -> torch.Tensor:
     """The gradient dX [M, K] of hqq_linear_gated's input, from the gradient dY [M, N]
     of its output; the two projections are computed anew from X."""
-    px = _matrix(X, "X")
-    M, K = X.shape
+    M, K, dev = _first(X, "X")
     act = _act(activation)
-    py = _matrix(dY, "dY", M, N, X)
-    g = HqqWeight(*_weight(gate, "gate", N, K, nbits, group_size, X.device))
-    u = HqqWeight(*_weight(up, "up", N, K, nbits, group_size, X.device))
-    need = hqq_linear_gated_backward_workspace(M, K, N, nbits, group_size)
+    px, py = _matrix(X, "X", M, K, X), _matrix(dY, "dY", M, N, X)
+    g = HqqWeight(*_weight(gate, "gate", N, K, nbits, group_size, dev))
+    u = HqqWeight(*_weight(up, "up", N, K, nbits, group_size, dev))
     if out is None:
-        out = torch.empty((M, K), dtype=X.dtype, device=X.device)
-    _call("hqq_linear_gated_backward", X.device, workspace, need, py, px, M, K, ctypes.byref(g), ctypes.byref(u), N,
-          nbits, group_size, _DT[X.dtype], act, _matrix(out, "out", M, K, X))
+        out = X.new_empty((M, K))
+    _call("hqq_linear_gated_backward", dev, workspace, (M, K, N, nbits, group_size), py, px, M, K, ctypes.byref(g),
+          ctypes.byref(u), N, nbits, group_size, _DT[X.dtype], act, _matrix(out, "out", M, K, X))
     return out
 
 
@@ -220,22 +233,23 @@ def hqq_linear_batch_backward(dYs, weights, K: int, nbits: int, group_size: int,
     weights read (hqq_linear_batch), from the gradients dYs of their outputs.
     weights: [(packed, scale, zero, N), ...], at most MAX_GRADS."""
     dYs, weights = list(dYs), list(weights)
-    if len(dYs) != len(weights) or not dYs:
-        raise ValueError(f"one dY for each weight, at least one: got {len(dYs)} and {len(weights)}")
-    if len(dYs) > MAX_GRADS:
-        raise ValueError(f"at most {MAX_GRADS} weights, got {len(dYs)}")
+    count = len(dYs)
+    if count != len(weights) or not dYs:
+        raise ValueError(f"one dY for each weight, at least one: got {count} and {len(weights)}")
+    if count > MAX_GRADS:
+        raise ValueError(f"at most {MAX_GRADS} weights, got {count}")
     first = dYs[0]
-    _matrix(first, "dYs[0]")
-    M, dev = first.shape[0], first.device
-    arr = (HqqLinearGrad * len(dYs))()
+    M, _, dev = _first(first, "dYs[0]")
+    arr = (HqqLinearGrad * count)()
+    widths = (ctypes.c_int64 * count)()
     for i, (dY, (packed, scale, zero, N)) in enumerate(zip(dYs, weights)):
-        arr[i] = HqqLinearGrad(*_weight((packed, scale, zero), f"weights[{i}]", N, K, nbits, group_size, dev), N,
-                               _matrix(dY, f"dYs[{i}]", M, N, first).value)
-    need = hqq_linear_batch_backward_workspace(M, K, [w[3] for w in weights], nbits, group_size)
+        widths[i] = N
+        arr[i] = HqqLinearGrad(*_weight((packed, scale, zero), "weights", N, K, nbits, group_size, dev), N,
+                               _matrix(dY, "dYs", M, N, first))
     if out is None:
-        out = torch.empty((M, K), dtype=first.dtype, device=dev)
-    _call("hqq_linear_batch_backward", dev, workspace, need, arr, len(dYs), M, K, nbits, group_size,
-          _DT[first.dtype], _matrix(out, "out", M, K, first))
+        out = first.new_empty((M, K))
+    _call("hqq_linear_batch_backward", dev, workspace, (M, K, widths, count, nbits, group_size), arr, count, M, K, nbits,
+          group_size, _DT[first.dtype], _matrix(out, "out", M, K, first))
     return out
 
 
@@ -251,16 +265,13 @@ def hqq_linear_cross_entropy(X: torch.Tensor, targets: torch.Tensor, packed, sca
     """Softmax cross entropy of the logits X . W_hat^T of a quantized head W [N, K]
     against targets (int64 [M]): (loss, lse), fp32 [M] each.  A row whose target lies
     outside [0, N) is ignored: its loss is 0.  The logits are never kept."""
-    px = _matrix(X, "X")
-    M, K = X.shape
-    dev = X.device
-    pt = _array(targets, "targets", (torch.int64,), M, dev)
+    M, K, dev = _first(X, "X")
+    px, pt = _matrix(X, "X", M, K, X), _array(targets, "targets", _I64, M, dev)
     w = HqqWeight(*_weight((packed, scale, zero), "head", N, K, nbits, group_size, dev))
-    need = hqq_linear_cross_entropy_workspace(M, K, N, nbits, group_size)
-    loss = torch.empty(M, dtype=torch.float32, device=dev) if loss is None else loss
-    lse = torch.empty(M, dtype=torch.float32, device=dev) if lse is None else lse
-    _call("hqq_linear_cross_entropy", dev, workspace, need, px, M, K, ctypes.byref(w), N, nbits, group_size,
-          _DT[X.dtype], pt, _array(loss, "loss", (torch.float32,), M, dev), _array(lse, "lse", (torch.float32,), M, dev))
+    loss = targets.new_empty(M, dtype=torch.float32) if loss is None else loss
+    lse = targets.new_empty(M, dtype=torch.float32) if lse is None else lse
+    _call("hqq_linear_cross_entropy", dev, workspace, (M, K, N, nbits, group_size), px, M, K, ctypes.byref(w), N, nbits,
+          group_size, _DT[X.dtype], pt, _array(loss, "loss", _F32, M, dev), _array(lse, "lse", _F32, M, dev))
     return loss, lse
 
 
@@ -269,16 +280,12 @@ def hqq_linear_cross_entropy_backward(dloss: torch.Tensor, X: torch.Tensor, targ
                                       group_size: int, out=None, workspace=None) -> torch.Tensor:
     """The gradient dX [M, K] of hqq_linear_cross_entropy's input, from the gradient
     dloss (fp32 [M]) of its losses and the lse that it returned.  Ignored rows get 0."""
-    px = _matrix(X, "X")
-    M, K = X.shape
-    dev = X.device
-    f32 = (torch.float32,)
-    pd, pl = _array(dloss, "dloss", f32, M, dev), _array(lse, "lse", f32, M, dev)
-    pt = _array(targets, "targets", (torch.int64,), M, dev)
+    M, K, dev = _first(X, "X")
+    px, pt = _matrix(X, "X", M, K, X), _array(targets, "targets", _I64, M, dev)
+    pd, pl = _array(dloss, "dloss", _F32, M, dev), _array(lse, "lse", _F32, M, dev)
     w = HqqWeight(*_weight((packed, scale, zero), "head", N, K, nbits, group_size, dev))
-    need = hqq_linear_cross_entropy_backward_workspace(M, K, N, nbits, group_size)
     if out is None:
-        out = torch.empty((M, K), dtype=X.dtype, device=dev)
-    _call("hqq_linear_cross_entropy_backward", dev, workspace, need, pd, px, M, K, ctypes.byref(w), N, nbits,
-          group_size, _DT[X.dtype], pt, pl, _matrix(out, "out", M, K, X))
+        out = X.new_empty((M, K))
+    _call("hqq_linear_cross_entropy_backward", dev, workspace, (M, K, N, nbits, group_size), pd, px, M, K,
+          ctypes.byref(w), N, nbits, group_size, _DT[X.dtype], pt, pl, _matrix(out, "out", M, K, X))
     return out
