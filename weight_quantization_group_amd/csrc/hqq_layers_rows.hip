@@ -38,21 +38,25 @@ __device__ __forceinline__ float2 join(float2 a, float2 b)
     return float2{m, a.y * expf(a.x - m) + b.y * expf(b.x - m)};
 }
 
-// one wave per row
+// one workgroup per row
 __global__ __launch_bounds__(kRowsBlock) void loss_kernel(LossArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * (kRowsBlock / 64) + (threadIdx.x >> 6);
-    if (m >= a.M)
-        return;
+    __shared__ float2 parts[kRowsBlock / 64];
+    const int64_t m = blockIdx.x;
     float2 s{-INFINITY, 0.0f};
-    for (int64_t b = lane; b < a.blocks; b += 64)
+    for (int64_t b = threadIdx.x; b < a.blocks; b += kRowsBlock)
         s = join(s, a.stats[m * a.blocks + b]);
 #pragma unroll
     for (int o = 1; o < 64; o *= 2)
         s = join(s, float2{__shfl_xor(s.x, o), __shfl_xor(s.y, o)});
-    if (lane != 0)
+    if ((threadIdx.x & 63) == 0)
+        parts[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x != 0)
         return;
+#pragma unroll
+    for (int w = 1; w < kRowsBlock / 64; ++w)
+        s = join(s, parts[w]);
     if (!a.first)
         s = join(a.state[m], s);
     if (!a.last) {
@@ -152,7 +156,7 @@ hipError_t launch_reduce(bool bf16, const ReduceArgs &a, hipStream_t s)
 
 hipError_t launch_loss(const LossArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL(loss_kernel, dim3(blocks_for(a.M, kRowsBlock / 64)), dim3(kRowsBlock), 0, s, a);
+    hipLaunchKernelGGL(loss_kernel, dim3((unsigned)a.M), dim3(kRowsBlock), 0, s, a);
     return hipGetLastError();
 }
 
