@@ -103,7 +103,7 @@ UnpackArgs unpack_args(const uint32_t *packed, const float *scale, const float *
     a.n = n;
     a.K = K;
     a.gshift = log2_group(group_size);
-    a.ldw = round_up(K, kStep);
+    a.ldw = pitch_for(K);
     return a;
 }
 
@@ -128,16 +128,19 @@ hipError_t whole_steps(const uint16_t *&A, int64_t m, int64_t depth, uint16_t *p
         return hipSuccess;
     const uint16_t *src = A;
     A = pad;
-    return launch_pad_rows(src, m, depth, pad, round_up(depth, kStep), s);
+    return launch_pad_rows(src, m, depth, pad, pitch_for(depth), s);
 }
 
-int64_t pad_values(int64_t m, int64_t depth) { return depth % kStep ? m * round_up(depth, kStep) : 0; }
+int64_t pad_values(int64_t m, int64_t depth) { return depth % kStep ? m * pitch_for(depth) : 0; }
 
-// one segment of whole steps, contiguous
-void single_segment(GemmArgs &g, const uint16_t *A, int64_t depth)
+// row pitch of an A that whole_steps has seen
+int64_t whole_pitch(int64_t depth) { return depth % kStep ? pitch_for(depth) : depth; }
+
+// one segment of whole steps
+void single_segment(GemmArgs &g, const uint16_t *A, int64_t depth, int64_t pitch)
 {
     g.A[0] = A;
-    g.lda[0] = depth;
+    g.lda[0] = pitch;
     g.step0[0] = 0;
     g.step0[1] = (int32_t)(depth / kStep);
     g.segs = 1;
@@ -256,7 +259,7 @@ struct GatedLayout {
         Carve c(p);
         W = X = nullptr;
         if (M > kFewRows) {
-            W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
+            W = c.take<uint16_t>(2 * round_up(N, 32) * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(M, K));
         }
         bytes = c.at;
@@ -273,11 +276,11 @@ struct GatedGradLayout {
         Carve c(p);
         W = WT = X = nullptr;
         if (M > kFewRows) {
-            W = c.take<uint16_t>(2 * round_up(N, 32) * round_up(K, kStep));
+            W = c.take<uint16_t>(2 * round_up(N, 32) * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(mc, K));
-            WT = c.take<uint16_t>(K * 2 * Np);
+            WT = c.take<uint16_t>(K * pitch_for(2 * Np));
         }
-        dGU = c.take<uint16_t>(mc * 2 * Np);
+        dGU = c.take<uint16_t>(mc * pitch_for(2 * Np));
         scale = c.take<float>(mc);
         inv = c.take<float>(mc);
         const int64_t n[2] = {N, N};
@@ -304,10 +307,12 @@ struct BatchGradLayout {
         }
         for (int i = 0; i < count; ++i)
             ldt += round_up(n[i], kStep);
+        const int64_t steps = ldt / kStep;
+        ldt = pitch_for(ldt);
         WT = c.take<uint16_t>(K * ldt);
         for (int i = 0; i < count; ++i)
             pad[i] = c.take_some<uint16_t>(pad_values(mc, n[i]));
-        part = c.take<float>(part_floats(M, K, ldt / kStep));
+        part = c.take<float>(part_floats(M, K, steps));
         bytes = c.at;
     }
 };
@@ -332,7 +337,7 @@ struct LossLayout {
         if (M > kFewRows) {
             piece = loss_piece(K, N);
             blocks = (piece + 63) / 64;
-            W = c.take<uint16_t>(piece * round_up(K, kStep));
+            W = c.take<uint16_t>(piece * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(M, K));
         } else {
             piece = N;
@@ -377,13 +382,13 @@ struct LossGradLayout {
             return;
         }
         piece = loss_grad_piece(M, K, N);
-        ldl = round_up(piece, kStep);
-        W = c.take<uint16_t>(piece * round_up(K, kStep));
+        ldl = pitch_for(piece);
+        W = c.take<uint16_t>(piece * pitch_for(K));
         WT = c.take<uint16_t>(K * ldl);
         dL = c.take<uint16_t>(mc * ldl);
         X = c.take_some<uint16_t>(pad_values(mc, K));
         rowf = c.take<float>(mc);
-        int64_t f = part_floats(M, K, ldl / kStep);
+        int64_t f = part_floats(M, K, (piece + kStep - 1) / kStep);
         const int64_t rest = N % piece;
         if (rest) {
             const int64_t f2 = part_floats(M, K, (rest + kStep - 1) / kStep);
@@ -453,7 +458,7 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
         f.g.act = act;
         return launch_skinny(nbits, bf16, f, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
     }
-    const int64_t ldw = round_up(K, kStep);
+    const int64_t ldw = pitch_for(K);
     for (int i = 0; i < 2; ++i) {
         const hqq_weight &w = i ? *up : *gate;
         UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
@@ -465,7 +470,7 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
     if (whole_steps(X, M, K, l.X, s) != hipSuccess)
         return HQQ_EHIP;
     GemmArgs g{};
-    single_segment(g, X, ldw);
+    single_segment(g, X, round_up(K, kStep), whole_pitch(K));
     g.B = l.W;
     g.ldb = ldw;
     g.M = (int32_t)M;
@@ -501,7 +506,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t ldw = round_up(K, kStep), Np = round_up(N, kStep);
+    const int64_t ldw = pitch_for(K), Np = round_up(N, kStep), ldg = pitch_for(2 * Np);
     if (M <= kFewRows) {
         if (!bf16 && launch_row_scale(dY, M, N, l.scale, l.inv, s) != hipSuccess)
             return HQQ_EHIP;
@@ -513,14 +518,14 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         f.g.M = (int32_t)M;
         f.g.N = (int32_t)N;
         f.g.out = l.dGU;
-        f.g.ldo = 2 * Np;
-        f.g.up_off = Np;
+        f.g.ldo = ldg;
+        f.g.fill = Np;
         f.g.act = act;
         f.g.dY = dY;
         f.g.rscale = bf16 ? nullptr : l.scale;
         SkinnyGradArgs b{};
-        add_grad(b, gate->packed, gate->scale, gate->zero, l.dGU, 2 * Np, N);
-        add_grad(b, up->packed, up->scale, up->zero, l.dGU + Np, 2 * Np, N);
+        add_grad(b, gate->packed, gate->scale, gate->zero, l.dGU, ldg, N);
+        add_grad(b, up->packed, up->scale, up->zero, l.dGU + Np, ldg, N);
         return launch_skinny(nbits, bf16, f, s) == hipSuccess &&
                        few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, bf16 ? nullptr : l.inv, s) ==
                            hipSuccess
@@ -533,7 +538,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         a.W = l.W;
         a.interleave = 1 + i;
         a.WT = l.WT + i * Np;
-        a.ldt = 2 * Np;
+        a.ldt = ldg;
         if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
             return HQQ_EHIP;
     }
@@ -546,7 +551,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         if (whole_steps(x, m, K, l.X, s) != hipSuccess)
             return HQQ_EHIP;
         GemmArgs g{};
-        single_segment(g, x, ldw);
+        single_segment(g, x, round_up(K, kStep), whole_pitch(K));
         g.B = l.W;
         g.ldb = ldw;
         g.M = (int32_t)m;
@@ -555,14 +560,14 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         g.dY = dY + m0 * N;
         g.rscale = bf16 ? nullptr : l.scale;
         g.out = l.dGU;
-        g.ldo = 2 * Np;
-        g.up_off = Np;
+        g.ldo = ldg;
+        g.fill = Np;
         if (launch_gemm(kOutGatedGrad, bf16, g, s) != hipSuccess)
             return HQQ_EHIP;
         GemmArgs p{};
-        single_segment(p, l.dGU, 2 * Np);
+        single_segment(p, l.dGU, 2 * Np, ldg);
         p.B = l.WT;
-        p.ldb = 2 * Np;
+        p.ldb = ldg;
         p.M = (int32_t)m;
         p.N = (int32_t)K;
         if (gradient_product(p, bf16, l.part, nullptr, true, true, dX + m0 * K, bf16 ? nullptr : l.inv, s) != hipSuccess)
@@ -628,7 +633,7 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
         g.segs = count;
         for (int i = 0; i < count; ++i) {
             g.A[i] = ws[i].dY + m0 * n[i];
-            g.lda[i] = round_up(n[i], kStep);
+            g.lda[i] = whole_pitch(n[i]);
             if (whole_steps(g.A[i], m, n[i], l.pad[i], s) != hipSuccess)
                 return HQQ_EHIP;
             g.step0[i + 1] = g.step0[i] + (int32_t)((n[i] + kStep - 1) / kStep);
@@ -666,7 +671,7 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t ldw = round_up(K, kStep);
+    const int64_t ldw = pitch_for(K);
     if (M <= kFewRows) {
         SkinnyArgs f{};
         f.w[0] = linear_args(X, *head, M, K, N, nbits, group_size);
@@ -689,7 +694,7 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
         UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
         a.W = l.W;
         GemmArgs g{};
-        single_segment(g, X, ldw);
+        single_segment(g, X, round_up(K, kStep), whole_pitch(K));
         g.B = l.W;
         g.ldb = ldw;
         g.M = (int32_t)M;
@@ -732,7 +737,7 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t ldw = round_up(K, kStep);
+    const int64_t ldw = pitch_for(K);
     const float unit = bf16 ? 1.0f : 1.0f / 32768.0f;     // of the rounded differences
     if (M <= kFewRows) {
         SkinnyArgs f{};
@@ -746,6 +751,7 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
         f.g.lse = lse;
         f.g.out = l.dL;
         f.g.ldo = l.ldl;
+        f.g.fill = l.ldl;
         SkinnyGradArgs b{};
         add_grad(b, head->packed, head->scale, head->zero, l.dL, l.ldl, N);
         return launch_loss_factor(dloss, targets, M, N, unit, l.rowf, s) == hipSuccess &&
@@ -766,9 +772,10 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
             a.W = l.W;
             a.WT = l.WT;
-            a.ldt = round_up(n, kStep);
+            const int64_t fill = round_up(n, kStep);
+            a.ldt = pitch_for(n);
             GemmArgs g{};
-            single_segment(g, x, ldw);
+            single_segment(g, x, round_up(K, kStep), whole_pitch(K));
             g.B = l.W;
             g.ldb = ldw;
             g.M = (int32_t)m;
@@ -779,8 +786,9 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             g.Nall = N;
             g.out = l.dL;
             g.ldo = a.ldt;
+            g.fill = fill;
             GemmArgs p{};
-            single_segment(p, l.dL, a.ldt);
+            single_segment(p, l.dL, fill, a.ldt);
             p.B = l.WT;
             p.ldb = a.ldt;
             p.M = (int32_t)m;

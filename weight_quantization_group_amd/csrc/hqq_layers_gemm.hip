@@ -104,7 +104,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
 #pragma unroll
             for (int t = 0; t < TN / 2; ++t) {
                 const int n = nw + 16 * t + 4 * l4;
-                if (m_in && n < g.up_off) {
+                if (m_in && n < g.fill) {
                     float y[4] = {0.f, 0.f, 0.f, 0.f}, vg[4], vu[4];
                     if (n < g.N)
                         load4<BF>(g.dY + (int64_t)m * g.N + n, y, g.N - n);
@@ -118,7 +118,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                     }
                     uint16_t *o = g.out + (int64_t)m * g.ldo + n;
                     store4<BF>(o, vg, 4);
-                    store4<BF>(o + g.up_off, vu, 4);
+                    store4<BF>(o + g.fill, vu, 4);
                 }
             }
         } else if constexpr (OUT == kOutStats) {
@@ -161,7 +161,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
 #pragma unroll
             for (int t = 0; t < TN; ++t) {
                 const int n = nw + 16 * t + 4 * l4;
-                if (m_in && n < g.ldo) {
+                if (m_in && n < g.fill) {
                     float v[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
@@ -175,16 +175,19 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
     }
 }
 
-// The tile of a workgroup.  Workgroups go to the 8 XCDs in turn: each XCD gets a
-// contiguous part of the tiles, in bands of kBand tile rows walked column by column,
-// so that the tiles that run on it at one time share rows of A and of B in its L2.
+// The tile and split of a workgroup.  Workgroups go to the 8 XCDs in turn: each XCD
+// gets a contiguous part of the tiles (of one split after the other), in bands of
+// kBand tile rows walked column by column, so that the tiles that run on it at one
+// time share rows of A and of B in its L2.
 constexpr int kBand = 4;
 
-__device__ __forceinline__ void tile_of(const GemmArgs &g, int &tm, int &tn)
+__device__ __forceinline__ void tile_of(const GemmArgs &g, int &tm, int &tn, int &split)
 {
-    const uint32_t T = (uint32_t)(g.tiles_m * g.tiles_n), id = blockIdx.x;
+    const uint32_t tiles = (uint32_t)(g.tiles_m * g.tiles_n), T = gridDim.x, id = blockIdx.x;
     const uint32_t q = T / 8, r = T % 8, x = id % 8;
-    const uint32_t t = x * q + (x < r ? x : r) + id / 8;
+    const uint32_t all = x * q + (x < r ? x : r) + id / 8;
+    split = (int)(all / tiles);
+    const uint32_t t = all - (uint32_t)split * tiles;
     const uint32_t band = t / (uint32_t)(kBand * g.tiles_n), first = band * kBand;
     const uint32_t rows = (uint32_t)g.tiles_m - first < kBand ? (uint32_t)g.tiles_m - first : kBand;
     const uint32_t l = t - first * (uint32_t)g.tiles_n;
@@ -211,8 +214,8 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    int tile_m, tile_n;
-    tile_of(g, tile_m, tile_n);
+    int tile_m, tile_n, split;
+    tile_of(g, tile_m, tile_n, split);
     const int m0 = tile_m * BM, n0 = tile_n * BNC;
 
     // DMA: wave w moves rows IA * 8 w ..., 8 rows per instruction; lane l fills
@@ -227,7 +230,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     uint32_t ldb2 = (uint32_t)(g.ldb * 2);
     const int steps = g.step0[g.segs];
     const int per = (steps + g.splits - 1) / g.splits;
-    const int s0 = (int)blockIdx.y * per;
+    const int s0 = split * per;
     const int s1 = s0 + per < steps ? s0 + per : steps;
     int seg = -1, seg_end = 0;
     const char *ab = nullptr;          // of the segment's (virtual) step 0
@@ -342,20 +345,20 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
 #pragma unroll
     for (int u = 0; u < TM; ++u)
         settle(acc[u]);
-    epilogue<OUT, ACT, BF, TM, TN>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, (int)blockIdx.y);
+    epilogue<OUT, ACT, BF, TM, TN>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, split);
 }
 
 // Tiles: 256 x 256 and 256 x 128 with 8 waves, one workgroup per CU, and 128 x 128
 // with 4 waves, two per CU.  Their times per 64-wide step with the chip full, in
-// bf16 on MI355X: 1.54, 0.92 and 0.98 us (42, 36 and 34 thousand outputs per CU
-// and us).  The fewest-time tile by rounds of workgroups over the CUs; where that
-// leaves CUs idle, the steps are split and a second pass adds the parts (about
-// 4 us and the parts' bytes at 4 TB/s).
+// bf16 on MI355X: 1.50, 0.98 and 0.95 us (44, 33 and 34 thousand outputs per CU
+// and us).  The tile of the fewest us by rounds of workgroups over the CUs; where
+// that leaves CUs idle, the steps are split and a second pass adds the parts (3 us
+// and the parts' and the result's bytes at 6 TB/s).
 struct Tile {
     int bm, bn, per_cu;
     double us;
 };
-constexpr Tile kTiles[3] = {{256, 256, 1, 1.54}, {256, 128, 1, 0.92}, {128, 128, 2, 0.98}};
+constexpr Tile kTiles[3] = {{256, 256, 1, 1.50}, {256, 128, 1, 0.98}, {128, 128, 2, 0.95}};
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 16;
 
@@ -367,7 +370,7 @@ double product_us(int tile, int64_t M, int64_t N, int64_t steps, int splits, boo
     const int64_t slots = kCus * t.per_cu;
     double us = (double)((wgs + slots - 1) / slots) * (2.0 + (double)((steps + splits - 1) / splits) * t.us);
     if (splits > 1 || parts)
-        us += 4.0 + (double)M * (double)N * 4.0 * splits * 2.0 / 4.0e6;
+        us += 3.0 + (double)M * (double)N * (4.0 * splits + 2.0) / 6.0e6;
     return us;
 }
 
@@ -397,7 +400,7 @@ hipError_t launch_tile(GemmArgs &g, hipStream_t s)
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + BNC - 1) / BNC;
     hipLaunchKernelGGL((gemm_kernel<OUT, ACT, BF, BM, BN, WM, WN>),
-                       dim3((unsigned)(g.tiles_m * g.tiles_n), (unsigned)g.splits), dim3(WM * WN * 64), 0, s, g);
+                       dim3((unsigned)(g.tiles_m * g.tiles_n * g.splits)), dim3(WM * WN * 64), 0, s, g);
     return hipGetLastError();
 }
 

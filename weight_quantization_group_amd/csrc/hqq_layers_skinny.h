@@ -41,7 +41,7 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
         if (m_in && n < g.N)
             g.out[(int64_t)m * g.ldo + n] = out1<BF>(act_any(g.act, c0, d) * c1);
     } else if (out == kOutGatedGrad) {
-        if (m_in && n < g.up_off) {
+        if (m_in && n < g.fill) {
             float vg = 0.0f, vu = 0.0f;
             if (n < g.N) {
                 float d;
@@ -52,7 +52,7 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
             }
             uint16_t *o = g.out + (int64_t)m * g.ldo + n;
             o[0] = out1<BF>(vg);
-            o[g.up_off] = out1<BF>(vu);
+            o[g.fill] = out1<BF>(vu);
         }
     } else if (out == kOutStats) {
         const int64_t at = m_in ? g.targets[m] : -1;
@@ -72,7 +72,7 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
             g.stats[(int64_t)m * g.blocks + n / 16] = float2{mx, sum};
     } else {
         const int64_t at = m_in ? g.targets[m] : -1;
-        if (m_in && n < g.ldo) {
+        if (m_in && n < g.fill) {
             float v = 0.0f;
             if (at >= 0 && at < g.Nall && n < g.N) {
                 const float p = exp2_fast((c0 - g.lse[m]) * kLog2e) - (n == at ? 1.0f : 0.0f);

@@ -33,7 +33,7 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
     const int64_t n0 = (int64_t)nb * 64 + 8 * nl;
     const int64_t runs = a.K / 8;
     const bool k_in = run < runs;
-    if (n0 >= round_up(a.n, 64) || run * 8 >= a.ldw)
+    if (n0 >= round_up(a.n, 64) || run * 8 >= round_up(a.K, 64))
         return;
 
     uint32_t v[8][4];     // row i: 8 values of the run
