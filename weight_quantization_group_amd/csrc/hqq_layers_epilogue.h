@@ -61,38 +61,15 @@ __device__ __forceinline__ float from16(uint16_t b, bool bf)
     return (float)h;
 }
 
-// four consecutive 16-bit values at p, of which the first cnt exist
+// four consecutive 16-bit values at p (8-byte aligned)
 template <bool BF>
-__device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4], int cnt)
+__device__ __forceinline__ void load4(const char *p, float (&v)[4])
 {
-    const uint32_t lo = out2<BF>(v[0], v[1]), hi = out2<BF>(v[2], v[3]);
-    if (cnt >= 4 && ((uintptr_t)p & 7u) == 0) {
-        *reinterpret_cast<uint2 *>(p) = uint2{lo, hi};
-    } else {
-        const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < cnt)
-                p[r] = h[r];
-    }
-}
-
-template <bool BF>
-__device__ __forceinline__ void load4(const uint16_t *p, float (&v)[4], int cnt)
-{
-    uint16_t h[4] = {0, 0, 0, 0};
-    if (cnt >= 4 && ((uintptr_t)p & 7u) == 0) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        h[0] = (uint16_t)u.x; h[1] = (uint16_t)(u.x >> 16); h[2] = (uint16_t)u.y; h[3] = (uint16_t)(u.y >> 16);
-    } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < cnt)
-                h[r] = p[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        v[r] = from16(h[r], BF);
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    v[0] = from16((uint16_t)u.x, BF);
+    v[1] = from16((uint16_t)(u.x >> 16), BF);
+    v[2] = from16((uint16_t)u.y, BF);
+    v[3] = from16((uint16_t)(u.y >> 16), BF);
 }
 
 }  // namespace

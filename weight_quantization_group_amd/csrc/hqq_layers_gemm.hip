@@ -60,117 +60,199 @@ __device__ __forceinline__ void settle(float4v (&c)[N])
 #endif
 }
 
-// What becomes of a wave's part of C: TM x TN blocks of 16 x 16; acc[u][t][r] of
-// lane l is C[m][n] with m = mw + 16 u + l % 16 and n = nw + 16 t + 4 (l / 16) + r.
-// Gated kinds: blocks t < TN / 2 are gate columns and t >= TN / 2 the up columns
-// of the same n = nw + 16 (t mod TN / 2) + ...
-template <int OUT, int ACT, bool BF, int TM, int TN>
-__device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)[TM][TN], int mw, int nw, int lane,
-                                         int z)
+// Eight consecutive 16-bit values at p, of which cnt exist (1 .. 8, or more).
+__device__ __forceinline__ void store8(uint16_t *p, uint4 v, int cnt)
+{
+    if (cnt >= 8 && ((uintptr_t)p & 15u) == 0) {
+        *reinterpret_cast<uint4 *>(p) = v;
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < cnt)
+                p[r] = (uint16_t)(w[r / 2] >> (16 * (r & 1)));
+    }
+}
+
+__device__ __forceinline__ uint4 load8(const uint16_t *p, int cnt)
+{
+    if (cnt >= 8 && ((uintptr_t)p & 15u) == 0)
+        return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+        if (r < cnt)
+            w[r / 2] |= (uint32_t)p[r] << (16 * (r & 1));
+    return uint4{w[0], w[1], w[2], w[3]};
+}
+
+// What becomes of a wave's part of C: TM x 4 blocks of 16 x 16; acc[u][t][r] of lane l is
+// C[m][n] with m = mw + 16 u + l % 16 and n = nw + 16 t + 4 (l / 16) + r.  Gated kinds:
+// t = 0, 1 are the gate columns and t = 2, 3 the up columns of the same 32 n.  Values go
+// through LDS (4 KB at st for the wave alone), 16 rows at a time, so that memory sees 16
+// bytes per lane and whole stretches of a row; they would otherwise be 32-byte pieces of
+// 16 rows per instruction.  A row's pitch there is 16 bytes more than its values, against
+// bank conflicts.
+template <int OUT, int ACT, bool BF, int TM>
+__device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)[TM][4], int mw, int nw, int lane,
+                                         int z, char *st)
 {
     const int l16 = lane & 15, l4 = lane >> 4;
+    if constexpr (OUT == kOutStore || OUT == kOutSoftGrad) {
+        constexpr int P = 144;
+        const int width = OUT == kOutStore ? g.N : (int)g.fill;
 #pragma unroll
-    for (int u = 0; u < TM; ++u) {
-        const int m = mw + 16 * u + l16;
-        const bool m_in = m < g.M;
-        if constexpr (OUT == kOutStore || OUT == kOutPart) {
-            const float f = OUT == kOutStore && g.rowf && m_in ? g.rowf[m] : 1.0f;
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const int n = nw + 16 * t + 4 * l4;
-                if (m_in && n < g.N) {
-                    if constexpr (OUT == kOutStore) {
-                        const float v[4] = {acc[u][t][0] * f, acc[u][t][1] * f, acc[u][t][2] * f, acc[u][t][3] * f};
-                        store4<BF>(g.out + (int64_t)m * g.ldo + n, v, g.N - n);
-                    } else {
-                        *reinterpret_cast<float4v *>(g.part + ((int64_t)z * g.M + m) * g.N + n) = acc[u][t];
-                    }
-                }
+        for (int u = 0; u < TM; ++u) {
+            const int m = mw + 16 * u + l16, mc = m < g.M ? m : g.M - 1;
+            float f = 1.0f, ref = 0.0f;
+            int64_t at = -1;
+            bool keep = true;
+            if constexpr (OUT == kOutStore) {
+                f = g.rowf ? g.rowf[mc] : 1.0f;
+            } else {
+                const int64_t tgt = g.targets[mc];
+                keep = tgt >= 0 && tgt < g.Nall;
+                at = tgt - g.n0 - nw;
+                ref = g.lse[mc];
+                f = BF ? 1.0f : 32768.0f;
             }
-        } else if constexpr (OUT == kOutGated) {
 #pragma unroll
-            for (int t = 0; t < TN / 2; ++t) {
-                const int n = nw + 16 * t + 4 * l4;
-                if (m_in && n < g.N) {
-                    float v[4], d;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = act_value<ACT>(acc[u][t][r], d) * acc[u][t + TN / 2][r];
-                    store4<BF>(g.out + (int64_t)m * g.ldo + n, v, g.N - n);
-                }
-            }
-        } else if constexpr (OUT == kOutGatedGrad) {
-            const float sc = g.rscale && m_in ? g.rscale[m] : 1.0f;
-#pragma unroll
-            for (int t = 0; t < TN / 2; ++t) {
-                const int n = nw + 16 * t + 4 * l4;
-                if (m_in && n < g.fill) {
-                    float y[4] = {0.f, 0.f, 0.f, 0.f}, vg[4], vu[4];
-                    if (n < g.N)
-                        load4<BF>(g.dY + (int64_t)m * g.N + n, y, g.N - n);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float d;
-                        const float f = act_value<ACT>(acc[u][t][r], d);
-                        const float ys = y[r] * sc;
-                        vg[r] = n + r < g.N ? ys * acc[u][t + TN / 2][r] * d : 0.0f;
-                        vu[r] = n + r < g.N ? ys * f : 0.0f;
-                    }
-                    uint16_t *o = g.out + (int64_t)m * g.ldo + n;
-                    store4<BF>(o, vg, 4);
-                    store4<BF>(o + g.fill, vu, 4);
-                }
-            }
-        } else if constexpr (OUT == kOutStats) {
-            // the row's max and sum of exp over this wave's columns, the target
-            // left out (a lane's columns, then the four lanes of the row)
-            const int64_t tgt = m_in ? g.targets[m] : -1;
-            const int64_t at = tgt >= 0 && tgt < g.Nall ? tgt - g.n0 : -1;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int t = 0; t < TN; ++t)
+            for (int t = 0; t < 4; ++t) {
+                const int n = 16 * t + 4 * l4;
+                float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int n = nw + 16 * t + 4 * l4 + r;
-                    if (n < g.N && n != at)
-                        mx = fmaxf(mx, acc[u][t][r]);
-                    if (n == at && n < g.N)
-                        g.tlogit[m] = acc[u][t][r];
+                    if constexpr (OUT == kOutStore) {
+                        v[r] = acc[u][t][r] * f;
+                    } else {
+                        const float p = exp2_fast((acc[u][t][r] - ref) * kLog2e) - (n + r == at ? 1.0f : 0.0f);
+                        v[r] = keep && nw + n + r < g.N ? p * f : 0.0f;
+                    }
                 }
+                *reinterpret_cast<uint2 *>(st + l16 * P + 2 * n) = uint2{out2<BF>(v[0], v[1]), out2<BF>(v[2], v[3])};
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = 8 * i + (lane >> 3), n = nw + 8 * (lane & 7), mr = mw + 16 * u + row;
+                const uint4 v = *reinterpret_cast<const uint4 *>(st + row * P + 16 * (lane & 7));
+                if (mr < g.M && n < width)
+                    store8(g.out + (int64_t)mr * g.ldo + n, v, width - n);
+            }
+        }
+    } else if constexpr (OUT == kOutPart) {
+        constexpr int P = 144;
+#pragma unroll
+        for (int u = 0; u < TM; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    *reinterpret_cast<float4v *>(st + l16 * P + 4 * (16 * t + 4 * l4)) = acc[u][2 * h + t];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = 8 * i + (lane >> 3), n = nw + 32 * h + 4 * (lane & 7), mr = mw + 16 * u + row;
+                    const float4v v = *reinterpret_cast<const float4v *>(st + row * P + 16 * (lane & 7));
+                    if (mr < g.M && n < g.N)
+                        *reinterpret_cast<float4v *>(g.part + ((int64_t)z * g.M + mr) * g.N + n) = v;
+                }
+            }
+    } else if constexpr (OUT == kOutGated || OUT == kOutGatedGrad) {
+        constexpr int P = 80;
+        constexpr bool GRAD = OUT == kOutGatedGrad;
+        char *sg = st, *su = st + 16 * P, *sy = st + 32 * P;
+        const int row4 = lane >> 2, n4 = nw + 8 * (lane & 3);      // coalesced: 4 lanes per row
+        uint4 y[TM];
+        if constexpr (GRAD) {
+            // all of dY at once where the tile is whole: loads behind branches come one by one
+            if (mw + 16 * TM <= g.M && nw + 32 <= g.N && g.N % 8 == 0) {
+#pragma unroll
+                for (int u = 0; u < TM; ++u)
+                    y[u] = *reinterpret_cast<const uint4 *>(g.dY + (int64_t)(mw + 16 * u + row4) * g.N + n4);
+            } else {
+#pragma unroll
+                for (int u = 0; u < TM; ++u) {
+                    const int mr = mw + 16 * u + row4;
+                    y[u] = mr < g.M && n4 < g.N ? load8(g.dY + (int64_t)mr * g.N + n4, g.N - n4) : uint4{0, 0, 0, 0};
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < TM; ++u) {
+            const int m = mw + 16 * u + l16, mc = m < g.M ? m : g.M - 1;
+            const float sc = GRAD && g.rscale ? g.rscale[mc] : 1.0f;
+            if constexpr (GRAD)
+                *reinterpret_cast<uint4 *>(sy + row4 * P + 16 * (lane & 3)) = y[u];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int n = 16 * t + 4 * l4;
+                float vg[4], vu[4], yv[4];
+                if constexpr (GRAD)
+                    load4<BF>(sy + l16 * P + 2 * n, yv);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float d;
+                    const float f = act_value<ACT>(acc[u][t][r], d);
+                    if constexpr (GRAD) {
+                        const float ys = yv[r] * sc;
+                        const bool in = nw + n + r < g.N;
+                        vg[r] = in ? ys * acc[u][t + 2][r] * d : 0.0f;
+                        vu[r] = in ? ys * f : 0.0f;
+                    } else {
+                        vg[r] = f * acc[u][t + 2][r];
+                    }
+                }
+                *reinterpret_cast<uint2 *>(sg + l16 * P + 2 * n) = uint2{out2<BF>(vg[0], vg[1]), out2<BF>(vg[2], vg[3])};
+                if constexpr (GRAD)
+                    *reinterpret_cast<uint2 *>(su + l16 * P + 2 * n) =
+                        uint2{out2<BF>(vu[0], vu[1]), out2<BF>(vu[2], vu[3])};
+            }
+            const int mr = mw + 16 * u + row4, width = GRAD ? (int)g.fill : g.N;
+            uint16_t *o = g.out + (int64_t)mr * g.ldo + n4;
+            const uint4 v = *reinterpret_cast<const uint4 *>(sg + row4 * P + 16 * (lane & 3));
+            if (mr < g.M && n4 < width)
+                store8(o, v, width - n4);
+            if constexpr (GRAD) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(su + row4 * P + 16 * (lane & 3));
+                if (mr < g.M && n4 < width)
+                    store8(o + g.fill, w, 8);
+            }
+        }
+    } else {   // kOutStats
+        // the row's max and sum of exp over this wave's 64 columns, the target left out (a
+        // lane's columns, then the four lanes of the row)
+#pragma unroll
+        for (int u = 0; u < TM; ++u) {
+            const int m = mw + 16 * u + l16;
+            const bool m_in = m < g.M;
+            const int64_t tgt = g.targets[m_in ? m : g.M - 1];
+            const int64_t at = tgt >= 0 && tgt < g.Nall ? tgt - g.n0 - nw : -1;
+            float mx = -INFINITY, tl = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int n = 16 * t + 4 * l4 + r;
+                    const float v = acc[u][t][r];
+                    mx = nw + n < g.N && n != at ? fmaxf(mx, v) : mx;
+                    tl = n == at ? v : tl;
+                }
+            if (m_in && at >= 0 && at < 64 && nw + at < g.N && ((at >> 2) & 3) == l4)
+                g.tlogit[m] = tl;
             mx = fmaxf(mx, __shfl_xor(mx, 16));
             mx = fmaxf(mx, __shfl_xor(mx, 32));
             const float ref = mx > -INFINITY ? mx * kLog2e : 0.0f;
             float sum = 0.0f;
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int n = nw + 16 * t + 4 * l4 + r;
-                    sum += n < g.N && n != at ? exp2_fast(__builtin_fmaf(acc[u][t][r], kLog2e, -ref)) : 0.0f;
+                    const int n = 16 * t + 4 * l4 + r;
+                    sum += nw + n < g.N && n != at ? exp2_fast(__builtin_fmaf(acc[u][t][r], kLog2e, -ref)) : 0.0f;
                 }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             if (m_in && l4 == 0 && nw < g.N)
-                g.stats[(int64_t)m * g.blocks + nw / (16 * TN)] = float2{mx, sum};
-        } else if constexpr (OUT == kOutSoftGrad) {
-            const int64_t tgt = m_in ? g.targets[m] : -1;
-            const bool keep = tgt >= 0 && tgt < g.Nall;
-            const int64_t at = tgt - g.n0;
-            const float ref = keep ? g.lse[m] : 0.0f;
-            const float sc = BF ? 1.0f : 32768.0f;
-#pragma unroll
-            for (int t = 0; t < TN; ++t) {
-                const int n = nw + 16 * t + 4 * l4;
-                if (m_in && n < g.fill) {
-                    float v[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float p = exp2_fast((acc[u][t][r] - ref) * kLog2e) - (n + r == at ? 1.0f : 0.0f);
-                        v[r] = keep && n + r < g.N ? p * sc : 0.0f;
-                    }
-                    store4<BF>(g.out + (int64_t)m * g.ldo + n, v, 4);
-                }
-            }
+                g.stats[(int64_t)m * g.blocks + nw / 64] = float2{mx, sum};
         }
     }
 }
@@ -341,11 +423,13 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     }
     if (s < s1)
         step(s, as0, bs0, as1, bs1);
-    __builtin_amdgcn_s_waitcnt(0x0070);       // no DMA outlives the workgroup
+    tile_barrier();        // no DMA is under way and no operand read: the buffers are free
 #pragma unroll
     for (int u = 0; u < TM; ++u)
         settle(acc[u]);
-    epilogue<OUT, ACT, BF, TM, TN>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, split);
+    static_assert(BM * 128 >= NW / 2 * 4096, "4 KB per wave");
+    char *st = reinterpret_cast<char *>(wave < NW / 2 ? as0 : as1) + (wave % (NW / 2)) * 4096;
+    epilogue<OUT, ACT, BF, TM>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, split, st);
 }
 
 // Tiles: 256 x 256 and 256 x 128 with 8 waves, one workgroup per CU, and 128 x 128
