@@ -91,19 +91,29 @@ struct Carve {
     }
 };
 
-UnpackArgs unpack_args(const uint32_t *packed, const float *scale, const float *zero, int64_t row0, int64_t n, int64_t K,
-                       int nbits, int group_size)
+UnpackArgs unpack_args(const hqq_weight &w, int64_t row0, int64_t n, int64_t K, int nbits, int group_size)
 {
     UnpackArgs a{};
+    a.count = 1;
     a.wpr = K * nbits / 32;
     a.gpl = K / group_size;
-    a.packed = packed + row0 * a.wpr;
-    a.scale = scale + row0 * a.gpl;
-    a.zero = zero + row0 * a.gpl;
+    a.packed[0] = w.packed + row0 * a.wpr;
+    a.scale[0] = w.scale + row0 * a.gpl;
+    a.zero[0] = w.zero + row0 * a.gpl;
     a.n = n;
     a.K = K;
     a.gshift = log2_group(group_size);
     a.ldw = pitch_for(K);
+    return a;
+}
+
+UnpackArgs unpack_pair(const hqq_weight &gate, const hqq_weight &up, int64_t n, int64_t K, int nbits, int group_size)
+{
+    UnpackArgs a = unpack_args(gate, 0, n, K, nbits, group_size);
+    a.count = 2;
+    a.packed[1] = up.packed;
+    a.scale[1] = up.scale;
+    a.zero[1] = up.zero;
     return a;
 }
 
@@ -277,8 +287,8 @@ struct GatedGradLayout {
         W = WT = X = nullptr;
         if (M > kFewRows) {
             W = c.take<uint16_t>(2 * round_up(N, 32) * pitch_for(K));
-            X = c.take_some<uint16_t>(pad_values(mc, K));
             WT = c.take<uint16_t>(K * pitch_for(2 * Np));
+            X = c.take_some<uint16_t>(pad_values(mc, K));
         }
         dGU = c.take<uint16_t>(mc * pitch_for(2 * Np));
         scale = c.take<float>(mc);
@@ -317,49 +327,47 @@ struct BatchGradLayout {
     }
 };
 
-// classes per piece: W_hat of a piece takes about 128 MiB
+// classes per piece: W_hat of a piece takes about 128 MiB (the cache behind the L2s
+// has 256 MB)
 int64_t loss_piece(int64_t K, int64_t N)
 {
-    int64_t p = (int64_t(64) << 20) / round_up(K, kStep) / 256 * 256;
+    int64_t p = (int64_t(64) << 20) / pitch_for(K) / 256 * 256;
     p = p < 4096 ? 4096 : p;
     return p < N ? p : N;
 }
 
 struct LossLayout {
     uint16_t *W, *X;
-    float2 *stats, *state;
+    float2 *stats;
     float *tlogit;
-    int64_t bytes, piece, blocks;
+    int64_t bytes, piece, pitch;      // classes per piece; blocks that a row of stats has room for
     LossLayout(void *p, int64_t M, int64_t K, int64_t N)
     {
         Carve c(p);
         W = X = nullptr;
         if (M > kFewRows) {
             piece = loss_piece(K, N);
-            blocks = (piece + 63) / 64;
+            pitch = N / piece * ((piece + 127) / 128) + (N % piece + 127) / 128;
             W = c.take<uint16_t>(piece * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(M, K));
         } else {
             piece = N;
-            blocks = (N + 15) / 16;
+            pitch = (N + 15) / 16;
         }
-        stats = c.take<float2>(M * blocks);
-        state = c.take<float2>(M);
+        stats = c.take<float2>(M * pitch);
         tlogit = c.take<float>(M);
         bytes = c.at;
     }
 };
 
 // classes per piece of the backward pass: the 16-bit gradients of a piece's
-// logits take at most about 64 MiB, W_hat 128 MiB
-int64_t loss_grad_piece(int64_t M, int64_t K, int64_t N)
+// logits take at most about 64 MiB (beside W_hat's 128 MiB in the cache)
+int64_t loss_grad_piece(int64_t m, int64_t K, int64_t N)
 {
-    const int64_t mc = M < kRowChunk ? M : kRowChunk;
-    int64_t p = (int64_t(32) << 20) / mc / 256 * 256;
-    const int64_t q = loss_piece(K, N);
+    const int64_t c = loss_piece(K, N);
+    int64_t p = (int64_t(32) << 20) / m / 256 * 256;
     p = p < 4096 ? 4096 : p;
-    p = p < q ? p : q;
-    return p < N ? p : N;
+    return p < c ? p : c;
 }
 
 struct LossGradLayout {
@@ -381,7 +389,7 @@ struct LossGradLayout {
             bytes = c.at;
             return;
         }
-        piece = loss_grad_piece(M, K, N);
+        piece = loss_grad_piece(mc, K, N);
         ldl = pitch_for(piece);
         W = c.take<uint16_t>(piece * pitch_for(K));
         WT = c.take<uint16_t>(K * ldl);
@@ -458,27 +466,22 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
         f.g.act = act;
         return launch_skinny(nbits, bf16, f, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
     }
-    const int64_t ldw = pitch_for(K);
-    for (int i = 0; i < 2; ++i) {
-        const hqq_weight &w = i ? *up : *gate;
-        UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
-        a.W = l.W;
-        a.interleave = 1 + i;
-        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
-            return HQQ_EHIP;
-    }
     if (whole_steps(X, M, K, l.X, s) != hipSuccess)
         return HQQ_EHIP;
+    UnpackArgs a = unpack_pair(*gate, *up, N, K, nbits, group_size);
+    a.W = l.W;
     GemmArgs g{};
     single_segment(g, X, round_up(K, kStep), whole_pitch(K));
     g.B = l.W;
-    g.ldb = ldw;
+    g.ldb = a.ldw;
     g.M = (int32_t)M;
     g.N = (int32_t)N;
     g.out = Y;
     g.ldo = N;
     g.act = act;
-    return launch_gemm(kOutGated, bf16, g, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
+    return launch_unpack_weight(nbits, bf16, a, s) == hipSuccess && launch_gemm(kOutGated, bf16, g, s) == hipSuccess
+               ? HQQ_OK
+               : HQQ_EHIP;
 }
 
 int64_t hqq_linear_gated_backward_workspace(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
@@ -506,7 +509,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t ldw = pitch_for(K), Np = round_up(N, kStep), ldg = pitch_for(2 * Np);
+    const int64_t Np = round_up(N, kStep), ldg = pitch_for(2 * Np);
     if (M <= kFewRows) {
         if (!bf16 && launch_row_scale(dY, M, N, l.scale, l.inv, s) != hipSuccess)
             return HQQ_EHIP;
@@ -519,9 +522,10 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         f.g.N = (int32_t)N;
         f.g.out = l.dGU;
         f.g.ldo = ldg;
-        f.g.fill = Np;
+        f.g.fill = f.g.up_off = Np;
         f.g.act = act;
         f.g.dY = dY;
+        f.g.ldy = N;
         f.g.rscale = bf16 ? nullptr : l.scale;
         SkinnyGradArgs b{};
         add_grad(b, gate->packed, gate->scale, gate->zero, l.dGU, ldg, N);
@@ -532,16 +536,13 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
                    ? HQQ_OK
                    : HQQ_EHIP;
     }
-    for (int i = 0; i < 2; ++i) {
-        const hqq_weight &w = i ? *up : *gate;
-        UnpackArgs a = unpack_args(w.packed, w.scale, w.zero, 0, N, K, nbits, group_size);
-        a.W = l.W;
-        a.interleave = 1 + i;
-        a.WT = l.WT + i * Np;
-        a.ldt = ldg;
-        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
-            return HQQ_EHIP;
-    }
+    UnpackArgs a = unpack_pair(*gate, *up, N, K, nbits, group_size);
+    a.W = l.W;
+    a.WT[0] = l.WT;
+    a.WT[1] = l.WT + Np;
+    a.ldt = ldg;
+    if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
+        return HQQ_EHIP;
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
         // fp16: dG and dU relative to the row's largest |dY| (bf16 has fp32's range)
@@ -553,24 +554,24 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         GemmArgs g{};
         single_segment(g, x, round_up(K, kStep), whole_pitch(K));
         g.B = l.W;
-        g.ldb = ldw;
+        g.ldb = a.ldw;
         g.M = (int32_t)m;
         g.N = (int32_t)N;
         g.act = act;
         g.dY = dY + m0 * N;
+        g.ldy = N;
         g.rscale = bf16 ? nullptr : l.scale;
         g.out = l.dGU;
         g.ldo = ldg;
-        g.fill = Np;
-        if (launch_gemm(kOutGatedGrad, bf16, g, s) != hipSuccess)
-            return HQQ_EHIP;
+        g.up_off = g.fill = Np;
         GemmArgs p{};
         single_segment(p, l.dGU, 2 * Np, ldg);
         p.B = l.WT;
         p.ldb = ldg;
         p.M = (int32_t)m;
         p.N = (int32_t)K;
-        if (gradient_product(p, bf16, l.part, nullptr, true, true, dX + m0 * K, bf16 ? nullptr : l.inv, s) != hipSuccess)
+        if (launch_gemm(kOutGatedGrad, bf16, g, s) != hipSuccess ||
+            gradient_product(p, bf16, l.part, nullptr, true, true, dX + m0 * K, bf16 ? nullptr : l.inv, s) != hipSuccess)
             return HQQ_EHIP;
     }
     return HQQ_OK;
@@ -620,8 +621,8 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
     }
     int64_t col = 0;
     for (int i = 0; i < count; ++i) {
-        UnpackArgs a = unpack_args(ws[i].packed, ws[i].scale, ws[i].zero, 0, n[i], K, nbits, group_size);
-        a.WT = l.WT + col;
+        UnpackArgs a = unpack_args(hqq_weight{ws[i].packed, ws[i].scale, ws[i].zero}, 0, n[i], K, nbits, group_size);
+        a.WT[0] = l.WT + col;
         a.ldt = l.ldt;
         if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
             return HQQ_EHIP;
@@ -671,7 +672,6 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t ldw = pitch_for(K);
     if (M <= kFewRows) {
         SkinnyArgs f{};
         f.w[0] = linear_args(X, *head, M, K, N, nbits, group_size);
@@ -682,35 +682,36 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
         f.g.Nall = N;
         f.g.targets = targets;
         f.g.stats = l.stats;
-        f.g.blocks = l.blocks;
+        f.g.blocks = l.pitch;
         f.g.tlogit = l.tlogit;
-        const LossArgs e{l.stats, l.blocks, M, N, l.state, l.tlogit, targets, loss, lse, 1, 1};
+        const LossArgs e{l.stats, l.pitch, l.pitch, M, N, l.tlogit, targets, loss, lse};
         return launch_skinny(nbits, bf16, f, s) == hipSuccess && launch_loss(e, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
     }
     if (whole_steps(X, M, K, l.X, s) != hipSuccess)
         return HQQ_EHIP;
+    int64_t blocks = 0;
     for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
         const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
-        UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
+        UnpackArgs a = unpack_args(*head, n0, n, K, nbits, group_size);
         a.W = l.W;
         GemmArgs g{};
         single_segment(g, X, round_up(K, kStep), whole_pitch(K));
         g.B = l.W;
-        g.ldb = ldw;
+        g.ldb = a.ldw;
         g.M = (int32_t)M;
         g.N = (int32_t)n;
-        g.stats = l.stats;
-        g.blocks = (n + 63) / 64;
+        g.stats = l.stats + blocks;
+        g.blocks = l.pitch;
         g.tlogit = l.tlogit;
         g.targets = targets;
         g.n0 = n0;
         g.Nall = N;
-        const LossArgs e{l.stats, g.blocks, M, N, l.state, l.tlogit, targets, loss, lse, n0 == 0, n0 + n == N};
-        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess || launch_gemm(kOutStats, bf16, g, s) != hipSuccess ||
-            launch_loss(e, s) != hipSuccess)
+        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess || launch_gemm(kOutStats, bf16, g, s) != hipSuccess)
             return HQQ_EHIP;
+        blocks += gemm_stats_blocks(M, n, g.step0[1]);
     }
-    return HQQ_OK;
+    const LossArgs e{l.stats, l.pitch, blocks, M, N, l.tlogit, targets, loss, lse};
+    return launch_loss(e, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
 }
 
 int64_t hqq_linear_cross_entropy_backward_workspace(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
@@ -737,7 +738,6 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t ldw = pitch_for(K);
     const float unit = bf16 ? 1.0f : 1.0f / 32768.0f;     // of the rounded differences
     if (M <= kFewRows) {
         SkinnyArgs f{};
@@ -769,15 +769,15 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             return HQQ_EHIP;
         for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
             const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
-            UnpackArgs a = unpack_args(head->packed, head->scale, head->zero, n0, n, K, nbits, group_size);
+            const int64_t fill = round_up(n, kStep), ldl = pitch_for(n);
+            UnpackArgs a = unpack_args(*head, n0, n, K, nbits, group_size);
             a.W = l.W;
-            a.WT = l.WT;
-            const int64_t fill = round_up(n, kStep);
-            a.ldt = pitch_for(n);
+            a.WT[0] = l.WT;
+            a.ldt = ldl;
             GemmArgs g{};
             single_segment(g, x, round_up(K, kStep), whole_pitch(K));
             g.B = l.W;
-            g.ldb = ldw;
+            g.ldb = a.ldw;
             g.M = (int32_t)m;
             g.N = (int32_t)n;
             g.targets = targets + m0;
@@ -785,12 +785,12 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             g.n0 = n0;
             g.Nall = N;
             g.out = l.dL;
-            g.ldo = a.ldt;
+            g.ldo = ldl;
             g.fill = fill;
             GemmArgs p{};
-            single_segment(p, l.dL, fill, a.ldt);
+            single_segment(p, l.dL, fill, ldl);
             p.B = l.WT;
-            p.ldb = a.ldt;
+            p.ldb = ldl;
             p.M = (int32_t)m;
             p.N = (int32_t)K;
             if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess ||

@@ -164,15 +164,15 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
         uint4 y[TM];
         if constexpr (GRAD) {
             // all of dY at once where the tile is whole: loads behind branches come one by one
-            if (mw + 16 * TM <= g.M && nw + 32 <= g.N && g.N % 8 == 0) {
+            if (mw + 16 * TM <= g.M && nw + 32 <= g.N && g.ldy % 8 == 0) {
 #pragma unroll
                 for (int u = 0; u < TM; ++u)
-                    y[u] = *reinterpret_cast<const uint4 *>(g.dY + (int64_t)(mw + 16 * u + row4) * g.N + n4);
+                    y[u] = *reinterpret_cast<const uint4 *>(g.dY + (int64_t)(mw + 16 * u + row4) * g.ldy + n4);
             } else {
 #pragma unroll
                 for (int u = 0; u < TM; ++u) {
                     const int mr = mw + 16 * u + row4;
-                    y[u] = mr < g.M && n4 < g.N ? load8(g.dY + (int64_t)mr * g.N + n4, g.N - n4) : uint4{0, 0, 0, 0};
+                    y[u] = mr < g.M && n4 < g.N ? load8(g.dY + (int64_t)mr * g.ldy + n4, g.N - n4) : uint4{0, 0, 0, 0};
                 }
             }
         }
@@ -214,12 +214,12 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
             if constexpr (GRAD) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(su + row4 * P + 16 * (lane & 3));
                 if (mr < g.M && n4 < width)
-                    store8(o + g.fill, w, 8);
+                    store8(o + g.up_off, w, 8);
             }
         }
     } else {   // kOutStats
         // the row's max and sum of exp over this wave's 64 columns, the target left out (a
-        // lane's columns, then the four lanes of the row)
+        // lane's columns, then the four lanes of the row), left at st for the tile's join
 #pragma unroll
         for (int u = 0; u < TM; ++u) {
             const int m = mw + 16 * u + l16;
@@ -251,10 +251,33 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                 }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (m_in && l4 == 0 && nw < g.N)
-                g.stats[(int64_t)m * g.blocks + nw / 64] = float2{mx, sum};
+            if (l4 == 0)
+                reinterpret_cast<float2 *>(st)[16 * u + l16] = float2{mx, sum};
         }
     }
+}
+
+// kOutStats: the (max, sum) of the WN waves that share a row become the tile's; part(w, r):
+// wave w's of its row r.
+template <int BM, int WM, int WN, typename Part>
+__device__ __forceinline__ void join_stats(const GemmArgs &g, int m0, int tile_n, Part &&part)
+{
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r >= BM || m0 + r >= g.M)
+        return;
+    float2 v[WN];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WN; ++w) {
+        v[w] = part((r / (BM / WM)) * WN + w, r % (BM / WM));
+        mx = fmaxf(mx, v[w].x);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WN; ++w)
+        sum += mx > -INFINITY ? v[w].y * exp2_fast((v[w].x - mx) * kLog2e) : v[w].y;   // (or a NaN, which stays)
+    g.stats[(int64_t)(m0 + r) * g.blocks + tile_n] = float2{mx, sum};
 }
 
 // The tile and split of a workgroup.  Workgroups go to the 8 XCDs in turn: each XCD
@@ -428,8 +451,11 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     for (int u = 0; u < TM; ++u)
         settle(acc[u]);
     static_assert(BM * 128 >= NW / 2 * 4096, "4 KB per wave");
-    char *st = reinterpret_cast<char *>(wave < NW / 2 ? as0 : as1) + (wave % (NW / 2)) * 4096;
+    auto scratch = [&](int w) { return reinterpret_cast<char *>(w < NW / 2 ? as0 : as1) + (w % (NW / 2)) * 4096; };
+    char *st = scratch(wave);
     epilogue<OUT, ACT, BF, TM>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, split, st);
+    if constexpr (OUT == kOutStats)
+        join_stats<BM, WM, WN>(g, m0, tile_n, [&](int w, int r) { return reinterpret_cast<const float2 *>(scratch(w))[r]; });
 }
 
 // Tiles: 256 x 256 and 256 x 128 with 8 waves, one workgroup per CU, and 128 x 128
@@ -536,6 +562,13 @@ hipError_t launch_dtype(GemmOut out, GemmArgs &g, hipStream_t s)
 hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s)
 {
     return bf16 ? launch_dtype<true>(out, g, s) : launch_dtype<false>(out, g, s);
+}
+
+int64_t gemm_stats_blocks(int64_t M, int64_t N, int64_t steps)
+{
+    int tile, splits;
+    pick_tile(M, N, steps, false, false, tile, splits, false);
+    return (N + kTiles[tile].bn - 1) / kTiles[tile].bn;
 }
 
 int gemm_splits(int64_t M, int64_t N, int64_t steps)

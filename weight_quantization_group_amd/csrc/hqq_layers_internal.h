@@ -13,16 +13,15 @@ constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * t
 // be null): W [n, K] row-major with columns K .. round_up(K, 64) - 1 zeroed, and
 // its transpose WT [K, n] with columns n .. round_up(n, 64) - 1 zeroed.
 struct UnpackArgs {
-    const uint32_t *packed;   // of the first row
-    const float *scale, *zero;
+    int count;                // 1, or 2: a gated pair (gate, up) of one shape and format
+    const uint32_t *packed[2];   // of the first row
+    const float *scale[2], *zero[2];
     int64_t n, K;
     int64_t wpr, gpl;         // words and groups per row
     int gshift;               // log2 of the group size
-    uint16_t *W;
+    uint16_t *W;              // a pair shares W: 32 rows of the one and 32 of the other in turn
     int64_t ldw;
-    int interleave;           // 0: row n at row n of W; a gated pair shares W, 32 rows of the one and
-                              // 32 of the other in turn: 1 its first (gate), 2 its second (up)
-    uint16_t *WT;
+    uint16_t *WT[2];
     int64_t ldt;
 };
 hipError_t launch_unpack_weight(int nbits, bool bf16, const UnpackArgs &a, hipStream_t s);
@@ -44,7 +43,7 @@ enum GemmOut {
     kOutPart,       // part[z] = C over this split's steps (fp32)
     kOutGated,      // out16 = act(C_gate) * C_up
     kOutGatedGrad,  // dG, dU from C_gate, C_up and dY
-    kOutStats,      // per row and 64 columns: max and sum of exp of the logits
+    kOutStats,      // per row and column tile: max and sum of exp of the logits
     kOutSoftGrad    // exp(C - lse) - onehot(target)
 };
 
@@ -66,9 +65,10 @@ struct GemmArgs {
     int act;
     const uint16_t *dY;              // kOutGatedGrad: [M, N]
     const float *rscale;             // per-row scale of dG and dU, or null
-    int64_t fill;                    // kOutGatedGrad, kOutSoftGrad: columns N .. fill - 1 of out are zeroed;
-                                     // kOutGatedGrad: dU's first column in out
-    float2 *stats;                   // kOutStats: [M, blocks] (max, sum)
+    int64_t ldy;                     // row pitch of dY
+    int64_t up_off;                  // kOutGatedGrad: dU's first column in out
+    int64_t fill;                    // kOutGatedGrad, kOutSoftGrad: columns N .. fill - 1 of out are zeroed
+    float2 *stats;                   // kOutStats: (max, sum) of row m and column tile i at [m * blocks + i]
     int64_t blocks;
     float *tlogit;                   // kOutStats: the target's logit, where it is in this piece
     const int64_t *targets;
@@ -76,6 +76,8 @@ struct GemmArgs {
     int64_t n0, Nall;                // first class of this piece, and all classes
 };
 hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s);
+// Column tiles of a kOutStats product (at most (N + 127) / 128).
+int64_t gemm_stats_blocks(int64_t M, int64_t N, int64_t steps);
 // Splits of the steps for a kOutPart product (none of them empty).
 int gemm_splits(int64_t M, int64_t N, int64_t steps);
 
@@ -123,16 +125,13 @@ struct ReduceArgs {
 };
 hipError_t launch_reduce(bool bf16, const ReduceArgs &a, hipStream_t s);
 
-// Cross entropy, the end of a piece: the blocks' (max, sum) of each row join
-// the row's state; last: loss and lse.
+// Cross entropy, the end: the blocks' (max, sum) of each row, then loss and lse.
 struct LossArgs {
-    const float2 *stats;
-    int64_t blocks, M, N;
-    float2 *state;
+    const float2 *stats;      // [M, pitch], of which blocks are set
+    int64_t pitch, blocks, M, N;
     const float *tlogit;
     const int64_t *targets;
     float *loss, *lse;
-    int first, last;
 };
 hipError_t launch_loss(const LossArgs &a, hipStream_t s);
 

@@ -17,6 +17,7 @@ __global__ __launch_bounds__(kRowsBlock) void reduce_kernel(ReduceArgs a)
     if (i >= total)
         return;
     float4v v = *reinterpret_cast<const float4v *>(a.part + i);
+#pragma unroll 8
     for (int z = 1; z < a.splits; ++z)
         v += *reinterpret_cast<const float4v *>(a.part + z * total + i);
     if (a.acc_in)
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(kRowsBlock) void loss_kernel(LossArgs a)
     const int64_t m = blockIdx.x;
     float2 s{-INFINITY, 0.0f};
     for (int64_t b = threadIdx.x; b < a.blocks; b += kRowsBlock)
-        s = join(s, a.stats[m * a.blocks + b]);
+        s = join(s, a.stats[m * a.pitch + b]);
 #pragma unroll
     for (int o = 1; o < 64; o *= 2)
         s = join(s, float2{__shfl_xor(s.x, o), __shfl_xor(s.y, o)});
@@ -57,12 +58,6 @@ __global__ __launch_bounds__(kRowsBlock) void loss_kernel(LossArgs a)
 #pragma unroll
     for (int w = 1; w < kRowsBlock / 64; ++w)
         s = join(s, parts[w]);
-    if (!a.first)
-        s = join(a.state[m], s);
-    if (!a.last) {
-        a.state[m] = s;
-        return;
-    }
     // lse of the others, then the target joins: with d = lse_others - l_t,
     // loss = log(1 + exp(d)), lse = l_t + loss
     const float others = s.x + logf(s.y);

@@ -46,13 +46,13 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
             if (n < g.N) {
                 float d;
                 const float f = act_any(g.act, c0, d);
-                const float y = from16(g.dY[(int64_t)m * g.N + n], BF) * (g.rscale ? g.rscale[m] : 1.0f);
+                const float y = from16(g.dY[(int64_t)m * g.ldy + n], BF) * (g.rscale ? g.rscale[m] : 1.0f);
                 vg = y * c1 * d;
                 vu = y * f;
             }
             uint16_t *o = g.out + (int64_t)m * g.ldo + n;
             o[0] = out1<BF>(vg);
-            o[g.fill] = out1<BF>(vu);
+            o[g.up_off] = out1<BF>(vu);
         }
     } else if (out == kOutStats) {
         const int64_t at = m_in ? g.targets[m] : -1;

@@ -26,6 +26,7 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int kl = lane & 7, nl = lane >> 3;
     // this workgroup's place in the order of its XCD
+    const int which = (int)blockIdx.y;
     const uint32_t T = gridDim.x, q = T / 8, rest = T % 8, x = blockIdx.x % 8;
     const uint32_t id = x * q + (x < rest ? x : rest) + blockIdx.x / 8;
     const uint32_t kblocks = (uint32_t)((a.K + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves)), nb = id / kblocks;
@@ -41,7 +42,7 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
     for (int i = 0; i < 8; ++i) {
         const int64_t n = n0 + i < a.n ? n0 + i : a.n - 1;
         const int64_t r = k_in ? run : runs - 1;
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(a.packed + n * a.wpr) + r * NB;
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(a.packed[which] + n * a.wpr) + r * NB;
         uint32_t w[2] = {0, 0};
         if constexpr (NB == 8) {
             const uint2 u = *reinterpret_cast<const uint2 *>(p);
@@ -55,8 +56,8 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
             w[0] = *p;
         }
         const int64_t g = n * a.gpl + ((8 * r) >> a.gshift);
-        const float z = a.zero[g];
-        const double R = reciprocal(a.scale[g]);
+        const float z = a.zero[which][g];
+        const double R = reciprocal(a.scale[which][g]);
         const bool in = k_in && n0 + i < a.n;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -70,7 +71,7 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (n0 + i < a.n) {
-                const int64_t n = n0 + i, row = a.interleave ? (n >> 5) * 64 + (n & 31) + 32 * (a.interleave - 1) : n;
+                const int64_t n = n0 + i, row = a.count == 2 ? (n >> 5) * 64 + (n & 31) + 32 * which : n;
                 *reinterpret_cast<uint4 *>(a.W + row * a.ldw + run * 8) = uint4{v[i][0], v[i][1], v[i][2], v[i][3]};
             }
     }
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
                 o.y = perm(v[3][k / 2], v[2][k / 2], sel);
                 o.z = perm(v[5][k / 2], v[4][k / 2], sel);
                 o.w = perm(v[7][k / 2], v[6][k / 2], sel);
-                *reinterpret_cast<uint4 *>(a.WT + (run * 8 + k) * a.ldt + n0) = o;
+                *reinterpret_cast<uint4 *>(a.WT[which] + (run * 8 + k) * a.ldt + n0) = o;
             }
         }
     }
@@ -93,9 +94,9 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
 template <int NB, bool BF>
 hipError_t launch_nb(const UnpackArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.K + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves) * ((a.n + 63) / 64)));
+    const dim3 grid((unsigned)((a.K + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves) * ((a.n + 63) / 64)), (unsigned)a.count);
     const dim3 block(kUnpackWaves * 64);
-    if (a.W && a.WT)
+    if (a.W && a.WT[0])
         hipLaunchKernelGGL((unpack_kernel<NB, BF, true, true>), grid, block, 0, s, a);
     else if (a.W)
         hipLaunchKernelGGL((unpack_kernel<NB, BF, true, false>), grid, block, 0, s, a);
