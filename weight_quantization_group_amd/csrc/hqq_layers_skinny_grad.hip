@@ -2,10 +2,10 @@
 // straight from the packed codes.
 //
 // The sum runs over the rows n of the weights while their codes run along k.  A
-// lane takes 8 rows n by 16 consecutive k, dequantizes them, and transposes 8 x 8
-// squares in registers (one byte permutation per pair of values; the rest renames
-// registers): operand j of its 16 MFMAs is column k = 16 (l % 16) + j of the rows
-// 8 (l / 16) .. + 7.  A wave covers 256 k and 32 rows per step; the next step's
+// lane takes 8 rows n by 8 consecutive k, dequantizes them, and transposes the
+// square in registers (one byte permutation per pair of values; the rest renames
+// registers): operand j of its 8 MFMAs is column k = 8 (l % 16) + j of the rows
+// 8 (l / 16) .. + 7.  A wave covers 128 k and 32 rows per step; the next step's
 // codes load under the current one's arithmetic.  Waves and workgroups split the
 // rows; the waves' sums meet in LDS, the workgroups' in a second launch, in a
 // fixed order.  Few rows of C leave this to the codes' bytes and the latency of
@@ -17,33 +17,25 @@ namespace {
 
 constexpr int kGradWaves = 8;
 
-// 16 consecutive codes of a row
+// 8 consecutive codes of a row
 template <int NB>
-struct Codes16 {
-    uint32_t w[NB == 1 ? 1 : NB / 2];
-};
-
-template <int NB>
-__device__ __forceinline__ void load_codes(Codes16<NB> &c, const uint8_t *p)
+__device__ __forceinline__ uint2 load_codes(const uint8_t *p)
 {
-    if constexpr (NB == 8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        c.w[0] = u.x; c.w[1] = u.y; c.w[2] = u.z; c.w[3] = u.w;
-    } else if constexpr (NB == 4) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        c.w[0] = u.x; c.w[1] = u.y;
-    } else if constexpr (NB == 2) {
-        c.w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else {
-        c.w[0] = *reinterpret_cast<const uint16_t *>(p);
-    }
+    if constexpr (NB == 8)
+        return *reinterpret_cast<const uint2 *>(p);
+    else if constexpr (NB == 4)
+        return uint2{*reinterpret_cast<const uint32_t *>(p), 0u};
+    else if constexpr (NB == 2)
+        return uint2{*reinterpret_cast<const uint16_t *>(p), 0u};
+    else
+        return uint2{*p, 0u};
 }
 
 // One step of a lane: the codes and meta of 8 rows, and its runs of A
-template <int NB, int MT, int G>
+template <int NB, int MT>
 struct GradBuf {
-    Codes16<NB> c[8];
-    float s[8][G], z[8][G];
+    uint2 c[8];
+    float s[8], z[8];
     uint4 a[MT];
 };
 
@@ -63,39 +55,36 @@ __device__ __forceinline__ uint4 load_run(const uint16_t *row, int n, int N)
     return uint4{w[0], w[1], w[2], w[3]};
 }
 
-// G: groups per 16 k (2 for groups of 8); AL: the runs of A are 16-byte aligned
-template <int NB, int MT, int G, bool BF, bool AL>
-__global__ __launch_bounds__(kGradWaves * 64) void skinny_grad_kernel(SkinnyGradArgs a)
+// AL: the runs of A are 16-byte aligned
+template <int NB, int MT, bool BF, bool AL>
+__global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 3))) void
+skinny_grad_kernel(SkinnyGradArgs a)
 {
     constexpr uint32_t MASK = (1u << NB) - 1u;
-    __shared__ float4v red[kGradWaves / 2][MT * 16][64];
+    __shared__ float4v red[kGradWaves / 2][MT * 8][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, l4 = lane >> 4;
-    const int kc_raw = (int)blockIdx.x * 256 + 16 * l16;
-    const int kc = kc_raw < a.K ? kc_raw : (int)a.K - 16;      // past K: any codes, never stored
+    const int kc_raw = (int)blockIdx.x * 128 + 8 * l16;
+    const int kc = kc_raw < a.K ? kc_raw : (int)a.K - 8;       // past K: any codes, never stored
     const int m0 = (int)blockIdx.z * 16 * MT;
     const int steps = a.step0[a.count];
     const int per = (steps + a.splits - 1) / a.splits;
     const int s0 = (int)blockIdx.y * per, s1 = s0 + per < steps ? s0 + per : steps;
 
     int j = 0;
-    GradBuf<NB, MT, G> buf;
+    GradBuf<NB, MT> buf;
     auto load = [&](int s) {
         while (s >= a.step0[j + 1])
             ++j;
         const int N = a.n[j], n0 = 32 * (s - a.step0[j]) + 8 * l4;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int n = n0 + i < N ? n0 + i : N - 1;
-            load_codes<NB>(buf.c[i], reinterpret_cast<const uint8_t *>(a.packed[j]) +
-                                         ((uint32_t)n * (uint32_t)a.wpr * 4u + (uint32_t)kc * NB / 8));
-#pragma unroll
-            for (int q = 0; q < G; ++q) {
-                const uint32_t g = (uint32_t)n * (uint32_t)a.gpl + ((uint32_t)(kc + 8 * q) >> a.gshift);
-                buf.s[i][q] = a.scale[j][g];
-                buf.z[i][q] = a.zero[j][g];
-            }
+            const uint32_t n = (uint32_t)(n0 + i < N ? n0 + i : N - 1);
+            const uint32_t g = n * (uint32_t)a.gpl + ((uint32_t)kc >> a.gshift);
+            buf.c[i] = load_codes<NB>(at<uint8_t>(a.packed[j], n * (uint32_t)a.wpr * 4u + (uint32_t)kc * NB / 8));
+            buf.s[i] = *at<float>(a.scale[j], 4 * g);
+            buf.z[i] = *at<float>(a.zero[j], 4 * g);
         }
 #pragma unroll
         for (int u = 0; u < MT; ++u) {
@@ -103,43 +92,38 @@ __global__ __launch_bounds__(kGradWaves * 64) void skinny_grad_kernel(SkinnyGrad
             buf.a[u] = load_run<AL>(a.A[j] + (int64_t)m * a.lda[j], n0, N);
         }
     };
-    float4v acc[MT][16];
+    float4v acc[MT][8];
 #pragma unroll
     for (int u = 0; u < MT; ++u)
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
+        for (int t = 0; t < 8; ++t)
             acc[u][t] = float4v{0.f, 0.f, 0.f, 0.f};
     if (s0 + wave < s1)
         load(s0 + wave);
     for (int s = s0 + wave; s < s1; s += kGradWaves) {
-        const GradBuf<NB, MT, G> cur = buf;
+        const GradBuf<NB, MT> cur = buf;
         if (s + kGradWaves < s1)
             load(s + kGradWaves);
-        double R[8];
+        uint32_t v[8][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t v[8][4];
+        for (int i = 0; i < 8; ++i) {
+            const double R = reciprocal(cur.s[i]);
+            const uint32_t w[2] = {cur.c[i].x, cur.c[i].y};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int q = h * (G - 1);
-                if (h < G)
-                    R[i] = reciprocal(cur.s[i][q]);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int b0 = (8 * h + 2 * t) * NB, b1 = b0 + NB;
-                    v[i][t] = out2<BF>(wq((float)((cur.c[i].w[b0 / 32] >> (b0 % 32)) & MASK), cur.z[i][q], R[i]),
-                                       wq((float)((cur.c[i].w[b1 / 32] >> (b1 % 32)) & MASK), cur.z[i][q], R[i]));
-                }
+            for (int t = 0; t < 4; ++t) {
+                const int b0 = 2 * t * NB, b1 = b0 + NB;
+                v[i][t] = out2<BF>(wq((float)((w[b0 / 32] >> (b0 % 32)) & MASK), cur.z[i], R),
+                                   wq((float)((w[b1 / 32] >> (b1 % 32)) & MASK), cur.z[i], R));
             }
+        }
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const uint32_t sel = t & 1 ? 0x07060302u : 0x05040100u;
-                const uint4 B{perm(v[1][t / 2], v[0][t / 2], sel), perm(v[3][t / 2], v[2][t / 2], sel),
-                              perm(v[5][t / 2], v[4][t / 2], sel), perm(v[7][t / 2], v[6][t / 2], sel)};
+        for (int t = 0; t < 8; ++t) {
+            const uint32_t sel = t & 1 ? 0x07060302u : 0x05040100u;
+            const uint4 B{perm(v[1][t / 2], v[0][t / 2], sel), perm(v[3][t / 2], v[2][t / 2], sel),
+                          perm(v[5][t / 2], v[4][t / 2], sel), perm(v[7][t / 2], v[6][t / 2], sel)};
 #pragma unroll
-                for (int u = 0; u < MT; ++u)
-                    acc[u][8 * h + t] = mfma<BF>(cur.a[u], B, acc[u][8 * h + t]);
-            }
+            for (int u = 0; u < MT; ++u)
+                acc[u][t] = mfma<BF>(cur.a[u], B, acc[u][t]);
         }
     }
     // halves of the waves hand their sums to the other half, three times
@@ -150,16 +134,16 @@ __global__ __launch_bounds__(kGradWaves * 64) void skinny_grad_kernel(SkinnyGrad
 #pragma unroll
             for (int u = 0; u < MT; ++u)
 #pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    red[wave - w][u * 16 + t][lane] = acc[u][t];
+                for (int t = 0; t < 8; ++t)
+                    red[wave - w][u * 8 + t][lane] = acc[u][t];
         }
         __syncthreads();
         if (wave < w) {
 #pragma unroll
             for (int u = 0; u < MT; ++u)
 #pragma unroll
-                for (int t = 0; t < 16; ++t)
-                    acc[u][t] += red[wave][u * 16 + t][lane];
+                for (int t = 0; t < 8; ++t)
+                    acc[u][t] += red[wave][u * 8 + t][lane];
         }
     }
     if (wave != 0 || kc_raw >= a.K)
@@ -175,41 +159,35 @@ __global__ __launch_bounds__(kGradWaves * 64) void skinny_grad_kernel(SkinnyGrad
             if (a.part) {
                 float4v *o = reinterpret_cast<float4v *>(a.part + ((int64_t)blockIdx.y * a.M + m) * a.K + kc);
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 2; ++t)
                     o[t] = float4v{acc[u][4 * t][r], acc[u][4 * t + 1][r], acc[u][4 * t + 2][r], acc[u][4 * t + 3][r]};
             } else {
                 const float f = a.rowf ? a.rowf[m] : 1.0f;
-                uint4 *o = reinterpret_cast<uint4 *>(a.out + (int64_t)m * a.K + kc);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    o[t] = uint4{out2<BF>(acc[u][8 * t][r] * f, acc[u][8 * t + 1][r] * f),
-                                 out2<BF>(acc[u][8 * t + 2][r] * f, acc[u][8 * t + 3][r] * f),
-                                 out2<BF>(acc[u][8 * t + 4][r] * f, acc[u][8 * t + 5][r] * f),
-                                 out2<BF>(acc[u][8 * t + 6][r] * f, acc[u][8 * t + 7][r] * f)};
+                *reinterpret_cast<uint4 *>(a.out + (int64_t)m * a.K + kc) =
+                    uint4{out2<BF>(acc[u][0][r] * f, acc[u][1][r] * f), out2<BF>(acc[u][2][r] * f, acc[u][3][r] * f),
+                          out2<BF>(acc[u][4][r] * f, acc[u][5][r] * f), out2<BF>(acc[u][6][r] * f, acc[u][7][r] * f)};
             }
         }
 }
 
-template <int NB, int MT, int G, bool BF>
+template <int NB, int MT, bool BF>
 hipError_t launch_al(const SkinnyGradArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.K + 255) / 256), (unsigned)a.splits, (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+    const dim3 grid((unsigned)((a.K + 127) / 128), (unsigned)a.splits, (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
     bool al = true;
     for (int i = 0; i < a.count; ++i)
         al = al && a.lda[i] % 8 == 0;
     if (al)
-        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, G, BF, true>), grid, dim3(kGradWaves * 64), 0, s, a);
+        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, true>), grid, dim3(kGradWaves * 64), 0, s, a);
     else
-        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, G, BF, false>), grid, dim3(kGradWaves * 64), 0, s, a);
+        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, false>), grid, dim3(kGradWaves * 64), 0, s, a);
     return hipGetLastError();
 }
 
 template <int NB, bool BF>
 hipError_t launch_mt(const SkinnyGradArgs &a, hipStream_t s)
 {
-    if (a.gshift == 3)
-        return a.M <= 16 ? launch_al<NB, 1, 2, BF>(a, s) : launch_al<NB, 2, 2, BF>(a, s);
-    return a.M <= 16 ? launch_al<NB, 1, 1, BF>(a, s) : launch_al<NB, 2, 1, BF>(a, s);
+    return a.M <= 16 ? launch_al<NB, 1, BF>(a, s) : launch_al<NB, 2, BF>(a, s);
 }
 
 }  // namespace
@@ -228,7 +206,7 @@ hipError_t launch_skinny_grad(int nbits, bool bf16, const SkinnyGradArgs &a, hip
 // About two workgroups per CU, each wave with a step at least; no part empty.
 int skinny_grad_splits(int64_t M, int64_t K, int64_t steps)
 {
-    const int64_t tiles = (K + 255) / 256 * (M <= 16 ? 1 : (M + 31) / 32);
+    const int64_t tiles = (K + 127) / 128 * (M <= 16 ? 1 : (M + 31) / 32);
     int64_t sp = (512 + tiles - 1) / tiles;
     const int64_t most = (steps + kGradWaves - 1) / kGradWaves;
     sp = sp < most ? sp : most;
