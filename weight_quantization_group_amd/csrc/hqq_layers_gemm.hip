@@ -22,10 +22,13 @@ __device__ __forceinline__ void dma16(const void *p, uint4 *lds)
 #endif
 }
 
+// The workgroup's barrier, with this wave's LDS accesses complete and at most VM of its
+// memory accesses under way.
+template <int VM>
 __device__ __forceinline__ void tile_barrier()
 {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt((VM & 15) | 0x0070 | (VM >> 4) << 14);   // vmcnt(VM) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -303,10 +306,10 @@ __device__ __forceinline__ void tile_of(const GemmArgs &g, int &tm, int &tn, int
 // A step is two halves of 32 k.  A wave's operands of one half are in registers
 // while those of the next are read from LDS under its matrix instructions: the
 // second half's from this step's buffers, then, behind the step's one barrier, the
-// next step's first half from the other buffers.  That barrier also frees this
-// step's buffers, and the DMA of the step after next goes into them under the
-// second half, a whole step ahead of its use.
-template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN>
+// next step's first half from the next buffers.  That barrier also frees this
+// step's buffers, and the DMA of the step S later goes into them under the second
+// half, S - 1 whole steps ahead of its use.
+template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
 {
     constexpr int NW = WM * WN;
@@ -315,7 +318,9 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     constexpr bool GATED = OUT == kOutGated || OUT == kOutGatedGrad;
     constexpr int BNC = GATED ? BN / 2 : BN;         // columns of the output per tile
     constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW;
+    // (arrays of their own: reads of one do not wait for the DMA into another)
     __shared__ uint4 as0[BM * 8], bs0[BN * 8], as1[BM * 8], bs1[BN * 8];
+    __shared__ uint4 as2[S > 2 ? BM * 8 : 1], bs2[S > 2 ? BN * 8 : 1], as3[S > 3 ? BM * 8 : 1], bs3[S > 3 ? BN * 8 : 1];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -408,14 +413,14 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     constexpr int DP = (IA + IB + TM - 1) / TM;
     auto step = [&](int s, uint4 *asc, uint4 *bsc, const uint4 *asn, const uint4 *bsn) {
         // past the end the DMA repeats the last step (in bounds, never used)
-        const int sn = s + 2 < s1 ? s + 2 : s1 - 1;
+        const int sn = s + S < s1 ? s + S : s1 - 1;
         if (sn >= seg_end)
             enter(sn);
         // (hides that the pitches do not change: the offsets are not to be kept)
         asm volatile("" : "+s"(lda2), "+s"(ldb2), "+v"(row_a), "+v"(row_b));
         __builtin_amdgcn_sched_barrier(0);
         half(1, asc, bsc, [](int) {});
-        tile_barrier();        // this step's reads are done, the next step has landed
+        tile_barrier<(S - 2) * (IA + IB)>();   // this step's reads are done, the next step has landed
         half(0, asn, bsn, [&](int i) {
 #pragma unroll
             for (int j = DP * i; j < DP * (i + 1); ++j) {
@@ -426,13 +431,19 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
             }
         });
     };
-    enter(s0);
-    dma(s0, as0, bs0);
-    const int sn = s0 + 1 < s1 ? s0 + 1 : s0;
-    if (sn >= seg_end)
-        enter(sn);
-    dma(sn, as1, bs1);
-    tile_barrier();
+    auto start = [&](int i, uint4 *as, uint4 *bs) {
+        const int sn = s0 + i < s1 ? s0 + i : s1 - 1;
+        if (sn >= seg_end)
+            enter(sn);
+        dma(sn, as, bs);
+    };
+    start(0, as0, bs0);
+    start(1, as1, bs1);
+    if constexpr (S > 2)
+        start(2, as2, bs2);
+    if constexpr (S > 3)
+        start(3, as3, bs3);
+    tile_barrier<(S - 1) * (IA + IB)>();
 #pragma unroll
     for (int t = 0; t < TN; ++t)
         b[t] = read_b(0, t, bs0);
@@ -440,17 +451,34 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     for (int u = 0; u < TM; ++u)
         a[u] = read_a(0, u, as0);
     int s = s0;
-    for (; s + 1 < s1; s += 2) {
+    for (; s + S <= s1; s += S) {
         step(s, as0, bs0, as1, bs1);
-        step(s + 1, as1, bs1, as0, bs0);
+        if constexpr (S == 2) {
+            step(s + 1, as1, bs1, as0, bs0);
+        } else {
+            step(s + 1, as1, bs1, as2, bs2);
+            if constexpr (S == 3) {
+                step(s + 2, as2, bs2, as0, bs0);
+            } else {
+                step(s + 2, as2, bs2, as3, bs3);
+                step(s + 3, as3, bs3, as0, bs0);
+            }
+        }
     }
     if (s < s1)
         step(s, as0, bs0, as1, bs1);
-    tile_barrier();        // no DMA is under way and no operand read: the buffers are free
+    if constexpr (S > 2)
+        if (s + 1 < s1)
+            step(s + 1, as1, bs1, as2, bs2);
+    if constexpr (S > 3)
+        if (s + 2 < s1)
+            step(s + 2, as2, bs2, as3, bs3);
+    tile_barrier<0>();     // no DMA is under way and no operand read: the buffers are free
 #pragma unroll
     for (int u = 0; u < TM; ++u)
         settle(acc[u]);
     static_assert(BM * 128 >= NW / 2 * 4096, "4 KB per wave");
+    static_assert(S >= 2 && S <= 4, "buffers");
     auto scratch = [&](int w) { return reinterpret_cast<char *>(w < NW / 2 ? as0 : as1) + (w % (NW / 2)) * 4096; };
     char *st = scratch(wave);
     epilogue<OUT, ACT, BF, TM>(g, acc, m0 + wm * (BM / WM), n0 + wn * (BNC / WN), lane, split, st);
@@ -458,42 +486,48 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
         join_stats<BM, WM, WN>(g, m0, tile_n, [&](int w, int r) { return reinterpret_cast<const float2 *>(scratch(w))[r]; });
 }
 
-// Tiles: 256 x 256 and 256 x 128 with 8 waves, one workgroup per CU, and 128 x 128
-// with 4 waves, two per CU.  Their times per 64-wide step with the chip full, in
-// bf16 on MI355X: 1.50, 0.98 and 0.95 us (44, 33 and 34 thousand outputs per CU
-// and us).  The tile of the fewest us by rounds of workgroups over the CUs; where
-// that leaves CUs idle, the steps are split and a second pass adds the parts (3 us
-// and the parts' and the result's bytes at 6 TB/s).
+// Tiles (rows x columns, buffers): 256 x 256 (2) and 256 x 128 (3) with 8 waves, 128 x
+// 128 (4) with 4 waves, one workgroup per CU, and 64 x 128 (3) with 4 waves, two per CU.
+// Their times per 64-wide step in bf16 on MI355X, with the chip full and with at most half
+// its workgroups running: 1.50 and 1.25 us, 0.88 and 0.80, 0.52, 0.60 and 0.40 (large
+// products: 44, 37, 32 and 27 thousand outputs per CU and us; the more buffers, the less
+// a step waits for memory: 256 x 128 with two ran 2048 x 4096 x 22016 in 373 us, with three
+// in 318).  The tile of the fewest us by rounds of workgroups over the CUs; where that
+// leaves CUs idle, the steps are split and a second pass adds the parts (3 us and the
+// parts' and the result's bytes at 6 TB/s).
 struct Tile {
     int bm, bn, per_cu;
-    double us;
+    double us, us_half;
 };
-constexpr Tile kTiles[3] = {{256, 256, 1, 1.50}, {256, 128, 1, 0.98}, {128, 128, 2, 0.95}};
+constexpr Tile kTiles[] = {{256, 256, 1, 1.50, 1.25}, {256, 128, 1, 0.88, 0.80}, {128, 128, 1, 0.52, 0.52},
+                           {64, 128, 2, 0.60, 0.40}};
+constexpr int kTileKinds = 4;
 constexpr int kCus = 256;
-constexpr int kMaxSplits = 16;
+constexpr int kMaxSplits = 32;
 
-double product_us(int tile, int64_t M, int64_t N, int64_t steps, int splits, bool gated, bool parts)
+double product_us(int tile, int64_t M, int64_t N, int64_t steps, int splits, bool gated)
 {
     const Tile &t = kTiles[tile];
     const int64_t bn = gated ? t.bn / 2 : t.bn;
     const int64_t wgs = (M + t.bm - 1) / t.bm * ((N + bn - 1) / bn) * splits;
-    const int64_t slots = kCus * t.per_cu;
-    double us = (double)((wgs + slots - 1) / slots) * (2.0 + (double)((steps + splits - 1) / splits) * t.us);
-    if (splits > 1 || parts)
+    const int64_t slots = kCus * t.per_cu, rest = wgs % slots;
+    const double step = (double)(wgs / slots) * t.us + (rest == 0 ? 0.0 : 2 * rest <= slots ? t.us_half : t.us);
+    double us = 3.0 + (double)((steps + splits - 1) / splits) * step;
+    if (splits > 1)
         us += 3.0 + (double)M * (double)N * (4.0 * splits + 2.0) / 6.0e6;
     return us;
 }
 
-void pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool parts, int &tile, int &splits, bool may_split)
+void pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool may_split, int &tile, int &splits)
 {
     double best = 0.0;
     tile = 0;
     splits = 1;
-    for (int t = 0; t < 3; ++t)
+    for (int t = 0; t < kTileKinds; ++t)
         for (int sp = 1; sp <= (may_split ? kMaxSplits : 1); ++sp) {
             if (sp > 1 && (steps / sp < 4 || (sp - 1) * ((steps + sp - 1) / sp) >= steps))
                 continue;       // a part has a few steps at least, and none is empty
-            const double us = product_us(t, M, N, steps, sp, gated, parts);
+            const double us = product_us(t, M, N, steps, sp, gated);
             if (best == 0.0 || us < best) {
                 best = us;
                 tile = t;
@@ -502,21 +536,21 @@ void pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool parts, int 
         }
 }
 
-template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN>
+template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN, int S>
 hipError_t launch_tile(GemmArgs &g, hipStream_t s)
 {
     constexpr bool GATED = OUT == kOutGated || OUT == kOutGatedGrad;
     constexpr int BNC = GATED ? BN / 2 : BN;
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + BNC - 1) / BNC;
-    hipLaunchKernelGGL((gemm_kernel<OUT, ACT, BF, BM, BN, WM, WN>),
+    hipLaunchKernelGGL((gemm_kernel<OUT, ACT, BF, BM, BN, WM, WN, S>),
                        dim3((unsigned)(g.tiles_m * g.tiles_n * g.splits)), dim3(WM * WN * 64), 0, s, g);
     return hipGetLastError();
 }
 
 void gradient_tile(int64_t M, int64_t N, int64_t steps, int &tile, int &splits)
 {
-    pick_tile(M, N, steps, false, false, tile, splits, true);
+    pick_tile(M, N, steps, false, true, tile, splits);
 }
 
 template <int OUT, int ACT, bool BF>
@@ -526,11 +560,12 @@ hipError_t launch_out(GemmArgs &g, hipStream_t s)
     if (OUT == kOutStore || OUT == kOutPart)
         gradient_tile(g.M, g.N, g.step0[g.segs], tile, sp);
     else
-        pick_tile(g.M, g.N, g.step0[g.segs], OUT == kOutGated || OUT == kOutGatedGrad, false, tile, sp, false);
+        pick_tile(g.M, g.N, g.step0[g.segs], OUT == kOutGated || OUT == kOutGatedGrad, false, tile, sp);
     switch (tile) {
-    case 0: return launch_tile<OUT, ACT, BF, 256, 256, 2, 4>(g, s);
-    case 1: return launch_tile<OUT, ACT, BF, 256, 128, 4, 2>(g, s);
-    default: return launch_tile<OUT, ACT, BF, 128, 128, 2, 2>(g, s);
+    case 0: return launch_tile<OUT, ACT, BF, 256, 256, 2, 4, 2>(g, s);
+    case 1: return launch_tile<OUT, ACT, BF, 256, 128, 4, 2, 3>(g, s);
+    case 2: return launch_tile<OUT, ACT, BF, 128, 128, 2, 2, 4>(g, s);
+    default: return launch_tile<OUT, ACT, BF, 64, 128, 2, 2, 3>(g, s);
     }
 }
 
@@ -567,7 +602,7 @@ hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s)
 int64_t gemm_stats_blocks(int64_t M, int64_t N, int64_t steps)
 {
     int tile, splits;
-    pick_tile(M, N, steps, false, false, tile, splits, false);
+    pick_tile(M, N, steps, false, false, tile, splits);
     return (N + kTiles[tile].bn - 1) / kTiles[tile].bn;
 }
 

@@ -15,7 +15,7 @@
 namespace hqq {
 namespace {
 
-constexpr int kGradWaves = 8;
+constexpr int kGradWaves = 4;
 
 // 8 consecutive codes of a row
 template <int NB>
@@ -126,7 +126,7 @@ skinny_grad_kernel(SkinnyGradArgs a)
                 acc[u][t] = mfma<BF>(cur.a[u], B, acc[u][t]);
         }
     }
-    // halves of the waves hand their sums to the other half, three times
+    // half of the waves hand their sums to the other half, until one has them all
 #pragma unroll
     for (int w = kGradWaves / 2; w > 0; w /= 2) {
         __syncthreads();
@@ -203,7 +203,9 @@ hipError_t launch_skinny_grad(int nbits, bool bf16, const SkinnyGradArgs &a, hip
     }
 }
 
-// About two workgroups per CU, each wave with a step at least; no part empty.
+// About two workgroups of four waves per CU, each wave with a step at least; no part
+// empty.  (Eight waves, or twice the workgroups: 27.8 and 27.4 us against 26.5 for 16 rows
+// through 4096 x 11008 at 4 bits.)
 int skinny_grad_splits(int64_t M, int64_t K, int64_t steps)
 {
     const int64_t tiles = (K + 127) / 128 * (M <= 16 ? 1 : (M + 31) / 32);
