@@ -28,6 +28,12 @@
  * bytes need no pointer).  Nothing in it has to be set before a call or kept
  * after it, so calls that follow each other on one stream may share one; calls
  * that may run at the same time (two streams, two captured graphs) may not.
+ *
+ * Routes.  Few rows are multiplied straight from the packed codes; for more,
+ * W_hat is unpacked into the workspace and a tiled product runs on it.  The
+ * choice goes by sizes and format, and both stay within the same bounds.  The
+ * environment variable HQQ_LAYERS_PATH=codes or =tiled, read at each call and by
+ * the *_workspace functions, forces one.
  */
 #ifndef HQQ_LAYERS_H
 #define HQQ_LAYERS_H

@@ -33,6 +33,13 @@ def hq():
     return w
 
 
+@pytest.fixture(params=["codes", "tiled"])
+def path(request, monkeypatch):
+    """Each route in turn, whatever the sizes: straight from the codes, and the tiled product."""
+    monkeypatch.setenv("HQQ_LAYERS_PATH", request.param)
+    return request.param
+
+
 def make_weight(seed, N, K, nbits, gs, dtype, std=None):
     """((packed, scale, zero) on the GPU, W_hat in 64 bits on the GPU) of random codes."""
     rng = np.random.RandomState(seed)
@@ -185,7 +192,7 @@ SIZES = [
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("M,K,N,nbits,gs", SIZES)
-def test_gated(hq, M, K, N, nbits, gs, dtype):
+def test_gated(hq, path, M, K, N, nbits, gs, dtype):
     act = ("silu", "gelu", "gelu_tanh")[(M + N) % 3]
     gate, Wg = make_weight(M + N, N, K, nbits, gs, dtype)
     up, Wu = make_weight(M + N + 1, N, K, nbits, gs, dtype)
@@ -198,7 +205,7 @@ def test_gated(hq, M, K, N, nbits, gs, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("M,K,N,nbits,gs", SIZES)
-def test_linear_backward(hq, M, K, N, nbits, gs, dtype):
+def test_linear_backward(hq, path, M, K, N, nbits, gs, dtype):
     w, W = make_weight(3 * M + N, N, K, nbits, gs, dtype)
     dY = normal(N, (M, N), dtype)
     dX = hq.hqq_linear_backward(dY, *w, K, nbits, gs)
@@ -214,7 +221,7 @@ def test_linear_backward(hq, M, K, N, nbits, gs, dtype):
     (150, 96, 4, 32, [1, 63, 65, 64]),
     (260, 320, 1, 64, list(range(1, 17))),
 ])
-def test_linear_batch_backward(hq, M, K, nbits, gs, Ns, dtype):
+def test_linear_batch_backward(hq, path, M, K, nbits, gs, Ns, dtype):
     """One sum over all weights; each alone in the other rows' place."""
     ws = [make_weight(50 + i, N, K, nbits, gs, dtype) for i, N in enumerate(Ns)]
     dYs = [normal(90 + i, (M, N), dtype) for i, N in enumerate(Ns)]
@@ -248,14 +255,14 @@ def loss_case(hq, M, K, N, nbits, gs, dtype, spread=1.0, targets=None):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("M,K,N,nbits,gs", SIZES)
-def test_cross_entropy(hq, M, K, N, nbits, gs, dtype):
+def test_cross_entropy(hq, path, M, K, N, nbits, gs, dtype):
     loss_case(hq, M, K, N, nbits, gs, dtype)
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("M,K,N", [(1, 4096, 20001), (9, 8192, 9001), (70, 4096, 17000), (300, 8192, 8300)])
-def test_cross_entropy_in_pieces(hq, M, K, N, dtype):
-    """More classes than a piece: targets in every piece, and at its first and last class."""
+def test_cross_entropy_in_pieces(hq, path, M, K, N, dtype):
+    """More classes than a piece of the tiled route: targets in every piece, and at its first and last class."""
     t = torch.randint(0, N, (M,), generator=torch.Generator().manual_seed(M))
     for i, edge in enumerate((8191, 8192, 16383, 16384, N - 1, 4095, 4096)):
         if i < M and edge < N:
@@ -264,7 +271,7 @@ def test_cross_entropy_in_pieces(hq, M, K, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
-def test_cross_entropy_peaked_rows(hq, dtype):
+def test_cross_entropy_peaked_rows(hq, path, dtype):
     """Logits far apart: one class holds nearly everything, as the target and as another."""
     M, K, N = 24, 256, 500
     head, W = make_weight(5, N, K, 4, 64, dtype)
@@ -282,7 +289,7 @@ def test_cross_entropy_peaked_rows(hq, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("M", [3, 70])
-def test_cross_entropy_ignored_rows(hq, dtype, M):
+def test_cross_entropy_ignored_rows(hq, path, dtype, M):
     """Rows without a target give 0, whatever their inputs hold; all rows may be such."""
     K, N = 128, 300
     head, W = make_weight(5, N, K, 4, 64, dtype)
@@ -304,7 +311,7 @@ def test_cross_entropy_ignored_rows(hq, dtype, M):
     assert (loss == 0).all() and (dX == 0).all()
 
 
-def test_fp16_small_gradients_keep_their_precision(hq):
+def test_fp16_small_gradients_keep_their_precision(hq, path):
     """Gradients near fp16's smallest normal number (a loss scale too low): dG and dU are formed
     relative to the row."""
     dtype = torch.float16
@@ -320,7 +327,7 @@ def test_fp16_small_gradients_keep_their_precision(hq):
 
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("M", [4, 96])
-def test_gated_saturated_activations(hq, act, M):
+def test_gated_saturated_activations(hq, path, act, M):
     """Projections up to several hundred: the activation's flat and linear ends."""
     dtype, K, N = torch.bfloat16, 64, 96
     gate, Wg = make_weight(1, N, K, 8, 64, dtype, std=4.0)
@@ -369,7 +376,7 @@ def chain(hq, dtype, M=37, K=128, F=192, V=400, nbits=4, gs=64):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
-def test_operators_together(hq, dtype):
+def test_operators_together(hq, path, dtype):
     """A block and a head as a fine-tuning step runs them: loss and gradient against autograd and
     against differences in 64 bits.  Three 16-bit intermediates on the way forward and three on the
     way back, each off by u of its size: as independent errors well within 16 u of the norm."""
@@ -391,7 +398,7 @@ def test_operators_together(hq, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("M", [1, 20, 150])
-def test_captured_and_replayed(hq, dtype, M):
+def test_captured_and_replayed(hq, path, dtype, M):
     """The whole step in a HIP graph, replayed with new inputs between eager calls: the same bits."""
     forward, backward, _, X, t = chain(hq, dtype, M=M)
     dloss = torch.ones(M, device="cuda")
@@ -441,7 +448,7 @@ def everything(hq, dtype, M, K, N, nbits, gs, ws=None):
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
 @pytest.mark.parametrize("M,K,N", [(1, 160, 77), (13, 256, 300), (200, 352, 515)])
-def test_workspace_contents_and_repeats(hq, dtype, M, K, N):
+def test_workspace_contents_and_repeats(hq, path, dtype, M, K, N):
     """A caller's workspace of the stated size, full of NaN (bytes 0xff) with a guard behind it:
     the same bits as without, twice, and the guard untouched."""
     plain = everything(hq, dtype, M, K, N, 4, 32)
@@ -459,7 +466,7 @@ def test_workspace_contents_and_repeats(hq, dtype, M, K, N):
         assert (g == 0xff).all()
 
 
-def test_outputs_in_larger_buffers(hq):
+def test_outputs_in_larger_buffers(hq, path):
     """Nothing is written outside the outputs (odd widths end inside vector stores)."""
     dtype, M, K, N = torch.float16, 45, 96, 67
     a, _ = make_weight(1, N, K, 4, 32, dtype)
@@ -476,6 +483,21 @@ def test_outputs_in_larger_buffers(hq):
         call(part.view(shape))
         assert (whole[:256] == 7).all() and (whole[256 + part.numel():] == 7).all()
         assert (part != 7).any()
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 32, 33, 64, 65, 96, 256, 257])
+def test_route_boundaries(hq, M):
+    """The sizes at which the library changes its route by itself, each operator."""
+    dtype, K, N = torch.bfloat16, 512, 1100
+    for nbits, gs in ((4, 64), (2, 16)):
+        a, Wa = make_weight(1, N, K, nbits, gs, dtype)
+        b, Wb = make_weight(2, N, K, nbits, gs, dtype)
+        X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+        check_gated(hq.hqq_linear_gated(X, a, b, N, nbits, gs), X, Wa, Wb, "silu")
+        check_gated_backward(hq.hqq_linear_gated_backward(dY, X, a, b, N, nbits, gs), dY, X, Wa, Wb, "silu")
+        y = dY.double()
+        within(hq.hqq_linear_backward(dY, *a, K, nbits, gs), *grad_bound([y], [torch.zeros_like(y)], [Wa], dtype))
+        loss_case(hq, M, K, N, nbits, gs, dtype)
 
 
 def test_two_streams_with_their_own_workspaces(hq):

@@ -115,7 +115,7 @@ CALLS = [gated, gated_backward, batch_backward, loss, loss_backward]
 @pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
 @pytest.mark.parametrize("kw,code", SIZES + [(dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE),
                                              (dict(ws=MIS), PTR), (dict(ws=None), PTR), (dict(size=-1), PTR),
-                                             (dict(M=40, size=0), WORKSPACE), (dict(M=40, ws=None, size=0), WORKSPACE)])
+                                             (dict(M=400, size=0), WORKSPACE), (dict(M=400, ws=None, size=0), WORKSPACE)])
 def test_rejects(w, lib, call, kw, code):
     assert call(w, lib, **kw) == code
 
@@ -161,7 +161,7 @@ def test_workspace_sizes(w):
             assert call(w, w.load_layers_library(), M=37, K=1056, N=2753, nbits=2, gs=32, size=need - 1) == WORKSPACE
         with pytest.raises(w.LayersError):
             fn(37, 1056, 2753, 3, 32)
-    assert w.hqq_linear_batch_backward_workspace(50, 128, [40, 7], 4, 64) > 0
+    assert w.hqq_linear_batch_backward_workspace(500, 128, [40, 7], 4, 64) > 0
     with pytest.raises(w.LayersError):
         w.hqq_linear_batch_backward_workspace(5, 128, [], 4, 64)
     with pytest.raises(w.LayersError):
@@ -194,4 +194,4 @@ def test_batch_width_limit(w, lib):
     N = 1 << 22
     arr = (HqqLinearGrad * 3)(*[HqqLinearGrad(A, A, A, N, A)] * 3)
     assert lib.hqq_linear_batch_backward(arr, 3, 1, 32, 1, 32, 0, A, A, 1 << 40, None) == SHAPE
-    assert lib.hqq_linear_batch_backward(arr, 2, 40, 32, 1, 32, 0, A, A, 0, None) == WORKSPACE
+    assert lib.hqq_linear_batch_backward(arr, 2, 400, 32, 1, 32, 0, A, A, 0, None) == WORKSPACE

@@ -3,6 +3,8 @@
 #include "hqq_layers_internal.h"
 
 #include <stdint.h>
+#include <stdlib.h>
+#include <string.h>
 
 namespace {
 
@@ -13,9 +15,6 @@ constexpr int64_t kMaxDepth = int64_t(1) << 17;
 constexpr int64_t kMaxWidth = int64_t(1) << 22;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int64_t kMaxBytes = int64_t(1) << 31;
-// Up to this many rows the kernels that work straight from the codes run; from
-// the next on, W_hat is unpacked and the tiled product runs.
-constexpr int64_t kFewRows = 32;
 // The backward passes keep 16-bit gradients of this many rows at a time.
 constexpr int64_t kRowChunk = 8192;
 
@@ -41,6 +40,31 @@ int check_sizes(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
     if (N * (K / group_size) * 4 >= kMaxBytes)
         return HQQ_EINVAL_SHAPE;
     return HQQ_OK;
+}
+
+// Whether a product runs straight from the codes (which every 32 rows dequantize
+// anew) or W_hat is unpacked for the tiled product.  n: all rows of its weights.
+// Measured crossovers on MI355X (bf16 or fp16, 512 x 512 to 4096 x 11008): gated
+// block at 4096 x 11008 4-bit g64, 64 rows 72 against 91 us, 96 rows 103 against 97;
+// 2048 x 5632 8-bit 32 rows 24 against 28, 64 rows 33 against 28; one weight backward,
+// 64 rows 41 against 48, 96 rows 63 against 56; the head at 1024 x 32003 4-bit, 32 rows
+// 32 against 35, 64 rows 51 against 35, and with 2-bit groups of 16 (a reciprocal per
+// 8 weights) 4 rows 31 against 35, 16 rows 38 against 35.  Small weights leave the CUs
+// room for the row blocks: 512 x 512, 192 rows 8 against 10.  HQQ_LAYERS_PATH=codes or
+// =tiled in the environment, read at each call, forces one (tests run both).
+enum Product { kPair, kBackward, kHead };
+
+bool straight(Product what, int64_t M, int64_t K, int64_t n, int nbits, int group_size)
+{
+    if (const char *e = getenv("HQQ_LAYERS_PATH")) {
+        if (strcmp(e, "codes") == 0)
+            return true;
+        if (strcmp(e, "tiled") == 0)
+            return false;
+    }
+    const bool tables = nbits == 4 && group_size >= 32;
+    const int64_t rows = what == kBackward ? 64 : what == kPair ? (tables ? 64 : 32) : group_size >= 32 ? 32 : 8;
+    return M <= rows || (M <= 256 && (M + 31) / 32 * K * n <= (tables ? 16 : 6) * 1000000);
 }
 
 int check_batch(int64_t M, int64_t K, const int64_t *n, int count, int nbits, int group_size)
@@ -216,6 +240,14 @@ void add_grad(SkinnyGradArgs &a, const uint32_t *packed, const float *scale, con
     a.step0[i + 1] = a.step0[i] + (int32_t)((n + 31) / 32);
 }
 
+int64_t sum_of(const int64_t *n, int count)
+{
+    int64_t t = 0;
+    for (int i = 0; i < count; ++i)
+        t += n[i];
+    return t;
+}
+
 // 32-row steps of the widths n
 int64_t grad_steps(const int64_t *n, int count)
 {
@@ -264,11 +296,11 @@ hipError_t few_rows_gradient(SkinnyGradArgs &a, bool bf16, int nbits, int group_
 struct GatedLayout {
     uint16_t *W, *X;
     int64_t bytes;
-    GatedLayout(void *p, int64_t M, int64_t K, int64_t N)
+    GatedLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
         Carve c(p);
         W = X = nullptr;
-        if (M > kFewRows) {
+        if (!few) {
             W = c.take<uint16_t>(2 * round_up(N, 32) * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(M, K));
         }
@@ -280,12 +312,12 @@ struct GatedGradLayout {
     uint16_t *W, *WT, *dGU, *X;
     float *scale, *inv, *part;
     int64_t bytes;
-    GatedGradLayout(void *p, int64_t M, int64_t K, int64_t N)
+    GatedGradLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
         const int64_t Np = round_up(N, kStep), mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
         W = WT = X = nullptr;
-        if (M > kFewRows) {
+        if (!few) {
             W = c.take<uint16_t>(2 * round_up(N, 32) * pitch_for(K));
             WT = c.take<uint16_t>(K * pitch_for(2 * Np));
             X = c.take_some<uint16_t>(pad_values(mc, K));
@@ -294,7 +326,7 @@ struct GatedGradLayout {
         scale = c.take<float>(mc);
         inv = c.take<float>(mc);
         const int64_t n[2] = {N, N};
-        part = c.take_some<float>(M > kFewRows ? part_floats(M, K, 2 * Np / kStep)
+        part = c.take_some<float>(!few ? part_floats(M, K, 2 * Np / kStep)
                                                : few_part_floats(M, K, grad_steps(n, 2)));
         bytes = c.at;
     }
@@ -304,13 +336,13 @@ struct BatchGradLayout {
     uint16_t *WT, *pad[HQQ_MAX_GRADS];
     float *part;
     int64_t bytes, ldt;
-    BatchGradLayout(void *p, int64_t M, int64_t K, const int64_t *n, int count)
+    BatchGradLayout(void *p, int64_t M, int64_t K, const int64_t *n, int count, bool few)
     {
         const int64_t mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
         ldt = 0;
         WT = nullptr;
-        if (M <= kFewRows) {
+        if (few) {
             part = c.take_some<float>(few_part_floats(M, K, grad_steps(n, count)));
             bytes = c.at;
             return;
@@ -341,11 +373,11 @@ struct LossLayout {
     float2 *stats;
     float *tlogit;
     int64_t bytes, piece, pitch;      // classes per piece; blocks that a row of stats has room for
-    LossLayout(void *p, int64_t M, int64_t K, int64_t N)
+    LossLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
         Carve c(p);
         W = X = nullptr;
-        if (M > kFewRows) {
+        if (!few) {
             piece = loss_piece(K, N);
             pitch = N / piece * ((piece + 127) / 128) + (N % piece + 127) / 128;
             W = c.take<uint16_t>(piece * pitch_for(K));
@@ -374,13 +406,13 @@ struct LossGradLayout {
     uint16_t *W, *WT, *dL, *X;
     float *rowf, *part, *acc;
     int64_t bytes, piece, ldl;
-    LossGradLayout(void *p, int64_t M, int64_t K, int64_t N)
+    LossGradLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
         const int64_t mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
         W = WT = X = nullptr;
         acc = nullptr;
-        if (M <= kFewRows) {
+        if (few) {
             piece = N;
             ldl = round_up(N, kStep);
             dL = c.take<uint16_t>(M * ldl);
@@ -432,7 +464,7 @@ int64_t hqq_linear_gated_workspace(int64_t M, int64_t K, int64_t N, int nbits, i
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return GatedLayout(nullptr, M, K, N).bytes;
+    return GatedLayout(nullptr, M, K, N, straight(kPair, M, K, 2 * N, nbits, group_size)).bytes;
 }
 
 int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate, const hqq_weight *up, int64_t N,
@@ -448,12 +480,13 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
     if (!gate || !up || !weight_ok(gate->packed, gate->scale, gate->zero) || !weight_ok(up->packed, up->scale, up->zero) ||
         !aligned(X, 16) || !aligned(Y, 16))
         return HQQ_EINVAL_PTR;
-    const GatedLayout l(workspace, M, K, N);
+    const bool few = straight(kPair, M, K, 2 * N, nbits, group_size);
+    const GatedLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    if (M <= kFewRows) {
+    if (few) {
         SkinnyArgs f{};
         f.w[0] = linear_args(X, *gate, M, K, N, nbits, group_size);
         f.w[1] = linear_args(X, *up, M, K, N, nbits, group_size);
@@ -488,7 +521,7 @@ int64_t hqq_linear_gated_backward_workspace(int64_t M, int64_t K, int64_t N, int
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return GatedGradLayout(nullptr, M, K, N).bytes;
+    return GatedGradLayout(nullptr, M, K, N, straight(kPair, M, K, 2 * N, nbits, group_size)).bytes;
 }
 
 int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate,
@@ -504,13 +537,14 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     if (!gate || !up || !weight_ok(gate->packed, gate->scale, gate->zero) || !weight_ok(up->packed, up->scale, up->zero) ||
         !aligned(X, 16) || !aligned(dY, 16) || !aligned(dX, 16))
         return HQQ_EINVAL_PTR;
-    const GatedGradLayout l(workspace, M, K, N);
+    const bool few = straight(kPair, M, K, 2 * N, nbits, group_size);
+    const GatedGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const int64_t Np = round_up(N, kStep), ldg = pitch_for(2 * Np);
-    if (M <= kFewRows) {
+    if (few) {
         if (!bf16 && launch_row_scale(dY, M, N, l.scale, l.inv, s) != hipSuccess)
             return HQQ_EHIP;
         SkinnyArgs f{};
@@ -585,7 +619,7 @@ int64_t hqq_linear_batch_backward_workspace(int64_t M, int64_t K, const int64_t 
         return HQQ_EINVAL_PTR;
     if (const int st = check_batch(M, K, n, count, nbits, group_size))
         return st;
-    return BatchGradLayout(nullptr, M, K, n, count).bytes;
+    return BatchGradLayout(nullptr, M, K, n, count, straight(kBackward, M, K, sum_of(n, count), nbits, group_size)).bytes;
 }
 
 int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, int64_t K, int nbits, int group_size,
@@ -607,12 +641,13 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
     for (int i = 0; i < count; ++i)
         if (!weight_ok(ws[i].packed, ws[i].scale, ws[i].zero) || !aligned(ws[i].dY, 16))
             return HQQ_EINVAL_PTR;
-    const BatchGradLayout l(workspace, M, K, n, count);
+    const bool few = straight(kBackward, M, K, sum_of(n, count), nbits, group_size);
+    const BatchGradLayout l(workspace, M, K, n, count, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    if (M <= kFewRows) {
+    if (few) {
         SkinnyGradArgs b{};
         for (int i = 0; i < count; ++i)
             add_grad(b, ws[i].packed, ws[i].scale, ws[i].zero, ws[i].dY, n[i], n[i]);
@@ -653,7 +688,7 @@ int64_t hqq_linear_cross_entropy_workspace(int64_t M, int64_t K, int64_t N, int 
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return LossLayout(nullptr, M, K, N).bytes;
+    return LossLayout(nullptr, M, K, N, straight(kHead, M, K, N, nbits, group_size)).bytes;
 }
 
 int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *head, int64_t N, int nbits,
@@ -667,12 +702,13 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
     if (!head || !weight_ok(head->packed, head->scale, head->zero) || !aligned(X, 16) || !aligned(targets, 8) ||
         !aligned(loss, 4) || !aligned(lse, 4))
         return HQQ_EINVAL_PTR;
-    const LossLayout l(workspace, M, K, N);
+    const bool few = straight(kHead, M, K, N, nbits, group_size);
+    const LossLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    if (M <= kFewRows) {
+    if (few) {
         SkinnyArgs f{};
         f.w[0] = linear_args(X, *head, M, K, N, nbits, group_size);
         f.out = kOutStats;
@@ -718,7 +754,7 @@ int64_t hqq_linear_cross_entropy_backward_workspace(int64_t M, int64_t K, int64_
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return LossGradLayout(nullptr, M, K, N).bytes;
+    return LossGradLayout(nullptr, M, K, N, straight(kHead, M, K, N, nbits, group_size)).bytes;
 }
 
 int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *head,
@@ -733,13 +769,14 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
     if (!head || !weight_ok(head->packed, head->scale, head->zero) || !aligned(X, 16) || !aligned(dX, 16) ||
         !aligned(targets, 8) || !aligned(dloss, 4) || !aligned(lse, 4))
         return HQQ_EINVAL_PTR;
-    const LossGradLayout l(workspace, M, K, N);
+    const bool few = straight(kHead, M, K, N, nbits, group_size);
+    const LossGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const float unit = bf16 ? 1.0f : 1.0f / 32768.0f;     // of the rounded differences
-    if (M <= kFewRows) {
+    if (few) {
         SkinnyArgs f{};
         f.w[0] = linear_args(X, *head, M, K, N, nbits, group_size);
         f.out = kOutSoftGrad;

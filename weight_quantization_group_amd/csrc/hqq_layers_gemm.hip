@@ -164,27 +164,32 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
         constexpr bool GRAD = OUT == kOutGatedGrad;
         char *sg = st, *su = st + 16 * P, *sy = st + 32 * P;
         const int row4 = lane >> 2, n4 = nw + 8 * (lane & 3);      // coalesced: 4 lanes per row
-        uint4 y[TM];
-        if constexpr (GRAD) {
-            // all of dY at once where the tile is whole: loads behind branches come one by one
+        // dY four blocks of rows at a time where the tile is whole: loads behind branches come
+        // one by one, and all eight take registers that the sums need
+        uint4 y[4];
+        auto load_y = [&](int u0) {
             if (mw + 16 * TM <= g.M && nw + 32 <= g.N && g.ldy % 8 == 0) {
 #pragma unroll
-                for (int u = 0; u < TM; ++u)
-                    y[u] = *reinterpret_cast<const uint4 *>(g.dY + (int64_t)(mw + 16 * u + row4) * g.ldy + n4);
+                for (int i = 0; i < 4; ++i)
+                    if (u0 + i < TM)
+                        y[i] = *reinterpret_cast<const uint4 *>(g.dY + (int64_t)(mw + 16 * (u0 + i) + row4) * g.ldy + n4);
             } else {
 #pragma unroll
-                for (int u = 0; u < TM; ++u) {
-                    const int mr = mw + 16 * u + row4;
-                    y[u] = mr < g.M && n4 < g.N ? load8(g.dY + (int64_t)mr * g.ldy + n4, g.N - n4) : uint4{0, 0, 0, 0};
+                for (int i = 0; i < 4; ++i) {
+                    const int mr = mw + 16 * (u0 + i) + row4;
+                    y[i] = mr < g.M && n4 < g.N ? load8(g.dY + (int64_t)mr * g.ldy + n4, g.N - n4) : uint4{0, 0, 0, 0};
                 }
             }
-        }
+        };
 #pragma unroll
         for (int u = 0; u < TM; ++u) {
             const int m = mw + 16 * u + l16, mc = m < g.M ? m : g.M - 1;
             const float sc = GRAD && g.rscale ? g.rscale[mc] : 1.0f;
-            if constexpr (GRAD)
-                *reinterpret_cast<uint4 *>(sy + row4 * P + 16 * (lane & 3)) = y[u];
+            if constexpr (GRAD) {
+                if (u % 4 == 0)
+                    load_y(u);
+                *reinterpret_cast<uint4 *>(sy + row4 * P + 16 * (lane & 3)) = y[u % 4];
+            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int n = 16 * t + 4 * l4;
