@@ -181,7 +181,7 @@ void single_segment(GemmArgs &g, const uint16_t *A, int64_t depth, int64_t pitch
     g.splits = 1;
 }
 
-// dX [M, K] = rowf * (A . WT^T): in one launch, or by split sums and a second;
+// dX [M, K] = rowf * (A . W): in one launch, or by split sums and a second;
 // acc: fp32 sums carried between pieces (null: one piece)
 hipError_t gradient_product(GemmArgs &g, bool bf16, float *part, float *acc, bool first, bool last, uint16_t *dX,
                             const float *rowf, hipStream_t s)
@@ -309,17 +309,16 @@ struct GatedLayout {
 };
 
 struct GatedGradLayout {
-    uint16_t *W, *WT, *dGU, *X;
+    uint16_t *W, *dGU, *X;
     float *scale, *inv, *part;
     int64_t bytes;
     GatedGradLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
-        const int64_t Np = round_up(N, kStep), mc = M < kRowChunk ? M : kRowChunk;
+        const int64_t Np = round_up(N, 32), mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
-        W = WT = X = nullptr;
+        W = X = nullptr;
         if (!few) {
-            W = c.take<uint16_t>(2 * round_up(N, 32) * pitch_for(K));
-            WT = c.take<uint16_t>(K * pitch_for(2 * Np));
+            W = c.take<uint16_t>(2 * Np * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(mc, K));
         }
         dGU = c.take<uint16_t>(mc * pitch_for(2 * Np));
@@ -333,28 +332,26 @@ struct GatedGradLayout {
 };
 
 struct BatchGradLayout {
-    uint16_t *WT, *pad[HQQ_MAX_GRADS];
+    uint16_t *W, *pad[HQQ_MAX_GRADS];
     float *part;
-    int64_t bytes, ldt;
+    int64_t bytes;
     BatchGradLayout(void *p, int64_t M, int64_t K, const int64_t *n, int count, bool few)
     {
         const int64_t mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
-        ldt = 0;
-        WT = nullptr;
+        W = nullptr;
         if (few) {
             part = c.take_some<float>(few_part_floats(M, K, grad_steps(n, count)));
             bytes = c.at;
             return;
         }
+        int64_t rows = 0;
         for (int i = 0; i < count; ++i)
-            ldt += round_up(n[i], kStep);
-        const int64_t steps = ldt / kStep;
-        ldt = pitch_for(ldt);
-        WT = c.take<uint16_t>(K * ldt);
+            rows += round_up(n[i], kStep);
+        W = c.take<uint16_t>(rows * pitch_for(K));
         for (int i = 0; i < count; ++i)
             pad[i] = c.take_some<uint16_t>(pad_values(mc, n[i]));
-        part = c.take<float>(part_floats(M, K, steps));
+        part = c.take<float>(part_floats(M, K, rows / kStep));
         bytes = c.at;
     }
 };
@@ -380,7 +377,7 @@ struct LossLayout {
         if (!few) {
             piece = loss_piece(K, N);
             pitch = N / piece * ((piece + 127) / 128) + (N % piece + 127) / 128;
-            W = c.take<uint16_t>(piece * pitch_for(K));
+            W = c.take<uint16_t>(round_up(piece, kStep) * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(M, K));
         } else {
             piece = N;
@@ -403,14 +400,14 @@ int64_t loss_grad_piece(int64_t m, int64_t K, int64_t N)
 }
 
 struct LossGradLayout {
-    uint16_t *W, *WT, *dL, *X;
+    uint16_t *W, *dL, *X;
     float *rowf, *part, *acc;
     int64_t bytes, piece, ldl;
     LossGradLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
         const int64_t mc = M < kRowChunk ? M : kRowChunk;
         Carve c(p);
-        W = WT = X = nullptr;
+        W = X = nullptr;
         acc = nullptr;
         if (few) {
             piece = N;
@@ -423,8 +420,7 @@ struct LossGradLayout {
         }
         piece = loss_grad_piece(mc, K, N);
         ldl = pitch_for(piece);
-        W = c.take<uint16_t>(piece * pitch_for(K));
-        WT = c.take<uint16_t>(K * ldl);
+        W = c.take<uint16_t>(round_up(piece, kStep) * pitch_for(K));
         dL = c.take<uint16_t>(mc * ldl);
         X = c.take_some<uint16_t>(pad_values(mc, K));
         rowf = c.take<float>(mc);
@@ -543,7 +539,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         return st;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t Np = round_up(N, kStep), ldg = pitch_for(2 * Np);
+    const int64_t Np = round_up(N, 32), ldg = pitch_for(2 * Np);
     if (few) {
         if (!bf16 && launch_row_scale(dY, M, N, l.scale, l.inv, s) != hipSuccess)
             return HQQ_EHIP;
@@ -572,9 +568,6 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     }
     UnpackArgs a = unpack_pair(*gate, *up, N, K, nbits, group_size);
     a.W = l.W;
-    a.WT[0] = l.WT;
-    a.WT[1] = l.WT + Np;
-    a.ldt = ldg;
     if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
         return HQQ_EHIP;
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
@@ -597,11 +590,11 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         g.rscale = bf16 ? nullptr : l.scale;
         g.out = l.dGU;
         g.ldo = ldg;
-        g.up_off = g.fill = Np;
+        g.fill = Np;
         GemmArgs p{};
         single_segment(p, l.dGU, 2 * Np, ldg);
-        p.B = l.WT;
-        p.ldb = ldg;
+        p.B = l.W;
+        p.ldb = a.ldw;
         p.M = (int32_t)m;
         p.N = (int32_t)K;
         if (launch_gemm(kOutGatedGrad, bf16, g, s) != hipSuccess ||
@@ -654,14 +647,13 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
         return few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, nullptr, s) == hipSuccess ? HQQ_OK
                                                                                                         : HQQ_EHIP;
     }
-    int64_t col = 0;
+    int64_t row = 0;
     for (int i = 0; i < count; ++i) {
         UnpackArgs a = unpack_args(hqq_weight{ws[i].packed, ws[i].scale, ws[i].zero}, 0, n[i], K, nbits, group_size);
-        a.WT[0] = l.WT + col;
-        a.ldt = l.ldt;
+        a.W = l.W + row * a.ldw;
         if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
             return HQQ_EHIP;
-        col += round_up(n[i], kStep);
+        row += round_up(n[i], kStep);
     }
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
@@ -674,8 +666,8 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
                 return HQQ_EHIP;
             g.step0[i + 1] = g.step0[i] + (int32_t)((n[i] + kStep - 1) / kStep);
         }
-        g.B = l.WT;
-        g.ldb = l.ldt;
+        g.B = l.W;
+        g.ldb = pitch_for(K);
         g.M = (int32_t)m;
         g.N = (int32_t)K;
         if (gradient_product(g, bf16, l.part, nullptr, true, true, dX + m0 * K, nullptr, s) != hipSuccess)
@@ -809,8 +801,6 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             const int64_t fill = round_up(n, kStep), ldl = pitch_for(n);
             UnpackArgs a = unpack_args(*head, n0, n, K, nbits, group_size);
             a.W = l.W;
-            a.WT[0] = l.WT;
-            a.ldt = ldl;
             GemmArgs g{};
             single_segment(g, x, round_up(K, kStep), whole_pitch(K));
             g.B = l.W;
@@ -826,8 +816,8 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             g.fill = fill;
             GemmArgs p{};
             single_segment(p, l.dL, fill, ldl);
-            p.B = l.WT;
-            p.ldb = ldl;
+            p.B = l.W;
+            p.ldb = a.ldw;
             p.M = (int32_t)m;
             p.N = (int32_t)K;
             if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess ||

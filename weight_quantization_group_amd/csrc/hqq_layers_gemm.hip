@@ -1,6 +1,7 @@
-// hqq_layers_gemm.hip -- the matrix product of the layers with many rows,
-// C [M, N] = A [M, R] . B [N, R]^T in 16-bit inputs and fp32 sums on the matrix
-// cores, and the operators' arithmetic on C while it is in registers.
+// hqq_layers_gemm.hip -- the matrix products of the layers with many rows, 16-bit
+// inputs and fp32 sums on the matrix cores: C [M, N] = A [M, R] . B [N, R]^T with the
+// operators' arithmetic on C while it is in registers, and C = A . B [R, N] for the
+// gradients.
 //
 // A workgroup computes a BM x BN tile of C with WM x WN waves.  Each 64-wide step
 // of A and B goes from memory to LDS by DMA (no registers), into two buffers in
@@ -19,6 +20,21 @@ __device__ __forceinline__ void dma16(const void *p, uint4 *lds)
 {
 #ifdef __HIP_DEVICE_COMPILE__
     __builtin_amdgcn_global_load_lds(p, (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+#endif
+}
+
+// ds_read_b64_tr_b16
+__device__ __forceinline__ uint2 read_tr(const char *lds)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    typedef short short4v __attribute__((ext_vector_type(4)));
+    const short4v v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) short4v *)const_cast<char *>(lds));
+    uint2 u;
+    __builtin_memcpy(&u, &v, 8);
+    return u;
+#else
+    return uint2{0, 0};
 #endif
 }
 
@@ -215,14 +231,15 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                         uint2{out2<BF>(vu[0], vu[1]), out2<BF>(vu[2], vu[3])};
             }
             const int mr = mw + 16 * u + row4, width = GRAD ? (int)g.fill : g.N;
-            uint16_t *o = g.out + (int64_t)mr * g.ldo + n4;
+            // (dG and dU in turn by 32 columns, as the weights' rows are)
+            uint16_t *o = g.out + (int64_t)mr * g.ldo + (GRAD ? nw + n4 : n4);
             const uint4 v = *reinterpret_cast<const uint4 *>(sg + row4 * P + 16 * (lane & 3));
             if (mr < g.M && n4 < width)
                 store8(o, v, width - n4);
             if constexpr (GRAD) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(su + row4 * P + 16 * (lane & 3));
                 if (mr < g.M && n4 < width)
-                    store8(o + g.up_off, w, 8);
+                    store8(o + 32, w, 8);
             }
         }
     } else {   // kOutStats
@@ -321,6 +338,7 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
     static_assert(TN == 4, "64 columns per wave: the softmax blocks and the gate / up halves");
     constexpr bool GATED = OUT == kOutGated || OUT == kOutGatedGrad;
+    constexpr bool DOWN = OUT == kOutStore || OUT == kOutPart;    // B [R, N]: the sum runs down its rows
     constexpr int BNC = GATED ? BN / 2 : BN;         // columns of the output per tile
     constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW;
     // (arrays of their own: reads of one do not wait for the DMA into another)
@@ -338,10 +356,16 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     // Rows past the end repeat the last.  The lanes' byte offsets from the tile's
     // first row are formed at each use: kept, they would cost registers.
     const uint32_t run16 = 16 * ((lane & 7) ^ (lane >> 3));
-    int row_a = IA * 8 * wave + (lane >> 3), row_b = IB * 8 * wave + (lane >> 3);
-    const int b0 = tile_n * BN, last_b = (GATED ? 2 * ((g.N + 31) / 32 * 32) : g.N) - b0 - 1;
+    // DOWN: a step of B is 64 rows of BN columns, RB of them per instruction; a row's
+    // 32-byte pieces are XOR-swizzled by its low bits, so that the transposing reads of 16
+    // rows spread over the banks.
+    constexpr int SB = BN / 8, RB = 64 / SB, MB = BN / 16 - 1;
+    int row_a = IA * 8 * wave + (lane >> 3);
+    int row_b = DOWN ? IB * RB * wave + lane / SB : IB * 8 * wave + (lane >> 3);
+    const int b0 = tile_n * BN;
+    const int last_b = DOWN ? (int)g.ldb - 8 : (GATED ? 2 * ((g.N + 31) / 32 * 32) : g.N) - b0 - 1;
     const int last_a = g.M - m0 - 1;
-    const char *bb = reinterpret_cast<const char *>(g.B + (int64_t)b0 * g.ldb);
+    const char *bb = reinterpret_cast<const char *>(DOWN ? g.B : g.B + (int64_t)b0 * g.ldb);
     uint32_t ldb2 = (uint32_t)(g.ldb * 2);
     const int steps = g.step0[g.segs];
     const int per = (steps + g.splits - 1) / g.splits;
@@ -361,8 +385,16 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
         dma16(ab + (int64_t)s * (2 * kStep) + ((uint32_t)r * lda2 + run16), as + (IA * wave + i) * 64);
     };
     auto dma_b = [&](int i, int s, uint4 *bs) {
-        const int r = row_b + 8 * i < last_b ? row_b + 8 * i : last_b;
-        dma16(bb + (int64_t)s * (2 * kStep) + ((uint32_t)r * ldb2 + run16), bs + (IB * wave + i) * 64);
+        if constexpr (DOWN) {
+            const int r = row_b + RB * i, slot = lane % SB;
+            const int c = b0 + 16 * ((slot >> 1) ^ (r & MB)) + 8 * (slot & 1);
+            // (columns past the pitch repeat its last; they are not stored)
+            dma16(bb + (int64_t)s * kStep * ldb2 + ((uint32_t)r * ldb2 + 2 * (uint32_t)(c < last_b ? c : last_b)),
+                  bs + (IB * wave + i) * 64);
+        } else {
+            const int r = row_b + 8 * i < last_b ? row_b + 8 * i : last_b;
+            dma16(bb + (int64_t)s * (2 * kStep) + ((uint32_t)r * ldb2 + run16), bs + (IB * wave + i) * 64);
+        }
     };
     auto dma = [&](int s, uint4 *as, uint4 *bs) {
 #pragma unroll
@@ -384,7 +416,22 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
         return reinterpret_cast<const uint4v *>(as)[(wm * (BM / WM) + 16 * u + l16) * 8 + ((4 * ks + l4) ^ sw)];
     };
     auto read_b = [&](int ks, int t, const uint4 *bs) {
-        return reinterpret_cast<const uint4v *>(bs)[(wn * (BN / WN) + 16 * t + l16) * 8 + ((4 * ks + l4) ^ sw)];
+        if constexpr (DOWN) {
+            // 8 rows of a column: two reads that transpose 4 rows x 16 columns among 16 lanes
+            // (lane i of them reads 8 bytes of row i / 4 and gets column i)
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int r = 8 * l4 + 4 * q + (l16 >> 2);
+                const uint2 v = read_tr(reinterpret_cast<const char *>(bs) + 32 * ks * (2 * BN) + r * (2 * BN) +
+                                        (((wn * 4 + t) ^ (r & MB)) * 32 + 8 * (l16 & 3)));
+                w[2 * q] = v.x;
+                w[2 * q + 1] = v.y;
+            }
+            return uint4v{w[0], w[1], w[2], w[3]};
+        } else {
+            return reinterpret_cast<const uint4v *>(bs)[(wn * (BN / WN) + 16 * t + l16) * 8 + ((4 * ks + l4) ^ sw)];
+        }
     };
     // One half: TM groups of TN matrix instructions; the reads of the next half's
     // operands (half ks of the given buffers) are spread over all but the last of

@@ -9,9 +9,9 @@ namespace hqq {
 
 constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// Dequantization of n rows of a weight into the workspace (either output may
-// be null): W [n, K] row-major with columns K .. round_up(K, 64) - 1 zeroed, and
-// its transpose WT [K, n] with columns n .. round_up(n, 64) - 1 zeroed.
+// Dequantization of n rows of a weight into the workspace: W [rows, K] row-major, its
+// columns K .. round_up(K, 64) - 1 and its rows past n zeroed.  One weight fills
+// round_up(n, 64) rows; a gated pair 2 round_up(n, 32), 32 of gate and 32 of up in turn.
 struct UnpackArgs {
     int count;                // 1, or 2: a gated pair (gate, up) of one shape and format
     const uint32_t *packed[2];   // of the first row
@@ -19,17 +19,16 @@ struct UnpackArgs {
     int64_t n, K;
     int64_t wpr, gpl;         // words and groups per row
     int gshift;               // log2 of the group size
-    uint16_t *W;              // a pair shares W: 32 rows of the one and 32 of the other in turn
+    uint16_t *W;
     int64_t ldw;
-    uint16_t *WT[2];
-    int64_t ldt;
 };
 hipError_t launch_unpack_weight(int nbits, bool bf16, const UnpackArgs &a, hipStream_t s);
 
-// The matrix product C [M, N] = A [M, R] . B [N, R]^T of 16-bit matrices with
-// fp32 sums, and what becomes of C.  A comes in segments along R, each a matrix
-// of its own of whole 64-wide steps; B is one matrix in the workspace.  Columns
-// that pad the last step of a segment are finite in A and zero in B.
+// The matrix product C [M, N] of 16-bit matrices with fp32 sums, and what becomes of C:
+// C = A [M, R] . B [N, R]^T, or, for the gradients (kOutStore, kOutPart), C = A . B [R, N].
+// A comes in segments along R, each a matrix of its own of whole 64-wide steps; B is
+// an unpacked weight (or several, one below the other).  Where padding meets in a
+// step, both are zero.
 constexpr int kStep = 64;            // depth of a step
 // Row pitch of a matrix in the workspace that the product reads: whole steps and
 // 128 bytes more, so that the rows of a tile do not all fall on the same cache
@@ -42,7 +41,7 @@ enum GemmOut {
     kOutStore,      // out16 = round(rowf * C)
     kOutPart,       // part[z] = C over this split's steps (fp32)
     kOutGated,      // out16 = act(C_gate) * C_up
-    kOutGatedGrad,  // dG, dU from C_gate, C_up and dY
+    kOutGatedGrad,  // dG, dU from C_gate, C_up and dY, in B's order of rows
     kOutStats,      // per row and column tile: max and sum of exp of the logits
     kOutSoftGrad    // exp(C - lse) - onehot(target)
 };
@@ -52,7 +51,7 @@ struct GemmArgs {
     int64_t lda[kMaxSegs];
     int32_t step0[kMaxSegs + 1];     // first step of each segment; step0[segs]: their number
     int segs;
-    const uint16_t *B;               // [N, ldb]; gated: [2 round_up(N, 32), ldb], see UnpackArgs
+    const uint16_t *B;               // [N, ldb] (gated: [2 round_up(N, 32), ldb]), or [R, ldb]
     int64_t ldb;                     // below 2^23
     int32_t M, N;
     int splits;                      // kOutPart: parts of the steps
@@ -66,7 +65,7 @@ struct GemmArgs {
     const uint16_t *dY;              // kOutGatedGrad: [M, N]
     const float *rscale;             // per-row scale of dG and dU, or null
     int64_t ldy;                     // row pitch of dY
-    int64_t up_off;                  // kOutGatedGrad: dU's first column in out
+    int64_t up_off;                  // kOutGatedGrad, few rows: dU's first column in out
     int64_t fill;                    // kOutGatedGrad, kOutSoftGrad: columns N .. fill - 1 of out are zeroed
     float2 *stats;                   // kOutStats: (max, sum) of row m and column tile i at [m * blocks + i]
     int64_t blocks;
