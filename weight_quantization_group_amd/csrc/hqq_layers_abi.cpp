@@ -115,30 +115,28 @@ struct Carve {
     }
 };
 
-UnpackArgs unpack_args(const hqq_weight &w, int64_t row0, int64_t n, int64_t K, int nbits, int group_size)
+UnpackArgs unpack_args(uint16_t *W, int64_t K, int nbits, int group_size)
 {
     UnpackArgs a{};
-    a.count = 1;
     a.wpr = K * nbits / 32;
     a.gpl = K / group_size;
-    a.packed[0] = w.packed + row0 * a.wpr;
-    a.scale[0] = w.scale + row0 * a.gpl;
-    a.zero[0] = w.zero + row0 * a.gpl;
-    a.n = n;
     a.K = K;
     a.gshift = log2_group(group_size);
+    a.W = W;
     a.ldw = pitch_for(K);
     return a;
 }
 
-UnpackArgs unpack_pair(const hqq_weight &gate, const hqq_weight &up, int64_t n, int64_t K, int nbits, int group_size)
+// rows first .. first + n - 1 of a weight, to W's row `row` (a pair's rows go in turn)
+void unpack_rows(UnpackArgs &a, const uint32_t *packed, const float *scale, const float *zero, int64_t first, int64_t n,
+                 int64_t row)
 {
-    UnpackArgs a = unpack_args(gate, 0, n, K, nbits, group_size);
-    a.count = 2;
-    a.packed[1] = up.packed;
-    a.scale[1] = up.scale;
-    a.zero[1] = up.zero;
-    return a;
+    const int i = a.count++;
+    a.packed[i] = packed + first * a.wpr;
+    a.scale[i] = scale + first * a.gpl;
+    a.zero[i] = zero + first * a.gpl;
+    a.n[i] = n;
+    a.row0[i] = row;
 }
 
 // floats of split sums that a product of up to M rows by N columns may need
@@ -154,15 +152,14 @@ int64_t part_floats(int64_t M, int64_t N, int64_t steps)
     return most;
 }
 
-// A [m, depth] whose rows end inside a step, copied with zeros up to its end (pad:
-// room for that, or null where they end with one)
-hipError_t whole_steps(const uint16_t *&A, int64_t m, int64_t depth, uint16_t *pad, hipStream_t s)
+// A [m, depth] for a product: itself, or where its rows end inside a step (pad: room
+// for that) its padded copy, which the unpacking launch makes
+const uint16_t *whole_steps(UnpackArgs &a, const uint16_t *A, int64_t m, int64_t depth, uint16_t *pad)
 {
     if (!pad)
-        return hipSuccess;
-    const uint16_t *src = A;
-    A = pad;
-    return launch_pad_rows(src, m, depth, pad, pitch_for(depth), s);
+        return A;
+    a.pad[a.pads++] = PadJob{A, pad, m, depth, pitch_for(depth)};
+    return pad;
 }
 
 int64_t pad_values(int64_t m, int64_t depth) { return depth % kStep ? m * pitch_for(depth) : 0; }
@@ -184,7 +181,7 @@ void single_segment(GemmArgs &g, const uint16_t *A, int64_t depth, int64_t pitch
 // dX [M, K] = rowf * (A . W): in one launch, or by split sums and a second;
 // acc: fp32 sums carried between pieces (null: one piece)
 hipError_t gradient_product(GemmArgs &g, bool bf16, float *part, float *acc, bool first, bool last, uint16_t *dX,
-                            const float *rowf, hipStream_t s)
+                            const RowFactor &rowf, hipStream_t s)
 {
     const int64_t M = g.M, K = g.N;
     g.splits = gemm_splits(M, K, g.step0[g.segs]);
@@ -264,7 +261,7 @@ int64_t few_part_floats(int64_t M, int64_t K, int64_t steps)
 }
 
 hipError_t few_rows_gradient(SkinnyGradArgs &a, bool bf16, int nbits, int group_size, int64_t M, int64_t K, float *part,
-                             uint16_t *dX, const float *rowf, hipStream_t s)
+                             uint16_t *dX, const RowFactor &rowf, hipStream_t s)
 {
     a.M = M;
     a.K = K;
@@ -401,7 +398,7 @@ int64_t loss_grad_piece(int64_t m, int64_t K, int64_t N)
 
 struct LossGradLayout {
     uint16_t *W, *dL, *X;
-    float *rowf, *part, *acc;
+    float *part, *acc;
     int64_t bytes, piece, ldl;
     LossGradLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
@@ -413,7 +410,6 @@ struct LossGradLayout {
             piece = N;
             ldl = round_up(N, kStep);
             dL = c.take<uint16_t>(M * ldl);
-            rowf = c.take<float>(M);
             part = c.take_some<float>(few_part_floats(M, K, grad_steps(&N, 1)));
             bytes = c.at;
             return;
@@ -423,7 +419,6 @@ struct LossGradLayout {
         W = c.take<uint16_t>(round_up(piece, kStep) * pitch_for(K));
         dL = c.take<uint16_t>(mc * ldl);
         X = c.take_some<uint16_t>(pad_values(mc, K));
-        rowf = c.take<float>(mc);
         int64_t f = part_floats(M, K, (piece + kStep - 1) / kStep);
         const int64_t rest = N % piece;
         if (rest) {
@@ -495,12 +490,12 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
         f.g.act = act;
         return launch_skinny(nbits, bf16, f, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
     }
-    if (whole_steps(X, M, K, l.X, s) != hipSuccess)
-        return HQQ_EHIP;
-    UnpackArgs a = unpack_pair(*gate, *up, N, K, nbits, group_size);
-    a.W = l.W;
+    UnpackArgs a = unpack_args(l.W, K, nbits, group_size);
+    a.pair = 1;
+    unpack_rows(a, gate->packed, gate->scale, gate->zero, 0, N, 0);
+    unpack_rows(a, up->packed, up->scale, up->zero, 0, N, 0);
     GemmArgs g{};
-    single_segment(g, X, round_up(K, kStep), whole_pitch(K));
+    single_segment(g, whole_steps(a, X, M, K, l.X), round_up(K, kStep), whole_pitch(K));
     g.B = l.W;
     g.ldb = a.ldw;
     g.M = (int32_t)M;
@@ -561,22 +556,24 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         add_grad(b, gate->packed, gate->scale, gate->zero, l.dGU, ldg, N);
         add_grad(b, up->packed, up->scale, up->zero, l.dGU + Np, ldg, N);
         return launch_skinny(nbits, bf16, f, s) == hipSuccess &&
-                       few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, bf16 ? nullptr : l.inv, s) ==
+                       few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, RowFactor{bf16 ? nullptr : l.inv}, s) ==
                            hipSuccess
                    ? HQQ_OK
                    : HQQ_EHIP;
     }
-    UnpackArgs a = unpack_pair(*gate, *up, N, K, nbits, group_size);
-    a.W = l.W;
-    if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
-        return HQQ_EHIP;
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
         // fp16: dG and dU relative to the row's largest |dY| (bf16 has fp32's range)
         if (!bf16 && launch_row_scale(dY + m0 * N, m, N, l.scale, l.inv, s) != hipSuccess)
             return HQQ_EHIP;
-        const uint16_t *x = X + m0 * K;
-        if (whole_steps(x, m, K, l.X, s) != hipSuccess)
+        UnpackArgs a = unpack_args(l.W, K, nbits, group_size);
+        a.pair = 1;
+        if (m0 == 0) {
+            unpack_rows(a, gate->packed, gate->scale, gate->zero, 0, N, 0);
+            unpack_rows(a, up->packed, up->scale, up->zero, 0, N, 0);
+        }
+        const uint16_t *x = whole_steps(a, X + m0 * K, m, K, l.X);
+        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
             return HQQ_EHIP;
         GemmArgs g{};
         single_segment(g, x, round_up(K, kStep), whole_pitch(K));
@@ -598,7 +595,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         p.M = (int32_t)m;
         p.N = (int32_t)K;
         if (launch_gemm(kOutGatedGrad, bf16, g, s) != hipSuccess ||
-            gradient_product(p, bf16, l.part, nullptr, true, true, dX + m0 * K, bf16 ? nullptr : l.inv, s) != hipSuccess)
+            gradient_product(p, bf16, l.part, nullptr, true, true, dX + m0 * K, RowFactor{bf16 ? nullptr : l.inv}, s) != hipSuccess)
             return HQQ_EHIP;
     }
     return HQQ_OK;
@@ -644,33 +641,30 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
         SkinnyGradArgs b{};
         for (int i = 0; i < count; ++i)
             add_grad(b, ws[i].packed, ws[i].scale, ws[i].zero, ws[i].dY, n[i], n[i]);
-        return few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, nullptr, s) == hipSuccess ? HQQ_OK
+        return few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, RowFactor{}, s) == hipSuccess ? HQQ_OK
                                                                                                         : HQQ_EHIP;
-    }
-    int64_t row = 0;
-    for (int i = 0; i < count; ++i) {
-        UnpackArgs a = unpack_args(hqq_weight{ws[i].packed, ws[i].scale, ws[i].zero}, 0, n[i], K, nbits, group_size);
-        a.W = l.W + row * a.ldw;
-        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
-            return HQQ_EHIP;
-        row += round_up(n[i], kStep);
     }
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
+        UnpackArgs a = unpack_args(l.W, K, nbits, group_size);
         GemmArgs g{};
         g.segs = count;
+        int64_t row = 0;
         for (int i = 0; i < count; ++i) {
-            g.A[i] = ws[i].dY + m0 * n[i];
+            if (m0 == 0)
+                unpack_rows(a, ws[i].packed, ws[i].scale, ws[i].zero, 0, n[i], row);
+            row += round_up(n[i], kStep);
+            g.A[i] = whole_steps(a, ws[i].dY + m0 * n[i], m, n[i], l.pad[i]);
             g.lda[i] = whole_pitch(n[i]);
-            if (whole_steps(g.A[i], m, n[i], l.pad[i], s) != hipSuccess)
-                return HQQ_EHIP;
-            g.step0[i + 1] = g.step0[i] + (int32_t)((n[i] + kStep - 1) / kStep);
+            g.step0[i + 1] = (int32_t)(row / kStep);
         }
+        if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess)
+            return HQQ_EHIP;
         g.B = l.W;
         g.ldb = pitch_for(K);
         g.M = (int32_t)m;
         g.N = (int32_t)K;
-        if (gradient_product(g, bf16, l.part, nullptr, true, true, dX + m0 * K, nullptr, s) != hipSuccess)
+        if (gradient_product(g, bf16, l.part, nullptr, true, true, dX + m0 * K, RowFactor{}, s) != hipSuccess)
             return HQQ_EHIP;
     }
     return HQQ_OK;
@@ -715,13 +709,13 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
         const LossArgs e{l.stats, l.pitch, l.pitch, M, N, l.tlogit, targets, loss, lse};
         return launch_skinny(nbits, bf16, f, s) == hipSuccess && launch_loss(e, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
     }
-    if (whole_steps(X, M, K, l.X, s) != hipSuccess)
-        return HQQ_EHIP;
     int64_t blocks = 0;
     for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
         const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
-        UnpackArgs a = unpack_args(*head, n0, n, K, nbits, group_size);
-        a.W = l.W;
+        UnpackArgs a = unpack_args(l.W, K, nbits, group_size);
+        unpack_rows(a, head->packed, head->scale, head->zero, n0, n, 0);
+        if (n0 == 0)
+            X = whole_steps(a, X, M, K, l.X);
         GemmArgs g{};
         single_segment(g, X, round_up(K, kStep), whole_pitch(K));
         g.B = l.W;
@@ -783,24 +777,23 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
         f.g.fill = l.ldl;
         SkinnyGradArgs b{};
         add_grad(b, head->packed, head->scale, head->zero, l.dL, l.ldl, N);
-        return launch_loss_factor(dloss, targets, M, N, unit, l.rowf, s) == hipSuccess &&
-                       launch_skinny(nbits, bf16, f, s) == hipSuccess &&
-                       few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX, l.rowf, s) == hipSuccess
+        return launch_skinny(nbits, bf16, f, s) == hipSuccess &&
+                       few_rows_gradient(b, bf16, nbits, group_size, M, K, l.part, dX,
+                                         RowFactor{nullptr, dloss, targets, N, unit}, s) == hipSuccess
                    ? HQQ_OK
                    : HQQ_EHIP;
     }
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
-        if (launch_loss_factor(dloss + m0, targets + m0, m, N, unit, l.rowf, s) != hipSuccess)
-            return HQQ_EHIP;
         const uint16_t *x = X + m0 * K;
-        if (whole_steps(x, m, K, l.X, s) != hipSuccess)
-            return HQQ_EHIP;
+        const RowFactor rowf{nullptr, dloss + m0, targets + m0, N, unit};
         for (int64_t n0 = 0; n0 < N; n0 += l.piece) {
             const int64_t n = N - n0 < l.piece ? N - n0 : l.piece;
             const int64_t fill = round_up(n, kStep), ldl = pitch_for(n);
-            UnpackArgs a = unpack_args(*head, n0, n, K, nbits, group_size);
-            a.W = l.W;
+            UnpackArgs a = unpack_args(l.W, K, nbits, group_size);
+            unpack_rows(a, head->packed, head->scale, head->zero, n0, n, 0);
+            if (n0 == 0)
+                x = whole_steps(a, x, m, K, l.X);
             GemmArgs g{};
             single_segment(g, x, round_up(K, kStep), whole_pitch(K));
             g.B = l.W;
@@ -822,7 +815,7 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
             p.N = (int32_t)K;
             if (launch_unpack_weight(nbits, bf16, a, s) != hipSuccess ||
                 launch_gemm(kOutSoftGrad, bf16, g, s) != hipSuccess ||
-                gradient_product(p, bf16, l.part, l.acc, n0 == 0, n0 + n == N, dX + m0 * K, l.rowf, s) != hipSuccess)
+                gradient_product(p, bf16, l.part, l.acc, n0 == 0, n0 + n == N, dX + m0 * K, rowf, s) != hipSuccess)
                 return HQQ_EHIP;
         }
     }

@@ -52,6 +52,16 @@ __device__ __forceinline__ float act_value(float g, float &d)
     }
 }
 
+__device__ __forceinline__ float row_factor(const RowFactor &r, int64_t m)
+{
+    if (r.f)
+        return r.f[m];
+    if (!r.dloss)
+        return 1.0f;
+    const int64_t t = r.targets[m];
+    return t >= 0 && t < r.N ? r.dloss[m] * r.mul : 0.0f;
+}
+
 __device__ __forceinline__ float from16(uint16_t b, bool bf)
 {
     if (bf)

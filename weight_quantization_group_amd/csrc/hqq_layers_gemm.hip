@@ -127,7 +127,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
             int64_t at = -1;
             bool keep = true;
             if constexpr (OUT == kOutStore) {
-                f = g.rowf ? g.rowf[mc] : 1.0f;
+                f = row_factor(g.rowf, mc);
             } else {
                 const int64_t tgt = g.targets[mc];
                 keep = tgt >= 0 && tgt < g.Nall;

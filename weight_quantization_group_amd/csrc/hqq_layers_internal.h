@@ -9,19 +9,34 @@ namespace hqq {
 
 constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// Dequantization of n rows of a weight into the workspace: W [rows, K] row-major, its
-// columns K .. round_up(K, 64) - 1 and its rows past n zeroed.  One weight fills
-// round_up(n, 64) rows; a gated pair 2 round_up(n, 32), 32 of gate and 32 of up in turn.
+// Dequantization into the workspace, before a tiled product: weight i's n[i] rows to
+// W [rows, K] row-major from row row0[i] on, columns K .. round_up(K, 64) - 1 zeroed, and
+// its rows past n[i] up to round_up(n[i], 64) zeroed.  pair: two weights of one n, 32 rows
+// of the first (gate) and 32 of the second (up) in turn, to 2 round_up(n, 32) rows.  In the
+// same launch, matrices whose rows end inside a 64-wide step are copied with zeros up
+// to its end.
+constexpr int kMaxSegs = HQQ_MAX_GRADS;
+
+struct PadJob {
+    const uint16_t *src;      // [M, N]
+    uint16_t *dst;            // [M, round_up(N, 64)], row pitch ldd
+    int64_t M, N, ldd;
+};
+
 struct UnpackArgs {
-    int count;                // 1, or 2: a gated pair (gate, up) of one shape and format
-    const uint32_t *packed[2];   // of the first row
-    const float *scale[2], *zero[2];
-    int64_t n, K;
+    int count, pair;
+    const uint32_t *packed[kMaxSegs];   // of the first row
+    const float *scale[kMaxSegs], *zero[kMaxSegs];
+    int64_t n[kMaxSegs], row0[kMaxSegs];
+    int64_t K;
     int64_t wpr, gpl;         // words and groups per row
     int gshift;               // log2 of the group size
     uint16_t *W;
     int64_t ldw;
+    int pads;
+    PadJob pad[kMaxSegs];
 };
+static_assert(sizeof(UnpackArgs) <= 4096, "kernel arguments within 4 KiB");
 hipError_t launch_unpack_weight(int nbits, bool bf16, const UnpackArgs &a, hipStream_t s);
 
 // The matrix product C [M, N] of 16-bit matrices with fp32 sums, and what becomes of C:
@@ -35,7 +50,15 @@ constexpr int kStep = 64;            // depth of a step
 // channels (measured at pitches of 8 KB: 330 us without, 296 us with, for 2048 x
 // 22016 x 4096).
 constexpr int64_t pitch_for(int64_t depth) { return round_up(depth, kStep) + 64; }
-constexpr int kMaxSegs = HQQ_MAX_GRADS;
+
+// The factor of a row of the results: f[m] if given; else, if given, a loss's dloss[m]
+// times mul where targets[m] is one of N classes, and 0 elsewhere; else 1.
+struct RowFactor {
+    const float *f, *dloss;
+    const int64_t *targets;
+    int64_t N;
+    float mul;
+};
 
 enum GemmOut {
     kOutStore,      // out16 = round(rowf * C)
@@ -60,7 +83,7 @@ struct GemmArgs {
     uint16_t *out;                   // [M, ldo]
     int64_t ldo;
     float *part;                     // kOutPart: [splits, M, N]
-    const float *rowf;               // kOutStore: per-row factor or null
+    RowFactor rowf;                  // kOutStore
     int act;
     const uint16_t *dY;              // kOutGatedGrad: [M, N]
     const float *rscale;             // per-row scale of dG and dU, or null
@@ -106,7 +129,7 @@ struct SkinnyGradArgs {
     int gshift, splits;
     float *part;
     uint16_t *out;
-    const float *rowf;
+    RowFactor rowf;
 };
 hipError_t launch_skinny_grad(int nbits, bool bf16, const SkinnyGradArgs &a, hipStream_t s);
 int skinny_grad_splits(int64_t M, int64_t K, int64_t steps);
@@ -120,7 +143,7 @@ struct ReduceArgs {
     const float *acc_in;
     float *acc_out;
     uint16_t *out;
-    const float *rowf;
+    RowFactor rowf;
 };
 hipError_t launch_reduce(bool bf16, const ReduceArgs &a, hipStream_t s);
 
@@ -134,13 +157,8 @@ struct LossArgs {
 };
 hipError_t launch_loss(const LossArgs &a, hipStream_t s);
 
-// rowf[m] = dloss[m] * mul, 0 for ignored rows
-hipError_t launch_loss_factor(const float *dloss, const int64_t *targets, int64_t M, int64_t N, float mul,
-                              float *rowf, hipStream_t s);
 // fp16 rows [M, N]: scale[m] = the power of two that brings max |row| to
 // [2^-7, 2^-6), inv[m] = 1 / scale[m] (1 for rows that are zero or not finite)
 hipError_t launch_row_scale(const uint16_t *rows, int64_t M, int64_t N, float *scale, float *inv, hipStream_t s);
-// dst [M, ldd] = src [M, N], columns N .. ldd - 1 zeroed
-hipError_t launch_pad_rows(const uint16_t *src, int64_t M, int64_t N, uint16_t *dst, int64_t ldd, hipStream_t s);
 
 }  // namespace hqq

@@ -1,7 +1,6 @@
 // hqq_layers_rows.hip -- the small row-wise kernels around the layers' products:
-// joining split sums and the softmax blocks, row factors, padded copies.
-#include "hqq_layers_internal.h"
-#include "hqq_linear_dev.h"
+// joining split sums and the softmax blocks, scales of rows.
+#include "hqq_layers_epilogue.h"
 
 namespace hqq {
 namespace {
@@ -26,7 +25,7 @@ __global__ __launch_bounds__(kRowsBlock) void reduce_kernel(ReduceArgs a)
         *reinterpret_cast<float4v *>(a.acc_out + i) = v;
         return;
     }
-    const float f = a.rowf ? a.rowf[i / a.N] : 1.0f;
+    const float f = row_factor(a.rowf, i / a.N);
     *reinterpret_cast<uint2 *>(a.out + i) = uint2{out2<BF>(v[0] * f, v[1] * f), out2<BF>(v[2] * f, v[3] * f)};
 }
 
@@ -74,14 +73,6 @@ __global__ __launch_bounds__(kRowsBlock) void loss_kernel(LossArgs a)
     a.lse[m] = (d > 0.0f ? others : lt) + tail;
 }
 
-__global__ __launch_bounds__(kRowsBlock) void loss_factor_kernel(const float *dloss, const int64_t *targets, int64_t M,
-                                                                 int64_t N, float mul, float *rowf)
-{
-    const int64_t m = (int64_t)blockIdx.x * kRowsBlock + threadIdx.x;
-    if (m < M)
-        rowf[m] = targets[m] >= 0 && targets[m] < N ? dloss[m] * mul : 0.0f;
-}
-
 // one workgroup per row; fp16 magnitudes compare as their bits
 __global__ __launch_bounds__(kRowsBlock) void row_scale_kernel(const uint16_t *rows, int64_t N, float *scale, float *inv)
 {
@@ -118,23 +109,6 @@ __global__ __launch_bounds__(kRowsBlock) void row_scale_kernel(const uint16_t *r
     }
 }
 
-__global__ __launch_bounds__(kRowsBlock) void pad_rows_kernel(const uint16_t *src, int64_t M, int64_t N, uint16_t *dst,
-                                                              int64_t ldd)
-{
-    const int64_t i = ((int64_t)blockIdx.x * kRowsBlock + threadIdx.x) * 8;
-    if (i >= M * ldd)
-        return;
-    const int64_t m = i / ldd, n = i - m * ldd;
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = n + 2 * j < N ? src[m * N + n + 2 * j] : 0u;
-        const uint32_t hi = n + 2 * j + 1 < N ? src[m * N + n + 2 * j + 1] : 0u;
-        w[j] = lo | hi << 16;
-    }
-    *reinterpret_cast<uint4 *>(dst + i) = uint4{w[0], w[1], w[2], w[3]};
-}
-
 unsigned blocks_for(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
 
 }  // namespace
@@ -155,24 +129,9 @@ hipError_t launch_loss(const LossArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_loss_factor(const float *dloss, const int64_t *targets, int64_t M, int64_t N, float mul, float *rowf,
-                              hipStream_t s)
-{
-    hipLaunchKernelGGL(loss_factor_kernel, dim3(blocks_for(M, kRowsBlock)), dim3(kRowsBlock), 0, s, dloss, targets, M, N,
-                       mul, rowf);
-    return hipGetLastError();
-}
-
 hipError_t launch_row_scale(const uint16_t *rows, int64_t M, int64_t N, float *scale, float *inv, hipStream_t s)
 {
     hipLaunchKernelGGL(row_scale_kernel, dim3((unsigned)M), dim3(kRowsBlock), 0, s, rows, N, scale, inv);
-    return hipGetLastError();
-}
-
-hipError_t launch_pad_rows(const uint16_t *src, int64_t M, int64_t N, uint16_t *dst, int64_t ldd, hipStream_t s)
-{
-    hipLaunchKernelGGL(pad_rows_kernel, dim3(blocks_for(M * ldd, 8 * kRowsBlock)), dim3(kRowsBlock), 0, s, src, M, N, dst,
-                       ldd);
     return hipGetLastError();
 }
 

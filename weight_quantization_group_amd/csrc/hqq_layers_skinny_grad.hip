@@ -162,7 +162,7 @@ skinny_grad_kernel(SkinnyGradArgs a)
                 for (int t = 0; t < 2; ++t)
                     o[t] = float4v{acc[u][4 * t][r], acc[u][4 * t + 1][r], acc[u][4 * t + 2][r], acc[u][4 * t + 3][r]};
             } else {
-                const float f = a.rowf ? a.rowf[m] : 1.0f;
+                const float f = row_factor(a.rowf, m);
                 *reinterpret_cast<uint4 *>(a.out + (int64_t)m * a.K + kc) =
                     uint4{out2<BF>(acc[u][0][r] * f, acc[u][1][r] * f), out2<BF>(acc[u][2][r] * f, acc[u][3][r] * f),
                           out2<BF>(acc[u][4][r] * f, acc[u][5][r] * f), out2<BF>(acc[u][6][r] * f, acc[u][7][r] * f)};
