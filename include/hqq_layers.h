@@ -33,7 +33,7 @@
  * W_hat is unpacked into the workspace and a tiled product runs on it.  The
  * choice goes by sizes and format, and both stay within the same bounds.  The
  * environment variable HQQ_LAYERS_PATH=codes or =tiled, read at each call and by
- * the *_workspace functions, forces one.
+ * the *_workspace functions, forces one (the codes up to 256 rows).
  */
 #ifndef HQQ_LAYERS_H
 #define HQQ_LAYERS_H

@@ -172,6 +172,18 @@ def test_workspace_sizes(w):
     assert w.hqq_linear_cross_entropy_backward_workspace(M, K, N, 4, 64) < logits / 16
 
 
+def test_forced_route_keeps_to_its_rows(w, monkeypatch):
+    """HQQ_LAYERS_PATH=codes holds up to 256 rows; beyond, the tiled route's workspace is asked for."""
+    def need(M):
+        return w.hqq_linear_gated_workspace(M, 1056, 2753, 2, 32)
+
+    monkeypatch.setenv("HQQ_LAYERS_PATH", "codes")
+    assert need(256) == 0 and need(1) == 0
+    codes = need(257), need(1 << 20)
+    monkeypatch.setenv("HQQ_LAYERS_PATH", "tiled")
+    assert need(1) > 0 and codes == (need(257), need(1 << 20))
+
+
 def test_binding_refuses_host_tensors(w):
     import torch
 

@@ -44,18 +44,24 @@ int check_sizes(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
 
 // Whether a product runs straight from the codes (which every 32 rows dequantize
 // anew) or W_hat is unpacked for the tiled product.  n: all rows of its weights.
-// Measured crossovers on MI355X (bf16 or fp16, 512 x 512 to 4096 x 11008): gated
-// block at 4096 x 11008 4-bit g64, 64 rows 72 against 91 us, 96 rows 103 against 97;
-// 2048 x 5632 8-bit 32 rows 24 against 28, 64 rows 33 against 28; one weight backward,
-// 64 rows 41 against 48, 96 rows 63 against 56; the head at 1024 x 32003 4-bit, 32 rows
-// 32 against 35, 64 rows 51 against 35, and with 2-bit groups of 16 (a reciprocal per
-// 8 weights) 4 rows 31 against 35, 16 rows 38 against 35.  Small weights leave the CUs
-// room for the row blocks: 512 x 512, 192 rows 8 against 10.  HQQ_LAYERS_PATH=codes or
-// =tiled in the environment, read at each call, forces one (tests run both).
-enum Product { kPair, kBackward, kHead };
+// Measured crossovers on MI355X (codes against unpacked, us): gated block at 4096 x
+// 11008 4-bit g64, 64 rows 71 against 92, 96 rows 102 against 99, its backward 32 rows
+// 81 against 127, 48 rows 131 against 128; at 2048 x 5632 8-bit 32 rows 25 against 28,
+// 48 rows 30 against 28, backward 16 rows 35 against 43, 32 rows 46 against 44; one
+// weight backward at 4096 x 11008, 64 rows 40 against 45, 96 rows 61 against 47; the
+// head at 1024 x 32003 4-bit, 32 rows 32 against 35, 48 rows 46 against 36, with 2-bit
+// groups of 16 (a reciprocal per 8 weights) 16 rows 38 against 36, its backward 4-bit
+// 16 rows 41 against 48, 32 rows 51 against 49.  Small weights leave the CUs room for
+// the row blocks: 512 x 512, 128 rows 7 against 10, backward 20 against 22.
+// HQQ_LAYERS_PATH=codes or =tiled in the environment, read at each call, forces one
+// (tests run both), the codes up to the 256 rows beyond which the rule never takes
+// them: their kernels address the activations by 32-bit offsets.
+enum Product { kPair, kPairGrad, kBackward, kHead, kHeadGrad };
 
 bool straight(Product what, int64_t M, int64_t K, int64_t n, int nbits, int group_size)
 {
+    if (M > 256)
+        return false;
     if (const char *e = getenv("HQQ_LAYERS_PATH")) {
         if (strcmp(e, "codes") == 0)
             return true;
@@ -63,8 +69,16 @@ bool straight(Product what, int64_t M, int64_t K, int64_t n, int nbits, int grou
             return false;
     }
     const bool tables = nbits == 4 && group_size >= 32;
-    const int64_t rows = what == kBackward ? 64 : what == kPair ? (tables ? 64 : 32) : group_size >= 32 ? 32 : 8;
-    return M <= rows || (M <= 256 && (M + 31) / 32 * K * n <= (tables ? 16 : 6) * 1000000);
+    const bool fine = group_size < 32;
+    int64_t rows = 64;
+    switch (what) {
+    case kPair: rows = tables ? 64 : 32; break;
+    case kPairGrad: rows = tables ? 32 : 16; break;
+    case kBackward: break;
+    case kHead: rows = fine ? 8 : 32; break;
+    case kHeadGrad: rows = fine ? 8 : 16; break;
+    }
+    return M <= rows || (M + 31) / 32 * K * n <= (tables ? 16 : 6) * 1000000;
 }
 
 int check_batch(int64_t M, int64_t K, const int64_t *n, int count, int nbits, int group_size)
@@ -512,7 +526,7 @@ int64_t hqq_linear_gated_backward_workspace(int64_t M, int64_t K, int64_t N, int
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return GatedGradLayout(nullptr, M, K, N, straight(kPair, M, K, 2 * N, nbits, group_size)).bytes;
+    return GatedGradLayout(nullptr, M, K, N, straight(kPairGrad, M, K, 2 * N, nbits, group_size)).bytes;
 }
 
 int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate,
@@ -528,7 +542,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     if (!gate || !up || !weight_ok(gate->packed, gate->scale, gate->zero) || !weight_ok(up->packed, up->scale, up->zero) ||
         !aligned(X, 16) || !aligned(dY, 16) || !aligned(dX, 16))
         return HQQ_EINVAL_PTR;
-    const bool few = straight(kPair, M, K, 2 * N, nbits, group_size);
+    const bool few = straight(kPairGrad, M, K, 2 * N, nbits, group_size);
     const GatedGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
@@ -740,7 +754,7 @@ int64_t hqq_linear_cross_entropy_backward_workspace(int64_t M, int64_t K, int64_
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return LossGradLayout(nullptr, M, K, N, straight(kHead, M, K, N, nbits, group_size)).bytes;
+    return LossGradLayout(nullptr, M, K, N, straight(kHeadGrad, M, K, N, nbits, group_size)).bytes;
 }
 
 int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *head,
@@ -755,7 +769,7 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
     if (!head || !weight_ok(head->packed, head->scale, head->zero) || !aligned(X, 16) || !aligned(dX, 16) ||
         !aligned(targets, 8) || !aligned(dloss, 4) || !aligned(lse, 4))
         return HQQ_EINVAL_PTR;
-    const bool few = straight(kHead, M, K, N, nbits, group_size);
+    const bool few = straight(kHeadGrad, M, K, N, nbits, group_size);
     const LossGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
