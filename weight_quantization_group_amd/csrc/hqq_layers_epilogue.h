@@ -19,6 +19,35 @@ __device__ __forceinline__ double reciprocal(float s)
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
+// the value of lane I of the caller's eight neighbours (lanes 8 i .. 8 i + 7)
+template <int I>
+__device__ __forceinline__ float from_eighth(float x)
+{
+    return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x18 | I << 5));
+}
+
+template <int I>
+__device__ __forceinline__ double from_eighth(double x)
+{
+    uint32_t w[2];
+    __builtin_memcpy(w, &x, 8);
+    w[0] = (uint32_t)__builtin_amdgcn_ds_swizzle((int)w[0], 0x18 | I << 5);
+    w[1] = (uint32_t)__builtin_amdgcn_ds_swizzle((int)w[1], 0x18 | I << 5);
+    __builtin_memcpy(&x, w, 8);
+    return x;
+}
+
+// z[i] and R[i] = 1 / s of row i: eight neighbouring lanes work on the same 8 rows and in
+// one group of each, lane i of them holds row i's scale and zero
+__device__ __forceinline__ void share_meta(float s, float z, double (&R)[8], float (&Z)[8])
+{
+    const double r = reciprocal(s);
+    R[0] = from_eighth<0>(r); R[1] = from_eighth<1>(r); R[2] = from_eighth<2>(r); R[3] = from_eighth<3>(r);
+    R[4] = from_eighth<4>(r); R[5] = from_eighth<5>(r); R[6] = from_eighth<6>(r); R[7] = from_eighth<7>(r);
+    Z[0] = from_eighth<0>(z); Z[1] = from_eighth<1>(z); Z[2] = from_eighth<2>(z); Z[3] = from_eighth<3>(z);
+    Z[4] = from_eighth<4>(z); Z[5] = from_eighth<5>(z); Z[6] = from_eighth<6>(z); Z[7] = from_eighth<7>(z);
+}
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // 2^x and 1 / x to about an ulp of fp32 (v_exp_f32, v_rcp_f32): the results are

@@ -83,9 +83,95 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
     }
 }
 
+// X where it stays in global memory: a wave fetches its step's rows in two halves (of
+// each lane quarter's 64 k, the first and the last 32), 64 bytes in a row per four
+// lanes, and turns them into operands through 4 MT KiB of LDS of its own.  (An operand
+// fetched directly touches a cache line per lane, and what was fetched is gone from the
+// L1 cache by the next operand: 59 against 39 us for the gated block of 24 rows through
+// 4096 x 11008 at 8 bits.)  Run j of quarter q of row r lies at 64 j + 16 q + (r ^ (j + 4 q))
+// of its 16-row block: the writes of 8 neighbouring lanes, and the reads, fall into
+// different banks.
+template <int MT>
+struct XHalf {
+    uint4 x[4 * MT];
+};
+
+template <bool KT, int MT>
+__device__ __forceinline__ void load_half(XHalf<MT> &b, const LinearArgs &a, uint32_t k, uint32_t row0, int rows, int lane)
+{
+    // k: of this lane's run (lane % 16); past K any run, cleared when it is stored
+    const uint32_t kk = KT && k >= (uint32_t)a.K ? (uint32_t)a.K - 8 : k;
+#pragma unroll
+    for (int t = 0; t < 4 * MT; ++t) {
+        const int r = lane / 16 + 4 * t < rows ? lane / 16 + 4 * t : rows - 1;
+        b.x[t] = *at<uint4>(a.X, 2 * ((row0 + (uint32_t)r) * (uint32_t)a.K + kk));
+    }
+}
+
+template <bool KT, int MT>
+__device__ __forceinline__ void store_half(const XHalf<MT> &b, uint4 *xs, uint32_t in, int lane)
+{
+    const int q = (lane >> 2) & 3, j = lane & 3;
+#pragma unroll
+    for (int t = 0; t < 4 * MT; ++t) {
+        const int r = lane / 16 + 4 * (t & 3);
+        uint4 v = run_order(b.x[t]);
+        if constexpr (KT)
+            v = and4(v, in);
+        xs[(t >> 2) * 256 + 64 * j + 16 * q + (r ^ (j + 4 * q))] = v;
+    }
+}
+
+// LDS of one wave: written by some lanes and read by others
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// acc += the operands of half H of a step
+template <int H, bool KT, bool BF, int NM, int NB, int MT, int GPC>
+__device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], const uint4 *xs, uint32_t km, int lane,
+                                             float4v (&acc)[NM][MT])
+{
+    Tab4 tab[NM];
+    if constexpr (NB == 4 && GPC < 8) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+            tab[m] = make_tab4<BF>(b[m].s[GPC == 1 ? 0 : H], b[m].z[GPC == 1 ? 0 : H]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint4 A[MT];
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+            A[u] = xs[u * 256 + 64 * j + (lane & 48) + ((lane & 15) ^ (j + 4 * (lane >> 4)))];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            uint4 B;
+            if constexpr (NB == 4 && GPC < 8)
+                B = lookup4(tab[m], b[m].w[4 * H + j]);
+            else
+                B = dequant_run<NB, GPC, BF>(b[m].w, 4 * H + j, b[m].s, b[m].z);
+            if constexpr (KT)
+                B = and4(B, km);
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+                acc[m][u] = mfma<BF>(A[u], B, acc[m][u]);
+        }
+    }
+}
+
+// Waves per SIMD that leave the registers for this step's codes and scales and the next's
+constexpr int waves_per_simd(int nm, int nb, int mt, int gpc)
+{
+    const int regs = nm * (4 * nb + 4 * gpc) + 20 * mt + 4 * nm * mt;
+    return regs <= 72 ? 4 : regs <= 130 ? 3 : 2;
+}
+
 // NM: matrices (2: gate and up).  The workgroup's waves split K.
 template <int NM, bool KT, int NB, int MT, int GPC, bool XL, bool BF>
-__global__ __launch_bounds__(kSkinnyWaves * 64) __attribute__((amdgpu_waves_per_eu(MT * NM > 2 || !XL ? 3 : 4))) void
+__global__ __launch_bounds__(kSkinnyWaves * 64) __attribute__((amdgpu_waves_per_eu(waves_per_simd(NM, NB, MT, GPC)))) void
 skinny_kernel(SkinnyArgs s)
 {
     const int WPB = blockDim.x >> 6;
@@ -101,11 +187,11 @@ skinny_kernel(SkinnyArgs s)
     const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
     const int mrows = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT);
     const uint32_t xrow = K / 8 + 1;
-    uint32_t xr[MT];      // rows past M repeat the last; their outputs are not stored
+    uint32_t xr[MT];      // XL; rows past M repeat the last, their outputs are not stored
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
         const int r = 16 * u + lane16 < mrows ? 16 * u + lane16 : mrows - 1;
-        xr[u] = XL ? (uint32_t)r * xrow : (uint32_t)((m0 + r) * a.K);
+        xr[u] = (uint32_t)r * xrow;
     }
 
     const int n_steps = (int)((K + kStepK - 1) / kStepK);
@@ -136,23 +222,50 @@ skinny_kernel(SkinnyArgs s)
 #pragma unroll
         for (int u = 0; u < MT; ++u)
             acc[j][u] = float4v{0.f, 0.f, 0.f, 0.f};
-    XRuns<XL ? 1 : MT> xg;
-    for (int i = 0; i < my; ++i) {
-        const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
-        const uint32_t k0 = kbase(i) + kLaneK * grp;
-        const uint32_t km0 = k0 < K ? 0xffffffffu : 0u;
-        const uint32_t km1 = k0 + 32 < K ? 0xffffffffu : 0u;
-        if constexpr (!XL)
-            load_x(xg, a, c, xr);
-        StepBuf<NB, GPC> cur[NM];
+    if constexpr (XL) {
+        const XRuns<1> none{};
+        for (int i = 0; i < my; ++i) {
+            const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
+            const uint32_t k0 = kbase(i) + kLaneK * grp;
+            const uint32_t km0 = k0 < K ? 0xffffffffu : 0u;
+            const uint32_t km1 = k0 + 32 < K ? 0xffffffffu : 0u;
+            StepBuf<NB, GPC> cur[NM];
 #pragma unroll
-        for (int j = 0; j < NM; ++j)
-            cur[j] = buf[j];
-        if (i + 1 < my)
-            load(i + 1);
+            for (int j = 0; j < NM; ++j)
+                cur[j] = buf[j];
+            if (i + 1 < my)
+                load(i + 1);
 #pragma unroll
-        for (int j = 0; j < NM; ++j)
-            compute_step<KT, NB, MT, GPC, XL, BF>(cur[j], xg, km0, km1, lds, xr, c, acc[j]);
+            for (int j = 0; j < NM; ++j)
+                compute_step<KT, NB, MT, GPC, XL, BF>(cur[j], none, km0, km1, lds, xr, c, acc[j]);
+        }
+    } else {
+        uint4 *xs = lds + wave * (256 * MT);
+        // the run this lane fetches, of the first half of step i
+        auto krun = [&](int i) { return kbase(i) + kLaneK * (uint32_t)((lane >> 2) & 3) + 8 * (uint32_t)(lane & 3); };
+        XHalf<MT> x;
+        if (my > 0)
+            load_half<KT>(x, a, krun(0), (uint32_t)m0, mrows, lane);
+        for (int i = 0; i < my; ++i) {
+            const uint32_t k0 = kbase(i) + kLaneK * grp, kr = krun(i);
+            StepBuf<NB, GPC> cur[NM];
+#pragma unroll
+            for (int j = 0; j < NM; ++j)
+                cur[j] = buf[j];
+            store_half<KT>(x, xs, kr < K ? 0xffffffffu : 0u, lane);
+            wave_fence();
+            load_half<KT>(x, a, kr + 32, (uint32_t)m0, mrows, lane);
+            if (i + 1 < my)
+                load(i + 1);
+            compute_half<0, KT, BF>(cur, xs, k0 < K ? 0xffffffffu : 0u, lane, acc);
+            wave_fence();
+            store_half<KT>(x, xs, kr + 32 < K ? 0xffffffffu : 0u, lane);
+            wave_fence();
+            if (i + 1 < my)
+                load_half<KT>(x, a, krun(i + 1), (uint32_t)m0, mrows, lane);
+            compute_half<1, KT, BF>(cur, xs, k0 + 32 < K ? 0xffffffffu : 0u, lane, acc);
+            wave_fence();
+        }
     }
 
     // the waves' sums: red[wave][matrix][4 u + r][lane]
@@ -190,6 +303,9 @@ hipError_t launch_xl(const SkinnyArgs &s, dim3 grid, int waves, hipStream_t st)
     if (XL) {
         const size_t x = (size_t)skinny_x_bytes(a.M < 16 * MT ? a.M : 16 * MT, a.K);
         lds = x > lds ? x : lds;
+    } else {
+        const size_t x = (size_t)waves * MT * 4096;
+        lds = x > lds ? x : lds;
     }
     if (a.K % kStepK != 0)
         hipLaunchKernelGGL((skinny_kernel<NM, true, NB, MT, GPC, XL, BF>), grid, dim3(waves * 64), lds, st, s);
@@ -205,10 +321,13 @@ hipError_t launch_gpc(const SkinnyArgs &s, hipStream_t st)
     const dim3 grid((unsigned)((s.cols + 15) / 16), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
     const int64_t blocks = (int64_t)grid.x * grid.y, steps = (a.K + kStepK - 1) / kStepK;
     const int waves = blocks < 512 && steps > 4 ? 8 : 4;
-    // X in LDS where that leaves the CU 16 waves
-    const int64_t x = skinny_x_bytes(a.M < 16 * MT ? a.M : 16 * MT, a.K);
-    return x <= (waves == 8 ? 64 : 40) * 1024 ? launch_xl<NM, NB, MT, GPC, true, BF>(s, grid, waves, st)
-                                              : launch_xl<NM, NB, MT, GPC, false, BF>(s, grid, waves, st);
+    // X in LDS as a whole for up to 4 rows, where that leaves the CU 16 waves (4096 x 11008
+    // 4-bit pair, 2 rows 22 against 25 us in halves; 8 or 16 rows through 1024 x 2816 to
+    // 1024 x 32003 lose 2-12 % by it)
+    if constexpr (MT == 1)
+        if (a.M <= 4 && skinny_x_bytes(a.M, a.K) <= (waves == 8 ? 64 : 40) * 1024)
+            return launch_xl<NM, NB, MT, GPC, true, BF>(s, grid, waves, st);
+    return launch_xl<NM, NB, MT, GPC, false, BF>(s, grid, waves, st);
 }
 
 template <int NM, int NB, bool BF>

@@ -31,11 +31,12 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t *p)
         return uint2{*p, 0u};
 }
 
-// One step of a lane: the codes and meta of 8 rows, and its runs of A
-template <int NB, int MT>
+// One step of a lane: the codes and meta of 8 rows (SH: of one, to be shared), and its
+// runs of A
+template <int NB, int MT, bool SH>
 struct GradBuf {
     uint2 c[8];
-    float s[8], z[8];
+    float s[SH ? 1 : 8], z[SH ? 1 : 8];
     uint4 a[MT];
 };
 
@@ -55,8 +56,9 @@ __device__ __forceinline__ uint4 load_run(const uint16_t *row, int n, int N)
     return uint4{w[0], w[1], w[2], w[3]};
 }
 
-// AL: the runs of A are 16-byte aligned
-template <int NB, int MT, bool BF, bool AL>
+// AL: the runs of A are 16-byte aligned.  SH: groups of 64 or more, of which eight lanes
+// fetch, and take the reciprocal of, one each
+template <int NB, int MT, bool BF, bool AL, bool SH>
 __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 3))) void
 skinny_grad_kernel(SkinnyGradArgs a)
 {
@@ -73,7 +75,7 @@ skinny_grad_kernel(SkinnyGradArgs a)
     const int s0 = (int)blockIdx.y * per, s1 = s0 + per < steps ? s0 + per : steps;
 
     int j = 0;
-    GradBuf<NB, MT> buf;
+    GradBuf<NB, MT, SH> buf;
     auto load = [&](int s) {
         while (s >= a.step0[j + 1])
             ++j;
@@ -81,8 +83,12 @@ skinny_grad_kernel(SkinnyGradArgs a)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t n = (uint32_t)(n0 + i < N ? n0 + i : N - 1);
-            const uint32_t g = n * (uint32_t)a.gpl + ((uint32_t)kc >> a.gshift);
             buf.c[i] = load_codes<NB>(at<uint8_t>(a.packed[j], n * (uint32_t)a.wpr * 4u + (uint32_t)kc * NB / 8));
+        }
+#pragma unroll
+        for (int i = 0; i < (SH ? 1 : 8); ++i) {
+            const int nr = n0 + (SH ? l16 & 7 : i);
+            const uint32_t g = (uint32_t)(nr < N ? nr : N - 1) * (uint32_t)a.gpl + ((uint32_t)kc >> a.gshift);
             buf.s[i] = *at<float>(a.scale[j], 4 * g);
             buf.z[i] = *at<float>(a.zero[j], 4 * g);
         }
@@ -101,19 +107,29 @@ skinny_grad_kernel(SkinnyGradArgs a)
     if (s0 + wave < s1)
         load(s0 + wave);
     for (int s = s0 + wave; s < s1; s += kGradWaves) {
-        const GradBuf<NB, MT> cur = buf;
+        const GradBuf<NB, MT, SH> cur = buf;
         if (s + kGradWaves < s1)
             load(s + kGradWaves);
+        double R[8];
+        float Z[8];
+        if constexpr (SH) {
+            share_meta(cur.s[0], cur.z[0], R, Z);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                R[i] = reciprocal(cur.s[i]);
+                Z[i] = cur.z[i];
+            }
+        }
         uint32_t v[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const double R = reciprocal(cur.s[i]);
             const uint32_t w[2] = {cur.c[i].x, cur.c[i].y};
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int b0 = 2 * t * NB, b1 = b0 + NB;
-                v[i][t] = out2<BF>(wq((float)((w[b0 / 32] >> (b0 % 32)) & MASK), cur.z[i], R),
-                                   wq((float)((w[b1 / 32] >> (b1 % 32)) & MASK), cur.z[i], R));
+                v[i][t] = out2<BF>(wq((float)((w[b0 / 32] >> (b0 % 32)) & MASK), Z[i], R[i]),
+                                   wq((float)((w[b1 / 32] >> (b1 % 32)) & MASK), Z[i], R[i]));
             }
         }
 #pragma unroll
@@ -170,18 +186,24 @@ skinny_grad_kernel(SkinnyGradArgs a)
         }
 }
 
+template <int NB, int MT, bool BF, bool AL>
+hipError_t launch_sh(const SkinnyGradArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.K + 127) / 128), (unsigned)a.splits, (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+    if (a.gshift >= 6)
+        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, true>), grid, dim3(kGradWaves * 64), 0, s, a);
+    else
+        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, false>), grid, dim3(kGradWaves * 64), 0, s, a);
+    return hipGetLastError();
+}
+
 template <int NB, int MT, bool BF>
 hipError_t launch_al(const SkinnyGradArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.K + 127) / 128), (unsigned)a.splits, (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
     bool al = true;
     for (int i = 0; i < a.count; ++i)
         al = al && a.lda[i] % 8 == 0;
-    if (al)
-        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, true>), grid, dim3(kGradWaves * 64), 0, s, a);
-    else
-        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, false>), grid, dim3(kGradWaves * 64), 0, s, a);
-    return hipGetLastError();
+    return al ? launch_sh<NB, MT, BF, true>(a, s) : launch_sh<NB, MT, BF, false>(a, s);
 }
 
 template <int NB, bool BF>
