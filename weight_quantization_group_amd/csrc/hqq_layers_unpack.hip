@@ -8,8 +8,10 @@
 // and each row of W written, in stretches of 128 bytes or more.  Workgroups go to the
 // 8 XCDs in turn; each XCD gets a contiguous part of them, so that the lines of codes,
 // scales and zeros that neighbours along k share are fetched into one L2 only.  Bound
-// by the bytes written: 32 us for the 90 M weights of a 4096 x 11008 pair at 4 bits
-// while W stays in the last-level cache, 64 us otherwise.
+// by the bytes: 52 us for the 90 M weights of a 4096 x 11008 pair at 4 bits in groups
+// of 64, 180 MB written and 56 read, 4.5 TB/s where a large copy reaches 5.1.  In groups
+// of 64 or more (SH) the eight lanes of a row fetch and invert one scale for one row
+// each and share them; without that the same took 64 us.
 #include "hqq_layers_epilogue.h"
 
 namespace hqq {
@@ -45,7 +47,7 @@ __device__ void pad_rows(const PadJob &p)
 // multiple of 8.  (A flat grid with a table of first workgroups costs loads of arguments
 // that wait for one another: 3 us of a
 // 26 us gated block, 333 rows through 1056 x 2753.)
-template <int NB, bool BF>
+template <int NB, bool BF, bool SH>
 __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
 {
     constexpr uint32_t MASK = (1u << NB) - 1u;
@@ -71,11 +73,24 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
     if (n0 >= rows || run * 8 >= round_up(a.K, 64))
         return;
 
+    const int64_t r = k_in ? run : runs - 1;
+    double R[8];
+    float Z[8];
+    if constexpr (SH) {
+        const int64_t n = n0 + kl < an ? n0 + kl : an - 1, g = n * a.gpl + ((8 * r) >> a.gshift);
+        share_meta(a.scale[which][g], a.zero[which][g], R, Z);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t n = n0 + i < an ? n0 + i : an - 1, g = n * a.gpl + ((8 * r) >> a.gshift);
+            R[i] = reciprocal(a.scale[which][g]);
+            Z[i] = a.zero[which][g];
+        }
+    }
     uint32_t v[8][4];     // row i: 8 values of the run
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t n = n0 + i < an ? n0 + i : an - 1;
-        const int64_t r = k_in ? run : runs - 1;
         const uint8_t *p = reinterpret_cast<const uint8_t *>(a.packed[which] + n * a.wpr) + r * NB;
         uint32_t w[2] = {0, 0};
         if constexpr (NB == 8) {
@@ -89,15 +104,12 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
         } else {
             w[0] = *p;
         }
-        const int64_t g = n * a.gpl + ((8 * r) >> a.gshift);
-        const float z = a.zero[which][g];
-        const double R = reciprocal(a.scale[which][g]);
         const bool in = k_in && n0 + i < an;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int b0 = 2 * j * NB, b1 = (2 * j + 1) * NB;
-            const float x = wq((float)((w[b0 / 32] >> (b0 % 32)) & MASK), z, R);
-            const float y = wq((float)((w[b1 / 32] >> (b1 % 32)) & MASK), z, R);
+            const float x = wq((float)((w[b0 / 32] >> (b0 % 32)) & MASK), Z[i], R[i]);
+            const float y = wq((float)((w[b1 / 32] >> (b1 % 32)) & MASK), Z[i], R[i]);
             v[i][j] = in ? out2<BF>(x, y) : 0u;
         }
     }
@@ -119,7 +131,10 @@ hipError_t launch_nb(const UnpackArgs &a, hipStream_t s)
         n = a.n[i] > n ? a.n[i] : n;
     const int64_t squares = (a.K + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves) * ((n + 63) / 64);
     const dim3 grid((unsigned)round_up(squares, 8), (unsigned)(a.count + a.pads));
-    hipLaunchKernelGGL((unpack_kernel<NB, BF>), grid, dim3(kUnpackWaves * 64), 0, s, a);
+    if (a.gshift >= 6)
+        hipLaunchKernelGGL((unpack_kernel<NB, BF, true>), grid, dim3(kUnpackWaves * 64), 0, s, a);
+    else
+        hipLaunchKernelGGL((unpack_kernel<NB, BF, false>), grid, dim3(kUnpackWaves * 64), 0, s, a);
     return hipGetLastError();
 }
 
