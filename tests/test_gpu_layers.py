@@ -555,3 +555,75 @@ def test_shapes_are_checked(hq):
     with pytest.raises(hq.LayersError) as e:
         hq.hqq_linear_gated_backward(dY, X, w, w, N, 4, 64, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     assert e.value.status == -11
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("K,N", [(96, 200), (512, 4500)])
+def test_more_rows_than_a_chunk(hq, dtype, K, N):
+    """The backward passes go over 8192 rows at a time: the last chunk is a short one."""
+    M = 8192 + 70
+    gate, Wg = make_weight(1, N, K, 4, 32, dtype)
+    up, Wu = make_weight(2, N, K, 4, 32, dtype)
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+    t = torch.from_numpy(np.random.RandomState(5).randint(-1, N + 1, M)).cuda()
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 32)
+    dXb = hq.hqq_linear_batch_backward([dY, dY], [gate + (N,), up + (N,)], K, 4, 32)
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *gate, N, 4, 32)
+    dloss = normal(6, (M,), torch.float32)
+    dXl = hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *gate, N, 4, 32)
+    for part in (slice(0, 40), slice(8150, 8230), slice(M - 30, M)):
+        x, y = X[part], dY[part]
+        check_gated_backward(dX[part], y, x, Wg, Wu, "silu", f"rows {part.start}")
+        z = torch.zeros_like(y.double())
+        within(dXb[part], *grad_bound([y.double()] * 2, [z, z], [Wg, Wu], dtype), f"rows {part.start}")
+        check_loss(loss[part], lse[part], x, Wg, t[part], f"rows {part.start}")
+        check_loss_backward(dXl[part], dloss[part], x, Wg, t[part], lse[part], f"rows {part.start}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M", [4, 20, 90])
+def test_bad_rows_keep_to_themselves(hq, path, dtype, M):
+    """NaN and infinities in one row of an input change that row of the results only."""
+    K, N = 160, 333
+    gate, _ = make_weight(1, N, K, 4, 32, dtype)
+    up, _ = make_weight(2, N, K, 4, 32, dtype)
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+    t = torch.from_numpy(np.random.RandomState(5).randint(0, N, M)).cuda()
+    dloss = normal(6, (M,), torch.float32)
+
+    def step(X, dY, dloss):
+        loss, lse = hq.hqq_linear_cross_entropy(X, t, *gate, N, 4, 32)
+        return (hq.hqq_linear_gated(X, gate, up, N, 4, 32), hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 32),
+                hq.hqq_linear_backward(dY, *gate, K, 4, 32), loss, lse,
+                hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *gate, N, 4, 32))
+
+    clean = step(X, dY, dloss)
+    X2, dY2, dloss2 = X.clone(), dY.clone(), dloss.clone()
+    X2[M - 1], dY2[M - 1, 7], dloss2[M - 1] = math.nan, math.nan, math.nan
+    X2[1, 5], dY2[1, 9], dloss2[1] = math.inf, -math.inf, math.inf
+    good = [m for m in range(M) if m not in (1, M - 1)]
+    for a, b in zip(step(X2, dY2, dloss2), clean):
+        assert torch.equal(a[good], b[good])
+        assert not torch.isfinite(a[M - 1]).any() and not torch.isfinite(a[1]).all()
+
+
+def test_the_most_rows(hq):
+    """2^20 rows: outputs past 4 GB, and a loss over half a million classes whose tiles fill a grid."""
+    dtype, M, K, N = torch.bfloat16, 1 << 20, 64, 2500
+    X = torch.randn(M, K, device="cuda", dtype=dtype)
+    rows = torch.tensor([0, 1, 12345, M // 2, M - 2, M - 1], device="cuda")
+    gate, Wg = make_weight(1, N, K, 4, 64, dtype)
+    up, Wu = make_weight(2, N, K, 4, 64, dtype)
+    Y = hq.hqq_linear_gated(X, gate, up, N, 4, 64)
+    assert Y.numel() * 2 > 1 << 32
+    check_gated(Y[rows], X[rows], Wg, Wu, "silu")
+    dX = hq.hqq_linear_gated_backward(Y, X, gate, up, N, 4, 64)
+    check_gated_backward(dX[rows], Y[rows], X[rows], Wg, Wu, "silu")
+    del Y, dX
+    torch.cuda.empty_cache()
+    N = 1 << 19
+    head, W = make_weight(3, N, K, 1, 64, dtype)
+    t = torch.randint(0, N, (M,), device="cuda")
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 1, 64)
+    check_loss(loss[rows], lse[rows], X[rows], W, t[rows])
+    torch.cuda.empty_cache()

@@ -184,6 +184,12 @@ def test_forced_route_keeps_to_its_rows(w, monkeypatch):
     assert need(1) > 0 and codes == (need(257), need(1 << 20))
 
 
+def test_workspace_holds_no_sums_that_one_launch_keeps(w):
+    """A product that is not split takes no room for partial sums: W_hat alone, rows apart by K + 64."""
+    K = N = 4096
+    assert w.hqq_linear_batch_backward_workspace(4096, K, [N], 4, 64) == N * (K + 64) * 2
+
+
 def test_binding_refuses_host_tensors(w):
     import torch
 

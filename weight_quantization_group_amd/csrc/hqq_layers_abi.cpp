@@ -153,14 +153,16 @@ void unpack_rows(UnpackArgs &a, const uint32_t *packed, const float *scale, cons
     a.row0[i] = row;
 }
 
-// floats of split sums that a product of up to M rows by N columns may need
-// (the largest over the row chunks: whole ones and the last)
-int64_t part_floats(int64_t M, int64_t N, int64_t steps)
+// floats of partial sums that a product of up to M rows by N columns may need (the
+// largest over the row chunks: whole ones and the last); one part is needed only where
+// its sums are carried on
+int64_t part_floats(int64_t M, int64_t N, int64_t steps, bool carried)
 {
     int64_t most = 0;
     for (const int64_t m : {M < kRowChunk ? M : kRowChunk, M % kRowChunk})
         if (m > 0) {
-            const int64_t f = (int64_t)gemm_splits(m, N, steps) * m * N;
+            const int64_t splits = gemm_splits(m, N, steps);
+            const int64_t f = splits > 1 || carried ? splits * m * N : 0;
             most = f > most ? f : most;
         }
     return most;
@@ -336,8 +338,8 @@ struct GatedGradLayout {
         scale = c.take<float>(mc);
         inv = c.take<float>(mc);
         const int64_t n[2] = {N, N};
-        part = c.take_some<float>(!few ? part_floats(M, K, 2 * Np / kStep)
-                                               : few_part_floats(M, K, grad_steps(n, 2)));
+        part = c.take_some<float>(few ? few_part_floats(M, K, grad_steps(n, 2))
+                                      : part_floats(M, K, 2 * Np / kStep, false));
         bytes = c.at;
     }
 };
@@ -362,17 +364,17 @@ struct BatchGradLayout {
         W = c.take<uint16_t>(rows * pitch_for(K));
         for (int i = 0; i < count; ++i)
             pad[i] = c.take_some<uint16_t>(pad_values(mc, n[i]));
-        part = c.take<float>(part_floats(M, K, rows / kStep));
+        part = c.take_some<float>(part_floats(M, K, rows / kStep, false));
         bytes = c.at;
     }
 };
 
 // classes per piece: W_hat of a piece takes about 128 MiB (the cache behind the L2s
-// has 256 MB)
+// has 256 MB); at most 65536, so that the tiles of 2^20 rows fit a grid
 int64_t loss_piece(int64_t K, int64_t N)
 {
     int64_t p = (int64_t(64) << 20) / pitch_for(K) / 256 * 256;
-    p = p < 4096 ? 4096 : p;
+    p = p < 4096 ? 4096 : p > 65536 ? 65536 : p;
     return p < N ? p : N;
 }
 
@@ -433,13 +435,13 @@ struct LossGradLayout {
         W = c.take<uint16_t>(round_up(piece, kStep) * pitch_for(K));
         dL = c.take<uint16_t>(mc * ldl);
         X = c.take_some<uint16_t>(pad_values(mc, K));
-        int64_t f = part_floats(M, K, (piece + kStep - 1) / kStep);
+        int64_t f = part_floats(M, K, (piece + kStep - 1) / kStep, piece < N);
         const int64_t rest = N % piece;
         if (rest) {
-            const int64_t f2 = part_floats(M, K, (rest + kStep - 1) / kStep);
+            const int64_t f2 = part_floats(M, K, (rest + kStep - 1) / kStep, true);
             f = f2 > f ? f2 : f;
         }
-        part = c.take<float>(f);
+        part = c.take_some<float>(f);
         acc = c.take<float>(piece < N ? mc * K : 0);
         bytes = c.at;
     }

@@ -48,6 +48,13 @@ __device__ __forceinline__ void share_meta(float s, float z, double (&R)[8], flo
     Z[4] = from_eighth<4>(z); Z[5] = from_eighth<5>(z); Z[6] = from_eighth<6>(z); Z[7] = from_eighth<7>(z);
 }
 
+// LDS of one wave: written by some lanes and read by others
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // 2^x and 1 / x to about an ulp of fp32 (v_exp_f32, v_rcp_f32): the results are

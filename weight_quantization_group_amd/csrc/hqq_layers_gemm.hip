@@ -150,6 +150,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                 }
                 *reinterpret_cast<uint2 *>(st + l16 * P + 2 * n) = uint2{out2<BF>(v[0], v[1]), out2<BF>(v[2], v[3])};
             }
+            wave_fence();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int row = 8 * i + (lane >> 3), n = nw + 8 * (lane & 7), mr = mw + 16 * u + row;
@@ -157,6 +158,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                 if (mr < g.M && n < width)
                     store8(g.out + (int64_t)mr * g.ldo + n, v, width - n);
             }
+            wave_fence();
         }
     } else if constexpr (OUT == kOutPart) {
         constexpr int P = 144;
@@ -167,6 +169,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     *reinterpret_cast<float4v *>(st + l16 * P + 4 * (16 * t + 4 * l4)) = acc[u][2 * h + t];
+                wave_fence();
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = 8 * i + (lane >> 3), n = nw + 32 * h + 4 * (lane & 7), mr = mw + 16 * u + row;
@@ -174,6 +177,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                     if (mr < g.M && n < g.N)
                         *reinterpret_cast<float4v *>(g.part + ((int64_t)z * g.M + mr) * g.N + n) = v;
                 }
+                wave_fence();
             }
     } else if constexpr (OUT == kOutGated || OUT == kOutGatedGrad) {
         constexpr int P = 80;
@@ -205,6 +209,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                 if (u % 4 == 0)
                     load_y(u);
                 *reinterpret_cast<uint4 *>(sy + row4 * P + 16 * (lane & 3)) = y[u % 4];
+                wave_fence();
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -230,6 +235,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                     *reinterpret_cast<uint2 *>(su + l16 * P + 2 * n) =
                         uint2{out2<BF>(vu[0], vu[1]), out2<BF>(vu[2], vu[3])};
             }
+            wave_fence();
             const int mr = mw + 16 * u + row4, width = GRAD ? (int)g.fill : g.N;
             // (dG and dU in turn by 32 columns, as the weights' rows are)
             uint16_t *o = g.out + (int64_t)mr * g.ldo + (GRAD ? nw + n4 : n4);
@@ -241,6 +247,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                 if (mr < g.M && n4 < width)
                     store8(o + 32, w, 8);
             }
+            wave_fence();
         }
     } else {   // kOutStats
         // the row's max and sum of exp over this wave's 64 columns, the target left out (a

@@ -122,13 +122,6 @@ __device__ __forceinline__ void store_half(const XHalf<MT> &b, uint4 *xs, uint32
     }
 }
 
-// LDS of one wave: written by some lanes and read by others
-__device__ __forceinline__ void wave_fence()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // acc += the operands of half H of a step
 template <int H, bool KT, bool BF, int NM, int NB, int MT, int GPC>
 __device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], const uint4 *xs, uint32_t km, int lane,
