@@ -4,12 +4,19 @@
 // gradients.
 //
 // A workgroup computes a BM x BN tile of C with WM x WN waves.  Each 64-wide step
-// of A and B goes from memory to LDS by DMA (no registers), into two buffers in
-// turn; a row's eight 16-byte runs are stored
-// XOR-swizzled by the row's low bits, so that the 16 rows of an operand read
-// spread over the banks.  The product is formed transposed (the rows of B are
-// the instruction's rows): a lane then holds 4 consecutive columns n of one row
-// m, which is what the row-wise softmax and the 16-bit stores want.
+// of A and B goes from memory to LDS by DMA (no registers), into S buffers in turn; a
+// row's eight 16-byte runs are stored XOR-swizzled by the row's low bits, so that the 16
+// rows of an operand read spread over the banks.  The product is formed transposed (the
+// rows of B are the instruction's rows): a lane then holds 4 consecutive columns n of one
+// row m, which is what the row-wise softmax and the 16-bit stores want.  For the gradients
+// the sum runs down the rows of W_hat as it lies there: LDS reads that transpose (4 rows x
+// 16 columns among 16 lanes) give the operands, so that no transposed copy of W_hat is
+// written (gated backward 2048 x 4096 x 11008, 707 us with one, 647 without).
+//
+// Bound by the matrix cores at the clock that the power limit leaves: 2048 x 4096 x 22016
+// with the gated epilogue takes 283 us, 1.31 PFLOP/s in bf16 on random data (1.74 on
+// zeros); the product of the gated gradient 2048 x 57344 x 8192 1.34.  Without the gated
+// gradient's epilogue (timed on a copy) a pass of 648 us would take 609.
 #include "hqq_layers_epilogue.h"
 
 namespace hqq {

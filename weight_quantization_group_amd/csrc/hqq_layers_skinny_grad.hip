@@ -8,8 +8,9 @@
 // 8 (l / 16) .. + 7.  A wave covers 128 k and 32 rows per step; the next step's
 // codes load under the current one's arithmetic.  Waves and workgroups split the
 // rows; the waves' sums meet in LDS, the workgroups' in a second launch, in a
-// fixed order.  Few rows of C leave this to the codes' bytes and the latency of
-// the two launches.
+// fixed order.  Bound by the arithmetic of the dequantization (about 5 instructions per
+// weight) and by the latency of two launches: 16 rows through 4096 x 11008 at 4 bits 25.8
+// us, of which about 4 are the second; through 4096 x 4096 16.
 #include "hqq_layers_epilogue.h"
 
 namespace hqq {
@@ -226,8 +227,8 @@ hipError_t launch_skinny_grad(int nbits, bool bf16, const SkinnyGradArgs &a, hip
 }
 
 // About two workgroups of four waves per CU, each wave with a step at least; no part
-// empty.  (Eight waves, or twice the workgroups: 27.8 and 27.4 us against 26.5 for 16 rows
-// through 4096 x 11008 at 4 bits.)
+// empty.  (Eight waves, or twice the workgroups, cost 5 and 3 % for 16 rows through 4096 x
+// 11008 at 4 bits.)
 int skinny_grad_splits(int64_t M, int64_t K, int64_t steps)
 {
     const int64_t tiles = (K + 127) / 128 * (M <= 16 ? 1 : (M + 31) / 32);
