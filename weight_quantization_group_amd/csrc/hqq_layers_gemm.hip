@@ -381,13 +381,15 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
     const int last_a = g.M - m0 - 1;
     const char *bb = reinterpret_cast<const char *>(DOWN ? g.B : g.B + (int64_t)b0 * g.ldb);
     uint32_t ldb2 = (uint32_t)(g.ldb * 2);
-    const int steps = g.step0[g.segs];
+    const int steps = g.steps;
     const int per = (steps + g.splits - 1) / g.splits;
     const int s0 = split * per;
     const int s1 = s0 + per < steps ? s0 + per : steps;
-    int seg = -1, seg_end = 0;
-    const char *ab = nullptr;          // of the segment's (virtual) step 0
-    uint32_t lda2 = 0;
+    // The first segment's fields come with the other arguments; those of a later one, read
+    // by its number, are loads that wait for one another.
+    int seg = 0, seg_end = g.step0[1];
+    const char *ab = reinterpret_cast<const char *>(g.A[0] + (int64_t)m0 * g.lda[0]);   // of the (virtual) step 0
+    uint32_t lda2 = (uint32_t)(g.lda[0] * 2);
     auto enter = [&](int s) {          // the segment of step s (not before the current one)
         while (s >= seg_end)
             seg_end = g.step0[++seg + 1];
@@ -609,6 +611,7 @@ hipError_t launch_tile(GemmArgs &g, hipStream_t s)
     constexpr int BNC = GATED ? BN / 2 : BN;
     g.tiles_m = (g.M + BM - 1) / BM;
     g.tiles_n = (g.N + BNC - 1) / BNC;
+    g.steps = g.step0[g.segs];
     hipLaunchKernelGGL((gemm_kernel<OUT, ACT, BF, BM, BN, WM, WN, S>),
                        dim3((unsigned)(g.tiles_m * g.tiles_n * g.splits)), dim3(WM * WN * 64), 0, s, g);
     return hipGetLastError();

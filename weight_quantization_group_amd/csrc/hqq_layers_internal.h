@@ -78,7 +78,7 @@ struct GemmArgs {
     int64_t ldb;                     // below 2^23
     int32_t M, N;
     int splits;                      // kOutPart: parts of the steps
-    int tiles_m, tiles_n;            // filled by the launcher
+    int tiles_m, tiles_n, steps;     // filled by the launcher
     // outputs
     uint16_t *out;                   // [M, ldo]
     int64_t ldo;
@@ -126,12 +126,12 @@ struct SkinnyGradArgs {
     int32_t n[kMaxSegs];
     int32_t step0[kMaxSegs + 1];     // first 32-row step of each weight
     int64_t M, K, wpr, gpl;
-    int gshift, splits;
+    int gshift, splits, steps;       // steps: filled by the launcher
     float *part;
     uint16_t *out;
     RowFactor rowf;
 };
-hipError_t launch_skinny_grad(int nbits, bool bf16, const SkinnyGradArgs &a, hipStream_t s);
+hipError_t launch_skinny_grad(int nbits, bool bf16, SkinnyGradArgs &a, hipStream_t s);
 int skinny_grad_splits(int64_t M, int64_t K, int64_t steps);
 
 // Sum of the parts: v = sum_z part[z] (+ acc_in), then out = round(rowf * v),

@@ -7,18 +7,37 @@ namespace {
 
 constexpr int kRowsBlock = 256;
 
-// parts of a split product added in split order in fp32; 4 values per lane
-template <bool BF>
+// Parts of a split product added in a fixed order in fp32; 4 values per lane.  GR: groups
+// of lanes that take a share of the parts each and join through LDS: 4 where the values
+// alone would leave most of the chip idle (16 parts of 16 x 4096, 4.6 us by one
+// group, 3.7 by 4).
+template <bool BF, int GR>
 __global__ __launch_bounds__(kRowsBlock) void reduce_kernel(ReduceArgs a)
 {
-    const int64_t i = ((int64_t)blockIdx.x * kRowsBlock + threadIdx.x) * 4;
+    constexpr int kLanes = kRowsBlock / GR;
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const int64_t i = ((int64_t)blockIdx.x * kLanes + lane) * 4;
     const int64_t total = a.M * a.N;
+    const int per = (a.splits + GR - 1) / GR, z0 = group * per, z1 = z0 + per < a.splits ? z0 + per : a.splits;
+    float4v v{0.f, 0.f, 0.f, 0.f};
+    if (i < total) {
+#pragma unroll 8
+        for (int z = z0; z < z1; ++z)
+            v += *reinterpret_cast<const float4v *>(a.part + z * total + i);
+    }
+    if constexpr (GR > 1) {
+        __shared__ float4v sums[GR - 1][kLanes];
+        if (group > 0)
+            sums[group - 1][lane] = v;
+        __syncthreads();
+        if (group > 0)
+            return;
+#pragma unroll
+        for (int r = 0; r < GR - 1; ++r)
+            v += sums[r][lane];
+    }
     if (i >= total)
         return;
-    float4v v = *reinterpret_cast<const float4v *>(a.part + i);
-#pragma unroll 8
-    for (int z = 1; z < a.splits; ++z)
-        v += *reinterpret_cast<const float4v *>(a.part + z * total + i);
     if (a.acc_in)
         v += *reinterpret_cast<const float4v *>(a.acc_in + i);
     if (a.acc_out) {
@@ -27,6 +46,18 @@ __global__ __launch_bounds__(kRowsBlock) void reduce_kernel(ReduceArgs a)
     }
     const float f = row_factor(a.rowf, i / a.N);
     *reinterpret_cast<uint2 *>(a.out + i) = uint2{out2<BF>(v[0] * f, v[1] * f), out2<BF>(v[2] * f, v[3] * f)};
+}
+
+template <bool BF>
+hipError_t launch_reduce_dtype(const ReduceArgs &a, hipStream_t s)
+{
+    const int64_t lanes = a.M * a.N / 4;
+    if (a.splits >= 8 && lanes <= 256 * kRowsBlock)
+        hipLaunchKernelGGL((reduce_kernel<BF, 4>), dim3((unsigned)((lanes + 63) / 64)), dim3(kRowsBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((reduce_kernel<BF, 1>), dim3((unsigned)((lanes + kRowsBlock - 1) / kRowsBlock)), dim3(kRowsBlock), 0,
+                           s, a);
+    return hipGetLastError();
 }
 
 // (max, sum) pairs of sums of exponentials; an empty one is (-inf, 0)
@@ -109,18 +140,11 @@ __global__ __launch_bounds__(kRowsBlock) void row_scale_kernel(const uint16_t *r
     }
 }
 
-unsigned blocks_for(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
-
 }  // namespace
 
 hipError_t launch_reduce(bool bf16, const ReduceArgs &a, hipStream_t s)
 {
-    const dim3 grid(blocks_for(a.M * a.N, 4 * kRowsBlock));
-    if (bf16)
-        hipLaunchKernelGGL((reduce_kernel<true>), grid, dim3(kRowsBlock), 0, s, a);
-    else
-        hipLaunchKernelGGL((reduce_kernel<false>), grid, dim3(kRowsBlock), 0, s, a);
-    return hipGetLastError();
+    return bf16 ? launch_reduce_dtype<true>(a, s) : launch_reduce_dtype<false>(a, s);
 }
 
 hipError_t launch_loss(const LossArgs &a, hipStream_t s)

@@ -71,32 +71,47 @@ skinny_grad_kernel(SkinnyGradArgs a)
     const int kc_raw = (int)blockIdx.x * 128 + 8 * l16;
     const int kc = kc_raw < a.K ? kc_raw : (int)a.K - 8;       // past K: any codes, never stored
     const int m0 = (int)blockIdx.z * 16 * MT;
-    const int steps = a.step0[a.count];
+    const int steps = a.steps;
     const int per = (steps + a.splits - 1) / a.splits;
     const int s0 = (int)blockIdx.y * per, s1 = s0 + per < steps ? s0 + per : steps;
 
-    int j = 0;
+    // The first weight's fields come with the other arguments; those of a later one, read
+    // by its number, are loads that wait for one another.
+    int j = 0, first = 0, end = a.step0[1], N = a.n[0];
+    const uint32_t *packed = a.packed[0];
+    const float *scale = a.scale[0], *zero = a.zero[0];
+    const uint16_t *A = a.A[0];
+    int64_t lda = a.lda[0];
     GradBuf<NB, MT, SH> buf;
     auto load = [&](int s) {
-        while (s >= a.step0[j + 1])
-            ++j;
-        const int N = a.n[j], n0 = 32 * (s - a.step0[j]) + 8 * l4;
+        if (s >= end) {
+            while (s >= end)
+                end = a.step0[++j + 1];
+            first = a.step0[j];
+            N = a.n[j];
+            packed = a.packed[j];
+            scale = a.scale[j];
+            zero = a.zero[j];
+            A = a.A[j];
+            lda = a.lda[j];
+        }
+        const int n0 = 32 * (s - first) + 8 * l4;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t n = (uint32_t)(n0 + i < N ? n0 + i : N - 1);
-            buf.c[i] = load_codes<NB>(at<uint8_t>(a.packed[j], n * (uint32_t)a.wpr * 4u + (uint32_t)kc * NB / 8));
+            buf.c[i] = load_codes<NB>(at<uint8_t>(packed, n * (uint32_t)a.wpr * 4u + (uint32_t)kc * NB / 8));
         }
 #pragma unroll
         for (int i = 0; i < (SH ? 1 : 8); ++i) {
             const int nr = n0 + (SH ? l16 & 7 : i);
             const uint32_t g = (uint32_t)(nr < N ? nr : N - 1) * (uint32_t)a.gpl + ((uint32_t)kc >> a.gshift);
-            buf.s[i] = *at<float>(a.scale[j], 4 * g);
-            buf.z[i] = *at<float>(a.zero[j], 4 * g);
+            buf.s[i] = *at<float>(scale, 4 * g);
+            buf.z[i] = *at<float>(zero, 4 * g);
         }
 #pragma unroll
         for (int u = 0; u < MT; ++u) {
             const int m = m0 + 16 * u + l16 < a.M ? m0 + 16 * u + l16 : (int)a.M - 1;
-            buf.a[u] = load_run<AL>(a.A[j] + (int64_t)m * a.lda[j], n0, N);
+            buf.a[u] = load_run<AL>(A + (int64_t)m * lda, n0, N);
         }
     };
     float4v acc[MT][8];
@@ -215,8 +230,9 @@ hipError_t launch_mt(const SkinnyGradArgs &a, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_skinny_grad(int nbits, bool bf16, const SkinnyGradArgs &a, hipStream_t s)
+hipError_t launch_skinny_grad(int nbits, bool bf16, SkinnyGradArgs &a, hipStream_t s)
 {
+    a.steps = a.step0[a.count];
     switch (nbits) {
     case 1: return bf16 ? launch_mt<1, true>(a, s) : launch_mt<1, false>(a, s);
     case 2: return bf16 ? launch_mt<2, true>(a, s) : launch_mt<2, false>(a, s);
