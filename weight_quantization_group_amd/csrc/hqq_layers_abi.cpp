@@ -161,8 +161,9 @@ int64_t part_floats(int64_t M, int64_t N, int64_t steps, bool carried)
     int64_t most = 0;
     for (const int64_t m : {M < kRowChunk ? M : kRowChunk, M % kRowChunk})
         if (m > 0) {
-            const int64_t splits = gemm_splits(m, N, steps);
-            const int64_t f = splits > 1 || carried ? splits * m * N : 0;
+            int tile, splits;
+            gemm_gradient_tile(m, N, steps, tile, splits);
+            const int64_t f = splits > 1 || carried ? (int64_t)splits * m * N : 0;
             most = f > most ? f : most;
         }
     return most;
@@ -200,7 +201,7 @@ hipError_t gradient_product(GemmArgs &g, bool bf16, float *part, float *acc, boo
                             const RowFactor &rowf, hipStream_t s)
 {
     const int64_t M = g.M, K = g.N;
-    g.splits = gemm_splits(M, K, g.step0[g.segs]);
+    gemm_gradient_tile(M, K, g.step0[g.segs], g.tile, g.splits);
     if (g.splits == 1 && first && last) {
         g.out = dX;
         g.ldo = K;

@@ -573,35 +573,33 @@ constexpr int kTileKinds = 4;
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 32;
 
-double product_us(int tile, int64_t M, int64_t N, int64_t steps, int splits, bool gated)
-{
-    const Tile &t = kTiles[tile];
-    const int64_t bn = gated ? t.bn / 2 : t.bn;
-    const int64_t wgs = (M + t.bm - 1) / t.bm * ((N + bn - 1) / bn) * splits;
-    const int64_t slots = kCus * t.per_cu, rest = wgs % slots;
-    const double step = (double)(wgs / slots) * t.us + (rest == 0 ? 0.0 : 2 * rest <= slots ? t.us_half : t.us);
-    double us = 3.0 + (double)((steps + splits - 1) / splits) * step;
-    if (splits > 1)
-        us += 3.0 + (double)M * (double)N * (4.0 * splits + 2.0) / 6.0e6;
-    return us;
-}
-
 void pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool may_split, int &tile, int &splits)
 {
     double best = 0.0;
     tile = 0;
     splits = 1;
-    for (int t = 0; t < kTileKinds; ++t)
+    for (int t = 0; t < kTileKinds; ++t) {
+        const Tile &k = kTiles[t];
+        const int64_t bn = gated ? k.bn / 2 : k.bn, slots = kCus * k.per_cu;
+        const int64_t tiles = (M + k.bm - 1) / k.bm * ((N + bn - 1) / bn);
         for (int sp = 1; sp <= (may_split ? kMaxSplits : 1); ++sp) {
-            if (sp > 1 && (steps / sp < 4 || (sp - 1) * ((steps + sp - 1) / sp) >= steps))
-                continue;       // a part has a few steps at least, and none is empty
-            const double us = product_us(t, M, N, steps, sp, gated);
+            if (sp > 1 && (steps / sp < 4 || tiles * (sp - 1) >= 4 * slots))
+                break;          // a part has a few steps at least; four rounds balance well enough
+            const int64_t per = (steps + sp - 1) / sp;
+            if ((sp - 1) * per >= steps)
+                continue;       // none is empty
+            const int64_t rest = tiles * sp % slots;
+            const double round = (double)(tiles * sp / slots) * k.us + (rest == 0 ? 0.0 : 2 * rest <= slots ? k.us_half : k.us);
+            double us = 3.0 + (double)per * round;
+            if (sp > 1)
+                us += 3.0 + (double)M * (double)N * (4.0 * sp + 2.0) / 6.0e6;
             if (best == 0.0 || us < best) {
                 best = us;
                 tile = t;
                 splits = sp;
             }
         }
+    }
 }
 
 template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN, int S>
@@ -617,18 +615,11 @@ hipError_t launch_tile(GemmArgs &g, hipStream_t s)
     return hipGetLastError();
 }
 
-void gradient_tile(int64_t M, int64_t N, int64_t steps, int &tile, int &splits)
-{
-    pick_tile(M, N, steps, false, true, tile, splits);
-}
-
 template <int OUT, int ACT, bool BF>
 hipError_t launch_out(GemmArgs &g, hipStream_t s)
 {
-    int tile, sp;
-    if (OUT == kOutStore || OUT == kOutPart)
-        gradient_tile(g.M, g.N, g.step0[g.segs], tile, sp);
-    else
+    int tile = g.tile, sp;
+    if (OUT != kOutStore && OUT != kOutPart)
         pick_tile(g.M, g.N, g.step0[g.segs], OUT == kOutGated || OUT == kOutGatedGrad, false, tile, sp);
     switch (tile) {
     case 0: return launch_tile<OUT, ACT, BF, 256, 256, 2, 4, 2>(g, s);
@@ -675,11 +666,9 @@ int64_t gemm_stats_blocks(int64_t M, int64_t N, int64_t steps)
     return (N + kTiles[tile].bn - 1) / kTiles[tile].bn;
 }
 
-int gemm_splits(int64_t M, int64_t N, int64_t steps)
+void gemm_gradient_tile(int64_t M, int64_t N, int64_t steps, int &tile, int &splits)
 {
-    int tile, splits;
-    gradient_tile(M, N, steps, tile, splits);
-    return splits;
+    pick_tile(M, N, steps, false, true, tile, splits);
 }
 
 }  // namespace hqq

@@ -77,7 +77,7 @@ struct GemmArgs {
     const uint16_t *B;               // [N, ldb] (gated: [2 round_up(N, 32), ldb]), or [R, ldb]
     int64_t ldb;                     // below 2^23
     int32_t M, N;
-    int splits;                      // kOutPart: parts of the steps
+    int tile, splits;                // kOutStore, kOutPart: by gemm_gradient_tile
     int tiles_m, tiles_n, steps;     // filled by the launcher
     // outputs
     uint16_t *out;                   // [M, ldo]
@@ -100,8 +100,9 @@ struct GemmArgs {
 hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s);
 // Column tiles of a kOutStats product (at most (N + 127) / 128).
 int64_t gemm_stats_blocks(int64_t M, int64_t N, int64_t steps);
-// Splits of the steps for a kOutPart product (none of them empty).
-int gemm_splits(int64_t M, int64_t N, int64_t steps);
+// The tile and the splits of the steps (none of them empty) for a kOutStore or kOutPart
+// product.
+void gemm_gradient_tile(int64_t M, int64_t N, int64_t steps, int &tile, int &splits);
 
 // Few rows, straight from the packed codes (hqq_layers_skinny.h): C [M, N] =
 // X . W_hat^T with g's fields for what becomes of it (kOutStats: 16 columns per

@@ -121,7 +121,12 @@ _F32, _I64 = (torch.float32,), (torch.int64,)
 
 
 def _array(t, name: str, dtypes, n: int, device) -> int:
-    """The address of a contiguous CUDA tensor of n values on device, checked."""
+    """The address of a contiguous CUDA tensor of n values on device (a CUDA device), checked."""
+    try:
+        if t.device == device and t.dtype in dtypes and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -148,6 +153,10 @@ def _first(t, name: str):
 
 def _matrix(t, name: str, rows: int, cols: int, like) -> int:
     """The address of a [rows, cols] CUDA tensor of like's dtype and device, checked."""
+    if t is like:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
     if isinstance(t, torch.Tensor) and t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
     return _array(t, name, (like.dtype,), rows * cols, like.device)
