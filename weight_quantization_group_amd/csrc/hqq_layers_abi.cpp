@@ -44,21 +44,28 @@ int check_sizes(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
 
 // Whether a product runs straight from the codes (which every 32 rows dequantize
 // anew) or W_hat is unpacked for the tiled product.  n: all rows of its weights.
-// Measured crossovers on MI355X (codes against unpacked, us): gated block at 4096 x
-// 11008 4-bit g64, 64 rows 71 against 92, 96 rows 102 against 99, its backward 32 rows
-// 81 against 127, 48 rows 131 against 128; at 2048 x 5632 8-bit 32 rows 25 against 28,
-// 48 rows 30 against 28, backward 16 rows 35 against 43, 32 rows 46 against 44; one
-// weight backward at 4096 x 11008, 64 rows 40 against 45, 96 rows 61 against 47; the
-// head at 1024 x 32003 4-bit, 32 rows 32 against 35, 48 rows 46 against 36, with 2-bit
-// groups of 16 (a reciprocal per 8 weights) 16 rows 38 against 36, its backward 4-bit
-// 16 rows 41 against 48, 32 rows 51 against 49.  Small weights leave the CUs room for
-// the row blocks: 512 x 512, 128 rows 7 against 10, backward 20 against 22.
+// By the rows, and for small weights, which leave the CUs room for the row blocks, by
+// blocks of 32 rows times weights.  Crossovers measured on MI355X in bf16, 1, 2, 4 and 8
+// bits, codes against unpacked in us at 4 bits:
+//              1024 x 2816              4096 x 11008               8192 x 28672
+//   pair       g64 128 rows 12/15       g64 64 54/80, 128 92/90    64 267/486, 128 524/503
+//              g16 64 15/16, 96 21/16   g16 32 70/92, 48 124/92    32 298/507, 64 573/511
+//   its grad.  g64 64 28/29, 96 32/30   g64 64 119/120, 96 174/132 64 628/656, 128 1061/695
+//              g16 32 27/27, 48 33/29   g32 32 89/120, 48 152/121  32 393/688, 64 771/690
+//   one grad.  g64 64 14/15, 96 16/15   g64 64 38/46, 96 57/48     64 174/239, 128 277/234
+//   head       g64 128 14/19            g64 64 45/52, 96 64/53     64 171/338, 128 337/340
+//              g16 96 18/19, 128 19/19  g16 32 47/54, 48 77/54     32 164/327, 64 306/328
+//   its grad.  g64 96 25/26, 128 27/26  g64 32 52/69, 48 74/70     64 339/434, 128 580/443
+//              g16 48 23/24, 64 25/25   g16 24 72/72, 32 74/73     32 276/426, 64 521/438
+// and heads of 1024 x 32003: g64 32 rows 27/35, 48 39/35, g16 32 38/36, their gradients
+// g64 32 44/46, 48 59/48, g16 16 51/46.  Groups of 8 and 16 cost a reciprocal each per
+// lane and are dear to dequantize twice.
 // HQQ_LAYERS_PATH=codes or =tiled in the environment, read at each call, forces one
 // (tests run both), the codes up to the 256 rows beyond which the rule never takes
 // them: their kernels address the activations by 32-bit offsets.
 enum Product { kPair, kPairGrad, kBackward, kHead, kHeadGrad };
 
-bool straight(Product what, int64_t M, int64_t K, int64_t n, int nbits, int group_size)
+bool straight(Product what, int64_t M, int64_t K, int64_t n, int group_size)
 {
     if (M > 256)
         return false;
@@ -68,17 +75,16 @@ bool straight(Product what, int64_t M, int64_t K, int64_t n, int nbits, int grou
         if (strcmp(e, "tiled") == 0)
             return false;
     }
-    const bool tables = nbits == 4 && group_size >= 32;
-    const bool fine = group_size < 32;
-    int64_t rows = 64;
+    const bool fine = group_size < 32, shallow = K < 2048;
+    int64_t rows = 64, work = 6;          // work: millions of weights times blocks of 32 rows
     switch (what) {
-    case kPair: rows = tables ? 64 : 32; break;
-    case kPairGrad: rows = tables ? 32 : 16; break;
+    case kPair: rows = fine ? 32 : 64; work = fine ? 12 : 24; break;
+    case kPairGrad: rows = group_size < 64 ? 32 : 64; work = fine ? 6 : 12; break;
     case kBackward: break;
-    case kHead: rows = fine ? 8 : 32; break;
-    case kHeadGrad: rows = fine ? 8 : 16; break;
+    case kHead: rows = fine || shallow ? 32 : 64; work = 12; break;
+    case kHeadGrad: rows = fine ? (shallow ? 8 : 32) : K * n > 100000000 ? 64 : 32; work = fine ? 6 : 9; break;
     }
-    return M <= rows || (M + 31) / 32 * K * n <= (tables ? 16 : 6) * 1000000;
+    return M <= rows || (M + 31) / 32 * K * n <= work * 1000000;
 }
 
 int check_batch(int64_t M, int64_t K, const int64_t *n, int count, int nbits, int group_size)
@@ -370,13 +376,37 @@ struct BatchGradLayout {
     }
 };
 
-// classes per piece: W_hat of a piece takes about 128 MiB (the cache behind the L2s
-// has 256 MB); at most 65536, so that the tiles of 2^20 rows fit a grid
-int64_t loss_piece(int64_t K, int64_t N)
+// Classes per piece: W_hat of a piece takes about 128 MiB (the cache behind the L2s has
+// 256 MB), `limit` classes at most.  Of the widths from 5/8 to 5/4 of that, the one whose
+// products take the least time by the tiles' model: few rows and a deep head leave tens of
+// tiles per piece, and a last piece of a few columns costs a whole round of them.  At most
+// 65536, so that the tiles of 2^20 rows fit a grid.
+int64_t loss_piece(int64_t M, int64_t K, int64_t N, int64_t limit)
 {
     int64_t p = (int64_t(64) << 20) / pitch_for(K) / 256 * 256;
-    p = p < 4096 ? 4096 : p > 65536 ? 65536 : p;
-    return p < N ? p : N;
+    p = p < limit ? p : limit;
+    p = p < 4096 ? 4096 : p > 52224 ? 52224 : p;
+    if (N <= p)
+        return N;
+    const int64_t steps = round_up(K, kStep) / kStep;
+    const int64_t by = p / 8 / 256 * 256;
+    double best = 0.0;
+    int64_t piece = p;
+    for (int64_t w = p - 3 * by; w <= p + 2 * by; w += by) {
+        if (w >= N) {
+            w = N;
+        }
+        double us = (double)(N / w) * gemm_us(M, w, steps);
+        if (N % w)
+            us += gemm_us(M, N % w, steps);
+        if (best == 0.0 || us < best) {
+            best = us;
+            piece = w;
+        }
+        if (w == N)
+            break;
+    }
+    return piece;
 }
 
 struct LossLayout {
@@ -389,7 +419,7 @@ struct LossLayout {
         Carve c(p);
         W = X = nullptr;
         if (!few) {
-            piece = loss_piece(K, N);
+            piece = loss_piece(M, K, N, N);
             pitch = N / piece * ((piece + 127) / 128) + (N % piece + 127) / 128;
             W = c.take<uint16_t>(round_up(piece, kStep) * pitch_for(K));
             X = c.take_some<uint16_t>(pad_values(M, K));
@@ -403,14 +433,11 @@ struct LossLayout {
     }
 };
 
-// classes per piece of the backward pass: the 16-bit gradients of a piece's
-// logits take at most about 64 MiB (beside W_hat's 128 MiB in the cache)
+// of the backward pass: the 16-bit gradients of a piece's logits take at most about 64
+// MiB (beside W_hat's in the cache)
 int64_t loss_grad_piece(int64_t m, int64_t K, int64_t N)
 {
-    const int64_t c = loss_piece(K, N);
-    int64_t p = (int64_t(32) << 20) / m / 256 * 256;
-    p = p < 4096 ? 4096 : p;
-    return p < c ? p : c;
+    return loss_piece(m, K, N, (int64_t(32) << 20) / m / 256 * 256);
 }
 
 struct LossGradLayout {
@@ -472,7 +499,7 @@ int64_t hqq_linear_gated_workspace(int64_t M, int64_t K, int64_t N, int nbits, i
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return GatedLayout(nullptr, M, K, N, straight(kPair, M, K, 2 * N, nbits, group_size)).bytes;
+    return GatedLayout(nullptr, M, K, N, straight(kPair, M, K, 2 * N, group_size)).bytes;
 }
 
 int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate, const hqq_weight *up, int64_t N,
@@ -488,7 +515,7 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
     if (!gate || !up || !weight_ok(gate->packed, gate->scale, gate->zero) || !weight_ok(up->packed, up->scale, up->zero) ||
         !aligned(X, 16) || !aligned(Y, 16))
         return HQQ_EINVAL_PTR;
-    const bool few = straight(kPair, M, K, 2 * N, nbits, group_size);
+    const bool few = straight(kPair, M, K, 2 * N, group_size);
     const GatedLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
@@ -529,7 +556,7 @@ int64_t hqq_linear_gated_backward_workspace(int64_t M, int64_t K, int64_t N, int
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return GatedGradLayout(nullptr, M, K, N, straight(kPairGrad, M, K, 2 * N, nbits, group_size)).bytes;
+    return GatedGradLayout(nullptr, M, K, N, straight(kPairGrad, M, K, 2 * N, group_size)).bytes;
 }
 
 int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *gate,
@@ -545,7 +572,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     if (!gate || !up || !weight_ok(gate->packed, gate->scale, gate->zero) || !weight_ok(up->packed, up->scale, up->zero) ||
         !aligned(X, 16) || !aligned(dY, 16) || !aligned(dX, 16))
         return HQQ_EINVAL_PTR;
-    const bool few = straight(kPairGrad, M, K, 2 * N, nbits, group_size);
+    const bool few = straight(kPairGrad, M, K, 2 * N, group_size);
     const GatedGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
@@ -626,7 +653,7 @@ int64_t hqq_linear_batch_backward_workspace(int64_t M, int64_t K, const int64_t 
         return HQQ_EINVAL_PTR;
     if (const int st = check_batch(M, K, n, count, nbits, group_size))
         return st;
-    return BatchGradLayout(nullptr, M, K, n, count, straight(kBackward, M, K, sum_of(n, count), nbits, group_size)).bytes;
+    return BatchGradLayout(nullptr, M, K, n, count, straight(kBackward, M, K, sum_of(n, count), group_size)).bytes;
 }
 
 int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, int64_t K, int nbits, int group_size,
@@ -648,7 +675,7 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
     for (int i = 0; i < count; ++i)
         if (!weight_ok(ws[i].packed, ws[i].scale, ws[i].zero) || !aligned(ws[i].dY, 16))
             return HQQ_EINVAL_PTR;
-    const bool few = straight(kBackward, M, K, sum_of(n, count), nbits, group_size);
+    const bool few = straight(kBackward, M, K, sum_of(n, count), group_size);
     const BatchGradLayout l(workspace, M, K, n, count, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
@@ -691,7 +718,7 @@ int64_t hqq_linear_cross_entropy_workspace(int64_t M, int64_t K, int64_t N, int 
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return LossLayout(nullptr, M, K, N, straight(kHead, M, K, N, nbits, group_size)).bytes;
+    return LossLayout(nullptr, M, K, N, straight(kHead, M, K, N, group_size)).bytes;
 }
 
 int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *head, int64_t N, int nbits,
@@ -705,7 +732,7 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
     if (!head || !weight_ok(head->packed, head->scale, head->zero) || !aligned(X, 16) || !aligned(targets, 8) ||
         !aligned(loss, 4) || !aligned(lse, 4))
         return HQQ_EINVAL_PTR;
-    const bool few = straight(kHead, M, K, N, nbits, group_size);
+    const bool few = straight(kHead, M, K, N, group_size);
     const LossLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
@@ -757,7 +784,7 @@ int64_t hqq_linear_cross_entropy_backward_workspace(int64_t M, int64_t K, int64_
 {
     if (const int st = check_sizes(M, K, N, nbits, group_size))
         return st;
-    return LossGradLayout(nullptr, M, K, N, straight(kHeadGrad, M, K, N, nbits, group_size)).bytes;
+    return LossGradLayout(nullptr, M, K, N, straight(kHeadGrad, M, K, N, group_size)).bytes;
 }
 
 int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int64_t M, int64_t K, const hqq_weight *head,
@@ -772,7 +799,7 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
     if (!head || !weight_ok(head->packed, head->scale, head->zero) || !aligned(X, 16) || !aligned(dX, 16) ||
         !aligned(targets, 8) || !aligned(dloss, 4) || !aligned(lse, 4))
         return HQQ_EINVAL_PTR;
-    const bool few = straight(kHeadGrad, M, K, N, nbits, group_size);
+    const bool few = straight(kHeadGrad, M, K, N, group_size);
     const LossGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;

@@ -573,7 +573,7 @@ constexpr int kTileKinds = 4;
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 32;
 
-void pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool may_split, int &tile, int &splits)
+double pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool may_split, int &tile, int &splits)
 {
     double best = 0.0;
     tile = 0;
@@ -600,6 +600,7 @@ void pick_tile(int64_t M, int64_t N, int64_t steps, bool gated, bool may_split, 
             }
         }
     }
+    return best;
 }
 
 template <int OUT, int ACT, bool BF, int BM, int BN, int WM, int WN, int S>
@@ -657,6 +658,12 @@ hipError_t launch_dtype(GemmOut out, GemmArgs &g, hipStream_t s)
 hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s)
 {
     return bf16 ? launch_dtype<true>(out, g, s) : launch_dtype<false>(out, g, s);
+}
+
+double gemm_us(int64_t M, int64_t N, int64_t steps)
+{
+    int tile, splits;
+    return pick_tile(M, N, steps, false, false, tile, splits);
 }
 
 int64_t gemm_stats_blocks(int64_t M, int64_t N, int64_t steps)

@@ -100,6 +100,8 @@ struct GemmArgs {
 hipError_t launch_gemm(GemmOut out, bool bf16, GemmArgs &g, hipStream_t s);
 // Column tiles of a kOutStats product (at most (N + 127) / 128).
 int64_t gemm_stats_blocks(int64_t M, int64_t N, int64_t steps);
+// The estimated time of a product that is not split.
+double gemm_us(int64_t M, int64_t N, int64_t steps);
 // The tile and the splits of the steps (none of them empty) for a kOutStore or kOutPart
 // product.
 void gemm_gradient_tile(int64_t M, int64_t N, int64_t steps, int &tile, int &splits);

@@ -129,10 +129,28 @@ __device__ __forceinline__ void store_half(const XHalf<MT> &b, uint4 *xs, uint32
     }
 }
 
-// acc += the operands of half H of a step
-template <int H, bool KT, bool BF, int NM, int NB, int MT, int GPC>
-__device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], const uint4 *xs, uint32_t km, int lane,
-                                             float4v (&acc)[NM][MT])
+// B operand j (8-k run j of a lane's 64) by direct quotients, in operand order
+template <int NB, int GPC, bool BF>
+__device__ __forceinline__ uint4 quotients(const StepBuf<NB, GPC> &b, int j)
+{
+    constexpr uint32_t MASK = (1u << NB) - 1u;
+    constexpr int ord[8] = {0, 2, 4, 6, 1, 3, 5, 7};
+    const int gi = GPC == 1 ? 0 : GPC == 2 ? (j >> 2) : j;
+    const double R = reciprocal(b.s[gi]);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int bit = (8 * j + ord[i]) * NB;
+        v[i] = wq((float)((b.w[bit / 32] >> (bit % 32)) & MASK), b.z[gi], R);
+    }
+    return uint4{out2<BF>(v[0], v[1]), out2<BF>(v[2], v[3]), out2<BF>(v[4], v[5]), out2<BF>(v[6], v[7])};
+}
+
+// acc += the operands of half H of a step; a(u, j): operand j of the half, of row block u.
+// km clears the weights of a lane whose half lies past K.
+template <int H, bool KT, bool BF, int NM, int NB, int MT, int GPC, typename RowRuns>
+__device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], uint32_t km, float4v (&acc)[NM][MT],
+                                             RowRuns &&a)
 {
     Tab4 tab[NM];
     if constexpr (NB == 4 && GPC < 8) {
@@ -145,14 +163,14 @@ __device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], co
         uint4 A[MT];
 #pragma unroll
         for (int u = 0; u < MT; ++u)
-            A[u] = xs[u * 256 + 64 * j + (lane & 48) + ((lane & 15) ^ (j + 4 * (lane >> 4)))];
+            A[u] = a(u, j);
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             uint4 B;
             if constexpr (NB == 4 && GPC < 8)
                 B = lookup4(tab[m], b[m].w[4 * H + j]);
             else
-                B = dequant_run<NB, GPC, BF>(b[m].w, 4 * H + j, b[m].s, b[m].z);
+                B = quotients<NB, GPC, BF>(b[m], 4 * H + j);
             if constexpr (KT)
                 B = and4(B, km);
 #pragma unroll
@@ -223,7 +241,6 @@ skinny_kernel(SkinnyArgs s)
         for (int u = 0; u < MT; ++u)
             acc[j][u] = float4v{0.f, 0.f, 0.f, 0.f};
     if constexpr (XL) {
-        const XRuns<1> none{};
         for (int i = 0; i < my; ++i) {
             const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
             const uint32_t k0 = kbase(i) + kLaneK * grp;
@@ -235,12 +252,18 @@ skinny_kernel(SkinnyArgs s)
                 cur[j] = buf[j];
             if (i + 1 < my)
                 load(i + 1);
-#pragma unroll
-            for (int j = 0; j < NM; ++j)
-                compute_step<KT, NB, MT, GPC, XL, BF>(cur[j], none, km0, km1, lds, xr, c, acc[j]);
+            auto runs = [&](uint32_t first, uint32_t km) {
+                return [&, first, km](int u, int j) {
+                    const uint4 A = lds[xr[u] + first + j];
+                    return KT ? and4(A, km) : A;
+                };
+            };
+            compute_half<0, KT, BF>(cur, km0, acc, runs(c.k0 >> 3, km0));
+            compute_half<1, KT, BF>(cur, km1, acc, runs(c.kh >> 3, km1));
         }
     } else {
         uint4 *xs = lds + wave * (256 * MT);
+        auto run = [&](int u, int j) { return xs[u * 256 + 64 * j + (lane & 48) + ((lane & 15) ^ (j + 4 * grp))]; };
         // the run this lane fetches, of the first half of step i
         auto krun = [&](int i) { return kbase(i) + kLaneK * (uint32_t)((lane >> 2) & 3) + 8 * (uint32_t)(lane & 3); };
         XHalf<MT> x;
@@ -257,13 +280,13 @@ skinny_kernel(SkinnyArgs s)
             load_half<KT>(x, a, kr + 32, (uint32_t)m0, mrows, lane);
             if (i + 1 < my)
                 load(i + 1);
-            compute_half<0, KT, BF>(cur, xs, k0 < K ? 0xffffffffu : 0u, lane, acc);
+            compute_half<0, KT, BF>(cur, k0 < K ? 0xffffffffu : 0u, acc, run);
             wave_fence();
             store_half<KT>(x, xs, kr + 32 < K ? 0xffffffffu : 0u, lane);
             wave_fence();
             if (i + 1 < my)
                 load_half<KT>(x, a, krun(i + 1), (uint32_t)m0, mrows, lane);
-            compute_half<1, KT, BF>(cur, xs, k0 + 32 < K ? 0xffffffffu : 0u, lane, acc);
+            compute_half<1, KT, BF>(cur, k0 + 32 < K ? 0xffffffffu : 0u, acc, run);
             wave_fence();
         }
     }
