@@ -129,13 +129,46 @@ __device__ __forceinline__ void store_half(const XHalf<MT> &b, uint4 *xs, uint32
     }
 }
 
+// Scales of a lane's 64 k: 1 (groups of 64 and more), 2 (32), 4 (16) or 8 (8)
+constexpr int groups_of(int gs) { return gs >= 64 ? 1 : 64 / gs; }
+
+// A lane's codes and scales of a step.  A half's 2 or 4 small groups lie next to each
+// other, on 8 and 16 bytes (K is a multiple of 32): one load each (fetched one by one,
+// the pair of 4096 x 11008 in groups of 16 took 57 us, now 32).
+template <int NB, int GPC>
+__device__ __forceinline__ void fetch(StepBuf<NB, GPC> &b, const LinearArgs &a, Chunk c, uint32_t nw, uint32_t ng)
+{
+    if constexpr (GPC <= 2) {
+        load_step(b, a, c, nw, ng);
+    } else {
+        StepBuf<NB, 1> codes;
+        load_step(codes, a, c, nw, ng);
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i)
+            b.w[i] = codes.w[i];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t g = 4 * (ng + ((h ? c.kh : c.k0) >> a.gshift));
+            if constexpr (GPC == 4) {
+                const float2 s = *at<float2>(a.scale, g), z = *at<float2>(a.zero, g);
+                b.s[2 * h] = s.x; b.s[2 * h + 1] = s.y;
+                b.z[2 * h] = z.x; b.z[2 * h + 1] = z.y;
+            } else {
+                const float4 s = *at<float4>(a.scale, g), z = *at<float4>(a.zero, g);
+                b.s[4 * h] = s.x; b.s[4 * h + 1] = s.y; b.s[4 * h + 2] = s.z; b.s[4 * h + 3] = s.w;
+                b.z[4 * h] = z.x; b.z[4 * h + 1] = z.y; b.z[4 * h + 2] = z.z; b.z[4 * h + 3] = z.w;
+            }
+        }
+    }
+}
+
 // B operand j (8-k run j of a lane's 64) by direct quotients, in operand order
 template <int NB, int GPC, bool BF>
 __device__ __forceinline__ uint4 quotients(const StepBuf<NB, GPC> &b, int j)
 {
     constexpr uint32_t MASK = (1u << NB) - 1u;
     constexpr int ord[8] = {0, 2, 4, 6, 1, 3, 5, 7};
-    const int gi = GPC == 1 ? 0 : GPC == 2 ? (j >> 2) : j;
+    const int gi = j * GPC / 8;
     const double R = reciprocal(b.s[gi]);
     float v[8];
 #pragma unroll
@@ -153,7 +186,7 @@ __device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], ui
                                              RowRuns &&a)
 {
     Tab4 tab[NM];
-    if constexpr (NB == 4 && GPC < 8) {
+    if constexpr (NB == 4 && GPC <= 2) {
 #pragma unroll
         for (int m = 0; m < NM; ++m)
             tab[m] = make_tab4<BF>(b[m].s[GPC == 1 ? 0 : H], b[m].z[GPC == 1 ? 0 : H]);
@@ -167,7 +200,7 @@ __device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], ui
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             uint4 B;
-            if constexpr (NB == 4 && GPC < 8)
+            if constexpr (NB == 4 && GPC <= 2)
                 B = lookup4(tab[m], b[m].w[4 * H + j]);
             else
                 B = quotients<NB, GPC, BF>(b[m], 4 * H + j);
@@ -220,7 +253,7 @@ skinny_kernel(SkinnyArgs s)
         const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
 #pragma unroll
         for (int j = 0; j < NM; ++j)
-            load_step(buf[j], s.w[j], c, nw, ng);
+            fetch(buf[j], s.w[j], c, nw, ng);
     };
     // the first codes are on their way before X is staged
     if (my > 0)
@@ -356,14 +389,13 @@ hipError_t launch_gpc(const SkinnyArgs &s, hipStream_t st)
 template <int NM, int NB, bool BF>
 hipError_t launch_mt(const SkinnyArgs &s, hipStream_t st)
 {
-    const int gpc = groups_per_chunk(s.w[0].gs);
-    if (s.w[0].M <= 16)
-        return gpc == 1   ? launch_gpc<NM, NB, 1, 1, BF>(s, st)
-               : gpc == 2 ? launch_gpc<NM, NB, 1, 2, BF>(s, st)
-                          : launch_gpc<NM, NB, 1, 8, BF>(s, st);
-    return gpc == 1   ? launch_gpc<NM, NB, 2, 1, BF>(s, st)
-           : gpc == 2 ? launch_gpc<NM, NB, 2, 2, BF>(s, st)
-                      : launch_gpc<NM, NB, 2, 8, BF>(s, st);
+    const bool one = s.w[0].M <= 16;
+    switch (groups_of(s.w[0].gs)) {
+    case 1: return one ? launch_gpc<NM, NB, 1, 1, BF>(s, st) : launch_gpc<NM, NB, 2, 1, BF>(s, st);
+    case 2: return one ? launch_gpc<NM, NB, 1, 2, BF>(s, st) : launch_gpc<NM, NB, 2, 2, BF>(s, st);
+    case 4: return one ? launch_gpc<NM, NB, 1, 4, BF>(s, st) : launch_gpc<NM, NB, 2, 4, BF>(s, st);
+    default: return one ? launch_gpc<NM, NB, 1, 8, BF>(s, st) : launch_gpc<NM, NB, 2, 8, BF>(s, st);
+    }
 }
 
 template <int NM>
