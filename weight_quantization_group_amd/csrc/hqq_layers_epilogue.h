@@ -19,33 +19,45 @@ __device__ __forceinline__ double reciprocal(float s)
     return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
-// the value of lane I of the caller's eight neighbours (lanes 8 i .. 8 i + 7)
-template <int I>
-__device__ __forceinline__ float from_eighth(float x)
+// x of lane I of the caller's SH neighbours (lanes SH i .. SH i + SH - 1)
+template <int SH, int I>
+__device__ __forceinline__ uint32_t from_neighbour(uint32_t x)
 {
-    return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(x), 0x18 | I << 5));
+    return (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, (0x1f & ~(SH - 1)) | I << 5);
 }
 
-template <int I>
-__device__ __forceinline__ double from_eighth(double x)
+// Z[i] and R[i] = 1 / s of row i of 8: SH neighbouring lanes work on the same rows and in
+// one group of each, and lane j of them holds the scales s[k] and zeros z[k] of rows SH k + j.
+template <int SH, int I = 0>
+__device__ __forceinline__ void share_meta(const float (&z)[8 / SH], const double (&r)[8 / SH], double (&R)[8], float (&Z)[8])
 {
-    uint32_t w[2];
-    __builtin_memcpy(w, &x, 8);
-    w[0] = (uint32_t)__builtin_amdgcn_ds_swizzle((int)w[0], 0x18 | I << 5);
-    w[1] = (uint32_t)__builtin_amdgcn_ds_swizzle((int)w[1], 0x18 | I << 5);
-    __builtin_memcpy(&x, w, 8);
-    return x;
+    if constexpr (I < 8) {
+        if constexpr (SH == 1) {
+            R[I] = r[I];
+            Z[I] = z[I];
+        } else {
+            uint32_t w[2], f;
+            __builtin_memcpy(w, &r[I / SH], 8);
+            __builtin_memcpy(&f, &z[I / SH], 4);
+            w[0] = from_neighbour<SH, I % SH>(w[0]);
+            w[1] = from_neighbour<SH, I % SH>(w[1]);
+            f = from_neighbour<SH, I % SH>(f);
+            __builtin_memcpy(&R[I], w, 8);
+            __builtin_memcpy(&Z[I], &f, 4);
+        }
+        share_meta<SH, I + 1>(z, r, R, Z);
+    }
 }
 
-// z[i] and R[i] = 1 / s of row i: eight neighbouring lanes work on the same 8 rows and in
-// one group of each, lane i of them holds row i's scale and zero
-__device__ __forceinline__ void share_meta(float s, float z, double (&R)[8], float (&Z)[8])
+// the same from the scales
+template <int SH>
+__device__ __forceinline__ void row_meta(const float (&s)[8 / SH], const float (&z)[8 / SH], double (&R)[8], float (&Z)[8])
 {
-    const double r = reciprocal(s);
-    R[0] = from_eighth<0>(r); R[1] = from_eighth<1>(r); R[2] = from_eighth<2>(r); R[3] = from_eighth<3>(r);
-    R[4] = from_eighth<4>(r); R[5] = from_eighth<5>(r); R[6] = from_eighth<6>(r); R[7] = from_eighth<7>(r);
-    Z[0] = from_eighth<0>(z); Z[1] = from_eighth<1>(z); Z[2] = from_eighth<2>(z); Z[3] = from_eighth<3>(z);
-    Z[4] = from_eighth<4>(z); Z[5] = from_eighth<5>(z); Z[6] = from_eighth<6>(z); Z[7] = from_eighth<7>(z);
+    double r[8 / SH];
+#pragma unroll
+    for (int i = 0; i < 8 / SH; ++i)
+        r[i] = reciprocal(s[i]);
+    share_meta<SH>(z, r, R, Z);
 }
 
 // LDS of one wave: written by some lanes and read by others

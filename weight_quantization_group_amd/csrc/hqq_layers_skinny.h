@@ -5,9 +5,8 @@
 // Forward (skinny_kernel), C [M, N] = X . W_hat^T: a workgroup owns 16 columns
 // n (of the gated block: the same 16 of gate and of up, which share the rows
 // of X) and its waves split K.  Lane l works on row n = l % 16 and, in each
-// 256-wide step, on the 64 consecutive k at 64 (l / 16): the codes of one
-// group (or a few), dequantized in registers to the eight operands of eight
-// 16x16x32 MFMAs.  The next step's codes load under the current one's
+// 256-wide step, on 64 k, the codes of one group or a few, dequantized in
+// registers to the eight operands of eight 16x16x32 MFMAs.  The next step's codes load under the current one's
 // arithmetic.  The waves add their sums through LDS, and the operator's
 // arithmetic follows there.
 //
@@ -90,12 +89,11 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
     }
 }
 
-// X where it stays in global memory: a wave fetches its step's rows in two halves (of
-// each lane quarter's 64 k, the first and the last 32), 64 bytes in a row per four
-// lanes, and turns them into operands through 4 MT KiB of LDS of its own.  (An operand
-// fetched directly touches a cache line per lane, and what was fetched is gone from the
-// L1 cache by the next operand: 59 against 39 us for the gated block of 24 rows through
-// 4096 x 11008 at 8 bits.)  Run j of quarter q of row r lies at 64 j + 16 q + (r ^ (j + 4 q))
+// X where it stays in global memory: a wave fetches its step's rows in two halves (each
+// lane quarter's first and second 32 k), 64 bytes or more in a row, and turns them into
+// operands through 4 MT KiB of LDS of its own.  (An operand fetched directly touches a
+// cache line per lane, and what was fetched is gone from the L1 cache by the next operand:
+// 59 against 41 us for the gated block of 24 rows through 4096 x 11008 at 8 bits.)  Run j of quarter q of row r lies at 64 j + 16 q + (r ^ (j + 4 q))
 // of its 16-row block: the writes of 8 neighbouring lanes, and the reads, fall into
 // different banks.
 template <int MT>
@@ -129,8 +127,32 @@ __device__ __forceinline__ void store_half(const XHalf<MT> &b, uint4 *xs, uint32
     }
 }
 
-// Scales of a lane's 64 k: 1 (groups of 64 and more), 2 (32), 4 (16) or 8 (8)
-constexpr int groups_of(int gs) { return gs >= 64 ? 1 : 64 / gs; }
+// A lane's 64 k of a 256-wide step are two halves of 32.  In groups of 64 and more, at up
+// to 4 bits, they lie next to each other in one group, whose scale (and table) serves both;
+// else the lane quarters' first halves lie side by side, then their second ones, so that
+// the loads of codes and of X cover whole lines (24 rows through 4096 x 11008 8-bit 43.4 ->
+// 40.8 us, 32 rows in groups of 16 55 -> 48; 2-bit groups of 64 lose, 27 -> 29).
+template <int GPC>
+struct Span {
+    static constexpr uint32_t lane = GPC == 1 ? 64 : 32;     // from quarter to quarter
+    static constexpr uint32_t half = GPC == 1 ? 32 : 128;    // from half to half
+};
+
+// Scales of a lane's 64 k
+constexpr int groups_of(int nbits, int gs) { return gs >= 64 && nbits < 8 ? 1 : gs >= 32 ? 2 : 64 / gs; }
+
+// Where the halves start; one past K (K % 256 != 0) is moved to the last 32 k, in bounds
+// and cleared
+template <bool KT, typename S>
+__device__ __forceinline__ Chunk halves(uint32_t kbase, int quarter, uint32_t K)
+{
+    uint32_t k0 = kbase + S::lane * (uint32_t)quarter, kh = k0 + S::half;
+    if constexpr (KT) {
+        k0 = k0 < K ? k0 : K - 32;
+        kh = kh < K ? kh : K - 32;
+    }
+    return Chunk{k0, kh};
+}
 
 // A lane's codes and scales of a step.  A half's 2 or 4 small groups lie next to each
 // other, on 8 and 16 bytes (K is a multiple of 32): one load each (fetched one by one,
@@ -225,6 +247,7 @@ template <int NM, bool KT, int NB, int MT, int GPC, bool XL, bool BF>
 __global__ __launch_bounds__(kSkinnyWaves * 64) __attribute__((amdgpu_waves_per_eu(waves_per_simd(NM, NB, MT, GPC)))) void
 skinny_kernel(SkinnyArgs s)
 {
+    using S = Span<GPC>;
     const int WPB = blockDim.x >> 6;
     extern __shared__ uint4 lds[];
     const LinearArgs &a = s.w[0];
@@ -250,7 +273,7 @@ skinny_kernel(SkinnyArgs s)
     auto kbase = [&](int i) { return (uint32_t)(wave + i * WPB) * kStepK; };
     StepBuf<NB, GPC> buf[NM];
     auto load = [&](int i) {
-        const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
+        const Chunk c = halves<KT, S>(kbase(i), grp, K);
 #pragma unroll
         for (int j = 0; j < NM; ++j)
             fetch(buf[j], s.w[j], c, nw, ng);
@@ -275,10 +298,10 @@ skinny_kernel(SkinnyArgs s)
             acc[j][u] = float4v{0.f, 0.f, 0.f, 0.f};
     if constexpr (XL) {
         for (int i = 0; i < my; ++i) {
-            const Chunk c = lane_chunk<KT>(kbase(i), grp, K);
-            const uint32_t k0 = kbase(i) + kLaneK * grp;
+            const Chunk c = halves<KT, S>(kbase(i), grp, K);
+            const uint32_t k0 = kbase(i) + S::lane * grp;
             const uint32_t km0 = k0 < K ? 0xffffffffu : 0u;
-            const uint32_t km1 = k0 + 32 < K ? 0xffffffffu : 0u;
+            const uint32_t km1 = k0 + S::half < K ? 0xffffffffu : 0u;
             StepBuf<NB, GPC> cur[NM];
 #pragma unroll
             for (int j = 0; j < NM; ++j)
@@ -298,28 +321,28 @@ skinny_kernel(SkinnyArgs s)
         uint4 *xs = lds + wave * (256 * MT);
         auto run = [&](int u, int j) { return xs[u * 256 + 64 * j + (lane & 48) + ((lane & 15) ^ (j + 4 * grp))]; };
         // the run this lane fetches, of the first half of step i
-        auto krun = [&](int i) { return kbase(i) + kLaneK * (uint32_t)((lane >> 2) & 3) + 8 * (uint32_t)(lane & 3); };
+        auto krun = [&](int i) { return kbase(i) + S::lane * (uint32_t)((lane >> 2) & 3) + 8 * (uint32_t)(lane & 3); };
         XHalf<MT> x;
         if (my > 0)
             load_half<KT>(x, a, krun(0), (uint32_t)m0, mrows, lane);
         for (int i = 0; i < my; ++i) {
-            const uint32_t k0 = kbase(i) + kLaneK * grp, kr = krun(i);
+            const uint32_t k0 = kbase(i) + S::lane * grp, kr = krun(i);
             StepBuf<NB, GPC> cur[NM];
 #pragma unroll
             for (int j = 0; j < NM; ++j)
                 cur[j] = buf[j];
             store_half<KT>(x, xs, kr < K ? 0xffffffffu : 0u, lane);
             wave_fence();
-            load_half<KT>(x, a, kr + 32, (uint32_t)m0, mrows, lane);
+            load_half<KT>(x, a, kr + S::half, (uint32_t)m0, mrows, lane);
             if (i + 1 < my)
                 load(i + 1);
             compute_half<0, KT, BF>(cur, k0 < K ? 0xffffffffu : 0u, acc, run);
             wave_fence();
-            store_half<KT>(x, xs, kr + 32 < K ? 0xffffffffu : 0u, lane);
+            store_half<KT>(x, xs, kr + S::half < K ? 0xffffffffu : 0u, lane);
             wave_fence();
             if (i + 1 < my)
                 load_half<KT>(x, a, krun(i + 1), (uint32_t)m0, mrows, lane);
-            compute_half<1, KT, BF>(cur, k0 + 32 < K ? 0xffffffffu : 0u, acc, run);
+            compute_half<1, KT, BF>(cur, k0 + S::half < K ? 0xffffffffu : 0u, acc, run);
             wave_fence();
         }
     }
@@ -390,8 +413,11 @@ template <int NM, int NB, bool BF>
 hipError_t launch_mt(const SkinnyArgs &s, hipStream_t st)
 {
     const bool one = s.w[0].M <= 16;
-    switch (groups_of(s.w[0].gs)) {
-    case 1: return one ? launch_gpc<NM, NB, 1, 1, BF>(s, st) : launch_gpc<NM, NB, 2, 1, BF>(s, st);
+    const int gpc = groups_of(NB, s.w[0].gs);
+    if constexpr (NB < 8)
+        if (gpc == 1)
+            return one ? launch_gpc<NM, NB, 1, 1, BF>(s, st) : launch_gpc<NM, NB, 2, 1, BF>(s, st);
+    switch (gpc) {
     case 2: return one ? launch_gpc<NM, NB, 1, 2, BF>(s, st) : launch_gpc<NM, NB, 2, 2, BF>(s, st);
     case 4: return one ? launch_gpc<NM, NB, 1, 4, BF>(s, st) : launch_gpc<NM, NB, 2, 4, BF>(s, st);
     default: return one ? launch_gpc<NM, NB, 1, 8, BF>(s, st) : launch_gpc<NM, NB, 2, 8, BF>(s, st);

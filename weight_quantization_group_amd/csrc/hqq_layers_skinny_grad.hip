@@ -32,12 +32,11 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t *p)
         return uint2{*p, 0u};
 }
 
-// One step of a lane: the codes and meta of 8 rows (SH: of one, to be shared), and its
-// runs of A
-template <int NB, int MT, bool SH>
+// One step of a lane: the codes of 8 rows, the meta of 8 / SH of them, and its runs of A
+template <int NB, int MT, int SH>
 struct GradBuf {
     uint2 c[8];
-    float s[SH ? 1 : 8], z[SH ? 1 : 8];
+    float s[8 / SH], z[8 / SH];
     uint4 a[MT];
 };
 
@@ -57,9 +56,9 @@ __device__ __forceinline__ uint4 load_run(const uint16_t *row, int n, int N)
     return uint4{w[0], w[1], w[2], w[3]};
 }
 
-// AL: the runs of A are 16-byte aligned.  SH: groups of 64 or more, of which eight lanes
-// fetch, and take the reciprocal of, one each
-template <int NB, int MT, bool BF, bool AL, bool SH>
+// AL: the runs of A are 16-byte aligned.  SH: neighbouring lanes whose 8 k lie in the same
+// groups (8 in groups of 64 and more); each fetches and inverts 8 / SH of the 8 scales
+template <int NB, int MT, bool BF, bool AL, int SH>
 __global__ __launch_bounds__(kGradWaves * 64) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 3))) void
 skinny_grad_kernel(SkinnyGradArgs a)
 {
@@ -102,8 +101,8 @@ skinny_grad_kernel(SkinnyGradArgs a)
             buf.c[i] = load_codes<NB>(at<uint8_t>(packed, n * (uint32_t)a.wpr * 4u + (uint32_t)kc * NB / 8));
         }
 #pragma unroll
-        for (int i = 0; i < (SH ? 1 : 8); ++i) {
-            const int nr = n0 + (SH ? l16 & 7 : i);
+        for (int i = 0; i < 8 / SH; ++i) {
+            const int nr = n0 + SH * i + (l16 & (SH - 1));
             const uint32_t g = (uint32_t)(nr < N ? nr : N - 1) * (uint32_t)a.gpl + ((uint32_t)kc >> a.gshift);
             buf.s[i] = *at<float>(scale, 4 * g);
             buf.z[i] = *at<float>(zero, 4 * g);
@@ -128,15 +127,7 @@ skinny_grad_kernel(SkinnyGradArgs a)
             load(s + kGradWaves);
         double R[8];
         float Z[8];
-        if constexpr (SH) {
-            share_meta(cur.s[0], cur.z[0], R, Z);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                R[i] = reciprocal(cur.s[i]);
-                Z[i] = cur.z[i];
-            }
-        }
+        row_meta<SH>(cur.s, cur.z, R, Z);
         uint32_t v[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -206,10 +197,12 @@ template <int NB, int MT, bool BF, bool AL>
 hipError_t launch_sh(const SkinnyGradArgs &a, hipStream_t s)
 {
     const dim3 grid((unsigned)((a.K + 127) / 128), (unsigned)a.splits, (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-    if (a.gshift >= 6)
-        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, true>), grid, dim3(kGradWaves * 64), 0, s, a);
-    else
-        hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, false>), grid, dim3(kGradWaves * 64), 0, s, a);
+    switch (a.gshift) {
+    case 3: hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, 1>), grid, dim3(kGradWaves * 64), 0, s, a); break;
+    case 4: hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, 2>), grid, dim3(kGradWaves * 64), 0, s, a); break;
+    case 5: hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, 4>), grid, dim3(kGradWaves * 64), 0, s, a); break;
+    default: hipLaunchKernelGGL((skinny_grad_kernel<NB, MT, BF, AL, 8>), grid, dim3(kGradWaves * 64), 0, s, a);
+    }
     return hipGetLastError();
 }
 

@@ -9,9 +9,9 @@
 // 8 XCDs in turn; each XCD gets a contiguous part of them, so that the lines of codes,
 // scales and zeros that neighbours along k share are fetched into one L2 only.  Bound
 // by the bytes: 52 us for the 90 M weights of a 4096 x 11008 pair at 4 bits in groups
-// of 64, 180 MB written and 56 read, 4.5 TB/s where a large copy reaches 5.1.  In groups
-// of 64 or more (SH) the eight lanes of a row fetch and invert one scale for one row
-// each and share them; without that the same took 64 us.
+// of 64, 180 MB written and 56 read, 4.5 TB/s where a large copy reaches 5.1.  The SH
+// lanes of a row that work in one group (8 in groups of 64 and more) fetch and invert the
+// scales of 8 / SH rows each and share them; without that the same took 64 us.
 #include "hqq_layers_epilogue.h"
 
 namespace hqq {
@@ -47,7 +47,7 @@ __device__ void pad_rows(const PadJob &p)
 // multiple of 8.  (A flat grid with a table of first workgroups costs loads of arguments
 // that wait for one another: 3 us of a
 // 26 us gated block, 333 rows through 1056 x 2753.)
-template <int NB, bool BF, bool SH>
+template <int NB, bool BF, int SH>
 __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
 {
     constexpr uint32_t MASK = (1u << NB) - 1u;
@@ -76,16 +76,16 @@ __global__ __launch_bounds__(kUnpackWaves * 64) void unpack_kernel(UnpackArgs a)
     const int64_t r = k_in ? run : runs - 1;
     double R[8];
     float Z[8];
-    if constexpr (SH) {
-        const int64_t n = n0 + kl < an ? n0 + kl : an - 1, g = n * a.gpl + ((8 * r) >> a.gshift);
-        share_meta(a.scale[which][g], a.zero[which][g], R, Z);
-    } else {
+    {
+        float sc[8 / SH], ze[8 / SH];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t n = n0 + i < an ? n0 + i : an - 1, g = n * a.gpl + ((8 * r) >> a.gshift);
-            R[i] = reciprocal(a.scale[which][g]);
-            Z[i] = a.zero[which][g];
+        for (int i = 0; i < 8 / SH; ++i) {
+            const int64_t nr = n0 + SH * i + (kl & (SH - 1)), n = nr < an ? nr : an - 1;
+            const int64_t g = n * a.gpl + ((8 * r) >> a.gshift);
+            sc[i] = a.scale[which][g];
+            ze[i] = a.zero[which][g];
         }
+        row_meta<SH>(sc, ze, R, Z);
     }
     uint32_t v[8][4];     // row i: 8 values of the run
 #pragma unroll
@@ -131,10 +131,12 @@ hipError_t launch_nb(const UnpackArgs &a, hipStream_t s)
         n = a.n[i] > n ? a.n[i] : n;
     const int64_t squares = (a.K + 64 * kUnpackWaves - 1) / (64 * kUnpackWaves) * ((n + 63) / 64);
     const dim3 grid((unsigned)round_up(squares, 8), (unsigned)(a.count + a.pads));
-    if (a.gshift >= 6)
-        hipLaunchKernelGGL((unpack_kernel<NB, BF, true>), grid, dim3(kUnpackWaves * 64), 0, s, a);
-    else
-        hipLaunchKernelGGL((unpack_kernel<NB, BF, false>), grid, dim3(kUnpackWaves * 64), 0, s, a);
+    switch (a.gshift) {
+    case 3: hipLaunchKernelGGL((unpack_kernel<NB, BF, 1>), grid, dim3(kUnpackWaves * 64), 0, s, a); break;
+    case 4: hipLaunchKernelGGL((unpack_kernel<NB, BF, 2>), grid, dim3(kUnpackWaves * 64), 0, s, a); break;
+    case 5: hipLaunchKernelGGL((unpack_kernel<NB, BF, 4>), grid, dim3(kUnpackWaves * 64), 0, s, a); break;
+    default: hipLaunchKernelGGL((unpack_kernel<NB, BF, 8>), grid, dim3(kUnpackWaves * 64), 0, s, a);
+    }
     return hipGetLastError();
 }
 
