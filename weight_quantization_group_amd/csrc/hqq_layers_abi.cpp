@@ -45,21 +45,19 @@ int check_sizes(int64_t M, int64_t K, int64_t N, int nbits, int group_size)
 // Whether a product runs straight from the codes (which every 32 rows dequantize
 // anew) or W_hat is unpacked for the tiled product.  n: all rows of its weights.
 // By the rows, and for small weights, which leave the CUs room for the row blocks, by
-// blocks of 32 rows times weights.  Crossovers measured on MI355X in bf16, 1, 2, 4 and 8
-// bits, codes against unpacked in us at 4 bits:
-//              1024 x 2816              4096 x 11008               8192 x 28672
-//   pair       g64 128 rows 12/15       g64 64 54/80, 128 92/90    64 267/486, 128 524/503
-//              g16 64 15/16, 96 21/16   g16 32 70/92, 48 124/92    32 298/507, 64 573/511
-//   its grad.  g64 64 28/29, 96 32/30   g64 64 119/120, 96 174/132 64 628/656, 128 1061/695
-//              g16 32 27/27, 48 33/29   g32 32 89/120, 48 152/121  32 393/688, 64 771/690
-//   one grad.  g64 64 14/15, 96 16/15   g64 64 38/46, 96 57/48     64 174/239, 128 277/234
-//   head       g64 128 14/19            g64 64 45/52, 96 64/53     64 171/338, 128 337/340
-//              g16 96 18/19, 128 19/19  g16 32 47/54, 48 77/54     32 164/327, 64 306/328
-//   its grad.  g64 96 25/26, 128 27/26  g64 32 52/69, 48 74/70     64 339/434, 128 580/443
-//              g16 48 23/24, 64 25/25   g16 24 72/72, 32 74/73     32 276/426, 64 521/438
-// and heads of 1024 x 32003: g64 32 rows 27/35, 48 39/35, g16 32 38/36, their gradients
-// g64 32 44/46, 48 59/48, g16 16 51/46.  Groups of 8 and 16 cost a reciprocal each per
-// lane and are dear to dequantize twice.
+// blocks of 32 rows times weights.  Crossovers measured on MI355X in bf16 at 1, 2, 4 and
+// 8 bits in groups of 8 to 128; rows, codes / unpacked in us at 4 bits (groups of 64, and
+// of 16 where they differ):
+//              1024 x 2816        1024 x 32003       4096 x 11008       8192 x 28672
+//   pair       128 12/15          64 39/53, 96 56/64 64 55/85, 128 94/85 96 391/496, 128 516/503
+//   its grad.  64 29/29, 96 32/30 32 61/78, 48 90/80 64 119/120, 96 178/123 64 620/654
+//     g16      64 30/30           32 74/96           32 92/127, 48 160/130 64 746/668
+//   one grad.  64 13/15, 96 16/15 32 35/33, 48 44/34 64 38/45, 96 58/50 64 162/240, 96 253/228
+//     g16                                            32 36/46, 48 50/47 64 219/248
+//   head       128 14/19          32 26/34, 48 37/34 64 45/53, 96 65/53 96 251/324, 128 327/320
+//   its grad.  96 25/26           32 43/45, 48 57/47 32 52/69, 48 74/70 64 327/435, 96 472/439
+// (Large weights leave the last-level cache between unpacking and use; a shallow weight
+// makes the few-rows kernels' ends weigh more.)
 // HQQ_LAYERS_PATH=codes or =tiled in the environment, read at each call, forces one
 // (tests run both), the codes up to the 256 rows beyond which the rule never takes
 // them: their kernels address the activations by 32-bit offsets.
@@ -75,14 +73,14 @@ bool straight(Product what, int64_t M, int64_t K, int64_t n, int group_size)
         if (strcmp(e, "tiled") == 0)
             return false;
     }
-    const bool fine = group_size < 32, shallow = K < 2048;
-    int64_t rows = 64, work = 6;          // work: millions of weights times blocks of 32 rows
+    const bool small_groups = group_size < 64, shallow = K < 2048, large = K * n > 200000000;
+    int64_t rows = 0, work = 0;           // work: millions of weights times blocks of 32 rows
     switch (what) {
-    case kPair: rows = fine ? 32 : 64; work = fine ? 12 : 24; break;
-    case kPairGrad: rows = group_size < 64 ? 32 : 64; work = fine ? 6 : 12; break;
-    case kBackward: break;
-    case kHead: rows = fine || shallow ? 32 : 64; work = 12; break;
-    case kHeadGrad: rows = fine ? (shallow ? 8 : 32) : K * n > 100000000 ? 64 : 32; work = fine ? 6 : 9; break;
+    case kPair: rows = large ? 96 : 64; work = 24; break;
+    case kPairGrad: rows = small_groups || shallow ? 32 : 64; work = 12; break;
+    case kBackward: rows = !large && (small_groups || shallow) ? 32 : 64; work = 6; break;
+    case kHead: rows = large ? 96 : shallow ? 32 : 64; work = 12; break;
+    case kHeadGrad: rows = large ? 64 : 32; work = 9; break;
     }
     return M <= rows || (M + 31) / 32 * K * n <= work * 1000000;
 }
