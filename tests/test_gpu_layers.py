@@ -627,3 +627,38 @@ def test_the_most_rows(hq):
     loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 1, 64)
     check_loss(loss[rows], lse[rows], X[rows], W, t[rows])
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("gs", [8, 16, 32, 64, 128, 256])
+@pytest.mark.parametrize("nbits", [1, 2, 4, 8])
+def test_every_format(hq, path, nbits, gs):
+    """Each code width and group size, with depths that end on a 256-wide step and inside one."""
+    for K in (512, 544 if gs <= 32 else 9 * gs if gs == 64 else 5 * gs):
+        for M, N in ((2, 50), (9, 33), (20, 70), (70, 40)):
+            for dtype in DTYPES:
+                tag = f"{M} x {K} x {N} {dtype}"
+                gate, Wg = make_weight(nbits, N, K, nbits, gs, dtype)
+                up, Wu = make_weight(gs, N, K, nbits, gs, dtype)
+                X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+                check_gated(hq.hqq_linear_gated(X, gate, up, N, nbits, gs), X, Wg, Wu, "silu", tag)
+                check_gated_backward(hq.hqq_linear_gated_backward(dY, X, gate, up, N, nbits, gs), dY, X, Wg, Wu, "silu", tag)
+                y = dY.double()
+                dX = hq.hqq_linear_batch_backward([dY, dY], [gate + (N,), up + (N,)], K, nbits, gs)
+                within(dX, *grad_bound([y, y], [torch.zeros_like(y)] * 2, [Wg, Wu], dtype), tag)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("nbits,gs", [(1, 32), (2, 16), (2, 64), (4, 8), (4, 16), (4, 32), (4, 64), (8, 8), (8, 32), (8, 128)])
+def test_weights_are_the_dequantized_ones(hq, path, nbits, gs, dtype):
+    """One-hot inputs give back W_hat, bit for bit what hqq_dequantize writes: rows through the
+    backward pass, and a single class's weights through the log-sum-exp of one logit."""
+    N, K = 200, 256
+    w, _ = make_weight(nbits + gs, N, K, nbits, gs, dtype, std=3.0)
+    want = hq.hqq_dequantize(*w, N, K, nbits, gs, 1, dtype=dtype)
+    eye = torch.eye(N, device="cuda", dtype=dtype)
+    assert torch.equal(hq.hqq_linear_backward(eye, *w, K, nbits, gs), want)
+    X, t = torch.eye(K, device="cuda", dtype=dtype), torch.zeros(K, dtype=torch.int64, device="cuda")
+    for n in (0, 7, N - 1):
+        row = tuple(a[n:n + 1].clone() for a in w)
+        _, lse = hq.hqq_linear_cross_entropy(X, t, *row, 1, nbits, gs)
+        assert torch.equal(lse, want[n].float()), n
