@@ -93,8 +93,9 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
 // lane quarter's first and second 32 k), 64 bytes or more in a row, and turns them into
 // operands through 4 MT KiB of LDS of its own.  (An operand fetched directly touches a
 // cache line per lane, and what was fetched is gone from the L1 cache by the next operand:
-// 59 against 41 us for the gated block of 24 rows through 4096 x 11008 at 8 bits.)  Run j of quarter q of row r lies at 64 j + 16 q + (r ^ (j + 4 q))
-// of its 16-row block: the writes of 8 neighbouring lanes, and the reads, fall into
+// 59 against 41 us for the gated block of 24 rows through 4096 x 11008 at 8 bits.)  Run j
+// of quarter q of row r lies at 64 j + 16 q + (r ^ (j + 4 q)) of its 16-row block: the
+// writes of 8 neighbouring lanes, and the reads, fall into
 // different banks.
 template <int MT>
 struct XHalf {
