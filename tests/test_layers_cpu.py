@@ -139,6 +139,25 @@ def test_rejects_row_arrays(w, lib):
         assert call(w, lib, targets=0x1004) == PTR
 
 
+def test_rejects_overlapping_outputs(w, lib):
+    """An output that shares bytes with an input, the other output or the workspace."""
+    far = [0x10000000 * i for i in range(1, 7)]
+    M, K, N = 4, 128, 40
+    need = w.hqq_linear_gated_backward_workspace(M, K, N, 4, 64)
+    x, y, ws = far[0], far[1], far[2]
+    assert gated(w, lib, X=x, Y=x + 2 * M * K - 16, ws=ws) == PTR
+    assert gated(w, lib, X=x, Y=x - 2 * M * N + 16, ws=ws) == PTR
+    for dX in (x, y, x + 2 * M * K - 16, y - 2 * M * K + 16, ws + need - 16):
+        assert gated_backward(w, lib, dY=y, X=x, dX=dX, ws=ws) == PTR
+    for dX in (A, y, y + 2 * M * N - 16):                  # A: the first weight's dY
+        assert batch_backward(w, lib, dY=y, dX=dX, ws=ws) == PTR
+    t = far[3]
+    for out in (dict(loss=x, lse=y), dict(loss=y, lse=t + 8 * M - 4), dict(loss=y, lse=y + 4 * M - 4), dict(loss=ws, lse=y)):
+        assert loss(w, lib, X=x, targets=t, ws=ws, **out) == PTR
+    for dX in (x, t, far[4], far[5]):
+        assert loss_backward(w, lib, X=x, targets=t, dloss=far[4], lse=far[5], dX=dX, ws=ws) == PTR
+
+
 def test_rejects_activation_and_counts(w, lib):
     for call in (gated, gated_backward):
         assert call(w, lib, act=3) == ACT and call(w, lib, act=-1) == ACT

@@ -6,6 +6,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <initializer_list>
+
 namespace {
 
 using namespace hqq;
@@ -111,6 +113,23 @@ int check_workspace(const void *ws, int64_t have, int64_t need)
     if (have < 0 || (!ws && have > 0) || (ws && !aligned(ws, 16)))
         return HQQ_EINVAL_PTR;
     return have < need ? HQQ_EWORKSPACE : HQQ_OK;
+}
+
+// Whether an output shares memory with something the call reads or uses
+struct Range {
+    const void *p;
+    int64_t bytes;
+};
+
+bool overlaps(Range out, std::initializer_list<Range> others)
+{
+    const uintptr_t a = (uintptr_t)out.p;
+    for (const Range &o : others) {
+        const uintptr_t b = (uintptr_t)o.p;
+        if (b && a < b + (uint64_t)o.bytes && b < a + (uint64_t)out.bytes)
+            return true;
+    }
+    return false;
 }
 
 // The workspace as a run of 256-byte aligned arrays; with a null base only
@@ -484,7 +503,7 @@ const char *hqq_layers_strerror(int status)
     case HQQ_EINVAL_NBITS: return "nbits must be 1, 2, 4 or 8";
     case HQQ_EINVAL_GROUP: return "group_size must be 8, 16, 32, 64, 128 or 256 and divide K";
     case HQQ_EINVAL_SHAPE: return "a size is out of range (K a multiple of 32; M, N, count >= 1 and within their limits)";
-    case HQQ_EINVAL_PTR: return "a pointer is NULL or misaligned";
+    case HQQ_EINVAL_PTR: return "a pointer is NULL or misaligned, or an output overlaps an input or the workspace";
     case HQQ_EHIP: return "a HIP kernel launch failed";
     case HQQ_EINVAL_DTYPE: return "dtype must be HQQ_DTYPE_FP16 or HQQ_DTYPE_BF16";
     case HQQ_EINVAL_ACT: return "act must be HQQ_ACT_SILU, HQQ_ACT_GELU or HQQ_ACT_GELU_TANH";
@@ -517,6 +536,8 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
     const GatedLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
+    if (overlaps({Y, 2 * M * N}, {{X, 2 * M * K}, {workspace, l.bytes}}))
+        return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     if (few) {
@@ -574,6 +595,8 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     const GatedGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
+    if (overlaps({dX, 2 * M * K}, {{X, 2 * M * K}, {dY, 2 * M * N}, {workspace, l.bytes}}))
+        return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const int64_t Np = round_up(N, 32), ldg = pitch_for(2 * Np);
@@ -677,6 +700,9 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
     const BatchGradLayout l(workspace, M, K, n, count, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
+    for (int i = 0; i < count; ++i)
+        if (overlaps({dX, 2 * M * K}, {{ws[i].dY, 2 * M * n[i]}, {workspace, l.bytes}}))
+            return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     if (few) {
@@ -734,6 +760,9 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
     const LossLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
+    if (overlaps({loss, 4 * M}, {{X, 2 * M * K}, {targets, 8 * M}, {lse, 4 * M}, {workspace, l.bytes}}) ||
+        overlaps({lse, 4 * M}, {{X, 2 * M * K}, {targets, 8 * M}, {workspace, l.bytes}}))
+        return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     if (few) {
@@ -801,6 +830,9 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
     const LossGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
+    if (overlaps({dX, 2 * M * K},
+                 {{X, 2 * M * K}, {targets, 8 * M}, {dloss, 4 * M}, {lse, 4 * M}, {workspace, l.bytes}}))
+        return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const float unit = bf16 ? 1.0f : 1.0f / 32768.0f;     // of the rounded differences
