@@ -237,6 +237,7 @@ __device__ __forceinline__ void compute_half(const StepBuf<NB, GPC> (&b)[NM], ui
 }
 
 // Waves per SIMD that leave the registers for this step's codes and scales and the next's
+// (three for the 8-bit pair of 32 rows would spill: 24 rows through 4096 x 11008 43 -> 49 us)
 constexpr int waves_per_simd(int nm, int nb, int mt, int gpc)
 {
     const int regs = nm * (4 * nb + 4 * gpc) + 20 * mt + 4 * nm * mt;
