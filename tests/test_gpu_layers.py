@@ -662,3 +662,19 @@ def test_weights_are_the_dequantized_ones(hq, path, nbits, gs, dtype):
         row = tuple(a[n:n + 1].clone() for a in w)
         _, lse = hq.hqq_linear_cross_entropy(X, t, *row, 1, nbits, gs)
         assert torch.equal(lse, want[n].float()), n
+
+
+def test_a_tensor_given_twice_has_to_fit(hq):
+    """The first gradient of a batch, and X given again as a gradient or as the output, are refused
+    where their width is not the weight's."""
+    dtype, M, K, N = torch.float16, 4, 128, 80
+    w, _ = make_weight(1, N, K, 4, 64, dtype)
+    X, narrow = normal(3, (M, K), dtype), normal(4, (M, 16), dtype)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_batch_backward([narrow], [w + (N,)], K, 4, 64)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_batch_backward([X, X], [w + (N,), w + (N,)], K, 4, 64)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_gated_backward(X, X, w, w, N, 4, 64)
+    with pytest.raises(ValueError):
+        hq.hqq_linear_gated(X, w, w, N, 4, 64, out=X)

@@ -232,3 +232,15 @@ def test_batch_width_limit(w, lib):
     arr = (HqqLinearGrad * 3)(*[HqqLinearGrad(A, A, A, N, A)] * 3)
     assert lib.hqq_linear_batch_backward(arr, 3, 1, 32, 1, 32, 0, A, A, 1 << 40, None) == SHAPE
     assert lib.hqq_linear_batch_backward(arr, 2, 400, 32, 1, 32, 0, A, A, 0, None) == WORKSPACE
+
+
+def test_binding_checks_the_shape_of_a_tensor_given_twice(w):
+    """The tensor that sets a call's dtype and device has to fit like any other: the first gradient
+    of a batch, or X given again as the gradient of an output of another width."""
+    import torch
+    from weight_quantization_group_amd.layers import _matrix
+
+    t = torch.zeros(4, 5, dtype=torch.float16)
+    for rows, cols in ((4, 500), (4, 4), (5, 5)):
+        with pytest.raises(ValueError):
+            _matrix(t, "dYs", rows, cols, t)

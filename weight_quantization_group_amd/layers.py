@@ -153,10 +153,6 @@ def _first(t, name: str):
 
 def _matrix(t, name: str, rows: int, cols: int, like) -> int:
     """The address of a [rows, cols] CUDA tensor of like's dtype and device, checked."""
-    if t is like:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
     if isinstance(t, torch.Tensor) and t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
     return _array(t, name, (like.dtype,), rows * cols, like.device)
