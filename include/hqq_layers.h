@@ -78,8 +78,9 @@ HQQ_API int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_
  *   dG = dY * U * act'(G),  dU = dY * act(G),  dX = dG . Wg_hat + dU . Wu_hat.
  *   dY [M, N] read, dX [M, K] written
  * dG and dU are formed in fp32 and rounded once to the dtype for the second
- * pair of products (fp16: relative to the row's largest |dY|, so that small
- * gradients keep their precision). */
+ * pair of products (fp16: times a power of two chosen per row from max |dY|,
+ * sum |X| and the weights' largest |W_hat|, so that neither small gradients nor
+ * small projections lose precision, and nothing overflows). */
 HQQ_API int64_t hqq_linear_gated_backward_workspace(int64_t M, int64_t K, int64_t N, int nbits,
                                                     int group_size);
 HQQ_API int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, int64_t K,

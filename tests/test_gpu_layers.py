@@ -678,3 +678,47 @@ def test_a_tensor_given_twice_has_to_fit(hq):
         hq.hqq_linear_gated_backward(X, X, w, w, N, 4, 64)
     with pytest.raises(ValueError):
         hq.hqq_linear_gated(X, w, w, N, 4, 64, out=X)
+
+
+@pytest.mark.parametrize("M", [5, 40])
+@pytest.mark.parametrize("gate_std,up_std", [(1.0, 1.0), (2.0 ** -6, 2.0 ** 6)])
+@pytest.mark.parametrize("xs", [2.0 ** -14, 2.0 ** -11, 2.0 ** -8, 2.0 ** -5, 1.0, 2.0 ** 10])
+def test_fp16_small_projections_keep_their_precision(hq, path, xs, gate_std, up_std, M):
+    """dG and dU shrink with the projections (activations of size xs) and with one weight beside
+    another, while dX stays of one size: they are formed relative to a bound b = max |dY| sum |X|
+    max |W_hat| of the row, brought to 2^13 at least.  Below fp16's normal range, 2^-14 there, a
+    rounding is off by 2^-25: by at most 2^-38 b in all."""
+    dtype, K, N = torch.float16, 512, 200
+    size = 1.0 / math.sqrt(K)
+    gate, Wg = make_weight(1, N, K, 4, 64, dtype, std=size * gate_std)
+    up, Wu = make_weight(2, N, K, 4, 64, dtype, std=size * up_std)
+    X, dY = normal(3, (M, K), dtype, xs), normal(4, (M, N), dtype, 2.0 ** -6 / xs)
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 64)
+    G, Up, f, d, eG, eU = gated_terms(X, Wg, Wu, "silu")
+    y, u = dY.double(), U[dtype]
+    dG, dU = y * Up * d, y * f
+    b = y.abs().amax(1, keepdim=True) * X.double().abs().sum(1, keepdim=True) * max(Wg.abs().max(), Wu.abs().max())
+    act_off = FN * (d.abs() + G.abs())
+    errG = 1.01 * y.abs() * ((Up.abs() + eU) * (1.2 * eG + act_off) + d.abs() * eU) + u * dG.abs() + 2.0 ** -38 * b
+    errU = 1.01 * y.abs() * (1.2 * eG + FN * f.abs()) + u * dU.abs() + 2.0 ** -38 * b
+    ref, bound = grad_bound([dG, dU], [errG * 1.01, errU * 1.01], [Wg, Wu], dtype)
+    within(dX, ref, bound)
+    # as independent errors, at most u of dG, dU and dX each: well within 4 u of the norm
+    assert (dX.double() - ref).norm() <= 4 * u * ref.norm()
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_fp16_rows_without_a_gradient(hq, path, M):
+    """Rows of zeros in dY or X give zeros, the least and the largest values that fp16 has stay finite."""
+    dtype, K, N = torch.float16, 96, 33
+    gate, _ = make_weight(1, N, K, 4, 32, dtype)
+    up, _ = make_weight(2, N, K, 4, 32, dtype)
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+    dY[0] = 0
+    X[1] = 0
+    dY[2], X[2] = 2.0 ** -24, 2.0 ** -24
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 32)
+    assert (dX[:3] == 0).all() and torch.isfinite(dX).all()
+    X[1], dY[1] = 65504.0, 2.0 ** -24
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 32)
+    assert torch.isfinite(dX[1]).all()

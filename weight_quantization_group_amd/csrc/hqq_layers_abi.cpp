@@ -347,7 +347,7 @@ struct GatedLayout {
 
 struct GatedGradLayout {
     uint16_t *W, *dGU, *X;
-    float *scale, *inv, *part;
+    float *row, *weight, *inv, *part;     // row, weight: a GradBound's
     int64_t bytes;
     GatedGradLayout(void *p, int64_t M, int64_t K, int64_t N, bool few)
     {
@@ -359,7 +359,8 @@ struct GatedGradLayout {
             X = c.take_some<uint16_t>(pad_values(mc, K));
         }
         dGU = c.take<uint16_t>(mc * pitch_for(2 * Np));
-        scale = c.take<float>(mc);
+        row = c.take<float>(mc);
+        weight = c.take<float>(kBoundParts);
         inv = c.take<float>(mc);
         const int64_t n[2] = {N, N};
         part = c.take_some<float>(few ? few_part_floats(M, K, grad_steps(n, 2))
@@ -600,8 +601,23 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     const int64_t Np = round_up(N, 32), ldg = pitch_for(2 * Np);
+    // fp16: dG and dU relative to a bound of the row's (bf16 has fp32's range)
+    auto bound_rows = [&](int64_t m0, int64_t m) {
+        if (bf16)
+            return hipSuccess;
+        BoundArgs b{X + m0 * K, dY + m0 * N, m, K, N, l.row};
+        b.scale[0] = gate->scale;
+        b.scale[1] = up->scale;
+        b.zero[0] = gate->zero;
+        b.zero[1] = up->zero;
+        b.groups = N * (K / group_size);
+        b.qmax = (float)((1 << nbits) - 1);
+        b.weight = m0 == 0 ? l.weight : nullptr;
+        return launch_grad_bound(b, s);
+    };
+    const GradBound bound = bf16 ? GradBound{} : GradBound{l.row, l.weight};
     if (few) {
-        if (!bf16 && launch_row_scale(dY, M, N, l.scale, l.inv, s) != hipSuccess)
+        if (bound_rows(0, M) != hipSuccess)
             return HQQ_EHIP;
         SkinnyArgs f{};
         f.w[0] = linear_args(X, *gate, M, K, N, nbits, group_size);
@@ -616,7 +632,8 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         f.g.act = act;
         f.g.dY = dY;
         f.g.ldy = N;
-        f.g.rscale = bf16 ? nullptr : l.scale;
+        f.g.bound = bound;
+        f.g.rinv = l.inv;
         SkinnyGradArgs b{};
         add_grad(b, gate->packed, gate->scale, gate->zero, l.dGU, ldg, N);
         add_grad(b, up->packed, up->scale, up->zero, l.dGU + Np, ldg, N);
@@ -628,8 +645,7 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     }
     for (int64_t m0 = 0; m0 < M; m0 += kRowChunk) {
         const int64_t m = M - m0 < kRowChunk ? M - m0 : kRowChunk;
-        // fp16: dG and dU relative to the row's largest |dY| (bf16 has fp32's range)
-        if (!bf16 && launch_row_scale(dY + m0 * N, m, N, l.scale, l.inv, s) != hipSuccess)
+        if (bound_rows(m0, m) != hipSuccess)
             return HQQ_EHIP;
         UnpackArgs a = unpack_args(l.W, K, nbits, group_size);
         a.pair = 1;
@@ -649,7 +665,8 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
         g.act = act;
         g.dY = dY + m0 * N;
         g.ldy = N;
-        g.rscale = bf16 ? nullptr : l.scale;
+        g.bound = bound;
+        g.rinv = l.inv;
         g.out = l.dGU;
         g.ldo = ldg;
         g.fill = Np;

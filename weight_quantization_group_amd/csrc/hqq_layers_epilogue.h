@@ -119,6 +119,34 @@ __device__ __forceinline__ float from16(uint16_t b, bool bf)
     return (float)h;
 }
 
+// The largest |W_hat| of the weights, from its parts; all lanes of the wave call.  (Rounding
+// keeps the order, so the largest quotient's fp16 value is the largest fp16 value.)
+__device__ __forceinline__ float weight_bound(const GradBound &b)
+{
+    const float4 p = reinterpret_cast<const float4 *>(b.weight)[threadIdx.x & 63];
+    float mx = fmaxf(fmaxf(p.x, p.y), fmaxf(p.z, p.w));
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2)
+        mx = fmaxf(mx, __shfl_xor(mx, o));
+    return (float)(_Float16)mx;
+}
+static_assert(kBoundParts == 4 * 64, "four parts per lane");
+
+// The power of two by which a row's dG and dU are multiplied in fp16, and its reciprocal.  With
+// b = max |dY| * sum |X| * max |W_hat|, |U| <= sum |X| max |W_hat| and |act(G)| <= |G|, so that
+// |dU| <= b and |dG| <= 1.13 b (max |act'|): b is brought to [2^13, 2^14), where nothing
+// overflows.  Usual sums of K products stay within 2^8 or so of their bound, which leaves them
+// some 20 binades of full precision.  1 where the bound is 0 (so are dG and dU) or not finite
+// (b is at least 2^-72 else, and at most 2^65: the exponents below are in range).
+__device__ __forceinline__ float grad_scale(float row, float weight, float &inv)
+{
+    const float b = row * weight;
+    const uint32_t e = __float_as_uint(b) >> 23;
+    const bool scaled = b > 0.0f && b < INFINITY;
+    inv = scaled ? __uint_as_float((e - 13) << 23) : 1.0f;
+    return scaled ? __uint_as_float((267 - e) << 23) : 1.0f;
+}
+
 // four consecutive 16-bit values at p (8-byte aligned)
 template <bool BF>
 __device__ __forceinline__ void load4(const char *p, float (&v)[4])

@@ -190,6 +190,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
         constexpr int P = 80;
         constexpr bool GRAD = OUT == kOutGatedGrad;
         char *sg = st, *su = st + 16 * P, *sy = st + 32 * P;
+        const float wb = GRAD && g.bound.row ? weight_bound(g.bound) : 0.0f;
         const int row4 = lane >> 2, n4 = nw + 8 * (lane & 3);      // coalesced: 4 lanes per row
         // dY four blocks of rows at a time where the tile is whole: loads behind branches come
         // one by one, and all eight take registers that the sums need
@@ -211,7 +212,13 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
 #pragma unroll
         for (int u = 0; u < TM; ++u) {
             const int m = mw + 16 * u + l16, mc = m < g.M ? m : g.M - 1;
-            const float sc = GRAD && g.rscale ? g.rscale[mc] : 1.0f;
+            float sc = 1.0f;
+            if (GRAD && g.bound.row) {
+                float inv;
+                sc = grad_scale(g.bound.row[mc], wb, inv);
+                if (nw == 0 && l4 == 0 && m < g.M)
+                    g.rinv[m] = inv;
+            }
             if constexpr (GRAD) {
                 if (u % 4 == 0)
                     load_y(u);

@@ -60,6 +60,13 @@ struct RowFactor {
     float mul;
 };
 
+// What bounds a row's |dG| and |dU| in fp16 (null: they are not scaled): row[m] = max |dY[m]|
+// * sum |X[m]| and the parts of the largest |quotient| of the weights.
+constexpr int kBoundParts = 256;
+struct GradBound {
+    const float *row, *weight;       // [M], [kBoundParts]
+};
+
 enum GemmOut {
     kOutStore,      // out16 = round(rowf * C)
     kOutPart,       // part[z] = C over this split's steps (fp32)
@@ -86,7 +93,8 @@ struct GemmArgs {
     RowFactor rowf;                  // kOutStore
     int act;
     const uint16_t *dY;              // kOutGatedGrad: [M, N]
-    const float *rscale;             // per-row scale of dG and dU, or null
+    GradBound bound;                 // of dG and dU, which are scaled by it
+    float *rinv;                     // kOutGatedGrad with a bound: 1 / the scale of each row, written
     int64_t ldy;                     // row pitch of dY
     int64_t up_off;                  // kOutGatedGrad, few rows: dU's first column in out
     int64_t fill;                    // kOutGatedGrad, kOutSoftGrad: columns N .. fill - 1 of out are zeroed
@@ -160,8 +168,16 @@ struct LossArgs {
 };
 hipError_t launch_loss(const LossArgs &a, hipStream_t s);
 
-// fp16 rows [M, N]: scale[m] = the power of two that brings max |row| to
-// [2^-7, 2^-6), inv[m] = 1 / scale[m] (1 for rows that are zero or not finite)
-hipError_t launch_row_scale(const uint16_t *rows, int64_t M, int64_t N, float *scale, float *inv, hipStream_t s);
+// A GradBound's arrays; weight is null where its parts are there already.
+struct BoundArgs {
+    const uint16_t *X, *dY;          // [M, K], [M, N], fp16
+    int64_t M, K, N;
+    float *row;
+    const float *scale[2], *zero[2]; // of gate and up, groups of each
+    int64_t groups;
+    float qmax;
+    float *weight;
+};
+hipError_t launch_grad_bound(const BoundArgs &a, hipStream_t s);
 
 }  // namespace hqq

@@ -1,5 +1,5 @@
 // hqq_layers_rows.hip -- the small row-wise kernels around the layers' products:
-// joining split sums and the softmax blocks, scales of rows.
+// joining split sums and the softmax blocks, bounds of the rows' gradients.
 #include "hqq_layers_epilogue.h"
 
 namespace hqq {
@@ -104,40 +104,89 @@ __global__ __launch_bounds__(kRowsBlock) void loss_kernel(LossArgs a)
     a.lse[m] = (d > 0.0f ? others : lt) + tail;
 }
 
-// one workgroup per row; fp16 magnitudes compare as their bits
-__global__ __launch_bounds__(kRowsBlock) void row_scale_kernel(const uint16_t *rows, int64_t N, float *scale, float *inv)
+// The workgroup's maximum and sum, in thread 0
+__device__ __forceinline__ float2 max_and_sum(float mx, float sum)
 {
-    __shared__ uint32_t top[kRowsBlock / 64];
-    const uint16_t *r = rows + (int64_t)blockIdx.x * N;
-    uint32_t mx = 0;
-    for (int64_t i = threadIdx.x; i < N; i += kRowsBlock) {
-        const uint32_t b = r[i] & 0x7fffu;
-        mx = b > mx ? b : mx;
-    }
+    __shared__ float2 parts[kRowsBlock / 64];
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) {
-        const uint32_t b = (uint32_t)__shfl_xor((int)mx, o);
-        mx = b > mx ? b : mx;
+        mx = fmaxf(mx, __shfl_xor(mx, o));
+        sum += __shfl_xor(sum, o);
     }
     if ((threadIdx.x & 63) == 0)
-        top[threadIdx.x >> 6] = mx;
+        parts[threadIdx.x >> 6] = float2{mx, sum};
     __syncthreads();
-    if (threadIdx.x == 0) {
 #pragma unroll
-        for (int w = 1; w < kRowsBlock / 64; ++w)
-            mx = top[w] > mx ? top[w] : mx;
-        float f = 1.0f;
-        if (mx > 0 && mx < 0x7c00u) {
-            _Float16 h;
-            const uint16_t b = (uint16_t)mx;
-            __builtin_memcpy(&h, &b, 2);
-            int e;
-            frexpf((float)h, &e);          // max = f * 2^e, f in [1/2, 1)
-            f = ldexpf(1.0f, -6 - e);
-        }
-        scale[blockIdx.x] = f;
-        inv[blockIdx.x] = 1.0f / f;
+    for (int w = 1; w < kRowsBlock / 64; ++w) {
+        mx = fmaxf(mx, parts[w].x);
+        sum += parts[w].y;
     }
+    return float2{mx, sum};
+}
+
+__device__ __forceinline__ float group_bound(float s, float z, float qmax)
+{
+    return fmaxf(fabsf(z), fabsf(qmax - z)) / fabsf(s);
+}
+
+// The first kBoundParts workgroups (if asked for) take the groups of the weights in turn: the
+// largest |code - zero| / |scale| is at an end of the codes.  One workgroup per row follows; a
+// row that is not finite makes the bound so (fp16 magnitudes compare as their bits).  Bound
+// by the launch and the meta's bytes: about 5 us of an fp16 backward pass of 1 or 16 rows
+// through 4096 x 11008 in groups of 64 (59 and 64 us; bf16, which needs no bound, 54 and 59).
+__global__ __launch_bounds__(kRowsBlock) void grad_bound_kernel(BoundArgs a)
+{
+    const int parts = a.weight ? kBoundParts : 0;
+    if ((int)blockIdx.x < parts) {
+        float mx = 0.0f;
+        const int64_t quads = a.groups / 4, first = (int64_t)blockIdx.x * kRowsBlock + threadIdx.x;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+#pragma unroll 4
+            for (int64_t i = first; i < quads; i += kBoundParts * kRowsBlock) {
+                const float4 s = reinterpret_cast<const float4 *>(a.scale[w])[i];
+                const float4 z = reinterpret_cast<const float4 *>(a.zero[w])[i];
+                mx = fmaxf(fmaxf(mx, group_bound(s.x, z.x, a.qmax)), group_bound(s.y, z.y, a.qmax));
+                mx = fmaxf(fmaxf(mx, group_bound(s.z, z.z, a.qmax)), group_bound(s.w, z.w, a.qmax));
+            }
+            if (first < a.groups % 4)
+                mx = fmaxf(mx, group_bound(a.scale[w][4 * quads + first], a.zero[w][4 * quads + first], a.qmax));
+        }
+        mx = max_and_sum(mx, 0.0f).x;
+        if (threadIdx.x == 0)
+            a.weight[blockIdx.x] = mx;
+        return;
+    }
+    const int64_t m = (int64_t)blockIdx.x - parts;
+    const uint16_t *y = a.dY + m * a.N, *x = a.X + m * a.K;
+    uint32_t top = 0;
+    if (a.N % 8 == 0) {
+        for (int64_t i = threadIdx.x; i < a.N / 8; i += kRowsBlock) {
+            const uint4 v = reinterpret_cast<const uint4 *>(y)[i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = w[j] & 0x7fffu, hi = w[j] >> 16 & 0x7fffu, b = lo > hi ? lo : hi;
+                top = b > top ? b : top;
+            }
+        }
+    } else {
+        for (int64_t i = threadIdx.x; i < a.N; i += kRowsBlock) {
+            const uint32_t b = y[i] & 0x7fffu;
+            top = b > top ? b : top;
+        }
+    }
+    float sum = 0.0f;
+    for (int64_t i = threadIdx.x; i < a.K / 8; i += kRowsBlock) {
+        const uint4 v = reinterpret_cast<const uint4 *>(x)[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sum += fabsf(from16((uint16_t)w[j], false)) + fabsf(from16((uint16_t)(w[j] >> 16), false));
+    }
+    const float2 r = max_and_sum(top >= 0x7c00u ? INFINITY : from16((uint16_t)top, false), sum);
+    if (threadIdx.x == 0)
+        a.row[m] = r.x * r.y;
 }
 
 }  // namespace
@@ -153,9 +202,9 @@ hipError_t launch_loss(const LossArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_row_scale(const uint16_t *rows, int64_t M, int64_t N, float *scale, float *inv, hipStream_t s)
+hipError_t launch_grad_bound(const BoundArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL(row_scale_kernel, dim3((unsigned)M), dim3(kRowsBlock), 0, s, rows, N, scale, inv);
+    hipLaunchKernelGGL(grad_bound_kernel, dim3((unsigned)(a.M + (a.weight ? kBoundParts : 0))), dim3(kRowsBlock), 0, s, a);
     return hipGetLastError();
 }
 

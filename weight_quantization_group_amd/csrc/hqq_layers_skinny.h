@@ -36,10 +36,10 @@ __device__ __forceinline__ float act_any(int act, float g, float &d)
                                  : act_value<HQQ_ACT_GELU_TANH>(g, d);
 }
 
-// One element C[m][n] (gated: of gate and of up).  For kOutStats the 16 lanes of a
+// One element C[m][n] (gated: of gate and of up; wb: weight_bound).  For kOutStats the 16 lanes of a
 // row hold its 16 columns; all lanes of the wave call.
 template <bool BF>
-__device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0, float c1, int m, int n)
+__device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float wb, float c0, float c1, int m, int n)
 {
     const bool m_in = m < g.M;
     if (out == kOutGated) {
@@ -50,9 +50,15 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float c0
         if (m_in && n < g.fill) {
             float vg = 0.0f, vu = 0.0f;
             if (n < g.N) {
-                float d;
+                float d, sc = 1.0f;
+                if (g.bound.row) {
+                    float inv;
+                    sc = grad_scale(g.bound.row[m], wb, inv);
+                    if (n == 0)
+                        g.rinv[m] = inv;
+                }
                 const float f = act_any(g.act, c0, d);
-                const float y = from16(g.dY[(int64_t)m * g.ldy + n], BF) * (g.rscale ? g.rscale[m] : 1.0f);
+                const float y = from16(g.dY[(int64_t)m * g.ldy + n], BF) * sc;
                 vg = y * c1 * d;
                 vu = y * f;
             }
@@ -360,6 +366,7 @@ skinny_kernel(SkinnyArgs s)
             for (int r = 0; r < 4; ++r)
                 red[((wave * NM + j) * MT * 4 + u * 4 + r) * 64 + lane] = acc[j][u][r];
     __syncthreads();
+    const float wb = s.g.bound.row ? weight_bound(s.g.bound) : 0.0f;
     for (int idx = threadIdx.x; idx < MT * 4 * 64; idx += WPB * 64) {
         const int v = idx >> 6, l = idx & 63;      // one v per wave
         float c[NM];
@@ -372,7 +379,7 @@ skinny_kernel(SkinnyArgs s)
         // sum r of lane l is C[4 (l / 16) + r][l % 16] of m tile u
         const int m = (int)m0 + 16 * (v >> 2) + 4 * (l >> 4) + (v & 3);
         const int nn = (int)blockIdx.x * 16 + (l & 15);
-        element<BF>(s.out, s.g, c[0], c[NM - 1], m, nn);
+        element<BF>(s.out, s.g, wb, c[0], c[NM - 1], m, nn);
     }
 }
 
