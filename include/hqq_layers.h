@@ -21,9 +21,9 @@
  * otherwise; all arguments are checked on the host before anything is enqueued;
  * calls only enqueue work on `stream` of the current device; nothing is
  * allocated and no state is kept.  Inputs and outputs are contiguous,
- * row-major, and outputs must not overlap inputs or the workspace
- * (HQQ_EINVAL_PTR).  Scales are
- * finite and not 0, as hqq_quantize writes them.
+ * row-major; outputs and the bytes of workspace that the call uses must not overlap
+ * its inputs, the weights' arrays among them, or one another (HQQ_EINVAL_PTR).
+ * Scales are finite and not 0, as hqq_quantize writes them.
  *
  * Workspace.  Each call takes a device workspace of at least the bytes that its
  * *_workspace function returns for the same sizes (HQQ_EWORKSPACE if smaller; 0

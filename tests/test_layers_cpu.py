@@ -244,3 +244,51 @@ def test_binding_checks_the_shape_of_a_tensor_given_twice(w):
     for rows, cols in ((4, 500), (4, 4), (5, 5)):
         with pytest.raises(ValueError):
             _matrix(t, "dYs", rows, cols, t)
+
+
+@pytest.mark.parametrize("route", ["codes", "tiled"])
+def test_rejects_writes_over_weights_and_inputs(w, lib, monkeypatch, route):
+    """Outputs over a weight's codes, scales or zeros, and a workspace over any input: refused."""
+    monkeypatch.setenv("HQQ_LAYERS_PATH", route)
+    from weight_quantization_group_amd.layers import HqqLinearGrad
+    x, y, o, p, s, z, t, ws = [0x10000000 * i for i in range(1, 9)]
+    M, K, N, fmt = 40, 128, 40, (4, 64)
+    codes, meta = N * K // 2, N * (K // 64) * 4
+    big = 1 << 40
+    first, other = weight(w, 0x7000000, 0x8000000, 0x9000000), weight(w, p, s, z)
+    f, g = ctypes.byref(first), ctypes.byref(other)
+    grads = (HqqLinearGrad * 2)(HqqLinearGrad(0x7000000, 0x8000000, 0x9000000, N, y + 4096 * 16), HqqLinearGrad(p, s, z, N, y))
+    sizes = (M, K, N, *fmt)
+
+    def gated_call(out, work):
+        return lib.hqq_linear_gated(x, M, K, f, g, N, *fmt, 0, 0, out, work, big, None)
+
+    def gated_grad(out, work):
+        return lib.hqq_linear_gated_backward(y, x, M, K, g, f, N, *fmt, 0, 0, out, work, big, None)
+
+    def batch(out, work):
+        return lib.hqq_linear_batch_backward(grads, 2, M, K, *fmt, 0, out, work, big, None)
+
+    def loss_call(out, work):
+        return lib.hqq_linear_cross_entropy(x, M, K, g, N, *fmt, 0, t, o, out, work, big, None)
+
+    def loss_grad(out, work):
+        return lib.hqq_linear_cross_entropy_backward(t + 4096, x, M, K, g, N, *fmt, 0, t, t + 8192, out, work, big, None)
+
+    def last(base, size):
+        return base + (size - 1) // 16 * 16
+
+    calls = {gated_call: (w.hqq_linear_gated_workspace(*sizes), {x: 2 * M * K}),
+             gated_grad: (w.hqq_linear_gated_backward_workspace(*sizes), {x: 2 * M * K, y: 2 * M * N}),
+             batch: (w.hqq_linear_batch_backward_workspace(M, K, [N, N], *fmt), {y: 2 * M * N, y + 4096 * 16: 2 * M * N}),
+             loss_call: (w.hqq_linear_cross_entropy_workspace(*sizes), {x: 2 * M * K, t: 8 * M}),
+             loss_grad: (w.hqq_linear_cross_entropy_backward_workspace(*sizes),
+                         {x: 2 * M * K, t: 8 * M, t + 4096: 4 * M, t + 8192: 4 * M})}
+    for call, (need, inputs) in calls.items():
+        for base, size in ((p, codes), (s, meta), (z, meta)):
+            assert call(base, ws) == PTR and call(last(base, size), ws) == PTR, call.__name__
+        for base, size in {**inputs, p: codes, s: meta, z: meta, o: 2 * M * N}.items():
+            if need and (base != o or call in (gated_call, gated_grad, batch)):
+                out = o if call is not loss_call else o + 4096
+                assert call(out, base) == PTR and call(out, last(base, size)) == PTR, call.__name__
+                assert call(out, base - (need - 16) // 256 * 256) == PTR, call.__name__

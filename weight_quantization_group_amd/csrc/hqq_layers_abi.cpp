@@ -115,7 +115,8 @@ int check_workspace(const void *ws, int64_t have, int64_t need)
     return have < need ? HQQ_EWORKSPACE : HQQ_OK;
 }
 
-// Whether an output shares memory with something the call reads or uses
+// Whether what the call writes (an output, or the workspace) shares memory with something
+// that it reads or uses
 struct Range {
     const void *p;
     int64_t bytes;
@@ -126,10 +127,27 @@ bool overlaps(Range out, std::initializer_list<Range> others)
     const uintptr_t a = (uintptr_t)out.p;
     for (const Range &o : others) {
         const uintptr_t b = (uintptr_t)o.p;
-        if (b && a < b + (uint64_t)o.bytes && b < a + (uint64_t)out.bytes)
+        if (out.bytes && o.bytes && a < b + (uint64_t)o.bytes && b < a + (uint64_t)out.bytes)
             return true;
     }
     return false;
+}
+
+// the same for the arrays of a weight [N, K]
+bool overlaps_weight(std::initializer_list<Range> written, const uint32_t *packed, const float *scale, const float *zero,
+                     int64_t N, int64_t K, int nbits, int group_size)
+{
+    const int64_t codes = N * (K * nbits / 32) * 4, meta = N * (K / group_size) * 4;
+    for (const Range &r : written)
+        if (overlaps(r, {{packed, codes}, {scale, meta}, {zero, meta}}))
+            return true;
+    return false;
+}
+
+bool overlaps_weight(std::initializer_list<Range> written, const hqq_weight &w, int64_t N, int64_t K, int nbits,
+                     int group_size)
+{
+    return overlaps_weight(written, w.packed, w.scale, w.zero, N, K, nbits, group_size);
 }
 
 // The workspace as a run of 256-byte aligned arrays; with a null base only
@@ -504,7 +522,7 @@ const char *hqq_layers_strerror(int status)
     case HQQ_EINVAL_NBITS: return "nbits must be 1, 2, 4 or 8";
     case HQQ_EINVAL_GROUP: return "group_size must be 8, 16, 32, 64, 128 or 256 and divide K";
     case HQQ_EINVAL_SHAPE: return "a size is out of range (K a multiple of 32; M, N, count >= 1 and within their limits)";
-    case HQQ_EINVAL_PTR: return "a pointer is NULL or misaligned, or an output overlaps an input or the workspace";
+    case HQQ_EINVAL_PTR: return "a pointer is NULL or misaligned, or an output or the workspace overlaps an input or one another";
     case HQQ_EHIP: return "a HIP kernel launch failed";
     case HQQ_EINVAL_DTYPE: return "dtype must be HQQ_DTYPE_FP16 or HQQ_DTYPE_BF16";
     case HQQ_EINVAL_ACT: return "act must be HQQ_ACT_SILU, HQQ_ACT_GELU or HQQ_ACT_GELU_TANH";
@@ -537,7 +555,9 @@ int hqq_linear_gated(const uint16_t *X, int64_t M, int64_t K, const hqq_weight *
     const GatedLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
-    if (overlaps({Y, 2 * M * N}, {{X, 2 * M * K}, {workspace, l.bytes}}))
+    const Range rx{X, 2 * M * K}, ry{Y, 2 * M * N}, rw{workspace, l.bytes};
+    if (overlaps(ry, {rx, rw}) || overlaps(rw, {rx}) || overlaps_weight({ry, rw}, *gate, N, K, nbits, group_size) ||
+        overlaps_weight({ry, rw}, *up, N, K, nbits, group_size))
         return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
@@ -596,7 +616,9 @@ int hqq_linear_gated_backward(const uint16_t *dY, const uint16_t *X, int64_t M, 
     const GatedGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
-    if (overlaps({dX, 2 * M * K}, {{X, 2 * M * K}, {dY, 2 * M * N}, {workspace, l.bytes}}))
+    const Range rx{X, 2 * M * K}, ry{dY, 2 * M * N}, rd{dX, 2 * M * K}, rw{workspace, l.bytes};
+    if (overlaps(rd, {rx, ry, rw}) || overlaps(rw, {rx, ry}) ||
+        overlaps_weight({rd, rw}, *gate, N, K, nbits, group_size) || overlaps_weight({rd, rw}, *up, N, K, nbits, group_size))
         return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
@@ -717,9 +739,15 @@ int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int64_t M, i
     const BatchGradLayout l(workspace, M, K, n, count, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
-    for (int i = 0; i < count; ++i)
-        if (overlaps({dX, 2 * M * K}, {{ws[i].dY, 2 * M * n[i]}, {workspace, l.bytes}}))
+    const Range rd{dX, 2 * M * K}, rw{workspace, l.bytes};
+    if (overlaps(rd, {rw}))
+        return HQQ_EINVAL_PTR;
+    for (int i = 0; i < count; ++i) {
+        const Range ry{ws[i].dY, 2 * M * n[i]};
+        if (overlaps(rd, {ry}) || overlaps(rw, {ry}) ||
+            overlaps_weight({rd, rw}, ws[i].packed, ws[i].scale, ws[i].zero, n[i], K, nbits, group_size))
             return HQQ_EINVAL_PTR;
+    }
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
     if (few) {
@@ -777,8 +805,9 @@ int hqq_linear_cross_entropy(const uint16_t *X, int64_t M, int64_t K, const hqq_
     const LossLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
-    if (overlaps({loss, 4 * M}, {{X, 2 * M * K}, {targets, 8 * M}, {lse, 4 * M}, {workspace, l.bytes}}) ||
-        overlaps({lse, 4 * M}, {{X, 2 * M * K}, {targets, 8 * M}, {workspace, l.bytes}}))
+    const Range rx{X, 2 * M * K}, rt{targets, 8 * M}, ro{loss, 4 * M}, re{lse, 4 * M}, rw{workspace, l.bytes};
+    if (overlaps(ro, {rx, rt, re, rw}) || overlaps(re, {rx, rt, rw}) || overlaps(rw, {rx, rt}) ||
+        overlaps_weight({ro, re, rw}, *head, N, K, nbits, group_size))
         return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
@@ -847,8 +876,9 @@ int hqq_linear_cross_entropy_backward(const float *dloss, const uint16_t *X, int
     const LossGradLayout l(workspace, M, K, N, few);
     if (const int st = check_workspace(workspace, workspace_bytes, l.bytes))
         return st;
-    if (overlaps({dX, 2 * M * K},
-                 {{X, 2 * M * K}, {targets, 8 * M}, {dloss, 4 * M}, {lse, 4 * M}, {workspace, l.bytes}}))
+    const Range rx{X, 2 * M * K}, rt{targets, 8 * M}, ro{dloss, 4 * M}, re{lse, 4 * M}, rd{dX, 2 * M * K}, rw{workspace, l.bytes};
+    if (overlaps(rd, {rx, rt, ro, re, rw}) || overlaps(rw, {rx, rt, ro, re}) ||
+        overlaps_weight({rd, rw}, *head, N, K, nbits, group_size))
         return HQQ_EINVAL_PTR;
     const bool bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
