@@ -722,3 +722,29 @@ def test_fp16_rows_without_a_gradient(hq, path, M):
     X[1], dY[1] = 65504.0, 2.0 ** -24
     dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 32)
     assert torch.isfinite(dX[1]).all()
+
+
+def test_workspace_of_another_stream_is_kept(hq):
+    """A workspace allocated on one stream, used on another and dropped: while the call may still
+    write it, the allocator does not give its memory to the first stream again."""
+    dtype, M, K, N = torch.bfloat16, 300, 128, 200
+    w, _ = make_weight(1, N, K, 4, 64, dtype)
+    X = normal(3, (M, K), dtype)
+    need = hq.hqq_linear_gated_workspace(M, K, N, 4, 64)
+    busy = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(50):
+        busy = busy @ busy * 1e-2                       # tens of milliseconds before the call's turn
+    Y = hq.hqq_linear_gated(X, w, w, N, 4, 64, workspace=ws)
+    where = ws.data_ptr()
+    del ws
+    with torch.cuda.stream(side):
+        again = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert not torch.cuda.current_stream().query()      # the call was still ahead
+    assert again.data_ptr() != where
+    torch.cuda.synchronize()
+    assert torch.equal(Y, hq.hqq_linear_gated(X, w, w, N, 4, 64))

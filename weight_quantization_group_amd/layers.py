@@ -177,7 +177,8 @@ def _act(activation: str) -> int:
 def _call(name: str, device, workspace, sizes, *args):
     """Run the library's call `name` on device's current stream, with a workspace of
     the size for `sizes` where none is given."""
-    if workspace is None:
+    given = workspace is not None
+    if not given:
         need = _bytes(name + "_workspace", *sizes)
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         ptr = workspace.data_ptr() if need else None
@@ -194,6 +195,9 @@ def _call(name: str, device, workspace, sizes, *args):
     else:
         with torch.cuda.device(device):
             st = f(*args, ptr, need, torch._C._cuda_getCurrentRawStream(device.index))
+    if given and need and not torch.cuda.is_current_stream_capturing():
+        # a workspace that belongs to another stream is not handed out again before this call's end
+        workspace.record_stream(torch.cuda.current_stream(device))
     if st != 0:
         raise LayersError(name, st)
 
