@@ -120,6 +120,8 @@ HQQ_API int hqq_linear_batch_backward(const hqq_linear_grad *ws, int count, int6
  *             share), so that a confident row's small loss keeps its precision
  * A row whose target lies outside [0, N) (-100, say) is ignored: loss 0; its
  * lse is still written.
+ * Infinite and NaN logits (an input that is not finite) give what these formulas
+ * give in IEEE arithmetic: lse +inf beside a +inf logit, -inf where all are -inf.
  *   targets int64 [M] (8-byte aligned), loss and lse fp32 [M] (4-byte aligned) */
 HQQ_API int64_t hqq_linear_cross_entropy_workspace(int64_t M, int64_t K, int64_t N, int nbits,
                                                    int group_size);

@@ -748,3 +748,47 @@ def test_workspace_of_another_stream_is_kept(hq):
     assert again.data_ptr() != where
     torch.cuda.synchronize()
     assert torch.equal(Y, hq.hqq_linear_gated(X, w, w, N, 4, 64))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M", [9, 70])
+def test_cross_entropy_infinite_logits(hq, path, dtype, M):
+    """Infinities among a row's logits give what the definition gives in IEEE arithmetic: lse is +inf
+    with a +inf logit and -inf where all are -inf, loss = lse - l_t."""
+    K, N = 160, 333
+    (packed, scale, zero), _ = make_weight(5, N, K, 4, 32, dtype)
+    zero[:, 0] = -1.0                                   # W_hat > 0 in the first 32 columns
+    W = hq.hqq_dequantize(packed, scale, zero, N, K, 4, 32, 1, dtype=dtype).double()
+    assert (W != 0).all() and (W[:, 40] > 0).any() and (W[:, 40] < 0).any()
+    X = normal(1, (M, K), dtype)
+    t = torch.randint(0, N, (M,), generator=torch.Generator().manual_seed(1)).cuda()
+    X[0, 3], X[1, 3] = math.inf, -math.inf              # all logits +inf, all -inf
+    X[2:5, 40] = math.inf                               # both
+    t[2], t[3], t[4] = int(W[:, 40].argmax()), int(W[:, 40].argmin()), -100
+    X[5, 7] = math.nan
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, packed, scale, zero, N, 4, 32)
+    L = X.double() @ W.T
+    ref = torch.logsumexp(L, 1)
+    want = torch.where((t >= 0) & (t < N), ref - L.gather(1, t.clamp(min=0)[:, None])[:, 0], torch.zeros_like(ref))
+    assert ref[:6].tolist()[:5] == [math.inf, -math.inf, math.inf, math.inf, math.inf] and want[3] == math.inf
+    for got, r in ((lse, ref), (loss, want)):
+        torch.testing.assert_close(got[:6].double(), r[:6], rtol=0, atol=0, equal_nan=True)
+    check_loss(loss[6:], lse[6:], X[6:], W, t[6:])
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_cross_entropy_near_the_largest_logits(hq, path, M):
+    """Logits up to fp32's last binade: lse is their maximum."""
+    K, N, dtype = 64, 200, torch.bfloat16
+    head, W = make_weight(5, N, K, 8, 64, dtype, std=0.5)
+    X = torch.zeros(M, K, dtype=dtype, device="cuda")
+    X[:, 9] = 1.1875 * 2.0 ** 127
+    L = X.double() @ W.T
+    assert 2.4e38 < L.max() < 3.4e38 and L.max() - L.min() > 3.5e38
+    t = torch.full((M,), int(L[0].argmin()), device="cuda")
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 8, 64)
+    # one exact product per logit; the least is about as far below 0: the difference overflows
+    assert torch.equal(lse.double(), L.amax(1)) and (loss == math.inf).all()
+    t = L.argmax(1)
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 8, 64)
+    assert torch.equal(lse.double(), L.amax(1)) and (loss == 0).all()

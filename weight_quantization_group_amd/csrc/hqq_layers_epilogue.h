@@ -100,6 +100,11 @@ __device__ __forceinline__ float act_value(float g, float &d)
     }
 }
 
+// A softmax block of logits is (max, sum of exp(logit - stats_ref(max))).  The reference is
+// the maximum where that is finite and 0 elsewhere, so that no inf - inf is formed: a block of
+// -inf has the sum 0, one with a +inf the sum +inf, and a NaN among the logits stays in the sum.
+__device__ __forceinline__ float stats_ref(float mx) { return fabsf(mx) < INFINITY ? mx : 0.0f; }
+
 __device__ __forceinline__ float row_factor(const RowFactor &r, int64_t m)
 {
     if (r.f)

@@ -286,14 +286,14 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const float4v (&acc)
                 g.tlogit[m] = tl;
             mx = fmaxf(mx, __shfl_xor(mx, 16));
             mx = fmaxf(mx, __shfl_xor(mx, 32));
-            const float ref = mx > -INFINITY ? mx * kLog2e : 0.0f;
+            const float ref = stats_ref(mx);
             float sum = 0.0f;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int n = 16 * t + 4 * l4 + r;
-                    sum += nw + n < g.N && n != at ? exp2_fast(__builtin_fmaf(acc[u][t][r], kLog2e, -ref)) : 0.0f;
+                    sum += nw + n < g.N && n != at ? exp2_fast((acc[u][t][r] - ref) * kLog2e) : 0.0f;
                 }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
@@ -322,7 +322,7 @@ __device__ __forceinline__ void join_stats(const GemmArgs &g, int m0, int tile_n
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < WN; ++w)
-        sum += mx > -INFINITY ? v[w].y * exp2_fast((v[w].x - mx) * kLog2e) : v[w].y;   // (or a NaN, which stays)
+        sum += fabsf(mx) < INFINITY ? v[w].y * exp2_fast((v[w].x - mx) * kLog2e) : v[w].y;
     g.stats[(int64_t)(m0 + r) * g.blocks + tile_n] = float2{mx, sum};
 }
 

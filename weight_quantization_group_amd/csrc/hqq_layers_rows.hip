@@ -64,8 +64,8 @@ hipError_t launch_reduce_dtype(const ReduceArgs &a, hipStream_t s)
 __device__ __forceinline__ float2 join(float2 a, float2 b)
 {
     const float m = fmaxf(a.x, b.x);
-    if (!(m > -INFINITY))
-        return float2{m, a.y + b.y};     // both empty (or a NaN, which stays)
+    if (!(fabsf(m) < INFINITY))
+        return float2{m, a.y + b.y};     // both empty, or a +inf: see stats_ref
     return float2{m, a.y * expf(a.x - m) + b.y * expf(b.x - m)};
 }
 
@@ -100,8 +100,10 @@ __global__ __launch_bounds__(kRowsBlock) void loss_kernel(LossArgs a)
     const float lt = a.tlogit[m];
     const float d = a.N > 1 ? others - lt : -INFINITY;
     const float tail = log1pf(expf(-fabsf(d)));
-    a.loss[m] = fmaxf(d, 0.0f) + tail;
-    a.lse[m] = (d > 0.0f ? others : lt) + tail;
+    // (lse - l_t of a target of +inf is inf - inf; an infinity that the target and the others
+    // share is lse)
+    a.loss[m] = lt < INFINITY ? fmaxf(d, 0.0f) + tail : NAN;
+    a.lse[m] = others == lt && !(fabsf(lt) < INFINITY) ? lt : (d > 0.0f ? others : lt) + tail;
 }
 
 // The workgroup's maximum and sum, in thread 0

@@ -75,8 +75,7 @@ __device__ __forceinline__ void element(GemmOut out, const GemmArgs &g, float wb
 #pragma unroll
         for (int o = 1; o < 16; o *= 2)
             mx = fmaxf(mx, __shfl_xor(mx, o));
-        const float ref = mx > -INFINITY ? mx * kLog2e : 0.0f;
-        float sum = in ? exp2_fast(__builtin_fmaf(c0, kLog2e, -ref)) : 0.0f;
+        float sum = in ? exp2_fast((c0 - stats_ref(mx)) * kLog2e) : 0.0f;
 #pragma unroll
         for (int o = 1; o < 16; o *= 2)
             sum += __shfl_xor(sum, o);
