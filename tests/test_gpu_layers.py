@@ -792,3 +792,28 @@ def test_cross_entropy_near_the_largest_logits(hq, path, M):
     t = L.argmax(1)
     loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 8, 64)
     assert torch.equal(lse.double(), L.amax(1)) and (loss == 0).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [4, 96])
+def test_gated_huge_projections(hq, path, act, M):
+    """Projections up to 2^60, whose squares and cubes overflow: act is 0 or the identity there and
+    act' 0 or 1.  (Exact inputs of one term per sum, so that G and U carry no error; dG and dU are
+    then off by a rounding each, and dX = dG Wg + dU Wu by two, its sum and its own.)"""
+    dtype, K, N = torch.bfloat16, 64, 96
+    gate, Wg = make_weight(1, N, K, 8, 64, dtype)
+    up, Wu = make_weight(2, N, K, 8, 64, dtype)
+    X = torch.zeros(M, K, dtype=dtype, device="cuda")
+    for m in range(M):
+        X[m, m % K] = (-1.0) ** m * 2.0 ** (45 + 15 * m / M // 1)
+    dY = normal(4, (M, N), dtype)
+    Y = hq.hqq_linear_gated(X, gate, up, N, 8, 64, activation=act)
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, 8, 64, activation=act)
+    x, y = X.double(), dY.double()
+    G, Up = x @ Wg.T, x @ Wu.T
+    assert G.abs().min() > 2.0 ** 20 and G.abs().max() > 2.0 ** 50
+    on = (G > 0).double()
+    u = U[dtype]
+    within(Y, on * G * Up, (u + FN) * (on * G * Up).abs() + 1e-30)
+    dG, dU = y * Up * on, y * G * on
+    within(dX, *grad_bound([dG, dU], [(u + FN) * 1.01 * dG.abs() + 1e-30, (u + FN) * 1.01 * dU.abs() + 1e-30], [Wg, Wu], dtype))

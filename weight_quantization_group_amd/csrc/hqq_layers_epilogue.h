@@ -94,8 +94,8 @@ __device__ __forceinline__ float act_value(float g, float &d)
     }
     const float e = exp2_fast(-kLog2e * y2);
     const float p = rcp_fast(1.0f + e);
-    // p (1 - p) = p^2 e; where e overflows p is 0 and so is the product
-    d = p + (e < INFINITY ? g * dy2 * (p * (p * e)) : 0.0f);
+    // p (1 - p) = p^2 e; 0 where e overflows (p is 0), and where e is 0 (dy2 may overflow)
+    d = p + (e > 0.0f && e < INFINITY ? g * dy2 * (p * (p * e)) : 0.0f);
     return g * p;
     }
 }
