@@ -817,3 +817,65 @@ def test_gated_huge_projections(hq, path, act, M):
     within(Y, on * G * Up, (u + FN) * (on * G * Up).abs() + 1e-30)
     dG, dU = y * Up * on, y * G * on
     within(dX, *grad_bound([dG, dU], [(u + FN) * 1.01 * dG.abs() + 1e-30, (u + FN) * 1.01 * dU.abs() + 1e-30], [Wg, Wu], dtype))
+
+
+def device_weight(seed, N, K, nbits, gs, dtype):
+    """make_weight for large weights: made on the GPU."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    words = torch.randint(-2 ** 31, 2 ** 31, (N, K * nbits // 32), dtype=torch.int32, device="cuda", generator=g)
+    qmax, std = (1 << nbits) - 1, 1.0 / math.sqrt(K)
+    lo, hi = ((2 + 0.5 * torch.randn(N, K // gs, device="cuda", generator=g)).abs() * std for _ in range(2))
+    scale = qmax / (hi + lo + 1e-3 * std)
+    zero = lo * scale
+    shifts = torch.arange(PER_WORD[nbits], dtype=torch.int32, device="cuda") * nbits
+    q = ((words[..., None] >> shifts) & qmax).float().view(N, K // gs, gs)
+    return (words, scale, zero), ((q - zero[..., None]) / scale[..., None]).to(dtype).view(N, K).double()
+
+
+def piece_edges(K, N, limit):
+    """Every class at which a piece of the vocabulary may begin: pieces are of p - 3 s to p + 2 s classes in
+    steps of s, p of those that 128 MiB of W_hat hold (at most `limit`, at least 4096) and s an eighth."""
+    p = max(4096, min((64 << 20) // (-(-K // 64) * 64 + 64) // 256 * 256, limit))
+    s = p // 8 // 256 * 256
+    assert N > p + 2 * s                                # more than one piece, whatever its width
+    return sorted({e for w in range(p - 3 * s, p + 2 * s + 1, s) for e in range(w, N, w)})
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M", [1, 9, 70, 300])
+def test_cross_entropy_at_piece_edges(hq, monkeypatch, M, dtype):
+    """More classes than a piece of the tiled route holds: targets at the last class of each piece and
+    the first of the next.  (A workspace smaller than W_hat shows that there are pieces.)"""
+    monkeypatch.setenv("HQQ_LAYERS_PATH", "tiled")
+    K, N = 16384, 9000
+    assert hq.hqq_linear_cross_entropy_workspace(M, K, N, 4, 64) < 2 * N * (K + 64)
+    assert hq.hqq_linear_cross_entropy_backward_workspace(M, K, N, 4, 64) < 2 * N * (K + 64)
+    head, W = device_weight(M, N, K, 4, 64, dtype)
+    classes = [c for e in piece_edges(K, N, 1 << 25) for c in (e - 1, e)] + [0, N - 1]
+    X, dloss = normal(1, (M, K), dtype), normal(2, (M,), torch.float32)
+    for i in range(0, len(classes), M):
+        t = torch.full((M,), 77)
+        part = classes[i:i + M]
+        t[:len(part)] = torch.tensor(part)
+        t = t.cuda()
+        loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 4, 64)
+        check_loss(loss, lse, X, W, t, str(part))
+        dX = hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *head, N, 4, 64)
+        check_loss_backward(dX, dloss, X, W, t, lse, str(part))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+def test_pieces_of_a_chunk_of_rows(hq, dtype):
+    """Pieces within chunks of 8192 rows, of which the last is a short one: the gradients of 8192
+    rows times all classes would not fit the workspace."""
+    M, K, N = 8192 + 70, 64, 5300
+    assert hq.hqq_linear_cross_entropy_backward_workspace(M, K, N, 4, 32) < 8192 * N * 2
+    head, W = device_weight(1, N, K, 4, 32, dtype)
+    X, dloss = normal(1, (M, K), dtype), normal(2, (M,), torch.float32)
+    classes = torch.tensor([c for e in piece_edges(K, N, 4096) for c in (e - 1, e)] + [0, N - 1, -1, N])
+    t = classes[torch.arange(M) % len(classes)].cuda()
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 4, 32)
+    dX = hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *head, N, 4, 32)
+    for part in (slice(0, 40), slice(8150, 8230), slice(M - 30, M)):
+        check_loss(loss[part], lse[part], X[part], W, t[part], f"rows {part.start}")
+        check_loss_backward(dX[part], dloss[part], X[part], W, t[part], lse[part], f"rows {part.start}")
