@@ -879,3 +879,23 @@ def test_pieces_of_a_chunk_of_rows(hq, dtype):
     for part in (slice(0, 40), slice(8150, 8230), slice(M - 30, M)):
         check_loss(loss[part], lse[part], X[part], W, t[part], f"rows {part.start}")
         check_loss_backward(dX[part], dloss[part], X[part], W, t[part], lse[part], f"rows {part.start}")
+
+
+@pytest.mark.parametrize("K,N,rows", [(512, 4000, [32, 33, 64, 65, 128, 129, 160, 161]), (2048, 10240, [32, 33, 64, 65])])
+def test_on_both_sides_of_the_route_limits(hq, K, N, rows):
+    """The operators on the rows at which each changes its route by itself: 64 and 160, 64, 64, 160 and 128 for
+    the smaller weight (gated, its gradient, the linear gradient, loss, its gradient), and 64 and 32 for the larger."""
+    dtype, nbits, gs = torch.bfloat16, 4, 64
+    a, Wa = device_weight(1, N, K, nbits, gs, dtype)
+    b, Wb = device_weight(2, N, K, nbits, gs, dtype)
+    for M in rows:
+        tag = f"{M} rows"
+        X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype)
+        check_gated(hq.hqq_linear_gated(X, a, b, N, nbits, gs), X, Wa, Wb, "silu", tag)
+        check_gated_backward(hq.hqq_linear_gated_backward(dY, X, a, b, N, nbits, gs), dY, X, Wa, Wb, "silu", tag)
+        y = dY.double()
+        within(hq.hqq_linear_backward(dY, *a, K, nbits, gs), *grad_bound([y], [torch.zeros_like(y)], [Wa], dtype), tag)
+        t, dloss = some_targets(M, M, N), normal(6, (M,), torch.float32)
+        loss, lse = hq.hqq_linear_cross_entropy(X, t, *a, N, nbits, gs)
+        check_loss(loss, lse, X, Wa, t, tag)
+        check_loss_backward(hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *a, N, nbits, gs), dloss, X, Wa, t, lse, tag)

@@ -292,3 +292,38 @@ def test_rejects_writes_over_weights_and_inputs(w, lib, monkeypatch, route):
                 out = o if call is not loss_call else o + 4096
                 assert call(out, base) == PTR and call(out, last(base, size)) == PTR, call.__name__
                 assert call(out, base - (need - 16) // 256 * 256) == PTR, call.__name__
+
+
+@pytest.mark.parametrize("name,K,N,gs,most", [
+    # large enough that the rows alone decide: up to `most` rows straight from the codes
+    ("gated", 2048, 10240, 64, 64), ("gated_backward", 2048, 10240, 64, 64), ("gated_backward", 2048, 10240, 32, 32),
+    ("batch_backward", 2048, 20480, 64, 64), ("batch_backward", 2048, 20480, 32, 32),
+    ("cross_entropy", 2048, 20480, 64, 64), ("cross_entropy_backward", 2048, 20480, 64, 32),
+    # shallow
+    ("gated_backward", 1024, 20480, 64, 32), ("cross_entropy", 1024, 20480, 64, 32),
+    # more than 200 million weights
+    ("gated", 8192, 14336, 64, 96), ("cross_entropy", 8192, 28672, 64, 96), ("cross_entropy_backward", 8192, 28672, 64, 64),
+    ("batch_backward", 8192, 28672, 32, 64),
+    # small: blocks of 32 rows times the weights
+    ("gated", 512, 4000, 64, 160), ("gated_backward", 512, 4000, 64, 64), ("batch_backward", 512, 4000, 64, 64),
+    ("cross_entropy", 512, 4000, 64, 160), ("cross_entropy_backward", 512, 4000, 64, 128), ("gated", 512, 1100, 64, 256),
+])
+def test_route_limits(w, monkeypatch, name, K, N, gs, most):
+    """The rows up to which each operator runs straight from the codes by itself, seen by the workspace
+    that it asks for beside those of the two forced routes."""
+    def need(M):
+        if name == "batch_backward":
+            return w.hqq_linear_batch_backward_workspace(M, K, [N], 4, gs)
+        return getattr(w, f"hqq_linear_{name}_workspace")(M, K, N, 4, gs)
+
+    def forced(route, M):
+        monkeypatch.setenv("HQQ_LAYERS_PATH", route)
+        n = need(M)
+        monkeypatch.delenv("HQQ_LAYERS_PATH")
+        return n
+
+    for M in (1, most, most + 1):
+        codes, tiled = forced("codes", M), forced("tiled", M)
+        if M <= 256:
+            assert codes != tiled
+        assert need(M) == (codes if M <= most else tiled), M
