@@ -899,3 +899,49 @@ def test_on_both_sides_of_the_route_limits(hq, K, N, rows):
         loss, lse = hq.hqq_linear_cross_entropy(X, t, *a, N, nbits, gs)
         check_loss(loss, lse, X, Wa, t, tag)
         check_loss_backward(hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *a, N, nbits, gs), dloss, X, Wa, t, lse, tag)
+
+
+# The largest tiles run where they fill the 256 CUs in one round (a few rows and columns less, so that
+# tiles end inside): rows, and columns per 2 N of the gated block or per N of the head
+LARGE = {"256x256": (2043, 8186), "256x128": (2043, 4090), "128x128": (1019, 4090)}
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("tile", LARGE)
+def test_large_tiles_gated(hq, tile, act, dtype):
+    M, N, K = LARGE[tile][0], LARGE[tile][1] // 2, 160
+    gate, Wg = device_weight(1, N, K, 4, 32, dtype)
+    up, Wu = device_weight(2, N, K, 4, 32, dtype)
+    X, dY = normal(3, (M, K), dtype, 1.5), normal(4, (M, N), dtype)
+    check_gated(hq.hqq_linear_gated(X, gate, up, N, 4, 32, activation=act), X, Wg, Wu, act)
+    check_gated_backward(hq.hqq_linear_gated_backward(dY, X, gate, up, N, 4, 32, activation=act), dY, X, Wg, Wu, act)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("tile", LARGE)
+def test_large_tiles_loss(hq, tile, dtype):
+    M, N = LARGE[tile]
+    K = 160
+    head, W = device_weight(5, N, K, 4, 32, dtype)
+    X, dloss, t = normal(1, (M, K), dtype), normal(2, (M,), torch.float32), some_targets(3, M, N)
+    loss, lse = hq.hqq_linear_cross_entropy(X, t, *head, N, 4, 32)
+    check_loss(loss, lse, X, W, t)
+    check_loss_backward(hq.hqq_linear_cross_entropy_backward(dloss, X, t, lse, *head, N, 4, 32), dloss, X, W, t, lse)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["fp16", "bf16"])
+@pytest.mark.parametrize("M,K,N", [
+    (2043, 8192, 200),        # one round of 256 x 256 tiles of dX, a few steps along N: not split
+    (2043, 4096, 200),        # of 256 x 128
+    (1019, 4096, 200),        # of 128 x 128
+    (2043, 8192, 20001),      # hundreds of steps, not split
+    (2043, 4096, 20001),      # half a round of 256 x 256: split
+])
+def test_large_tiles_gradient(hq, M, K, N, dtype):
+    w, W = device_weight(7, N, K, 4, 64, dtype)
+    dY = normal(4, (M, N), dtype)
+    dX = hq.hqq_linear_backward(dY, *w, K, 4, 64)
+    for part in (slice(0, 300), slice(900, 1019), slice(M - 200, M)):
+        y = dY[part].double()
+        within(dX[part], *grad_bound([y], [torch.zeros_like(y)], [W], dtype), f"rows {part.start}")
