@@ -13,10 +13,12 @@
 // 16 columns among 16 lanes) give the operands, so that no transposed copy of W_hat is
 // written (gated backward 2048 x 4096 x 11008, 707 us with one, 647 without).
 //
-// Bound by the matrix cores at the clock that the power limit leaves: 2048 x 4096 x 22016
-// with the gated epilogue takes 283 us, 1.31 PFLOP/s in bf16 on random data (1.74 on
-// zeros); the product of the gated gradient 2048 x 57344 x 8192 1.34.  Without the gated
-// gradient's epilogue (timed on a copy) a pass of 648 us would take 609.
+// Bound by the matrix cores, at the clock that the power limit leaves on random data (zeros
+// run faster): 2048 x 4096 x 22016 with the gated epilogue takes 287 us, 1.29 PFLOP/s in bf16,
+// where torch's product of 8192^3 reaches 1.42 to 1.57.  Its 688 tiles are 2.69 rounds of the
+// CUs, so that a tenth of it is the last round's idle part; nothing runs under a workgroup's
+// epilogue, and the gated gradient's costs 23 us more (310).  The products of the gradients:
+// 2048 x 22016 x 4096 in two splits 1.42 PFLOP/s without their sum, 2048 x 57344 x 8192 1.46.
 #include "hqq_layers_epilogue.h"
 
 namespace hqq {
@@ -564,7 +566,9 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_kernel(GemmArgs g)
 // Tiles (rows x columns, buffers): 256 x 256 (2) and 256 x 128 (3) with 8 waves, 128 x
 // 128 (4) with 4 waves, one workgroup per CU, and 64 x 128 (3) with 4 waves, two per CU.
 // Their times per 64-wide step in bf16 on MI355X, with the chip full and with at most half
-// its workgroups running: 1.50 and 1.25 us, 0.88 and 0.80, 0.52, 0.60 and 0.40 (large
+// its workgroups running: 1.50 and 1.25 us, 0.88 and 0.80, 0.52, 0.60 and 0.40, for either
+// order of B (in traces of the gradients 1.47 to 1.51 at 125 to 896 steps of 256 x 256, and 1.8
+// with the ends counted at 80) (large
 // products: 44, 37, 32 and 27 thousand outputs per CU and us; the more buffers, the less
 // a step waits for memory: 256 x 128 with two ran 2048 x 4096 x 22016 in 373 us, with three
 // in 318).  The tile of the fewest us by rounds of workgroups over the CUs; where that

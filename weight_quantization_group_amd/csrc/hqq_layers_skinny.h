@@ -11,10 +11,11 @@
 // arithmetic follows there.
 //
 // Bound by the dequantization's instructions (a table of a group's 16 values and 2.6
-// instructions per lookup at 4 bits, about 6 per weight otherwise; half of the cycles
-// issue) and by the launch's ramp: a 4096 x 11008 pair, 1 row 4-bit g64 20 us for 56 MB of
-// codes, scales and zeros, 24 rows 8-bit g128 40 us for 96 MB; 8 rows of a 4096 x 32000
-// head 36 us for 82 MB.  Four waves per workgroup, eight below 512 workgroups: 5, 6 and 7
+// instructions per lookup at 4 bits, about 6 per weight otherwise) and by the launch's ramp: a
+// 4096 x 11008 pair, 1 row 4-bit g64 20 us for 56 MB of codes, scales and zeros, 24 rows
+// 8-bit g128 39 us for 96 MB; 8 rows of a 4096 x 32000 head 36 us for 82 MB.  VALU
+// instructions issue in 54, 43 and 61 % of these kernels' cycles; the waves wait for codes, X or
+// LDS in 28, 21 and 22 % of their time, and in 37, 40 and 54 % for their turn to issue.  Four waves per workgroup, eight below 512 workgroups: 5, 6 and 7
 // leave the SIMDs uneven and cost up to 37 %.
 #pragma once
 

@@ -9,8 +9,9 @@
 // codes load under the current one's arithmetic.  Waves and workgroups split the
 // rows; the waves' sums meet in LDS, the workgroups' in a second launch, in a
 // fixed order.  Bound by the arithmetic of the dequantization (about 5 instructions per
-// weight) and by the latency of two launches: 16 rows through 4096 x 11008 at 4 bits 24.4
-// us, of which about 4 are the second; through 4096 x 4096 14.8.
+// weight) and by the latency of two launches: 16 rows through 4096 x 11008 at 4 bits 23.5
+// us, of which about 4 are the second; through 4096 x 4096 15, with VALU instructions in a
+// third of the first launch's cycles.
 #include "hqq_layers_epilogue.h"
 
 namespace hqq {

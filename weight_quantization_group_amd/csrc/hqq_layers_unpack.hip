@@ -8,8 +8,8 @@
 // and each row of W written, in stretches of 128 bytes or more.  Workgroups go to the
 // 8 XCDs in turn; each XCD gets a contiguous part of them, so that the lines of codes,
 // scales and zeros that neighbours along k share are fetched into one L2 only.  Bound
-// by the bytes: 52 us for the 90 M weights of a 4096 x 11008 pair at 4 bits in groups
-// of 64, 180 MB written and 56 read, 4.5 TB/s where a large copy reaches 5.1.  The SH
+// by the bytes: 49 us for the 90 M weights of a 4096 x 11008 pair at 4 bits in groups
+// of 64, 180 MB written and 56 read, 4.8 TB/s where a large copy reaches 5.2.  The SH
 // lanes of a row that work in one group (8 in groups of 64 and more) fetch and invert the
 // scales of 8 / SH rows each and share them; without that the same took 64 us.
 #include "hqq_layers_epilogue.h"
