@@ -945,3 +945,28 @@ def test_large_tiles_gradient(hq, M, K, N, dtype):
     for part in (slice(0, 300), slice(900, 1019), slice(M - 200, M)):
         y = dY[part].double()
         within(dX[part], *grad_bound([y], [torch.zeros_like(y)], [W], dtype), f"rows {part.start}")
+
+
+@pytest.mark.parametrize("nbits,gs", [(1, 8), (4, 8), (8, 64)])
+def test_fp16_groups_of_equal_weights(hq, path, nbits, gs):
+    """Groups of equal weights hold one code at scale 1, and the bound of the weights counts the whole
+    range of codes there (255 beside weights of 2^-14): small weights keep their precision among them."""
+    dtype, M, K, N = torch.float16, 12, 544 if gs == 8 else 576, 200
+    weights = []
+    for seed, value in ((1, 0.0), (2, 2.0 ** -13)):
+        (packed, scale, zero), _ = make_weight(seed, N, K, nbits, gs, dtype, std=2.0 ** -14)
+        scale[::3, 1::2], zero[::3, 1::2] = 1.0, -value
+        codes = hq.hqq_unpack(packed, N, K, nbits, gs, 1)
+        codes.view(N, K // gs, gs)[::3, 1::2] = 0
+        packed = hq.hqq_pack(codes, nbits, gs, 1)
+        weights.append(((packed, scale, zero), hq.hqq_dequantize(packed, scale, zero, N, K, nbits, gs, 1, dtype=dtype).double()))
+    (gate, Wg), (up, Wu) = weights
+    assert max(Wg.abs().max(), Wu.abs().max()) < 2.0 ** -11
+    X, dY = normal(3, (M, K), dtype), normal(4, (M, N), dtype, 2.0 ** 13)
+    dX = hq.hqq_linear_gated_backward(dY, X, gate, up, N, nbits, gs)
+    G, Up, f, d, eG, eU = gated_terms(X, Wg, Wu, "silu")
+    ref = (dY.double() * Up * d) @ Wg + (dY.double() * f) @ Wu
+    # dX is about 2^-7, within the normal range:
+    # as independent errors, at most u of dG, dU and dX each
+    assert ref.abs().mean() > 2.0 ** -14
+    assert (dX.double() - ref).norm() <= 4 * U[dtype] * ref.norm()

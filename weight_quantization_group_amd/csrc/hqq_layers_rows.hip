@@ -132,7 +132,8 @@ __device__ __forceinline__ float group_bound(float s, float z, float qmax)
 }
 
 // The first kBoundParts workgroups (if asked for) take the groups of the weights in turn: the
-// largest |code - zero| / |scale| is at an end of the codes.  One workgroup per row follows; a
+// largest |code - zero| / |scale| is at an end of the codes (used or not: a loose bound costs
+// headroom only, of which there is plenty).  One workgroup per row follows; a
 // row that is not finite makes the bound so (fp16 magnitudes compare as their bits).  Bound
 // by the launch and the meta's bytes: about 5 us of an fp16 backward pass of 1 or 16 rows
 // through 4096 x 11008 in groups of 64 (59 and 64 us; bf16, which needs no bound, 54 and 59).
