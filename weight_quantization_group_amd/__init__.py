@@ -591,3 +591,7 @@ from .layers import (  # noqa: E402,F401  (needs the names above)
     hqq_linear_cross_entropy_backward_workspace, hqq_linear_cross_entropy_workspace, hqq_linear_gated,
     hqq_linear_gated_backward, hqq_linear_gated_backward_workspace, hqq_linear_gated_workspace,
     load_layers_library)
+
+from .cache import (  # noqa: E402,F401
+    CACHE_EXPORTS, CACHE_LIB_PATH, CacheError, QuantizedCache, hqq_cache_attention, hqq_cache_attention_workspace,
+    hqq_cache_read, hqq_cache_strerror, hqq_cache_write, load_cache_library)

@@ -1,4 +1,4 @@
-"""Build the HIP libraries ``libhqq.so`` and ``libhqq_layers.so`` for gfx950, in-tree.
+"""Build the HIP libraries ``libhqq.so``, ``libhqq_layers.so`` and ``libhqq_cache.so`` for gfx950, in-tree.
 
     python -m weight_quantization_group_amd.build
 
@@ -32,6 +32,10 @@ LAYERS_LIB = os.path.join(PKG, "libhqq_layers.so")
 LAYERS_SOURCES = ["hqq_layers_abi.cpp", "hqq_layers_unpack.hip", "hqq_layers_gemm.hip", "hqq_layers_rows.hip",
                   "hqq_layers_skinny_one.hip", "hqq_layers_skinny_pair.hip", "hqq_layers_skinny_grad.hip"]
 
+CACHE_LIB = os.path.join(PKG, "libhqq_cache.so")
+CACHE_SOURCES = ["hqq_cache_abi.cpp", "hqq_cache_codec.hip", "hqq_cache_join.hip", "hqq_cache_attention_b2.hip",
+                 "hqq_cache_attention_b4.hip", "hqq_cache_attention_b8.hip"]
+
 FLAGS = ["-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-fvisibility=hidden",
          "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -59,14 +63,16 @@ def _link(lib: str, objs, libs=()) -> None:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    todo = SOURCES + LAYERS_SOURCES
+    todo = SOURCES + LAYERS_SOURCES + CACHE_SOURCES
     with cf.ThreadPoolExecutor(max_workers=len(todo)) as ex:
         objs = dict(zip(todo, ex.map(_compile, todo)))
     _link(LIB, [objs[s] for s in SOURCES], ["-lhipblaslt"])
     _link(LAYERS_LIB, [objs[s] for s in LAYERS_SOURCES])
+    _link(CACHE_LIB, [objs[s] for s in CACHE_SOURCES])
     if verbose:
         print("built", LIB)
         print("built", LAYERS_LIB)
+        print("built", CACHE_LIB)
     return LIB
 
 

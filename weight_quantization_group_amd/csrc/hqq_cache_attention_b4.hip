@@ -1,0 +1,11 @@
+// hqq_cache_attention_b4.hip -- the cache's attention at 4 bits.
+#include "hqq_cache_attention.h"
+
+namespace hqq {
+
+hipError_t launch_cache_attention_b4(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s)
+{
+    return launch_cache_attention<4>(dim, group_size, a, s);
+}
+
+}  // namespace hqq

@@ -1,0 +1,233 @@
+// hqq_cache_codec.hip -- writing tokens into the quantized key-value cache and
+// reading them back.
+//
+// A lane takes 8 consecutive values of a row (one 16-byte load or store), so a
+// group is 4 to 32 neighbouring lanes of one wave; blockIdx.y is the side (k, v).
+#include "hqq_cache_internal.h"
+
+namespace hqq {
+namespace {
+
+constexpr int kBlock = 256;
+
+template <bool BF>
+__device__ __forceinline__ float widen(uint16_t v)
+{
+    if constexpr (BF) {
+        return __uint_as_float((uint32_t)v << 16);
+    } else {
+        _Float16 h;
+        __builtin_memcpy(&h, &v, 2);
+        return (float)h;
+    }
+}
+
+// one fp32 -> 16-bit value, round to nearest even
+template <bool BF>
+__device__ __forceinline__ uint16_t narrow(float v)
+{
+    uint16_t u;
+    if constexpr (BF) {
+        const __bf16 h = (__bf16)v;
+        __builtin_memcpy(&u, &h, 2);
+    } else {
+        const _Float16 h = (_Float16)v;
+        __builtin_memcpy(&u, &h, 2);
+    }
+    return u;
+}
+
+// This lane's row, and its slot's row of the cache (-1: skipped)
+template <int D>
+struct Place {
+    static constexpr int kLanes = D / 8;              // lanes of a row
+    static constexpr int kRows = kBlock / kLanes;     // rows of a workgroup
+    int chunk;
+    int32_t row, token, head;
+    int64_t cache_row;
+    bool valid;
+
+    __device__ __forceinline__ explicit Place(const CacheCodecArgs &a)
+    {
+        const int local = threadIdx.x / kLanes;
+        chunk = threadIdx.x - local * kLanes;
+        row = (int32_t)blockIdx.x * kRows + local;
+        valid = local < kRows && row < a.rows;
+        cache_row = -1;
+        token = head = 0;
+        if (!valid)
+            return;
+        token = (int32_t)((uint32_t)row / (uint32_t)a.heads);
+        head = row - token * a.heads;
+        const int64_t slot = a.slots[token];
+        if (slot >= 0 && slot < a.slot_count)
+            cache_row = (((slot >> a.page_shift) * a.heads + head) << a.page_shift) + (slot & a.page_mask);
+    }
+};
+
+// The values (code - zero) / scale in fp32, rounded once
+template <bool BF>
+__device__ __forceinline__ uint4 values16(const float (&code)[8], float scale, float zero)
+{
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = narrow<BF>((code[j] - zero) / scale);
+    uint4 r;
+    __builtin_memcpy(&r, v, 16);
+    return r;
+}
+
+template <int NB, int D, int GS, bool BF>
+__global__ __launch_bounds__(kBlock) void cache_write_kernel(CacheCodecArgs a)
+{
+    const int side = blockIdx.y;
+    const Place<D> p(a);
+    float x[8];
+    if (p.valid) {
+        const uint16_t *src = a.x[side] + p.token * a.token_stride[side] + p.head * a.head_stride[side] + p.chunk * 8;
+        const uint4 raw = *reinterpret_cast<const uint4 *>(src);
+        uint16_t h[8];
+        __builtin_memcpy(h, &raw, 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = widen<BF>(h[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = 0.0f;
+    }
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+        lo = fminf(lo, x[j]);
+        hi = fmaxf(hi, x[j]);
+    }
+#pragma unroll
+    for (int o = 1; o < GS / 8; o *= 2) {
+        lo = fminf(lo, __shfl_xor(lo, o));
+        hi = fmaxf(hi, __shfl_xor(hi, o));
+    }
+    if (!p.valid)
+        return;
+    uint16_t *hat = a.hat[side] ? a.hat[side] + (int64_t)p.row * D + p.chunk * 8 : nullptr;
+    if (p.cache_row < 0) {
+        if (hat)
+            *reinterpret_cast<uint4 *>(hat) = uint4{0, 0, 0, 0};
+        return;
+    }
+    constexpr float qmax = (float)((1 << NB) - 1);
+    const float range = hi - lo;
+    const float scale = range == 0.0f ? 1.0f : qmax / range;
+    const float zero = -(lo * scale);
+    float code[8];
+    uint64_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        code[j] = fminf(fmaxf(rintf(fmaf(x[j], scale, zero)), 0.0f), qmax);
+        bits |= (uint64_t)(uint32_t)code[j] << (NB * j);
+    }
+    constexpr int kRowBytes = D * NB / 8;
+    char *dst = (char *)a.packed[side] + p.cache_row * kRowBytes + p.chunk * NB;
+    if constexpr (NB == 8)
+        *reinterpret_cast<uint2 *>(dst) = uint2{(uint32_t)bits, (uint32_t)(bits >> 32)};
+    else if constexpr (NB == 4)
+        *reinterpret_cast<uint32_t *>(dst) = (uint32_t)bits;
+    else
+        *reinterpret_cast<uint16_t *>(dst) = (uint16_t)bits;
+    if (p.chunk % (GS / 8) == 0) {
+        const int64_t g = p.cache_row * (D / GS) + p.chunk / (GS / 8);
+        a.scale[side][g] = scale;
+        a.zero[side][g] = zero;
+    }
+    if (hat)
+        *reinterpret_cast<uint4 *>(hat) = values16<BF>(code, scale, zero);
+}
+
+template <int NB, int D, int GS, bool BF>
+__global__ __launch_bounds__(kBlock) void cache_read_kernel(CacheCodecArgs a)
+{
+    const int side = blockIdx.y;
+    const Place<D> p(a);
+    if (!p.valid)
+        return;
+    uint4 *dst = reinterpret_cast<uint4 *>(a.hat[side] + (int64_t)p.row * D + p.chunk * 8);
+    if (p.cache_row < 0) {
+        *dst = uint4{0, 0, 0, 0};
+        return;
+    }
+    constexpr int kRowBytes = D * NB / 8;
+    const char *src = (const char *)a.packed[side] + p.cache_row * kRowBytes + p.chunk * NB;
+    uint64_t bits;
+    if constexpr (NB == 8) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(src);
+        bits = (uint64_t)w.y << 32 | w.x;
+    } else if constexpr (NB == 4) {
+        bits = *reinterpret_cast<const uint32_t *>(src);
+    } else {
+        bits = *reinterpret_cast<const uint16_t *>(src);
+    }
+    const int64_t g = p.cache_row * (D / GS) + p.chunk / (GS / 8);
+    const float scale = a.scale[side][g], zero = a.zero[side][g];
+    float code[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        code[j] = (float)(uint32_t)(bits >> (NB * j) & ((1u << NB) - 1));
+    *dst = values16<BF>(code, scale, zero);
+}
+
+template <int NB, int D, int GS, bool BF>
+hipError_t launch(bool write, const CacheCodecArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.rows + Place<D>::kRows - 1) / Place<D>::kRows), 2);
+    if (write)
+        hipLaunchKernelGGL((cache_write_kernel<NB, D, GS, BF>), grid, dim3(kBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((cache_read_kernel<NB, D, GS, BF>), grid, dim3(kBlock), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int NB, bool BF>
+hipError_t launch_format(bool write, int dim, int gs, const CacheCodecArgs &a, hipStream_t s)
+{
+    switch (dim * 1024 + gs) {
+    case 64 * 1024 + 32: return launch<NB, 64, 32, BF>(write, a, s);
+    case 64 * 1024 + 64: return launch<NB, 64, 64, BF>(write, a, s);
+    case 96 * 1024 + 32: return launch<NB, 96, 32, BF>(write, a, s);
+    case 128 * 1024 + 32: return launch<NB, 128, 32, BF>(write, a, s);
+    case 128 * 1024 + 64: return launch<NB, 128, 64, BF>(write, a, s);
+    case 128 * 1024 + 128: return launch<NB, 128, 128, BF>(write, a, s);
+    case 192 * 1024 + 64: return launch<NB, 192, 64, BF>(write, a, s);
+    case 256 * 1024 + 64: return launch<NB, 256, 64, BF>(write, a, s);
+    case 256 * 1024 + 128: return launch<NB, 256, 128, BF>(write, a, s);
+    case 256 * 1024 + 256: return launch<NB, 256, 256, BF>(write, a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int NB>
+hipError_t launch_bits(bool write, int dim, int gs, bool bf16, const CacheCodecArgs &a, hipStream_t s)
+{
+    return bf16 ? launch_format<NB, true>(write, dim, gs, a, s) : launch_format<NB, false>(write, dim, gs, a, s);
+}
+
+hipError_t launch_all(bool write, int nbits, int dim, int gs, bool bf16, const CacheCodecArgs &a, hipStream_t s)
+{
+    return nbits == 2   ? launch_bits<2>(write, dim, gs, bf16, a, s)
+           : nbits == 4 ? launch_bits<4>(write, dim, gs, bf16, a, s)
+                        : launch_bits<8>(write, dim, gs, bf16, a, s);
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s)
+{
+    return launch_all(true, nbits, dim, group_size, bf16, a, s);
+}
+
+hipError_t launch_cache_read(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s)
+{
+    return launch_all(false, nbits, dim, group_size, bf16, a, s);
+}
+
+}  // namespace hqq

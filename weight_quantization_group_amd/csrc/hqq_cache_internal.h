@@ -1,0 +1,62 @@
+// hqq_cache_internal.h -- declarations shared by the cache library's own
+// translation units.
+#pragma once
+
+#include "hqq_cache.h"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hqq {
+
+// Arguments of the write and read kernels, either side's at [0] (k) and [1] (v).
+struct CacheCodecArgs {
+    uint32_t *packed[2];
+    float *scale[2], *zero[2];
+    const uint16_t *x[2];            // write: rows of 16-bit values
+    int64_t token_stride[2], head_stride[2];
+    uint16_t *hat[2];                // read's outputs; write: null, or the values written
+    const int64_t *slots;
+    int64_t slot_count;              // pages * page_size
+    int32_t tokens, heads, rows;     // rows = tokens * heads
+    int32_t page_shift, page_mask;
+};
+
+// Attention: sequences are cut into items of `chunk` tokens, a number that the device
+// finds from the lengths (cache_plan), so that all items of a key-value head number at
+// most items_per_head + batch.
+struct CacheAttentionArgs {
+    const uint32_t *packed[2];
+    const float *scale[2], *zero[2];
+    const uint16_t *Q;
+    int64_t q_batch_stride, q_head_stride;
+    const int32_t *table, *lengths;
+    uint16_t *out;
+    float *lse;                      // may be null
+    float *part;                     // [items, q_heads, dim] sums of items of split sequences
+    float2 *part_ml;                 // [items, q_heads] their maxima and sums of weights
+    int32_t batch, q_heads, heads, G;
+    int32_t row_tiles;               // blocks of 16 q heads of a key-value head
+    int32_t pages, page_shift, page_mask, table_width;
+    int32_t window;                  // 0: none
+    int32_t items_per_head;
+    float scale_log2;                // softmax_scale * log2(e)
+    int32_t bf16;
+};
+
+// Tokens that a workgroup takes in one step: 4 waves with 32 each.
+constexpr int kCacheTile = 32;
+constexpr int kCacheWaves = 4;
+constexpr int kCacheStep = kCacheTile * kCacheWaves;
+// Workgroups that an attention call is cut into, about.
+constexpr int kCacheTarget = 1024;
+
+hipError_t launch_cache_write(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
+hipError_t launch_cache_read(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
+hipError_t launch_cache_attention_b2(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
+hipError_t launch_cache_attention_b4(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
+hipError_t launch_cache_attention_b8(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
+// joins the items of split sequences
+hipError_t launch_cache_join(int dim, const CacheAttentionArgs &a, hipStream_t s);
+
+}  // namespace hqq
