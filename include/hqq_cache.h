@@ -26,6 +26,11 @@
  * allocated and no state is kept.  Outputs and the workspace must not overlap
  * inputs, the cache's arrays or one another (HQQ_EINVAL_PTR).  A call of no
  * tokens (no sequences) does nothing and needs no pointers but the cache's.
+ *
+ * Strides.  Keys, values and queries are rows of dim 16-bit values: row (t, h)
+ * starts at t * token_stride + h * head_stride values, strides >= 0 and
+ * multiples of 8 (HQQ_EINVAL_SHAPE), so that they can be a part of a wider
+ * projection's output.  Other inputs and all outputs are contiguous.
  */
 #ifndef HQQ_CACHE_H
 #define HQQ_CACHE_H
@@ -54,15 +59,6 @@ typedef struct hqq_cache {
     int32_t page_size, heads, dim, nbits, group_size;
 } hqq_cache;
 
-/* Rows of 16-bit values, one per token (or sequence) and head: row (t, h) is
- * the dim values at data + t * token_stride + h * head_stride, strides in
- * values and multiples of 8, so that keys, values or queries can be a part of
- * a wider projection's output. */
-typedef struct hqq_rows {
-    const uint16_t *data;
-    int64_t token_stride, head_stride;
-} hqq_rows;
-
 /* Quantize `tokens` tokens into the cache at their slots: each group with the
  * scale, zero and codes that hqq_quantize gives it at iters = 0,
  *   scale = qmax / (max - min), zero = -(min * scale)  (1, -min where max = min)
@@ -77,9 +73,10 @@ typedef struct hqq_rows {
  * the difference of a group's largest and smallest is finite in fp32 and either
  * 0 or at least 2^-118 (fp16 values always are).
  * Limit of write and read (HQQ_EINVAL_SHAPE): tokens * heads at most 2^26. */
-HQQ_API int hqq_cache_write(const hqq_cache *cache, const hqq_rows *K, const hqq_rows *V, int64_t tokens,
-                            const int64_t *slots, int dtype, uint16_t *K_hat, uint16_t *V_hat,
-                            void *stream);
+HQQ_API int hqq_cache_write(const hqq_cache *cache, const uint16_t *K, int64_t k_token_stride,
+                            int64_t k_head_stride, const uint16_t *V, int64_t v_token_stride,
+                            int64_t v_head_stride, int64_t tokens, const int64_t *slots, int dtype,
+                            uint16_t *K_hat, uint16_t *V_hat, void *stream);
 
 /* Read tokens back: K and V [tokens, heads, dim] of dtype receive the values
  * (code - zero) / scale at the slots (fp32, rounded once: what
@@ -119,10 +116,11 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  * run at the same time (two streams, two captured graphs) need one each. */
 HQQ_API int64_t hqq_cache_attention_workspace(const hqq_cache *cache, int64_t batch, int64_t q_heads,
                                               int64_t table_width);
-HQQ_API int hqq_cache_attention(const hqq_cache *cache, const hqq_rows *Q, int64_t batch, int64_t q_heads,
-                                const int32_t *table, int64_t table_width, const int32_t *lengths,
-                                float softmax_scale, int64_t window, int dtype, uint16_t *out, float *lse,
-                                void *workspace, int64_t workspace_bytes, void *stream);
+HQQ_API int hqq_cache_attention(const hqq_cache *cache, const uint16_t *Q, int64_t q_batch_stride,
+                                int64_t q_head_stride, int64_t batch, int64_t q_heads, const int32_t *table,
+                                int64_t table_width, const int32_t *lengths, float softmax_scale,
+                                int64_t window, int dtype, uint16_t *out, float *lse, void *workspace,
+                                int64_t workspace_bytes, void *stream);
 
 /* Static description of a status code of this header or of hqq.h. */
 HQQ_API const char *hqq_cache_strerror(int status);

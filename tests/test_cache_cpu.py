@@ -63,24 +63,21 @@ def cache(pages=10, page_size=16, heads=2, dim=128, nbits=4, gs=64, kp=KP, ks=KS
     return HqqCache(HqqCacheSide(kp, ks, kz), HqqCacheSide(vp, vs, vz), pages, page_size, heads, dim, nbits, gs)
 
 
-def rows(data, token, head):
-    from weight_quantization_group_amd.cache import HqqRows
-    return None if data == "none" else ctypes.byref(HqqRows(data, token, head))
-
-
-def write(lib, k=X, v=Y, tokens=4, slots=S, dtype=0, k_hat=None, v_hat=None, token=256, head=128, c=None, **kw):
+def write(lib, k=X, v=Y, tokens=4, slots=S, dtype=0, k_hat=None, v_hat=None, token=256, head=128, k_strides=None,
+          v_strides=None, c=None, **kw):
     c = None if c == "none" else ctypes.byref(cache(**kw))
-    return lib.hqq_cache_write(c, rows(k, token, head), rows(v, token, head), tokens, slots, dtype, k_hat, v_hat, None)
+    return lib.hqq_cache_write(c, k, *(k_strides or (token, head)), v, *(v_strides or (token, head)), tokens, slots, dtype,
+                               k_hat, v_hat, None)
 
 
 def read(lib, k=X, v=Y, tokens=4, slots=S, dtype=0, c=None, **kw):
     return lib.hqq_cache_read(None if c == "none" else ctypes.byref(cache(**kw)), slots, tokens, dtype, k, v, None)
 
 
-def attention(lib, q=X, batch=3, q_heads=4, table=T, width=20, lengths=L, scale=0.1, window=0, dtype=0, out=O, lse=P,
-              ws=W, size=1 << 30, token=512, head=128, c=None, **kw):
+def attention(lib, q=X, batch=3, q_heads=4, table=T, width=40, lengths=L, scale=0.1, window=0, dtype=0, out=O, lse=P,
+              ws=W, size=1 << 32, token=512, head=128, c=None, **kw):
     c = None if c == "none" else ctypes.byref(cache(**kw))
-    return lib.hqq_cache_attention(c, rows(q, token, head), batch, q_heads, table, width, lengths, scale, window, dtype,
+    return lib.hqq_cache_attention(c, q, token, head, batch, q_heads, table, width, lengths, scale, window, dtype,
                                    out, lse, ws, size, None)
 
 
@@ -107,10 +104,11 @@ def test_rejects_layouts(lib, call, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(tokens=-1), SHAPE), (dict(tokens=(1 << 25) + 1), SHAPE), (dict(tokens=1 << 62), SHAPE),
-    (dict(k="none"), PTR), (dict(v="none"), PTR), (dict(k=None), PTR), (dict(v=Y + 8), PTR), (dict(slots=None), PTR),
+    (dict(k=None), PTR), (dict(v=None), PTR), (dict(k=X + 2), PTR), (dict(v=Y + 8), PTR), (dict(slots=None), PTR),
     (dict(slots=S + 4), PTR), (dict(k_hat=O), PTR), (dict(v_hat=O), PTR), (dict(k_hat=O + 8, v_hat=P), PTR),
     (dict(token=4), SHAPE), (dict(token=-256), SHAPE), (dict(head=12), SHAPE), (dict(head=-8), SHAPE),
     (dict(token=1 << 62), SHAPE), (dict(head=1 << 40), SHAPE),
+    (dict(k_strides=(260, 128)), SHAPE), (dict(v_strides=(256, 130)), SHAPE),
 ])
 def test_write_rejects(lib, kw, code):
     assert write(lib, **kw) == code
@@ -131,7 +129,7 @@ def test_read_rejects(lib, kw, code):
     (dict(width=0), SHAPE), (dict(width=-1), SHAPE), (dict(width=(1 << 26) + 1), SHAPE), (dict(width=1 << 62), SHAPE),
     (dict(scale=0.0), PARAM), (dict(scale=-1.0), PARAM), (dict(scale=float("nan")), PARAM),
     (dict(scale=float("inf")), PARAM), (dict(scale=3e38), PARAM), (dict(window=-1), PARAM),
-    (dict(q="none"), PTR), (dict(q=None), PTR), (dict(q=X + 8), PTR), (dict(token=12), SHAPE), (dict(head=-8), SHAPE),
+    (dict(q=None), PTR), (dict(q=X + 2), PTR), (dict(q=X + 8), PTR), (dict(token=12), SHAPE), (dict(head=-8), SHAPE),
     (dict(table=None), PTR), (dict(table=T + 2), PTR), (dict(lengths=None), PTR), (dict(lengths=L + 1), PTR),
     (dict(out=None), PTR), (dict(out=O + 8), PTR), (dict(lse=P + 2), PTR), (dict(ws=None), PTR), (dict(ws=W + 8), PTR),
     (dict(size=-1), PTR), (dict(size=0), WORKSPACE), (dict(ws=None, size=0), WORKSPACE), (dict(size=4096), WORKSPACE),
@@ -141,23 +139,25 @@ def test_attention_rejects(lib, kw, code):
 
 
 def test_a_call_of_nothing_needs_no_pointers(lib):
-    assert write(lib, k="none", v="none", tokens=0, slots=None) == 0
+    assert write(lib, k=None, v=None, tokens=0, slots=None) == 0
     assert read(lib, k=None, v=None, tokens=0, slots=None) == 0
-    assert attention(lib, q="none", batch=0, table=None, lengths=None, out=None, lse=None, ws=None, size=0) == 0
+    assert attention(lib, q=None, batch=0, table=None, lengths=None, out=None, lse=None, ws=None, size=0) == 0
     # but a cache and a format
     assert write(lib, tokens=0, nbits=3) == NBITS and read(lib, tokens=0, kp=None) == PTR
     assert attention(lib, batch=0, q_heads=3) == SHAPE
 
 
 def test_workspace(w, lib):
-    """None where no sequence can exceed a workgroup's step of 128 tokens; else a part of dim sums and two
-    statistics per query head and item, items about 1024 workgroups' worth and one more per sequence."""
+    """None where no sequence can exceed 512 tokens; else dim sums and two statistics per query head and
+    segment: as many segments as runs (the chip's workgroups per key-value head) and sequences."""
     def need(batch, q_heads, width, **kw):
         return lib.hqq_cache_attention_workspace(ctypes.byref(cache(**kw)), batch, q_heads, width)
 
-    assert need(3, 4, 8) == 0 and need(3, 4, 9) > 0 and need(0, 4, 9) == 0
-    items = 1024 // 2 + 3
-    assert need(3, 4, 100) == items * 4 * 128 * 4 + -(-items * 4 * 8 // 256) * 256
+    assert need(3, 4, 32) == 0 and need(3, 4, 33) > 0 and need(0, 4, 33) == 0
+    sizes = {need(b, 4, 100) for b in (1, 2, 3)}
+    assert len(sizes) == 3 and max(sizes) - min(sizes) <= 2 * (4 * 128 * 4 + 4 * 8) + 512
+    segments = (need(3, 4, 100) // (4 * 128 * 4 + 4 * 8))
+    assert 256 // 2 + 3 <= segments <= 4 * 256 * 8 + 3
     for kw, code in LAYOUTS[:29]:
         assert need(3, 4, 9, **kw) == code
     assert lib.hqq_cache_attention_workspace(None, 3, 4, 9) == PTR
@@ -194,7 +194,7 @@ def test_rejects_writes_over_what_is_read(lib):
     for base, size in arrays + [(S, 32)]:
         for at in (base, last(base, size), base - row + 16):
             assert read(lib, k=at) == PTR and read(lib, v=at) == PTR
-    q_row, table, ws = 3 * 4 * 128 * 2, 3 * 20 * 4, lib.hqq_cache_attention_workspace(ctypes.byref(cache()), 3, 4, 20)
+    q_row, table, ws = 3 * 4 * 128 * 2, 3 * 40 * 4, lib.hqq_cache_attention_workspace(ctypes.byref(cache()), 3, 4, 40)
     inputs = arrays + [(X, q_row), (T, table), (L, 12)]
     for base, size in inputs:
         for at in (base, last(base, size)):

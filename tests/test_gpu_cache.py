@@ -571,21 +571,18 @@ def test_graph_and_streams(hq):
 def test_outputs_given(hq):
     """Rows beside a given output's keep what they held; the C call may leave out lse."""
     g = rng(18)
-    c = filled(hq, g, 40, 16, 1, 64, 4, 32)
-    Q, table, n = batch_of(c, g, torch.float16, [100, 400], 3)
+    c = filled(hq, g, 80, 16, 1, 64, 4, 32)
+    Q, table, n = batch_of(c, g, torch.float16, [100, 900], 3)
     want = hq.hqq_cache_attention(c, Q, table, n)
     room, row = torch.full((6, 3, 64), 7.0, device="cuda").half(), torch.full((8, 3), 7.0, device="cuda")
     got = hq.hqq_cache_attention(c, Q, table, n, out=room[2:4], lse=row[3:5])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert bool((room[:2] == 7).all()) and bool((room[4:] == 7).all()) and bool((row[:3] == 7).all()) and bool((row[5:] == 7).all())
-    from weight_quantization_group_amd.cache import _rows
-    import ctypes
-    q = _rows(Q, "Q", c)
     size = hq.hqq_cache_attention_workspace(c, 2, 3, table.shape[1])
-    ws, out = torch.empty(size, dtype=torch.uint8, device="cuda"), torch.empty_like(Q)
+    ws, out = torch.empty(max(16, size), dtype=torch.uint8, device="cuda"), torch.empty_like(Q)
     st = hq.load_cache_library().hqq_cache_attention(
-        c._ptr, ctypes.addressof(q), 2, 3, table.data_ptr(), table.shape[1], n.data_ptr(), 0.125, 0, 0, out.data_ptr(),
-        None, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+        c._ptr, Q.data_ptr(), 3 * 64, 64, 2, 3, table.data_ptr(), table.shape[1], n.data_ptr(), 0.125, 0, 0,
+        out.data_ptr(), None, ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
     assert st == 0 and torch.equal(out, want[0])
 
 
@@ -604,7 +601,7 @@ def test_binding_refuses(hq):
     K = torch.zeros(5, 2, 128, device="cuda").half()
     s = torch.arange(5, device="cuda")
     Q, table, n = torch.zeros(3, 4, 128, device="cuda").half(), torch.zeros(3, 2, device="cuda").int(), torch.ones(3, device="cuda").int()
-    big = torch.zeros(3, 20, device="cuda").int()
+    big = torch.zeros(3, 40, device="cuda").int()
     bad = [
         (TypeError, lambda: hq.hqq_cache_write(c, K.cpu(), K, s)),
         (TypeError, lambda: hq.hqq_cache_write(c, K.float(), K.float(), s)),

@@ -38,11 +38,6 @@ class HqqCache(ctypes.Structure):
                 ("group_size", ctypes.c_int32)]
 
 
-class HqqRows(ctypes.Structure):
-    """struct hqq_rows of include/hqq_cache.h"""
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
 class CacheError(HQQError):
     def __init__(self, fn: str, status: int):
         RuntimeError.__init__(self, f"{fn} failed: {hqq_cache_strerror(status)} (status {status})")
@@ -62,10 +57,10 @@ def load_cache_library(path: str = CACHE_LIB_PATH):
     L = ctypes.CDLL(path)
     P, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
     for name, args, res in (
-            ("hqq_cache_write", [P, P, P, i64, P, i32, P, P, P], i32),
+            ("hqq_cache_write", [P, P, i64, i64, P, i64, i64, i64, P, i32, P, P, P], i32),
             ("hqq_cache_read", [P, P, i64, i32, P, P, P], i32),
             ("hqq_cache_attention_workspace", [P, i64, i64, i64], i64),
-            ("hqq_cache_attention", [P, P, i64, i64, P, i64, P, f32, i64, i32, P, P, P, i64, P], i32),
+            ("hqq_cache_attention", [P, P, i64, i64, i64, i64, P, i64, P, f32, i64, i32, P, P, P, i64, P], i32),
             ("hqq_cache_strerror", [i32], ctypes.c_char_p)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
@@ -78,10 +73,18 @@ def hqq_cache_strerror(status: int) -> str:
 
 
 _DT = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
+_F32, _I64, _I32 = (torch.float32,), (torch.int64,), (torch.int32,)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _tensor(t, name: str, dtypes, shape, device) -> int:
-    """The address of a contiguous CUDA tensor of this shape on device, checked."""
+def _tensor(t, name: str, dtypes, shape, index: int) -> int:
+    """The address of a contiguous CUDA tensor of this shape on device `index`, checked."""
+    try:
+        if t.get_device() == index and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -90,9 +93,7 @@ def _tensor(t, name: str, dtypes, shape, device) -> int:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache is on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, the cache is on cuda:{index}")
 
 
 class QuantizedCache:
@@ -116,6 +117,7 @@ class QuantizedCache:
         if nbits not in (2, 4, 8):
             raise ValueError(f"nbits must be 2, 4 or 8, got {nbits}")
         self.nbits, self.group_size, self.device = int(nbits), int(group_size), packed.device
+        self._index = packed.get_device()
         self.pages, self.heads, self.page_size, words = packed.shape
         self.dim = words * 32 // self.nbits
         meta = (self.pages, self.heads, self.page_size, self.dim // self.group_size if self.group_size > 0 else 0)
@@ -123,15 +125,17 @@ class QuantizedCache:
         for name, side in (("k", self._k), ("v", self._v)):
             if len(side) != 3:
                 raise ValueError(f"{name} must be (packed, scale, zero)")
-            sides.append(HqqCacheSide(_tensor(side[0], name + " packed", _U32, packed.shape, self.device),
-                                      _tensor(side[1], name + " scale", (torch.float32,), meta, self.device),
-                                      _tensor(side[2], name + " zero", (torch.float32,), meta, self.device)))
+            sides.append(HqqCacheSide(_tensor(side[0], name + " packed", _U32, packed.shape, self._index),
+                                      _tensor(side[1], name + " scale", _F32, meta, self._index),
+                                      _tensor(side[2], name + " zero", _F32, meta, self._index)))
         # the library's layout checks, which need no device
         if min(packed.shape) < 1 or max(packed.shape) >= 1 << 31:
             raise ValueError(f"packed must not be empty, got {list(packed.shape)}")
         self._c = HqqCache(*sides, self.pages, self.page_size, self.heads, self.dim, self.nbits, self.group_size)
         self._ptr = ctypes.addressof(self._c)
-        _bytes(self, 1, self.heads, 1)
+        self._softmax_scale = 1.0 / math.sqrt(self.dim)
+        self._room = None, 0          # the sizes last asked for, and their workspace's bytes
+        _bytes(self, (1, self.heads, 1))
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, dim: int, nbits: int, group_size: int, device="cuda"):
@@ -157,45 +161,49 @@ class QuantizedCache:
         return self._v
 
 
-def _bytes(cache: QuantizedCache, batch: int, q_heads: int, table_width: int) -> int:
-    n = cache._lib.hqq_cache_attention_workspace(cache._ptr, batch, q_heads, table_width)
+def _bytes(cache: QuantizedCache, sizes) -> int:
+    if cache._room[0] == sizes:
+        return cache._room[1]
+    n = cache._lib.hqq_cache_attention_workspace(cache._ptr, *sizes)
     if n < 0:
         raise CacheError("hqq_cache_attention_workspace", n)
+    cache._room = sizes, n
     return n
 
 
 def hqq_cache_attention_workspace(cache: QuantizedCache, batch: int, q_heads: int, table_width: int) -> int:
     """Bytes of workspace of hqq_cache_attention for these sizes."""
-    return _bytes(cache, batch, q_heads, table_width)
+    return _bytes(cache, (batch, q_heads, table_width))
 
 
-def _rows(t, name: str, cache: QuantizedCache, dtype=None) -> HqqRows:
-    """[rows, heads, dim] values of 16 bits with any strides of rows and heads, checked."""
+def _rows(t, name: str, cache: QuantizedCache):
+    """(address, stride of the rows, stride of the heads, shape) of [rows, heads, dim] values of 16
+    bits with any strides of rows and heads, checked."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DT or dtype not in (None, t.dtype):
-        raise TypeError(f"{name} must be {dtype or 'float16 or bfloat16'}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != cache.dim:
-        raise ValueError(f"{name} must be [rows, heads, {cache.dim}], got {list(t.shape)}")
-    if t.device != cache.device:
+    if t.dtype not in _DT:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.dim:
+        raise ValueError(f"{name} must be [rows, heads, {cache.dim}], got {list(shape)}")
+    if t.get_device() != cache._index:
         raise ValueError(f"{name} is on {t.device}, the cache is on {cache.device}")
-    rows, heads, _ = t.shape
-    s = t.stride()
-    if s[2] != 1:
+    a, b, c = t.stride()
+    if c != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return HqqRows(t.data_ptr(), s[0] if rows > 1 else 0, s[1] if heads > 1 else 0)
+    return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, shape
 
 
-def _call(cache: QuantizedCache, name: str, *args) -> None:
-    """Run the library's call `name` on the cache's device and its current stream."""
-    f, dev = getattr(cache._lib, name), cache.device
-    if torch.cuda.current_device() == dev.index:
-        st = f(cache._ptr, *args, torch._C._cuda_getCurrentRawStream(dev.index))
+def _call(cache: QuantizedCache, f, *args) -> None:
+    """Run the library's call f on the cache's device and its current stream."""
+    index = cache._index
+    if _current_device() == index:
+        st = f(cache._ptr, *args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = f(cache._ptr, *args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(index):
+            st = f(cache._ptr, *args, _raw_stream(index))
     if st != 0:
-        raise CacheError(name, st)
+        raise CacheError(f.__name__, st)
 
 
 def hqq_cache_write(cache: QuantizedCache, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
@@ -205,15 +213,19 @@ def hqq_cache_write(cache: QuantizedCache, K: torch.Tensor, V: torch.Tensor, slo
     cache (-1, say) skips its token; the others must differ.  K and V may be parts of a
     wider tensor (strides multiples of 8, addresses of 16 bytes).  values: also return
     what the cache now stands for, (K_hat, V_hat), with zeros for skipped tokens."""
-    rows = _rows(K, "K", cache), _rows(V, "V", cache, K.dtype if isinstance(K, torch.Tensor) else None)
-    tokens = K.shape[0]
-    if K.shape[1] != cache.heads or V.shape != K.shape:
-        raise ValueError(f"K and V must be [{tokens}, {cache.heads}, {cache.dim}], got {list(K.shape)} and {list(V.shape)}")
-    at = _tensor(slots, "slots", (torch.int64,), (tokens,), cache.device)
-    hat = (torch.empty(K.shape, dtype=K.dtype, device=cache.device),
-           torch.empty(K.shape, dtype=K.dtype, device=cache.device)) if values else None
-    _call(cache, "hqq_cache_write", ctypes.addressof(rows[0]), ctypes.addressof(rows[1]), tokens, at, _DT[K.dtype],
-          *((hat[0].data_ptr(), hat[1].data_ptr()) if values else (None, None)))
+    pk, k_token, k_head, shape = _rows(K, "K", cache)
+    pv, v_token, v_head, v_shape = _rows(V, "V", cache)
+    tokens, dtype = shape[0], K.dtype
+    if V.dtype != dtype:
+        raise TypeError(f"K and V must have one dtype, got {dtype} and {V.dtype}")
+    if shape[1] != cache.heads or v_shape != shape:
+        raise ValueError(f"K and V must be [{tokens}, {cache.heads}, {cache.dim}], got {list(shape)} and {list(v_shape)}")
+    at = _tensor(slots, "slots", _I64, (tokens,), cache._index)
+    hat = to_k = to_v = None
+    if values:
+        hat = (torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device))
+        to_k, to_v = hat[0].data_ptr(), hat[1].data_ptr()
+    _call(cache, cache._lib.hqq_cache_write, pk, k_token, k_head, pv, v_token, v_head, tokens, at, _DT[dtype], to_k, to_v)
     return hat
 
 
@@ -221,15 +233,15 @@ def hqq_cache_read(cache: QuantizedCache, slots: torch.Tensor, dtype=torch.float
     """The keys and values at slots (int64 [tokens]) as (K, V), [tokens, heads, dim] of dtype
     (out's, where out = (K, V) is given); zeros at a slot outside the cache."""
     tokens = slots.numel() if isinstance(slots, torch.Tensor) else 0
-    at = _tensor(slots, "slots", (torch.int64,), (tokens,), cache.device)
+    at = _tensor(slots, "slots", _I64, (tokens,), cache._index)
     shape = (tokens, cache.heads, cache.dim)
     if out is None:
         out = (torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device))
     K, V = out
-    if K.dtype not in _DT:
-        raise TypeError(f"dtype must be float16 or bfloat16, got {K.dtype}")
-    _call(cache, "hqq_cache_read", at, tokens, _DT[K.dtype], _tensor(K, "out K", (K.dtype,), shape, cache.device),
-          _tensor(V, "out V", (K.dtype,), shape, cache.device))
+    if not isinstance(K, torch.Tensor) or K.dtype not in _DT:
+        raise TypeError("out must be float16 or bfloat16 tensors, dtype one of these")
+    _call(cache, cache._lib.hqq_cache_read, at, tokens, _DT[K.dtype], _tensor(K, "out K", (K.dtype,), shape, cache._index),
+          _tensor(V, "out V", (K.dtype,), shape, cache._index))
     return K, V
 
 
@@ -242,36 +254,36 @@ def hqq_cache_attention(cache: QuantizedCache, Q: torch.Tensor, table: torch.Ten
     neighbours.  softmax_scale: 1 / sqrt(dim) where not given.  window: only the last
     `window` tokens count (0: all).  A sequence of no tokens gives 0 and -inf; the tokens of a
     page outside the cache (-1, say) do not count."""
-    q = _rows(Q, "Q", cache)
-    batch, q_heads, _ = Q.shape
+    pq, q_row, q_head, shape = _rows(Q, "Q", cache)
+    batch, q_heads, _ = shape
+    index, dtype, dev = cache._index, Q.dtype, cache.device
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [batch, pages of a sequence]")
     width = table.shape[1]
-    dev = cache.device
-    pt = _tensor(table, "table", _U32[:1], (batch, width), dev)
-    pl = _tensor(lengths, "lengths", _U32[:1], (batch,), dev)
-    need = _bytes(cache, batch, q_heads, width)
+    pt = _tensor(table, "table", _I32, (batch, width), index)
+    pl = _tensor(lengths, "lengths", _I32, (batch,), index)
+    need = _bytes(cache, (batch, q_heads, width))
     if out is None:
-        out = torch.empty(batch, q_heads, cache.dim, dtype=Q.dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
         po = out.data_ptr()
     else:
-        po = _tensor(out, "out", (Q.dtype,), (batch, q_heads, cache.dim), dev)
+        po = _tensor(out, "out", (dtype,), shape, index)
     if lse is None:
-        lse = torch.empty(batch, q_heads, dtype=torch.float32, device=dev)
+        lse = torch.empty((batch, q_heads), dtype=torch.float32, device=dev)
         pe = lse.data_ptr()
     else:
-        pe = _tensor(lse, "lse", (torch.float32,), (batch, q_heads), dev)
+        pe = _tensor(lse, "lse", _F32, (batch, q_heads), index)
     given = workspace is not None
     if given:
         if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous CUDA tensor")
-        if workspace.device != dev:
+        if workspace.get_device() != index:
             raise ValueError(f"workspace is on {workspace.device}, the cache is on {dev}")
         need = workspace.numel() * workspace.element_size()
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call(cache, "hqq_cache_attention", ctypes.addressof(q), batch, q_heads, pt, width, pl,
-          1.0 / math.sqrt(cache.dim) if softmax_scale is None else softmax_scale, window, _DT[Q.dtype], po, pe,
+    _call(cache, cache._lib.hqq_cache_attention, pq, q_row, q_head, batch, q_heads, pt, width, pl,
+          cache._softmax_scale if softmax_scale is None else softmax_scale, window, _DT[dtype], po, pe,
           workspace.data_ptr() if need else None, need)
     if given and need and not torch.cuda.is_current_stream_capturing():
         # a workspace that belongs to another stream is not handed out again before this call's end

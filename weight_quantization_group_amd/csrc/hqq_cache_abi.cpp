@@ -55,14 +55,19 @@ int check_dtype(int dtype)
     return dtype == HQQ_DTYPE_FP16 || dtype == HQQ_DTYPE_BF16 ? HQQ_OK : HQQ_EINVAL_DTYPE;
 }
 
-// [tokens, heads] rows of dim values: whole 16-byte loads, whose span fits
-int check_rows(const hqq_rows *r, int64_t tokens, int64_t heads)
+// [tokens, heads] rows of 16-bit values: whole 16-byte loads, whose span fits
+struct Rows {
+    const uint16_t *data;
+    int64_t token_stride, head_stride;
+};
+
+int check_rows(const Rows &r, int64_t tokens, int64_t heads)
 {
-    if (!r || !aligned(r->data, 16))
+    if (!aligned(r.data, 16))
         return HQQ_EINVAL_PTR;
     constexpr int64_t kMaxStride = int64_t(1) << 40;
-    if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride % 8 != 0 || r->head_stride % 8 != 0 ||
-        r->token_stride > kMaxStride / tokens || r->head_stride > kMaxStride / heads)
+    if (r.token_stride < 0 || r.head_stride < 0 || r.token_stride % 8 != 0 || r.head_stride % 8 != 0 ||
+        r.token_stride > kMaxStride / tokens || r.head_stride > kMaxStride / heads)
         return HQQ_EINVAL_SHAPE;
     return HQQ_OK;
 }
@@ -72,7 +77,7 @@ struct Range {
     int64_t bytes;
 };
 
-Range rows_range(const hqq_rows &r, int64_t tokens, int64_t heads, int64_t dim)
+Range rows_range(const Rows &r, int64_t tokens, int64_t heads, int64_t dim)
 {
     return Range{r.data, 2 * ((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + dim)};
 }
@@ -142,9 +147,22 @@ int check_batch(const hqq_cache &c, int64_t batch, int64_t q_heads, int64_t tabl
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+// Runs per key-value head and row tile, `columns` of those: as many workgroups as the chip
+// holds, or some rounds of them where that divides better.
+int32_t workers_for(int64_t columns, int resident)
+{
+    const int64_t slots = (int64_t)kCus * resident;
+    int64_t best = slots / columns, rounds = 1;
+    for (int64_t r = 2; r <= 4; ++r)
+        if (r * slots / columns * rounds > best * r * 11 / 10) {
+            best = r * slots / columns;
+            rounds = r;
+        }
+    return (int32_t)(best < 1 ? 1 : best);
+}
+
 struct AttentionLayout {
-    int32_t row_tiles, items_per_head;
-    bool split;                      // whether a sequence can be cut at all
+    int32_t row_tiles, workers;      // workers: 0 where no sequence is split
     float *part = nullptr;
     float2 *part_ml = nullptr;
     int64_t bytes = 0;
@@ -152,14 +170,13 @@ struct AttentionLayout {
     {
         const int64_t G = q_heads / c.heads;
         row_tiles = (int32_t)((G + 15) / 16);
-        const int64_t per = kCacheTarget / (c.heads * row_tiles);
-        items_per_head = (int32_t)(per < 1 ? 1 : per);
-        split = batch && table_width * c.page_size > kCacheStep;
-        if (!split)
+        workers = 0;
+        if (batch == 0 || table_width * c.page_size <= kCacheWhole)
             return;
-        const int64_t items = items_per_head + batch;
-        const int64_t sums = round_up(items * q_heads * c.dim * 4, 256);
-        bytes = sums + round_up(items * q_heads * 8, 256);
+        workers = workers_for(c.heads * row_tiles, cache_resident(c.dim, c.group_size));
+        const int64_t segments = workers + batch;
+        const int64_t sums = round_up(segments * q_heads * c.dim * 4, 256);
+        bytes = sums + round_up(segments * q_heads * 8, 256);
         if (ws) {
             part = (float *)ws;
             part_ml = (float2 *)((char *)ws + sums);
@@ -171,8 +188,9 @@ struct AttentionLayout {
 
 extern "C" {
 
-int hqq_cache_write(const hqq_cache *cache, const hqq_rows *K, const hqq_rows *V, int64_t tokens, const int64_t *slots,
-                    int dtype, uint16_t *K_hat, uint16_t *V_hat, void *stream)
+int hqq_cache_write(const hqq_cache *cache, const uint16_t *K, int64_t k_token_stride, int64_t k_head_stride,
+                    const uint16_t *V, int64_t v_token_stride, int64_t v_head_stride, int64_t tokens,
+                    const int64_t *slots, int dtype, uint16_t *K_hat, uint16_t *V_hat, void *stream)
 {
     if (const int st = check_cache(cache))
         return st;
@@ -183,7 +201,8 @@ int hqq_cache_write(const hqq_cache *cache, const hqq_rows *K, const hqq_rows *V
         return st;
     if (tokens == 0)
         return HQQ_OK;
-    for (const hqq_rows *r : {K, V})
+    const Rows x[2] = {{K, k_token_stride, k_head_stride}, {V, v_token_stride, v_head_stride}};
+    for (const Rows &r : x)
         if (const int st = check_rows(r, tokens, c.heads))
             return st;
     if (!aligned(slots, 8) || !K_hat != !V_hat || (K_hat && (!aligned(K_hat, 16) || !aligned(V_hat, 16))))
@@ -191,15 +210,14 @@ int hqq_cache_write(const hqq_cache *cache, const hqq_rows *K, const hqq_rows *V
     const CacheRanges r(c);
     const int64_t hat = 2 * tokens * c.heads * c.dim;
     if (written_overlaps({r.kp, r.ks, r.kz, r.vp, r.vs, r.vz, {K_hat, hat}, {V_hat, hat}},
-                         {rows_range(*K, tokens, c.heads, c.dim), rows_range(*V, tokens, c.heads, c.dim),
+                         {rows_range(x[0], tokens, c.heads, c.dim), rows_range(x[1], tokens, c.heads, c.dim),
                           {slots, 8 * tokens}}))
         return HQQ_EINVAL_PTR;
     CacheCodecArgs a = codec_args(c, slots, tokens);
     for (int i = 0; i < 2; ++i) {
-        const hqq_rows &x = i ? *V : *K;
-        a.x[i] = x.data;
-        a.token_stride[i] = x.token_stride;
-        a.head_stride[i] = x.head_stride;
+        a.x[i] = x[i].data;
+        a.token_stride[i] = x[i].token_stride;
+        a.head_stride[i] = x[i].head_stride;
     }
     a.hat[0] = K_hat;
     a.hat[1] = V_hat;
@@ -243,9 +261,10 @@ int64_t hqq_cache_attention_workspace(const hqq_cache *cache, int64_t batch, int
     return AttentionLayout(nullptr, *cache, batch, q_heads, table_width).bytes;
 }
 
-int hqq_cache_attention(const hqq_cache *cache, const hqq_rows *Q, int64_t batch, int64_t q_heads, const int32_t *table,
-                        int64_t table_width, const int32_t *lengths, float softmax_scale, int64_t window, int dtype,
-                        uint16_t *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream)
+int hqq_cache_attention(const hqq_cache *cache, const uint16_t *Q, int64_t q_batch_stride, int64_t q_head_stride,
+                        int64_t batch, int64_t q_heads, const int32_t *table, int64_t table_width,
+                        const int32_t *lengths, float softmax_scale, int64_t window, int dtype, uint16_t *out, float *lse,
+                        void *workspace, int64_t workspace_bytes, void *stream)
 {
     if (const int st = check_cache(cache))
         return st;
@@ -258,7 +277,8 @@ int hqq_cache_attention(const hqq_cache *cache, const hqq_rows *Q, int64_t batch
         return HQQ_EINVAL_PARAM;
     if (batch == 0)
         return HQQ_OK;
-    if (const int st = check_rows(Q, batch, q_heads))
+    const Rows q{Q, q_batch_stride, q_head_stride};
+    if (const int st = check_rows(q, batch, q_heads))
         return st;
     if (!aligned(table, 4) || !aligned(lengths, 4) || !aligned(out, 16) || (lse && !aligned(lse, 4)) ||
         workspace_bytes < 0 || (!workspace && workspace_bytes > 0) || (workspace && !aligned(workspace, 16)))
@@ -268,7 +288,7 @@ int hqq_cache_attention(const hqq_cache *cache, const hqq_rows *Q, int64_t batch
         return HQQ_EWORKSPACE;
     const CacheRanges r(c);
     if (written_overlaps({{out, 2 * batch * q_heads * c.dim}, {lse, 4 * batch * q_heads}, {workspace, l.bytes}},
-                         {r.kp, r.ks, r.kz, r.vp, r.vs, r.vz, rows_range(*Q, batch, q_heads, c.dim),
+                         {r.kp, r.ks, r.kz, r.vp, r.vs, r.vz, rows_range(q, batch, q_heads, c.dim),
                           {table, 4 * batch * table_width}, {lengths, 4 * batch}}))
         return HQQ_EINVAL_PTR;
     CacheAttentionArgs a{};
@@ -278,9 +298,9 @@ int hqq_cache_attention(const hqq_cache *cache, const hqq_rows *Q, int64_t batch
         a.scale[i] = s.scale;
         a.zero[i] = s.zero;
     }
-    a.Q = Q->data;
-    a.q_batch_stride = Q->token_stride;
-    a.q_head_stride = Q->head_stride;
+    a.Q = Q;
+    a.q_batch_stride = q_batch_stride;
+    a.q_head_stride = q_head_stride;
     a.table = table;
     a.lengths = lengths;
     a.out = out;
@@ -297,7 +317,7 @@ int hqq_cache_attention(const hqq_cache *cache, const hqq_rows *Q, int64_t batch
     a.page_mask = c.page_size - 1;
     a.table_width = (int32_t)table_width;
     a.window = window > INT32_MAX ? 0 : (int32_t)window;
-    a.items_per_head = l.items_per_head;
+    a.workers = l.workers;
     a.scale_log2 = softmax_scale * 1.44269504088896340736f;
     a.bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
@@ -306,7 +326,7 @@ int hqq_cache_attention(const hqq_cache *cache, const hqq_rows *Q, int64_t batch
                                         : launch_cache_attention_b8(c.dim, c.group_size, a, s);
     if (e != hipSuccess)
         return HQQ_EHIP;
-    return !l.split || launch_cache_join(c.dim, a, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
+    return !l.workers || launch_cache_join(c.dim, a, s) == hipSuccess ? HQQ_OK : HQQ_EHIP;
 }
 
 const char *hqq_cache_strerror(int status)

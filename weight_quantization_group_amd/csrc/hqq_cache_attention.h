@@ -1,6 +1,6 @@
 // hqq_cache_attention.h -- attention of one new token over the quantized cache:
-// one workgroup takes an item (a run of tokens of one sequence and key-value head)
-// for 16 query heads.  Included by hqq_cache_attention_b{2,4,8}.hip, one width each.
+// one workgroup takes a run of tokens of one key-value head for 16 query heads.
+// Included by hqq_cache_attention_b{2,4,8}.hip, one width each.
 //
 // Mathematics.  With q scaled by a power of two per row, codes c, and r = 1 / scale:
 //   s_t = sum_g r_tg (sum_{d in g} q_d c_td  -  z_tg sum_{d in g} q_d)
@@ -27,7 +27,6 @@ namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef float float4v __attribute__((ext_vector_type(4)));
 typedef float float2v __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ half8 operand(const uint32_t (&r)[4])
@@ -37,28 +36,38 @@ __device__ __forceinline__ half8 operand(const uint32_t (&r)[4])
     return h;
 }
 
-// Field f of both half words of x as fp16 subnormals, times field_factor.  The fields are
-// brought to the upper bits of the 10 that a subnormal has: the matrix units align the
-// products of a sum by their operands' exponents, and a subnormal counts with the least
-// one, so low fields lose that many bits of the sum (error of lse at 2 bits 1.5e-6 with the
-// fields in their places).
-template <int NB>
+// Field f of both half words of x as fp16 subnormals, times field_factor.  The matrix
+// units align the products of a sum by their operands' exponents, and a subnormal counts with
+// the least one, so a low field loses bits of the sum.  PRECISE (keys): the fields are brought
+// to the upper bits of the 10 that a subnormal has (error of lse at 2 bits 1.5e-6 without);
+// values, whose weights have 11 bits, leave them where that saves a shift.
+template <int NB, bool PRECISE>
 __device__ __forceinline__ uint32_t field(uint32_t x, int f)
 {
     if constexpr (NB == 8) {
         return (f ? x >> 8 : x) & 0x00ff00ffu;
     } else if constexpr (NB == 4) {
-        return (f == 0 ? x << 4 : x >> (4 * f - 4)) & 0x00f000f0u;
+        if constexpr (PRECISE)
+            return (f == 0 ? x << 4 : x >> (4 * f - 4)) & 0x00f000f0u;
+        else
+            return (f < 2 ? x : x >> 8) & (f % 2 ? 0x00f000f0u : 0x000f000fu);
     } else {
-        const int left = 6 - 4 * (f / 2);
-        return (left > 0 ? x << left : x >> -left) & (f % 2 ? 0x03000300u : 0x00c000c0u);
+        if constexpr (PRECISE) {
+            const int left = 6 - 4 * (f / 2);
+            return (left > 0 ? x << left : x >> -left) & (f % 2 ? 0x03000300u : 0x00c000c0u);
+        } else {
+            return f < 5 ? x & (0x00030003u << (2 * f)) : (x >> 10) & (0x00030003u << (2 * (f - 5)));
+        }
     }
 }
 
-template <int NB>
+template <int NB, bool PRECISE>
 constexpr float field_factor(int f)
 {
-    return NB == 8 ? 1.0f : NB == 4 ? 16.0f : f % 2 ? 256.0f : 64.0f;
+    return NB == 8   ? 1.0f
+           : NB == 4 ? (PRECISE || f % 2 ? 16.0f : 1.0f)
+           : PRECISE ? (f % 2 ? 256.0f : 64.0f)
+                     : (float)(1 << (2 * (f < 5 ? f : f - 5)));
 }
 
 // How a lane's gs / 4 codes of a token's group stand in the operands of the first
@@ -109,17 +118,37 @@ __device__ __forceinline__ float widen16(uint16_t v, bool bf16)
     return bf16 ? __uint_as_float((uint32_t)v << 16) : (float)h;
 }
 
+// the values of the other half of the wave, and of the other row of 16 in the same half, beside
+// this lane's
+struct Two {
+    float a, b;
+};
+
+__device__ __forceinline__ Two halves(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return Two{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
+__device__ __forceinline__ Two rows(float v)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return Two{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
 // sum, or maximum, over the 4 lanes that share a column
 __device__ __forceinline__ float column_sum(float v)
 {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const Two h = halves(v);
+    const Two r = rows(h.a + h.b);
+    return r.a + r.b;
 }
 
 __device__ __forceinline__ float column_max(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    const Two h = halves(v);
+    const Two r = rows(fmaxf(h.a, h.b));
+    return fmaxf(r.a, r.b);
 }
 
 __device__ __forceinline__ float power_of_two(int e)      // -126 <= e <= 127
@@ -145,6 +174,8 @@ struct CacheAttention {
     static constexpr int kValueWords = (kValueBytes + 3) / 4;
     static constexpr int kCodes = GS / 16;                      // ... and codes: products per group
     static constexpr int kMetas = NG <= 2 ? 1 : 2;              // a tile's groups over the lanes
+    static constexpr int kPerChunk = kValueBits < 16 ? kCodes : 16 / NB;      // codes of a half word
+    static constexpr int kChunks = kValueBits < 16 ? 1 : kValueBits / 16;
     static constexpr int kPitch = D + 4;
 
     struct alignas(16) Shared {
@@ -155,18 +186,134 @@ struct CacheAttention {
         float2 ml[kCacheWaves][16];
     };
 
-    static __device__ __forceinline__ void run(const CacheAttentionArgs &a, Shared &sh)
+    // The tile's two subtiles: each 16 consecutive rows of a page
+    struct Where {
+        int at;
+        int64_t row[2];
+        bool there[2];
+        bool whole;      // all its tokens count
+        bool joined;     // its subtiles are of one page
+    };
+    // ... and what is loaded of them
+    struct Meta {
+        float ks[kMetas], kz[kMetas], vs[kMetas], vz[kMetas];
+    };
+    typedef uint32_t KeyWords[2][NG][(Keys::kBytes + 3) / 4];
+    typedef uint32_t ValueWords[8][NG][kValueWords];
+
+    const CacheAttentionArgs &a;
+    const int lane, wave, col, quad, head;
+    // the segment: tokens [begin, end) of sequence b, of which those from `first` on count
+    int b, begin, end, first;
+
+    __device__ __forceinline__ CacheAttention(const CacheAttentionArgs &args)
+        : a(args), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), col(lane & 15),
+          quad(lane >> 4),
+          head(blockIdx.x % args.heads)
     {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        const int col = lane & 15, quad = lane >> 4;
-        const int head = blockIdx.x % a.heads, row_tile = blockIdx.x / a.heads;
-        const CacheItem item = cache_item(a, blockIdx.y);
-        if (item.batch < 0)
-            return;
-        const int b = item.batch;
+    }
+
+    // The pages of 32 of this wave's tiles from tile `at` on: subtile i's in lane i
+    __device__ __forceinline__ int pages_from(int at) const
+    {
+        const int token = at + (lane >> 1) * kCacheStep + (lane & 1) * 16;
+        return token < end ? a.table[(int64_t)b * a.table_width + (token >> a.page_shift)] : -1;
+    }
+
+    __device__ __forceinline__ Where where(int at, int pages, int tile) const
+    {
+        Where w;
+        w.at = at;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int page = __builtin_amdgcn_readlane(pages, 2 * (tile & 31) + t);
+            w.there[t] = page >= 0 && page < a.pages;
+            w.row[t] = (((int64_t)(w.there[t] ? page : 0) * a.heads + head) << a.page_shift) +
+                       ((at + 16 * t) & a.page_mask);
+        }
+        w.whole = w.there[0] && w.there[1] && at >= first && at + kCacheTile <= end;
+        w.joined = a.page_shift > 4;
+        return w;
+    }
+
+    __device__ __forceinline__ bool counts(const Where &w, int t, int place) const
+    {
+        const int token = w.at + 16 * t + place;
+        return token >= first && token < end && w.there[t];
+    }
+
+    __device__ __forceinline__ void load_keys(const Where &w, KeyWords &kw) const
+    {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                load_words<Keys::kBytes>(kw[t][g], (const char *)a.packed[0] + w.row[t] * kRowBytes + col * kRowBytes +
+                                                       g * (GS * NB / 8) + quad * Keys::kBytes);
+    }
+
+    __device__ __forceinline__ void load_values(const Where &w, ValueWords &vw) const
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                load_words<kValueBytes>(vw[j][g], (const char *)a.packed[1] + w.row[j / 4] * kRowBytes +
+                                                      (4 * quad + j % 4) * kRowBytes + g * (GS * NB / 8) +
+                                                      (col * kValueBits) / 8);
+    }
+
+    // Scales and zeros lie over the lanes as token col and, along the quads, group (and
+    // subtile, where the groups leave room)
+    static __device__ __forceinline__ int meta_tile(int i, int quad) { return NG <= 2 ? quad / NG : i; }
+    static __device__ __forceinline__ int meta_group(int quad) { return NG <= 2 ? quad % NG : quad < NG ? quad : 0; }
+    static __device__ __forceinline__ bool meta_there(int i, int quad) { return NG <= 2 ? quad / NG < 2 : quad < NG; }
+
+    __device__ __forceinline__ void load_meta(const Where &w, Meta &m) const
+    {
+#pragma unroll
+        for (int i = 0; i < kMetas; ++i) {
+            const int t = meta_tile(i, quad);
+            // tokens that do not count: 1 / scale and zero of 0, whatever the page holds there
+            m.ks[i] = m.vs[i] = INFINITY;
+            m.kz[i] = m.vz[i] = 0.0f;
+            const bool in = w.whole || (t ? counts(w, 1, col) : counts(w, 0, col));
+            if (meta_there(i, quad) && in) {
+                if (w.joined) {          // the tile's rows follow each other: one base for the wave
+                    const int64_t base = w.row[0] * NG;
+                    const uint32_t from = (16 * t + col) * NG + meta_group(quad);
+                    m.ks[i] = (a.scale[0] + base)[from], m.kz[i] = (a.zero[0] + base)[from];
+                    m.vs[i] = (a.scale[1] + base)[from], m.vz[i] = (a.zero[1] + base)[from];
+                } else {
+                    const int64_t from = ((t ? w.row[1] : w.row[0]) + col) * NG + meta_group(quad);
+                    m.ks[i] = a.scale[0][from], m.kz[i] = a.zero[0][from];
+                    m.vs[i] = a.scale[1][from], m.vz[i] = a.zero[1][from];
+                }
+            }
+        }
+    }
+
+    // One segment, from q to the output or the workspace's slot
+    __device__ __forceinline__ void segment(Shared &sh, int slot, bool whole_sequence)
+    {
+        const int row_tile = blockIdx.x / a.heads;
         const int in_group = row_tile * 16 + col;               // this column's q head within the group
         const bool real = in_group < a.G;
         const int q_head = head * a.G + (real ? in_group : 0);
+
+        // ---- the first tile's loads
+        const int at0 = begin + wave * kCacheTile;
+        const int tiles = at0 < end ? (end - at0 + kCacheStep - 1) / kCacheStep : 0;
+        int pages = pages_from(at0);
+        KeyWords kw;
+        ValueWords vw;
+        Meta next_meta;
+        Where next = where(at0, pages, 0);
+        if (tiles > 0) {
+            load_meta(next, next_meta);
+            load_keys(next, kw);
+            load_values(next, vw);
+        }
 
         // ---- q: operands of the first product, and each group's sum
         uint32_t q16[NG][Keys::kUnits][4];
@@ -203,14 +350,13 @@ struct CacheAttention {
                 for (int u = 0; u < Keys::kUnits; ++u)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        constexpr float kUnit = 0x1p-24f;
-                        const float factor = field_factor<NB>(Keys::field_of(u, r)) * kUnit;
-                        const float inv = f / (factor / kUnit);
+                        const float factor = field_factor<NB, true>(Keys::field_of(u, r));
+                        const float inv = f / factor;
                         half2v h;
                         h[0] = (_Float16)(q[g][Keys::lo(u, r)] * inv);
                         h[1] = (_Float16)(q[g][Keys::hi(u, r)] * inv);
                         __builtin_memcpy(&q16[g][u][r], &h, 4);
-                        sum += ((float)h[0] + (float)h[1]) * factor;
+                        sum += ((float)h[0] + (float)h[1]) * (factor * 0x1p-24f);
                     }
                 q_sum[g] = column_sum(sum);
             }
@@ -239,87 +385,42 @@ struct CacheAttention {
             for (int i = 0; i < kCodes; ++i)
                 o[g][i] = float4v{0.f, 0.f, 0.f, 0.f};
         }
-        const int32_t *pages = a.table + (int64_t)b * a.table_width;
+        float lane_unit = v_unit[0];                            // of the group whose scales this lane loads
         float (*meta)[NG][kCacheTile] = sh.meta[wave];
 
-        for (int at = item.begin + wave * kCacheTile; at < item.end; at += kCacheStep) {
-            // ---- the tile's two pages (or one twice)
-            int64_t row[2];
-            bool there[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int token = at + 16 * t;
-                const int page = token < item.end ? pages[token >> a.page_shift] : -1;
-                there[t] = page >= 0 && page < a.pages;
-                row[t] = (((int64_t)(there[t] ? page : 0) * a.heads + head) << a.page_shift) + (token & a.page_mask);
-            }
-            const bool whole = there[0] && there[1] && at >= item.first && at + kCacheTile <= item.end;
+        for (int tile = 0; tile < tiles; ++tile) {
+            const Where now = next;
+            const bool more = tile + 1 < tiles;
 
-            // ---- loads
-            uint32_t kw[2][NG][(Keys::kBytes + 3) / 4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    load_words<Keys::kBytes>(kw[t][g], (const char *)a.packed[0] + (row[t] + col) * kRowBytes +
-                                                           g * (GS * NB / 8) + quad * Keys::kBytes);
-            uint32_t vw[8][NG][kValueWords];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    load_words<kValueBytes>(vw[j][g], (const char *)a.packed[1] +
-                                                          (row[j / 4] + 4 * quad + j % 4) * kRowBytes +
-                                                          g * (GS * NB / 8) + (col * kValueBits) / 8);
-            float rz[kMetas];                                   // (r z) of k: token col, group along the quads
-            float raise = 0.0f;
-            int own_group[kMetas];
+            // ---- scales: reciprocals (to 1 ulp), to the layout of the scores through LDS
+            float rz[kMetas];                                   // (r z) of k
             float vr[kMetas];
-            int at_lds[kMetas];
-            bool has[kMetas];
+            float raise = 0.0f;
 #pragma unroll
             for (int i = 0; i < kMetas; ++i) {
-                const int t = NG <= 2 ? quad / NG : i;
-                const int g = NG <= 2 ? quad % NG : quad;
-                has[i] = NG <= 2 ? t < 2 : g < NG;
-                own_group[i] = has[i] ? g : -1;
-                const int token = at + 16 * t + col;
-                const bool counts = has[i] && token >= item.first && token < item.end && (t ? there[1] : there[0]);
-                float ks = 1.0f, kz = 0.0f, vs = 1.0f, vz = 0.0f;
-                if (counts) {
-                    const int64_t from = ((t ? row[1] : row[0]) + col) * NG + g;
-                    ks = a.scale[0][from], kz = a.zero[0][from];
-                    vs = a.scale[1][from], vz = a.zero[1][from];
+                const float kr = __builtin_amdgcn_rcpf(next_meta.ks[i]) * 0x1p12f;  // the codes' 2^-24 taken back, half here
+                vr[i] = __builtin_amdgcn_rcpf(next_meta.vs[i]);
+                rz[i] = kr * next_meta.kz[i];
+                if (meta_there(i, quad)) {
+                    float *to = &meta[0][meta_group(quad)][16 * meta_tile(i, quad) + col];
+                    to[0] = kr;
+                    to[2 * NG * kCacheTile] = next_meta.vz[i];
                 }
-                // tokens that do not count: r and z of 0, whatever the page holds there
-                const float kr = counts ? 0x1p12f / ks : 0.0f;     // the codes' 2^-24 taken back, half here
-                vr[i] = counts ? 1.0f / vs : 0.0f;
-                rz[i] = kr * kz;
-                at_lds[i] = 16 * t + col;
-                if (has[i]) {
-                    meta[0][g][at_lds[i]] = kr;
-                    meta[2][g][at_lds[i]] = vz;
-                }
-                // a group's r of v beyond the unit that its weights are held in?
-                float unit = v_unit[0];
-#pragma unroll
-                for (int k = 1; k < NG; ++k)
-                    unit = own_group[i] == k ? v_unit[k] : unit;
-                raise = fmaxf(raise, vr[i] * unit);
+                raise = fmaxf(raise, vr[i]);
             }
-            if (__any(!(raise <= 0x1p15f))) {
+            // a group's r of v beyond the unit that its weights are held in?
+            if (__any(!(raise * lane_unit <= 0x1p15f))) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     float most = 0.0f;
 #pragma unroll
                     for (int i = 0; i < kMetas; ++i)
-                        most = fmaxf(most, own_group[i] == g ? vr[i] : 0.0f);
+                        most = fmaxf(most, meta_there(i, quad) && meta_group(quad) == g ? vr[i] : 0.0f);
 #pragma unroll
                     for (int off = 1; off < 64; off *= 2)
                         most = fmaxf(most, __shfl_xor(most, off));
                     // most * unit in [2^14, 2^15)
-                    const int e = (int)(__float_as_uint(most) >> 23) - 127;
-                    const int ue = 14 - e;
+                    const int ue = 14 - ((int)(__float_as_uint(most) >> 23) - 127);
                     const float unit = power_of_two(ue < -120 ? -120 : ue > 120 ? 120 : ue);
                     if (unit < v_unit[g]) {
                         const float f = unit / v_unit[g];
@@ -330,16 +431,12 @@ struct CacheAttention {
                             o[g][i] *= f;
                     }
                 }
+                lane_unit = pick(v_unit, meta_group(quad));
             }
 #pragma unroll
-            for (int i = 0; i < kMetas; ++i) {
-                float unit = v_unit[0];
-#pragma unroll
-                for (int k = 1; k < NG; ++k)
-                    unit = own_group[i] == k ? v_unit[k] : unit;
-                if (has[i])
-                    meta[1][own_group[i]][at_lds[i]] = vr[i] * unit;
-            }
+            for (int i = 0; i < kMetas; ++i)
+                if (meta_there(i, quad))
+                    meta[1][meta_group(quad)][16 * meta_tile(i, quad) + col] = vr[i] * lane_unit;
             wave_lds_fence();
 
             // ---- scores
@@ -353,16 +450,15 @@ struct CacheAttention {
                     float4v acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int u = 0; u < Keys::kUnits; ++u) {
-                        uint32_t regs[4], halves[4];
-                        __builtin_memcpy(halves, q16[g][u], 16);
+                        uint32_t regs[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             uint32_t x = kw[t][g][Keys::word_of(u, r)];
                             if constexpr (Keys::kHalf)
                                 x = (x & 0xffu) | (x >> 8) << 16;
-                            regs[r] = field<NB>(x, Keys::field_of(u, r));
+                            regs[r] = field<NB, true>(x, Keys::field_of(u, r));
                         }
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(halves), acc, 0, 0, 0);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(q16[g][u]), acc, 0, 0, 0);
                     }
                     const float4v r4 = *reinterpret_cast<const float4v *>(&meta[0][g][16 * t + 4 * quad]);
 #pragma unroll
@@ -373,15 +469,21 @@ struct CacheAttention {
                 for (int r = 0; r < 4; ++r)
                     s[t][r] = v[r];
             }
-            if (!whole) {
+            // the keys' registers are free: the next tile's go there while the weights are formed
+            if (more) {
+                if ((tile & 31) == 31)
+                    pages = pages_from(now.at + kCacheStep);
+                next = where(now.at + kCacheStep, pages, tile + 1);
+                load_meta(next, next_meta);
+                load_keys(next, kw);
+            }
+            if (!now.whole) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int token = at + 16 * t + 4 * quad + r;
-                        if (!(token >= item.first && token < item.end && there[t]))
+                    for (int r = 0; r < 4; ++r)
+                        if (!counts(now, t, 4 * quad + r))
                             s[t][r] = -INFINITY;
-                    }
             }
 
             // ---- weights
@@ -430,8 +532,6 @@ struct CacheAttention {
                         __builtin_memcpy(&w16[2 * t + k], &h, 4);
                     }
                 }
-                constexpr int kPerChunk = kValueBits < 16 ? kCodes : 16 / NB;      // codes of a half word
-                constexpr int kChunks = kValueBits < 16 ? 1 : kValueBits / 16;
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     uint32_t x[4];
@@ -450,12 +550,14 @@ struct CacheAttention {
                         uint32_t regs[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            regs[k] = field<NB>(x[k], f);
+                            regs[k] = field<NB, false>(x[k], f);
                         float4v &acc = o[g][c * kPerChunk + f];
                         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(w16), acc, 0, 0, 0);
                     }
                 }
             }
+            if (more)
+                load_values(next, vw);
             wave_lds_fence();       // the next tile's scales go where these were
         }
 
@@ -464,10 +566,9 @@ struct CacheAttention {
 #pragma unroll
         for (int g = 0; g < NG; ++g)
             z_sum[g] = column_sum(z_sum[g]);
-        __syncthreads();
         if (quad == 0)
             sh.ml[wave][col] = float2{m2, total};
-        __syncthreads();
+        __syncthreads();            // also: no wave reads scales any more, whose place the sums take
         float m_all = -INFINITY, total_all = 0.0f;
 #pragma unroll
         for (int w = 0; w < kCacheWaves; ++w)
@@ -477,17 +578,19 @@ struct CacheAttention {
         for (int w = 0; w < kCacheWaves; ++w)
             total_all += sh.ml[w][col].y * __builtin_amdgcn_exp2f(sh.ml[w][col].x - ref);
         const float own = __builtin_amdgcn_exp2f(m2 - ref);
+        if (real) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float back = own / v_unit[g];
+            for (int g = 0; g < NG; ++g) {
+                const float back = own / v_unit[g];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int i = 0; i < kCodes; ++i) {
-                    constexpr int kPerChunk = kValueBits < 16 ? kCodes : 16 / NB;
-                    const float unit = 0x1p24f / field_factor<NB>(i % kPerChunk);
-                    sh.sums[wave][col][g * GS + (4 * quad + r) * kCodes + i] = fmaf(o[g][i][r], unit, -z_sum[g]) * back;
-                }
+                    for (int i = 0; i < kCodes; ++i) {
+                        const float unit = 0x1p24f / field_factor<NB, false>(i % kPerChunk);
+                        sh.sums[wave][col][g * GS + (4 * quad + r) * kCodes + i] =
+                            fmaf(o[g][i][r], unit, -z_sum[g]) * back;
+                    }
+            }
         }
         __syncthreads();
         // 16 threads a head; each takes D / 16 dims, 4 at a time
@@ -495,42 +598,77 @@ struct CacheAttention {
         const int g_head = row_tile * 16 + h;
         // m_all and total_all are this lane's column's; its row's are another lane's
         const float m_row = __shfl(m_all, h), total_row = __shfl(total_all, h);
-        if (g_head >= a.G)
-            return;
-        const int64_t out_head = head * a.G + g_head;
-        const int64_t out_row = (int64_t)b * a.q_heads + out_head;
-        const float inv = item.count > 1 ? 1.0f : total_row > 0.0f || !(total_row == total_row) ? 1.0f / total_row : 0.0f;
-        float *part_row = item.count > 1 ? a.part + ((int64_t)item.index * a.q_heads + out_head) * D : nullptr;
-        for (int d = part * 4; d < D; d += 64) {
-            float4v v{0.f, 0.f, 0.f, 0.f};
+        if (g_head < a.G) {
+            const int64_t out_head = head * a.G + g_head;
+            const int64_t out_row = (int64_t)b * a.q_heads + out_head;
+            const int64_t part_row = (int64_t)slot * a.q_heads + out_head;
+            const float inv = cache_inverse(total_row);
 #pragma unroll
-            for (int w = 0; w < kCacheWaves; ++w)
-                v += *reinterpret_cast<const float4v *>(&sh.sums[w][h][d]);
-            if (part_row)
-                *reinterpret_cast<float4v *>(part_row + d) = v;
-            else
-                *reinterpret_cast<uint2 *>(a.out + out_row * D + d) = cache_round4(v * inv, a.bf16);
+            for (int d = part * 4; d < D; d += 64) {
+                float4v v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < kCacheWaves; ++w)
+                    v += *reinterpret_cast<const float4v *>(&sh.sums[w][h][d]);
+                if (whole_sequence)
+                    *reinterpret_cast<uint2 *>(a.out + out_row * D + d) = cache_round4(v * inv, a.bf16);
+                else
+                    *reinterpret_cast<float4v *>(a.part + part_row * D + d) = v;
+            }
+            if (part == 0) {
+                if (!whole_sequence)
+                    a.part_ml[part_row] = float2{m_row, total_row};
+                else if (a.lse)
+                    a.lse[out_row] = cache_lse(m_row, total_row);
+            }
         }
-        if (part == 0) {
-            if (part_row)
-                a.part_ml[(int64_t)item.index * a.q_heads + out_head] = float2{m_row, total_row};
-            else if (a.lse)
-                a.lse[out_row] = cache_lse(m_row, total_row);
+        __syncthreads();            // the next segment's scales go where the sums were
+    }
+
+    static __device__ __forceinline__ float pick(const float (&v)[NG], int g)
+    {
+        float r = v[0];
+#pragma unroll
+        for (int i = 1; i < NG; ++i)
+            r = g == i ? v[i] : r;
+        return r;
+    }
+
+    __device__ __forceinline__ void run(Shared &sh)
+    {
+        const int worker = blockIdx.y;
+        int64_t at = 0, stop = 1, start = 0;
+        b = worker;                  // a sequence each, or a run of tiles
+        if (a.workers) {
+            const int64_t run = cache_run(a, lane);
+            at = worker * run;
+            stop = at + run;
+            b = cache_find(a, at, lane, start);
+        }
+        for (; at < stop && b < a.batch; ++b) {
+            const CacheSpan s = cache_span(a, b);
+            const int64_t next = start + s.tiles, upto = a.workers && stop < next ? stop : next;
+            first = s.first;
+            begin = s.base + (int)(at - start) * kCacheTile;
+            end = upto < next ? s.base + (int)(upto - start) * kCacheTile : s.length;
+            segment(sh, worker + b, at == start && upto == next);
+            at = a.workers ? upto : stop;
+            start = next;
         }
     }
 };
 
 template <int NB, int GS, int NG>
-__global__ __launch_bounds__(64 * kCacheWaves) void cache_attention_kernel(CacheAttentionArgs a)
+__global__ __launch_bounds__(64 * kCacheWaves, cache_resident(GS * NG, GS)) void cache_attention_kernel(CacheAttentionArgs a)
 {
     __shared__ typename CacheAttention<NB, GS, NG>::Shared sh;
-    CacheAttention<NB, GS, NG>::run(a, sh);
+    CacheAttention<NB, GS, NG> attention(a);
+    attention.run(sh);
 }
 
 template <int NB, int GS, int NG>
 hipError_t launch_attention(const CacheAttentionArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)(a.items_per_head + a.batch));
+    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)(a.workers ? a.workers : a.batch));
     hipLaunchKernelGGL((cache_attention_kernel<NB, GS, NG>), grid, dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }

@@ -22,9 +22,8 @@ struct CacheCodecArgs {
     int32_t page_shift, page_mask;
 };
 
-// Attention: sequences are cut into items of `chunk` tokens, a number that the device
-// finds from the lengths (cache_plan), so that all items of a key-value head number at
-// most items_per_head + batch.
+// Attention: all sequences' tokens are cut into `workers` equal runs per key-value head
+// and row tile (hqq_cache_plan.h), or, workers = 0, a workgroup takes a sequence.
 struct CacheAttentionArgs {
     const uint32_t *packed[2];
     const float *scale[2], *zero[2];
@@ -33,13 +32,13 @@ struct CacheAttentionArgs {
     const int32_t *table, *lengths;
     uint16_t *out;
     float *lse;                      // may be null
-    float *part;                     // [items, q_heads, dim] sums of items of split sequences
-    float2 *part_ml;                 // [items, q_heads] their maxima and sums of weights
+    float *part;                     // [workers + batch, q_heads, dim] sums of split sequences' segments
+    float2 *part_ml;                 // [workers + batch, q_heads] their maxima and sums of weights
     int32_t batch, q_heads, heads, G;
     int32_t row_tiles;               // blocks of 16 q heads of a key-value head
     int32_t pages, page_shift, page_mask, table_width;
     int32_t window;                  // 0: none
-    int32_t items_per_head;
+    int32_t workers;
     float scale_log2;                // softmax_scale * log2(e)
     int32_t bf16;
 };
@@ -48,15 +47,20 @@ struct CacheAttentionArgs {
 constexpr int kCacheTile = 32;
 constexpr int kCacheWaves = 4;
 constexpr int kCacheStep = kCacheTile * kCacheWaves;
-// Workgroups that an attention call is cut into, about.
-constexpr int kCacheTarget = 1024;
+// Workgroups of the attention kernel that a CU holds at a time: what their registers
+// (which grow with dim and with its groups) leave room for.
+constexpr int cache_resident(int dim, int gs) { return dim <= 128 && dim / gs <= 2 ? 3 : 2; }
+constexpr int kCus = 256;
+
+// Sequences of at most this many tokens are not split.
+constexpr int kCacheWhole = 512;
 
 hipError_t launch_cache_write(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
 hipError_t launch_cache_read(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
 hipError_t launch_cache_attention_b2(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
 hipError_t launch_cache_attention_b4(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
 hipError_t launch_cache_attention_b8(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
-// joins the items of split sequences
+// joins the segments of split sequences
 hipError_t launch_cache_join(int dim, const CacheAttentionArgs &a, hipStream_t s);
 
 }  // namespace hqq

@@ -1,30 +1,36 @@
-// hqq_cache_join.hip -- joins the items of sequences that were split over their
-// length: one workgroup per sequence and query head.
+// hqq_cache_join.hip -- joins the segments of sequences that were split over their
+// length: one query head of one sequence per workgroup, or per wave where there are enough.
 #include "hqq_cache_plan.h"
 
 namespace hqq {
 namespace {
 
-typedef float float4v __attribute__((ext_vector_type(4)));
-
 constexpr int kJoinBlock = 256;
 
-template <int D>
+// WAVES: waves per query head
+template <int D, int WAVES>
 __global__ __launch_bounds__(kJoinBlock) void cache_join_kernel(CacheAttentionArgs a)
 {
-    constexpr int kLanes = D / 4, kGroups = kJoinBlock / kLanes;
-    __shared__ float4v sums[kGroups][kLanes];
-    const int head = blockIdx.x, b = blockIdx.y;
-    const int lane = threadIdx.x & 63;
-    const int chunk = cache_chunk(a, lane);
-    const int count = cache_items(cache_span(a, b), chunk);
-    if (count == 1)
-        return;                       // the item wrote the output itself
-    int64_t before = 0;
+    constexpr int kLanes = D / 4;                           // lanes of a row, 4 dims each
+    constexpr int kAtOnce = kJoinBlock / kLanes / (4 / WAVES);   // segments read at a time
+    constexpr int kHeads = 4 / WAVES;
+    __shared__ float4v sums[kHeads][kAtOnce][kLanes];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int local = wave / WAVES, thread = threadIdx.x - local * WAVES * 64;
+    const int head = blockIdx.x * kHeads + local, b = blockIdx.y;
+    const int64_t run = cache_run(a, lane);
+    int64_t start = 0;
     for (int i = lane; i < b; i += 64)
-        before += cache_items(cache_span(a, i), chunk);
-    before = wave_sum(before);
-    const float2 *ml = a.part_ml + before * a.q_heads + head;
+        start += cache_span(a, i).tiles;
+    start = wave_sum(start);
+    const int64_t w0 = start / run;
+    const int count = (int)((start + cache_span(a, b).tiles - 1) / run - w0) + 1;
+    if (count == 1)
+        return;                       // the one segment wrote the output itself
+    const bool real = head < a.q_heads;
+    const int64_t slot = w0 + b;
+    const float2 *ml = a.part_ml + slot * a.q_heads + (real ? head : 0);
+    const float *part = a.part + (slot * a.q_heads + (real ? head : 0)) * D;
     float m = -INFINITY;
     for (int i = lane; i < count; i += 64)
         m = fmaxf(m, ml[(int64_t)i * a.q_heads].x);
@@ -40,24 +46,24 @@ __global__ __launch_bounds__(kJoinBlock) void cache_join_kernel(CacheAttentionAr
 #pragma unroll
     for (int o = 1; o < 64; o *= 2)
         total += __shfl_xor(total, o);
-    const int group = threadIdx.x / kLanes, at = threadIdx.x % kLanes;
+    const int group = thread / kLanes, at = thread % kLanes;
     float4v v{0.f, 0.f, 0.f, 0.f};
-    if (group < kGroups)
-        for (int i = group; i < count; i += kGroups) {
+    if (group < kAtOnce) {
+#pragma unroll 4
+        for (int i = group; i < count; i += kAtOnce) {
             const float w = __builtin_amdgcn_exp2f(ml[(int64_t)i * a.q_heads].x - ref);
-            v += w * *reinterpret_cast<const float4v *>(a.part + ((before + i) * a.q_heads + head) * D + 4 * at);
+            v += w * *reinterpret_cast<const float4v *>(part + (int64_t)i * a.q_heads * D + 4 * at);
         }
-    if (group < kGroups)
-        sums[group][at] = v;
-    __syncthreads();
-    if (group != 0)
+        sums[local][group][at] = v;
+    }
+    __syncthreads();                  // (count is one number for all of the workgroup)
+    if (group != 0 || !real)
         return;
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i)
-        v += sums[i][at];
-    const float inv = total > 0.0f || !(total == total) ? 1.0f / total : 0.0f;
+    for (int i = 1; i < kAtOnce; ++i)
+        v += sums[local][i][at];
     const int64_t row = (int64_t)b * a.q_heads + head;
-    *reinterpret_cast<uint2 *>(a.out + row * D + 4 * at) = cache_round4(v * inv, a.bf16);
+    *reinterpret_cast<uint2 *>(a.out + row * D + 4 * at) = cache_round4(v * cache_inverse(total), a.bf16);
     if (at == 0 && a.lse)
         a.lse[row] = cache_lse(m, total);
 }
@@ -65,7 +71,12 @@ __global__ __launch_bounds__(kJoinBlock) void cache_join_kernel(CacheAttentionAr
 template <int D>
 hipError_t launch_join(const CacheAttentionArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((cache_join_kernel<D>), dim3((unsigned)a.q_heads, (unsigned)a.batch), dim3(kJoinBlock), 0, s, a);
+    if ((int64_t)a.q_heads * a.batch > 1024)
+        hipLaunchKernelGGL((cache_join_kernel<D, 1>), dim3((unsigned)((a.q_heads + 3) / 4), (unsigned)a.batch),
+                           dim3(kJoinBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((cache_join_kernel<D, 4>), dim3((unsigned)a.q_heads, (unsigned)a.batch), dim3(kJoinBlock), 0,
+                           s, a);
     return hipGetLastError();
 }
 

@@ -1,5 +1,12 @@
-// hqq_cache_plan.h -- how an attention call's sequences are cut into items, found
-// on the device (the lengths are there), and the ends that items and join share.
+// hqq_cache_plan.h -- how an attention call's sequences are shared out over the
+// workgroups, found on the device (the lengths are there), and the ends that the
+// attention and the join have in common.
+//
+// The tokens of all sequences, in tiles of 32 and one sequence after the other, are cut
+// into `workers` equal runs; workgroup w of a key-value head takes run w, whatever
+// sequences it crosses, so that all of them end together however ragged the batch is.  The
+// part of a sequence that a run holds is a segment.  Runs and sequences both advance along
+// the tiles, so segment (w, b) has slot w + b in the workspace to itself.
 #pragma once
 
 #include "hqq_cache_internal.h"
@@ -7,17 +14,19 @@
 namespace hqq {
 namespace {
 
-// One item: tokens [begin, end) of sequence `batch`, of which those from `first` on count.
-struct CacheItem {
-    int batch;         // -1: no such item
-    int begin, end, first;
-    int index;         // the item's place in the workspace
-    int count;         // items of the sequence
-};
+typedef float float4v __attribute__((ext_vector_type(4)));
 
 struct CacheSpan {
     int first, base, length;   // first token that counts, its tile's first token, the length
+    int tiles;                 // tiles from base on, at least one (it writes the output)
 };
+
+// A 64-bit value that is the same in all lanes, as such
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
 __device__ __forceinline__ CacheSpan cache_span(const CacheAttentionArgs &a, int b)
 {
@@ -25,17 +34,9 @@ __device__ __forceinline__ CacheSpan cache_span(const CacheAttentionArgs &a, int
     int n = a.lengths[b];
     n = n < 0 ? 0 : n > most ? (int)most : n;
     const int first = a.window > 0 && n > a.window ? n - a.window : 0;
-    return CacheSpan{first, first & ~(kCacheTile - 1), n};
-}
-
-__device__ __forceinline__ int wave_inclusive_sum(int v, int lane)
-{
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const int up = __shfl_up(v, o);
-        v += lane >= o ? up : 0;
-    }
-    return v;
+    const int base = first & ~(kCacheTile - 1);
+    const int tiles = (n - base + kCacheTile - 1) / kCacheTile;
+    return CacheSpan{first, base, n, tiles < 1 ? 1 : tiles};
 }
 
 __device__ __forceinline__ int64_t wave_sum(int64_t v)
@@ -46,63 +47,44 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v)
     return v;
 }
 
-// Tokens per item: what splits all sequences into about items_per_head items, in whole
-// workgroup steps.  A sequence of n tokens has ceil(n / chunk) items, at least one, so all of
-// them number at most items_per_head + batch.
-__device__ __forceinline__ int cache_chunk(const CacheAttentionArgs &a, int lane)
+// Tiles per run: whole workgroup steps, as many as cover all sequences.
+__device__ __forceinline__ int64_t cache_run(const CacheAttentionArgs &a, int lane)
 {
-    int64_t tokens = 0;
-    for (int b = lane; b < a.batch; b += 64) {
-        const CacheSpan s = cache_span(a, b);
-        tokens += s.length - s.base;
-    }
-    tokens = wave_sum(tokens);
-    const int64_t per = (tokens + a.items_per_head - 1) / a.items_per_head;
-    const int64_t chunk = (per + kCacheStep - 1) / kCacheStep * kCacheStep;
-    return chunk < kCacheStep ? kCacheStep : chunk > (1 << 30) ? 1 << 30 : (int)chunk;
+    int64_t tiles = 0;
+    for (int b = lane; b < a.batch; b += 64)
+        tiles += cache_span(a, b).tiles;
+    tiles = wave_sum(tiles);
+    const int64_t per = (tiles + a.workers - 1) / a.workers;
+    return uniform((per + kCacheWaves - 1) / kCacheWaves * kCacheWaves);
 }
 
-__device__ __forceinline__ int cache_items(const CacheSpan &s, int chunk)
+// The sequence that holds tile `at` (batch behind the last), and its first tile
+__device__ __forceinline__ int cache_find(const CacheAttentionArgs &a, int64_t at, int lane, int64_t &start)
 {
-    const int n = s.length - s.base;
-    return n <= chunk ? 1 : (int)(((int64_t)n + chunk - 1) / chunk);
-}
-
-// Item `index` of a key-value head; every wave finds it by itself.
-__device__ __forceinline__ CacheItem cache_item(const CacheAttentionArgs &a, int index)
-{
-    const int lane = threadIdx.x & 63;
-    const int chunk = cache_chunk(a, lane);
-    int before = 0;
+    int64_t before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         const int b = b0 + lane;
-        CacheSpan s{0, 0, 0};
-        int n = 0;
-        if (b < a.batch) {
-            s = cache_span(a, b);
-            n = cache_items(s, chunk);
+        const int64_t tiles = b < a.batch ? cache_span(a, b).tiles : 0;
+        int64_t upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const int64_t up = __shfl_up(upto, o);
+            upto += lane >= o ? up : 0;
         }
-        const int upto = before + wave_inclusive_sum(n, lane);
-        const uint64_t mine = __ballot(index < upto);
-        if (mine) {
-            const int src = __ffsll((unsigned long long)mine) - 1;
-            const int count = __shfl(n, src), start = __shfl(upto, src) - count;
-            const int base = __shfl(s.base, src), length = __shfl(s.length, src);
-            CacheItem it;
-            it.batch = __builtin_amdgcn_readfirstlane(b0 + src);
-            it.first = __builtin_amdgcn_readfirstlane(__shfl(s.first, src));
-            it.count = __builtin_amdgcn_readfirstlane(count);
-            it.index = index;
-            it.begin = __builtin_amdgcn_readfirstlane(base + (index - start) * chunk);
-            it.end = __builtin_amdgcn_readfirstlane(length - it.begin > chunk ? it.begin + chunk : length);
-            return it;
+        upto += before;
+        const uint64_t behind = __ballot(at < upto);
+        if (behind) {
+            const int src = __ffsll((unsigned long long)behind) - 1;
+            start = uniform(__shfl(upto - tiles, src));
+            return __builtin_amdgcn_readfirstlane(b0 + src);
         }
         before = __shfl(upto, 63);
     }
-    return CacheItem{-1, 0, 0, 0, 0, 0};
+    start = 0;
+    return a.batch;
 }
 
-__device__ __forceinline__ uint2 cache_round4(const float __attribute__((ext_vector_type(4))) v, bool bf16)
+__device__ __forceinline__ uint2 cache_round4(float4v v, bool bf16)
 {
     uint16_t u[4];
 #pragma unroll
@@ -119,6 +101,9 @@ __device__ __forceinline__ uint2 cache_round4(const float __attribute__((ext_vec
     __builtin_memcpy(&r, u, 8);
     return r;
 }
+
+// 1 / total; 0 where nothing counted
+__device__ __forceinline__ float cache_inverse(float total) { return total == 0.0f ? 0.0f : 1.0f / total; }
 
 // log(total * 2^m2); -infinity where nothing counted
 __device__ __forceinline__ float cache_lse(float m2, float total)
