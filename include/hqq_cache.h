@@ -107,7 +107,7 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  * second product (with its own exponent, down to 2^-29 of the largest).
  * softmax_scale is > 0 and at most 2^100, window >= 0 (HQQ_EINVAL_PARAM); batch
  * at most 2^15, q_heads 2^16, batch * q_heads 2^28, table_width * page_size 2^30
- * (HQQ_EINVAL_SHAPE).
+ * and batch times that 2^37 (HQQ_EINVAL_SHAPE).
  * The result does not depend on what else runs: sums are added in an order
  * that sizes and lengths set.
  *

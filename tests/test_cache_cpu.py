@@ -74,7 +74,7 @@ def read(lib, k=X, v=Y, tokens=4, slots=S, dtype=0, c=None, **kw):
     return lib.hqq_cache_read(None if c == "none" else ctypes.byref(cache(**kw)), slots, tokens, dtype, k, v, None)
 
 
-def attention(lib, q=X, batch=3, q_heads=4, table=T, width=40, lengths=L, scale=0.1, window=0, dtype=0, out=O, lse=P,
+def attention(lib, q=X, batch=3, q_heads=4, table=T, width=80, lengths=L, scale=0.1, window=0, dtype=0, out=O, lse=P,
               ws=W, size=1 << 32, token=512, head=128, c=None, **kw):
     c = None if c == "none" else ctypes.byref(cache(**kw))
     return lib.hqq_cache_attention(c, q, token, head, batch, q_heads, table, width, lengths, scale, window, dtype,
@@ -126,7 +126,7 @@ def test_read_rejects(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(batch=-1), SHAPE), (dict(batch=(1 << 15) + 1), SHAPE), (dict(q_heads=0), SHAPE), (dict(q_heads=3), SHAPE),
     (dict(q_heads=-2), SHAPE), (dict(q_heads=(1 << 16) + 2), SHAPE), (dict(batch=1 << 15, q_heads=1 << 14), SHAPE),
-    (dict(width=0), SHAPE), (dict(width=-1), SHAPE), (dict(width=(1 << 26) + 1), SHAPE), (dict(width=1 << 62), SHAPE),
+    (dict(width=0), SHAPE), (dict(width=-1), SHAPE), (dict(width=(1 << 26) + 1), SHAPE), (dict(batch=1 << 8, width=(1 << 25) + 1), SHAPE), (dict(width=1 << 62), SHAPE),
     (dict(scale=0.0), PARAM), (dict(scale=-1.0), PARAM), (dict(scale=float("nan")), PARAM),
     (dict(scale=float("inf")), PARAM), (dict(scale=3e38), PARAM), (dict(window=-1), PARAM),
     (dict(q=None), PTR), (dict(q=X + 2), PTR), (dict(q=X + 8), PTR), (dict(token=12), SHAPE), (dict(head=-8), SHAPE),
@@ -148,12 +148,12 @@ def test_a_call_of_nothing_needs_no_pointers(lib):
 
 
 def test_workspace(w, lib):
-    """None where no sequence can exceed 512 tokens; else dim sums and two statistics per query head and
+    """None where no sequence can exceed 1024 tokens; else dim sums and two statistics per query head and
     segment: as many segments as runs (the chip's workgroups per key-value head) and sequences."""
     def need(batch, q_heads, width, **kw):
         return lib.hqq_cache_attention_workspace(ctypes.byref(cache(**kw)), batch, q_heads, width)
 
-    assert need(3, 4, 32) == 0 and need(3, 4, 33) > 0 and need(0, 4, 33) == 0
+    assert need(3, 4, 64) == 0 and need(3, 4, 65) > 0 and need(0, 4, 65) == 0
     sizes = {need(b, 4, 100) for b in (1, 2, 3)}
     assert len(sizes) == 3 and max(sizes) - min(sizes) <= 2 * (4 * 128 * 4 + 4 * 8) + 512
     segments = (need(3, 4, 100) // (4 * 128 * 4 + 4 * 8))
@@ -194,7 +194,7 @@ def test_rejects_writes_over_what_is_read(lib):
     for base, size in arrays + [(S, 32)]:
         for at in (base, last(base, size), base - row + 16):
             assert read(lib, k=at) == PTR and read(lib, v=at) == PTR
-    q_row, table, ws = 3 * 4 * 128 * 2, 3 * 40 * 4, lib.hqq_cache_attention_workspace(ctypes.byref(cache()), 3, 4, 40)
+    q_row, table, ws = 3 * 4 * 128 * 2, 3 * 80 * 4, lib.hqq_cache_attention_workspace(ctypes.byref(cache()), 3, 4, 80)
     inputs = arrays + [(X, q_row), (T, table), (L, 12)]
     for base, size in inputs:
         for at in (base, last(base, size)):

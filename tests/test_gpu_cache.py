@@ -571,8 +571,8 @@ def test_graph_and_streams(hq):
 def test_outputs_given(hq):
     """Rows beside a given output's keep what they held; the C call may leave out lse."""
     g = rng(18)
-    c = filled(hq, g, 80, 16, 1, 64, 4, 32)
-    Q, table, n = batch_of(c, g, torch.float16, [100, 900], 3)
+    c = filled(hq, g, 150, 16, 1, 64, 4, 32)
+    Q, table, n = batch_of(c, g, torch.float16, [100, 1900], 3)
     want = hq.hqq_cache_attention(c, Q, table, n)
     room, row = torch.full((6, 3, 64), 7.0, device="cuda").half(), torch.full((8, 3), 7.0, device="cuda")
     got = hq.hqq_cache_attention(c, Q, table, n, out=room[2:4], lse=row[3:5])
@@ -601,7 +601,7 @@ def test_binding_refuses(hq):
     K = torch.zeros(5, 2, 128, device="cuda").half()
     s = torch.arange(5, device="cuda")
     Q, table, n = torch.zeros(3, 4, 128, device="cuda").half(), torch.zeros(3, 2, device="cuda").int(), torch.ones(3, device="cuda").int()
-    big = torch.zeros(3, 40, device="cuda").int()
+    big = torch.zeros(3, 80, device="cuda").int()
     bad = [
         (TypeError, lambda: hq.hqq_cache_write(c, K.cpu(), K, s)),
         (TypeError, lambda: hq.hqq_cache_write(c, K.float(), K.float(), s)),

@@ -140,7 +140,8 @@ int check_tokens(const hqq_cache &c, int64_t tokens)
 int check_batch(const hqq_cache &c, int64_t batch, int64_t q_heads, int64_t table_width)
 {
     if (batch < 0 || batch > (1 << 15) || q_heads < 1 || q_heads > (1 << 16) || q_heads % c.heads != 0 ||
-        batch * q_heads > (1 << 28) || table_width < 1 || table_width > (1 << 30) / c.page_size)
+        batch * q_heads > (1 << 28) || table_width < 1 || table_width > (1 << 30) / c.page_size ||
+        batch * table_width * c.page_size > int64_t(1) << 37)
         return HQQ_EINVAL_SHAPE;
     return HQQ_OK;
 }

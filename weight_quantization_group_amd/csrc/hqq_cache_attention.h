@@ -180,7 +180,10 @@ struct CacheAttention {
 
     struct alignas(16) Shared {
         union {
-            float meta[kCacheWaves][3][NG][kCacheTile];         // r of k, scaled r of v, z of v
+            struct {
+                uint4 q[NG][Keys::kUnits][64];                  // operands of the first product
+                float meta[kCacheWaves][3][NG][kCacheTile];     // r of k, scaled r of v, z of v
+            };
             float sums[kCacheWaves][16][kPitch];
         };
         float2 ml[kCacheWaves][16];
@@ -315,8 +318,8 @@ struct CacheAttention {
             load_values(next, vw);
         }
 
-        // ---- q: operands of the first product, and each group's sum
-        uint32_t q16[NG][Keys::kUnits][4];
+        // ---- q: operands of the first product (in LDS: 16 to 32 registers; every wave writes the
+        // same), and each group's sum
         float q_sum[NG];
         float score_scale;                                      // scores to exponents of 2
         {
@@ -347,7 +350,8 @@ struct CacheAttention {
             for (int g = 0; g < NG; ++g) {
                 float sum = 0.0f;
 #pragma unroll
-                for (int u = 0; u < Keys::kUnits; ++u)
+                for (int u = 0; u < Keys::kUnits; ++u) {
+                    uint32_t q16[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float factor = field_factor<NB, true>(Keys::field_of(u, r));
@@ -355,9 +359,11 @@ struct CacheAttention {
                         half2v h;
                         h[0] = (_Float16)(q[g][Keys::lo(u, r)] * inv);
                         h[1] = (_Float16)(q[g][Keys::hi(u, r)] * inv);
-                        __builtin_memcpy(&q16[g][u][r], &h, 4);
+                        __builtin_memcpy(&q16[r], &h, 4);
                         sum += ((float)h[0] + (float)h[1]) * (factor * 0x1p-24f);
                     }
+                    sh.q[g][u][lane] = uint4{q16[0], q16[1], q16[2], q16[3]};
+                }
                 q_sum[g] = column_sum(sum);
             }
         }
@@ -440,16 +446,20 @@ struct CacheAttention {
             wave_lds_fence();
 
             // ---- scores
-            float s[2][4];
+            float4v s[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float4v v = __builtin_amdgcn_mfma_f32_16x16x4f32(rz[NG <= 2 ? 0 : t], q_zero[t],
-                                                                 float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            for (int t = 0; t < 2; ++t)
+                s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(rz[NG <= 2 ? 0 : t], q_zero[t], float4v{0.f, 0.f, 0.f, 0.f}, 0,
+                                                            0, 0);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    float4v acc{0.f, 0.f, 0.f, 0.f};
+            for (int g = 0; g < NG; ++g) {
+                float4v acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-                    for (int u = 0; u < Keys::kUnits; ++u) {
+                for (int u = 0; u < Keys::kUnits; ++u) {
+                    const uint4 q4 = sh.q[g][u][lane];
+                    const uint32_t q16[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
                         uint32_t regs[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
@@ -458,16 +468,16 @@ struct CacheAttention {
                                 x = (x & 0xffu) | (x >> 8) << 16;
                             regs[r] = field<NB, true>(x, Keys::field_of(u, r));
                         }
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(q16[g][u]), acc, 0, 0, 0);
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(q16), acc[t], 0, 0, 0);
                     }
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
                     const float4v r4 = *reinterpret_cast<const float4v *>(&meta[0][g][16 * t + 4 * quad]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        v[r] = fmaf(acc[r], r4[r], v[r]);
+                        s[t][r] = fmaf(acc[t][r], r4[r], s[t][r]);
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    s[t][r] = v[r];
             }
             // the keys' registers are free: the next tile's go there while the weights are formed
             if (more) {
@@ -636,23 +646,37 @@ struct CacheAttention {
     __device__ __forceinline__ void run(Shared &sh)
     {
         const int worker = blockIdx.y;
-        int64_t at = 0, stop = 1, start = 0;
-        b = worker;                  // a sequence each, or a run of tiles
-        if (a.workers) {
-            const int64_t run = cache_run(a, lane);
-            at = worker * run;
-            stop = at + run;
-            b = cache_find(a, at, lane, start);
+        int at = 0, start = 0, stop;
+        bool cross = false;
+        CacheSpan s;
+        int slot = 0;
+        if (a.workers == 0) {        // a sequence each
+            b = worker;
+            s = cache_span(a, b);
+            stop = s.steps;
+        } else {
+            const CachePlan plan(a, lane);
+            const int64_t from = (int64_t)worker * plan.run;
+            if (from > 1 << 30)          // behind the last step
+                return;
+            at = (int)from;
+            stop = at + plan.run;
+            cross = plan.cross;
+            b = plan.find(a, at, lane, start, s);
+            slot = plan.slot(worker, b);
         }
-        for (; at < stop && b < a.batch; ++b) {
-            const CacheSpan s = cache_span(a, b);
-            const int64_t next = start + s.tiles, upto = a.workers && stop < next ? stop : next;
+        while (b < a.batch) {
+            const int next = start + s.steps, upto = stop < next ? stop : next;
             first = s.first;
-            begin = s.base + (int)(at - start) * kCacheTile;
-            end = upto < next ? s.base + (int)(upto - start) * kCacheTile : s.length;
-            segment(sh, worker + b, at == start && upto == next);
-            at = a.workers ? upto : stop;
-            start = next;
+            begin = s.base + (at - start) * kCacheStep;
+            end = upto < next ? s.base + (upto - start) * kCacheStep : s.length;
+            segment(sh, slot, at == start && upto == next);
+            if (!cross || upto == stop)
+                return;
+            at = start = next;
+            ++slot;
+            if (++b < a.batch)
+                s = cache_span(a, b);
         }
     }
 };
@@ -668,7 +692,7 @@ __global__ __launch_bounds__(64 * kCacheWaves, cache_resident(GS * NG, GS)) void
 template <int NB, int GS, int NG>
 hipError_t launch_attention(const CacheAttentionArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)(a.workers ? a.workers : a.batch));
+    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)(a.workers + a.batch));
     hipLaunchKernelGGL((cache_attention_kernel<NB, GS, NG>), grid, dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }

@@ -22,8 +22,8 @@ struct CacheCodecArgs {
     int32_t page_shift, page_mask;
 };
 
-// Attention: all sequences' tokens are cut into `workers` equal runs per key-value head
-// and row tile (hqq_cache_plan.h), or, workers = 0, a workgroup takes a sequence.
+// Attention: all sequences' tokens are cut into about `workers` equal runs per key-value
+// head and row tile (hqq_cache_plan.h), or, workers = 0, a workgroup takes a sequence.
 struct CacheAttentionArgs {
     const uint32_t *packed[2];
     const float *scale[2], *zero[2];
@@ -53,7 +53,7 @@ constexpr int cache_resident(int dim, int gs) { return dim <= 128 && dim / gs <=
 constexpr int kCus = 256;
 
 // Sequences of at most this many tokens are not split.
-constexpr int kCacheWhole = 512;
+constexpr int kCacheWhole = 1024;
 
 hipError_t launch_cache_write(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
 hipError_t launch_cache_read(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);

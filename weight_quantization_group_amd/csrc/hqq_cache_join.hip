@@ -18,17 +18,17 @@ __global__ __launch_bounds__(kJoinBlock) void cache_join_kernel(CacheAttentionAr
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int local = wave / WAVES, thread = threadIdx.x - local * WAVES * 64;
     const int head = blockIdx.x * kHeads + local, b = blockIdx.y;
-    const int64_t run = cache_run(a, lane);
-    int64_t start = 0;
-    for (int i = lane; i < b; i += 64)
-        start += cache_span(a, i).tiles;
+    const CachePlan plan(a, lane);
+    int start = lane < b ? plan.padded(plan.mine.steps) : 0;
+    for (int i = lane + 64; i < b; i += 64)
+        start += plan.padded(cache_span(a, i).steps);
     start = wave_sum(start);
-    const int64_t w0 = start / run;
-    const int count = (int)((start + cache_span(a, b).tiles - 1) / run - w0) + 1;
+    const int w0 = start / plan.run;
+    const int count = (start + plan.padded(cache_span(a, b).steps) - 1) / plan.run - w0 + 1;
     if (count == 1)
         return;                       // the one segment wrote the output itself
     const bool real = head < a.q_heads;
-    const int64_t slot = w0 + b;
+    const int64_t slot = plan.slot(w0, b);
     const float2 *ml = a.part_ml + slot * a.q_heads + (real ? head : 0);
     const float *part = a.part + (slot * a.q_heads + (real ? head : 0)) * D;
     float m = -INFINITY;

@@ -2,11 +2,11 @@
 // workgroups, found on the device (the lengths are there), and the ends that the
 // attention and the join have in common.
 //
-// The tokens of all sequences, in tiles of 32 and one sequence after the other, are cut
-// into `workers` equal runs; workgroup w of a key-value head takes run w, whatever
-// sequences it crosses, so that all of them end together however ragged the batch is.  The
-// part of a sequence that a run holds is a segment.  Runs and sequences both advance along
-// the tiles, so segment (w, b) has slot w + b in the workspace to itself.
+// The tokens of all sequences, in steps of a workgroup and one sequence after the other, are
+// cut into runs of equal length, about `workers` of them; workgroup w of a key-value head
+// takes run w.  Long runs cross from one sequence to the next, so that all of them end
+// together however ragged the batch is; short ones do not, as each segment (a run's part
+// of a sequence) has a prologue and an end of its own that cost as much as some steps.
 #pragma once
 
 #include "hqq_cache_internal.h"
@@ -18,15 +18,8 @@ typedef float float4v __attribute__((ext_vector_type(4)));
 
 struct CacheSpan {
     int first, base, length;   // first token that counts, its tile's first token, the length
-    int tiles;                 // tiles from base on, at least one (it writes the output)
+    int steps;                 // workgroup steps from base on, at least one (it writes the output)
 };
-
-// A 64-bit value that is the same in all lanes, as such
-__device__ __forceinline__ int64_t uniform(int64_t v)
-{
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
 
 __device__ __forceinline__ CacheSpan cache_span(const CacheAttentionArgs &a, int b)
 {
@@ -35,54 +28,93 @@ __device__ __forceinline__ CacheSpan cache_span(const CacheAttentionArgs &a, int
     n = n < 0 ? 0 : n > most ? (int)most : n;
     const int first = a.window > 0 && n > a.window ? n - a.window : 0;
     const int base = first & ~(kCacheTile - 1);
-    const int tiles = (n - base + kCacheTile - 1) / kCacheTile;
-    return CacheSpan{first, base, n, tiles < 1 ? 1 : tiles};
+    const int steps = (n - base + kCacheStep - 1) / kCacheStep;
+    return CacheSpan{first, base, n, steps < 1 ? 1 : steps};
 }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v)
+__device__ __forceinline__ int wave_sum(int v)
 {
 #pragma unroll
     for (int o = 1; o < 64; o *= 2)
         v += __shfl_xor(v, o);
-    return v;
+    return __builtin_amdgcn_readfirstlane(v);
 }
 
-// Tiles per run: whole workgroup steps, as many as cover all sequences.
-__device__ __forceinline__ int64_t cache_run(const CacheAttentionArgs &a, int lane)
-{
-    int64_t tiles = 0;
-    for (int b = lane; b < a.batch; b += 64)
-        tiles += cache_span(a, b).tiles;
-    tiles = wave_sum(tiles);
-    const int64_t per = (tiles + a.workers - 1) / a.workers;
-    return uniform((per + kCacheWaves - 1) / kCacheWaves * kCacheWaves);
-}
+// Runs of more steps than this cross sequences.
+constexpr int kCacheCross = 8;
 
-// The sequence that holds tile `at` (batch behind the last), and its first tile
-__device__ __forceinline__ int cache_find(const CacheAttentionArgs &a, int64_t at, int lane, int64_t &start)
-{
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) {
-        const int b = b0 + lane;
-        const int64_t tiles = b < a.batch ? cache_span(a, b).tiles : 0;
-        int64_t upto = tiles;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const int64_t up = __shfl_up(upto, o);
-            upto += lane >= o ? up : 0;
-        }
-        upto += before;
-        const uint64_t behind = __ballot(at < upto);
-        if (behind) {
-            const int src = __ffsll((unsigned long long)behind) - 1;
-            start = uniform(__shfl(upto - tiles, src));
-            return __builtin_amdgcn_readfirstlane(b0 + src);
-        }
-        before = __shfl(upto, 63);
+// Every wave finds the same plan by itself; lane l holds sequence l's span.  All steps number at
+// most 2^30 (batch * table_width * page_size <= 2^37).
+struct CachePlan {
+    CacheSpan mine;            // of sequence `lane` (steps 0: there is none)
+    int run;                   // steps per run
+    bool cross;
+
+    __device__ __forceinline__ CachePlan(const CacheAttentionArgs &a, int lane)
+    {
+        mine = lane < a.batch ? cache_span(a, lane) : CacheSpan{0, 0, 0, 0};
+        const int steps = sum(a, lane, 1);
+        run = (steps + a.workers - 1) / a.workers;
+        cross = run > kCacheCross;
+        // runs that keep to their sequences are more: lengthened until one round holds them
+        if (!cross)
+            for (int i = 0; i < 3 && sum(a, lane, run) > a.workers; ++i)
+                run += (run + 3) / 4;
     }
-    start = 0;
-    return a.batch;
-}
+
+    // runs of `size` steps that the sequences take
+    __device__ __forceinline__ int sum(const CacheAttentionArgs &a, int lane, int size) const
+    {
+        int n = runs(mine.steps, size);
+        for (int b = lane + 64; b < a.batch; b += 64)
+            n += runs(cache_span(a, b).steps, size);
+        return wave_sum(n);
+    }
+
+    static __device__ __forceinline__ int runs(int steps, int size)
+    {
+        return size == 1 ? steps : (uint32_t)(steps + size - 1) / (uint32_t)size;
+    }
+
+    // a sequence's steps in the order of runs
+    __device__ __forceinline__ int padded(int steps) const { return cross ? steps : runs(steps, run) * run; }
+
+    // the workspace's place of segment (w, b): runs and sequences both advance
+    __device__ __forceinline__ int slot(int w, int b) const { return cross ? w + b : w; }
+
+    // The sequence that holds step `at`, its first step and span (batch: behind the last)
+    __device__ __forceinline__ int find(const CacheAttentionArgs &a, int at, int lane, int &start, CacheSpan &span) const
+    {
+        int before = 0;
+        CacheSpan s = mine;
+        for (int b0 = 0; b0 < a.batch; b0 += 64) {
+            if (b0)
+                s = b0 + lane < a.batch ? cache_span(a, b0 + lane) : CacheSpan{0, 0, 0, 0};
+            const int steps = padded(s.steps);
+            int upto = steps;
+#pragma unroll
+            for (int o = 1; o < 64; o *= 2) {
+                const int up = __shfl_up(upto, o);
+                upto += lane >= o ? up : 0;
+            }
+            upto += before;
+            const uint64_t behind = __ballot(at < upto);
+            if (behind) {
+                const int src = __ffsll((unsigned long long)behind) - 1;
+                start = __builtin_amdgcn_readlane(upto - steps, src);
+                span.first = __builtin_amdgcn_readlane(s.first, src);
+                span.base = __builtin_amdgcn_readlane(s.base, src);
+                span.length = __builtin_amdgcn_readlane(s.length, src);
+                span.steps = __builtin_amdgcn_readlane(s.steps, src);
+                return __builtin_amdgcn_readfirstlane(b0 + src);
+            }
+            before = __builtin_amdgcn_readlane(upto, 63);
+        }
+        start = 0;
+        span = CacheSpan{0, 0, 0, 0};
+        return a.batch;
+    }
+};
 
 __device__ __forceinline__ uint2 cache_round4(float4v v, bool bf16)
 {
