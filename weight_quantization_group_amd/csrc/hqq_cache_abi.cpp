@@ -150,9 +150,9 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Runs per key-value head and row tile, `columns` of those: as many workgroups as the chip
 // holds, or some rounds of them where that divides better.
-int32_t workers_for(int64_t columns, int resident)
+int32_t workers_for(int64_t columns)
 {
-    const int64_t slots = (int64_t)kCus * resident;
+    const int64_t slots = (int64_t)kCus * kCacheResident;
     int64_t best = slots / columns, rounds = 1;
     for (int64_t r = 2; r <= 4; ++r)
         if (r * slots / columns * rounds > best * r * 11 / 10) {
@@ -174,7 +174,7 @@ struct AttentionLayout {
         workers = 0;
         if (batch == 0 || table_width * c.page_size <= kCacheWhole)
             return;
-        workers = workers_for(c.heads * row_tiles, cache_resident(c.dim, c.group_size));
+        workers = workers_for(c.heads * row_tiles);
         const int64_t segments = workers + batch;
         const int64_t sums = round_up(segments * q_heads * c.dim * 4, 256);
         bytes = sums + round_up(segments * q_heads * 8, 256);

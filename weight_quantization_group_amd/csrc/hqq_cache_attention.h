@@ -12,15 +12,19 @@
 // output row (second).
 //
 // Operand layouts (16x16x32): S = K Q^T has a token per row and a head per column, so
-// a lane holds 4 tokens of one head; these are the contraction slots of the second
-// product O^T = V^T P^T, for which a lane needs exactly its own 8 tokens of the 32:
-// the weights never leave their lane.  For V a lane pairs the words of two
-// tokens, whose equal fields are neighbours in the contraction.  A group's dims are
-// dealt to the rows of whole products (lane m of 16 has gs / 16 consecutive dims),
-// as one product has one p_t r_tg per token.
+// a lane holds 4 tokens of each 16 for one head.  These are its contraction slots in the
+// second product O^T = V^T P^T, for which it needs just its own tokens: the weights never
+// leave their lane.  V's side of it wants 8 tokens of one dim per lane, against rows of dims in
+// memory: the transposing LDS reads (of 4 or 8 bits an element; two 2-bit codes count as one
+// of 4) hand a lane the codes of its own tokens, in the order of the rows that it names.
+//
+// A wave takes tiles of 32 tokens, its loads whole lines in 16-byte pieces over the lanes, a tile
+// ahead in registers; through LDS they reach the operands' lanes.
 #pragma once
 
 #include "hqq_cache_plan.h"
+
+#include <type_traits>
 
 namespace hqq {
 namespace {
@@ -28,6 +32,7 @@ namespace {
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ half8 operand(const uint32_t (&r)[4])
 {
@@ -36,38 +41,51 @@ __device__ __forceinline__ half8 operand(const uint32_t (&r)[4])
     return h;
 }
 
-// Field f of both half words of x as fp16 subnormals, times field_factor.  The matrix
-// units align the products of a sum by their operands' exponents, and a subnormal counts with
-// the least one, so a low field loses bits of the sum.  PRECISE (keys): the fields are brought
-// to the upper bits of the 10 that a subnormal has (error of lse at 2 bits 1.5e-6 without);
-// values, whose weights have 11 bits, leave them where that saves a shift.
-template <int NB, bool PRECISE>
-__device__ __forceinline__ uint32_t field(uint32_t x, int f)
+// Field f of both half words of a word of keys as fp16 subnormals, times key_factor.  The
+// matrix units align the products of a sum by their operands' exponents, and a subnormal
+// counts with the least one, so a low field loses bits of the sum: they are brought to the
+// upper bits of the 10 that a subnormal has (error of lse at 2 bits 1.5e-6 without).
+template <int NB>
+__device__ __forceinline__ uint32_t key_field(uint32_t x, int f)
 {
     if constexpr (NB == 8) {
         return (f ? x >> 8 : x) & 0x00ff00ffu;
     } else if constexpr (NB == 4) {
-        if constexpr (PRECISE)
-            return (f == 0 ? x << 4 : x >> (4 * f - 4)) & 0x00f000f0u;
-        else
-            return (f < 2 ? x : x >> 8) & (f % 2 ? 0x00f000f0u : 0x000f000fu);
+        return (f == 0 ? x << 4 : x >> (4 * f - 4)) & 0x00f000f0u;
     } else {
-        if constexpr (PRECISE) {
-            const int left = 6 - 4 * (f / 2);
-            return (left > 0 ? x << left : x >> -left) & (f % 2 ? 0x03000300u : 0x00c000c0u);
-        } else {
-            return f < 5 ? x & (0x00030003u << (2 * f)) : (x >> 10) & (0x00030003u << (2 * (f - 5)));
-        }
+        const int left = 6 - 4 * (f / 2);
+        return (left > 0 ? x << left : x >> -left) & (f % 2 ? 0x03000300u : 0x00c000c0u);
     }
 }
 
-template <int NB, bool PRECISE>
-constexpr float field_factor(int f)
+template <int NB>
+constexpr float key_factor(int f)
 {
-    return NB == 8   ? 1.0f
-           : NB == 4 ? (PRECISE || f % 2 ? 16.0f : 1.0f)
-           : PRECISE ? (f % 2 ? 256.0f : 64.0f)
-                     : (float)(1 << (2 * (f < 5 ? f : f - 5)));
+    return NB == 8 ? 1.0f : NB == 4 ? 16.0f : f % 2 ? 256.0f : 64.0f;
+}
+
+// The same for a lane's values: word x holds 8 tokens of 4 bits (or 4 of 8), field f is tokens f and
+// f + 4 (f and f + 2) of it, i the code within 4 bits.  They come out times token_factor and
+// dim_factor; weights have 11 bits, so the fields stay low where that saves a shift.
+template <int NB>
+__device__ __forceinline__ uint32_t value_field(uint32_t x, int f, int i)
+{
+    if constexpr (NB == 8)
+        return (f ? x >> 8 : x) & 0x00ff00ffu;
+    else
+        return (f < 2 ? x : x >> 8) & (NB == 4 ? 0x000f000fu : 0x00030003u << (2 * i)) << (4 * (f % 2));
+}
+
+template <int NB>
+__device__ __forceinline__ float token_factor(int token)
+{
+    return NB == 8 ? 1.0f : token & 1 ? 16.0f : 1.0f;
+}
+
+template <int NB>
+constexpr float dim_factor(int i)
+{
+    return NB == 2 && i ? 4.0f : 1.0f;
 }
 
 // How a lane's gs / 4 codes of a token's group stand in the operands of the first
@@ -151,6 +169,13 @@ __device__ __forceinline__ float column_max(float v)
     return fmaxf(r.a, r.b);
 }
 
+// the value of the lane CTRL & 15 places on in the row of 16 (0x121 to 0x12f: rotated)
+template <int CTRL>
+__device__ __forceinline__ float dpp_float(float v)
+{
+    return __uint_as_float(__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+
 __device__ __forceinline__ float power_of_two(int e)      // -126 <= e <= 127
 {
     return __uint_as_float((uint32_t)(e + 127) << 23);
@@ -164,159 +189,218 @@ __device__ __forceinline__ void wave_lds_fence()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+typedef int int2v __attribute__((ext_vector_type(2)));
+
+// 16 rows of 16 4-bit elements (8 rows of 8-bit ones) over 16 lanes, 8 bytes each: lane l gets
+// element l of every row
+template <int NB>
+__device__ __forceinline__ int2v read_transposed(const char *lds)
+{
+    const auto p = (__attribute__((address_space(3))) int2v *)lds;
+    if constexpr (NB == 8)
+        return __builtin_amdgcn_ds_read_tr8_b64_v2i32(p);
+    else
+        return __builtin_amdgcn_ds_read_tr4_b64_v2i32(p);
+}
+
 template <int NB, int GS, int NG>
 struct CacheAttention {
     static constexpr int D = GS * NG;
     static constexpr int kRowBytes = D * NB / 8;
     typedef KeyOrder<NB, GS> Keys;
-    static constexpr int kValueBits = GS * NB / 16;             // a lane's bits of a token's group
-    static constexpr int kValueBytes = kValueBits < 8 ? 1 : kValueBits / 8;
-    static constexpr int kValueWords = (kValueBytes + 3) / 4;
-    static constexpr int kCodes = GS / 16;                      // ... and codes: products per group
-    static constexpr int kMetas = NG <= 2 ? 1 : 2;              // a tile's groups over the lanes
-    static constexpr int kPerChunk = kValueBits < 16 ? kCodes : 16 / NB;      // codes of a half word
-    static constexpr int kChunks = kValueBits < 16 ? 1 : kValueBits / 16;
+    static constexpr int kTile = kCacheTile, kStep = kCacheStep;
+    static constexpr int kSubs = kTile / 16;                    // subtiles: 16 consecutive rows of a page
+    static constexpr int kPieces = (kSubs * kRowBytes + 63) / 64;       // 16-byte pieces per lane and tile
+    // a tile's scales over the lanes: token col, and 4 of (subtile, group) along the quads
+    static constexpr int kGroups = NG == 3 ? 4 : NG;
+    static constexpr int kMetas = (kSubs * kGroups + 3) / 4;
+    static constexpr int kPerQuads = 4 / kGroups;               // subtiles along the quads
+    // transposed reads, of kCodes dims per lane
+    static constexpr int kCodes = NB == 2 ? 2 : 1;
+    static constexpr int kBlockDims = 16 * kCodes;
+    static constexpr int kBlocks = D / kBlockDims;
+    static constexpr int kReadBlocks = NB == 8 ? 1 : 2;         // blocks of a transposed read
     static constexpr int kPitch = D + 4;
 
     struct alignas(16) Shared {
         union {
             struct {
-                uint4 q[NG][Keys::kUnits][64];                  // operands of the first product
-                float meta[kCacheWaves][3][NG][kCacheTile];     // r of k, scaled r of v, z of v
+                uint4v q[NG][Keys::kUnits][64];                 // operands of the first product
+                uint4v rows[kCacheWaves][2][kSubs * kRowBytes]; // a tile's rows of k and of v
+                float meta[kCacheWaves][3][NG][kTile];          // r of k, scaled r of v, z of v
             };
             float sums[kCacheWaves][16][kPitch];
         };
         float2 ml[kCacheWaves][16];
     };
 
-    // The tile's two subtiles: each 16 consecutive rows of a page
     struct Where {
         int at;
-        int64_t row[2];
-        bool there[2];
-        bool whole;      // all its tokens count
-        bool joined;     // its subtiles are of one page
+        int64_t row[kSubs];
+        bool there[kSubs];
+        bool whole;                                             // all the tile's tokens count
     };
-    // ... and what is loaded of them
-    struct Meta {
+    struct Loads {
+        uint4v k[kPieces], v[kPieces];
         float ks[kMetas], kz[kMetas], vs[kMetas], vz[kMetas];
     };
-    typedef uint32_t KeyWords[2][NG][(Keys::kBytes + 3) / 4];
-    typedef uint32_t ValueWords[8][NG][kValueWords];
 
     const CacheAttentionArgs &a;
-    const int lane, wave, col, quad, head;
+    const int lane, wave, col, quad;
+    int head, row_tile, worker;
     // the segment: tokens [begin, end) of sequence b, of which those from `first` on count
     int b, begin, end, first;
 
     __device__ __forceinline__ CacheAttention(const CacheAttentionArgs &args)
         : a(args), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), col(lane & 15),
-          quad(lane >> 4),
-          head(blockIdx.x % args.heads)
+          quad(lane >> 4)
     {
+        // Workgroups go to the 8 XCDs in turn: the heads of one run, whose parts of a page lie
+        // together, to one of them
+        const uint32_t id = blockIdx.y * gridDim.x + blockIdx.x, turn = id >> 3;
+        const uint32_t column = turn % gridDim.x;
+        worker = (int)(turn / gridDim.x * 8 + (id & 7));
+        head = (int)(column % (uint32_t)a.heads);
+        row_tile = (int)(column / (uint32_t)a.heads);
     }
 
-    // The pages of 32 of this wave's tiles from tile `at` on: subtile i's in lane i
+    // The pages of this wave's next 64 subtiles from tile `at` on, one in each lane
     __device__ __forceinline__ int pages_from(int at) const
     {
-        const int token = at + (lane >> 1) * kCacheStep + (lane & 1) * 16;
-        return token < end ? a.table[(int64_t)b * a.table_width + (token >> a.page_shift)] : -1;
+        const int token = at + lane / kSubs * kStep + lane % kSubs * 16;
+        int page = token < end ? a.table[(int64_t)b * a.table_width + (token >> a.page_shift)] : -1;
+        // waited for here: tiles that do not come here must not wait for their own loads at its use
+        asm volatile("" : "+v"(page));
+        return page;
     }
 
     __device__ __forceinline__ Where where(int at, int pages, int tile) const
     {
         Where w;
         w.at = at;
+        w.whole = at >= first && at + kTile <= end;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int page = __builtin_amdgcn_readlane(pages, 2 * (tile & 31) + t);
+        for (int t = 0; t < kSubs; ++t) {
+            const int page = __builtin_amdgcn_readlane(pages, (kSubs * tile + t) & 63);
             w.there[t] = page >= 0 && page < a.pages;
+            w.whole = w.whole && w.there[t];
             w.row[t] = (((int64_t)(w.there[t] ? page : 0) * a.heads + head) << a.page_shift) +
                        ((at + 16 * t) & a.page_mask);
         }
-        w.whole = w.there[0] && w.there[1] && at >= first && at + kCacheTile <= end;
-        w.joined = a.page_shift > 4;
         return w;
+    }
+
+    template <typename T>
+    static __device__ __forceinline__ T of_subtile(const T (&v)[kSubs], int t)
+    {
+        T r = v[0];
+#pragma unroll
+        for (int i = 1; i < kSubs; ++i)
+            r = t == i ? v[i] : r;
+        return r;
     }
 
     __device__ __forceinline__ bool counts(const Where &w, int t, int place) const
     {
         const int token = w.at + 16 * t + place;
-        return token >= first && token < end && w.there[t];
+        return token >= first && token < end && of_subtile(w.there, t);
     }
 
-    __device__ __forceinline__ void load_keys(const Where &w, KeyWords &kw) const
+    // A lane's i-th piece of a tile; the last lanes may come to the last piece again
+    __device__ __forceinline__ int piece(int i) const
     {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                load_words<Keys::kBytes>(kw[t][g], (const char *)a.packed[0] + w.row[t] * kRowBytes + col * kRowBytes +
-                                                       g * (GS * NB / 8) + quad * Keys::kBytes);
+        const int x = lane + 64 * i;
+        return (kSubs * kRowBytes) % 64 == 0 || x < kSubs * kRowBytes ? x : kSubs * kRowBytes - 1;
     }
 
-    __device__ __forceinline__ void load_values(const Where &w, ValueWords &vw) const
-    {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                load_words<kValueBytes>(vw[j][g], (const char *)a.packed[1] + w.row[j / 4] * kRowBytes +
-                                                      (4 * quad + j % 4) * kRowBytes + g * (GS * NB / 8) +
-                                                      (col * kValueBits) / 8);
-    }
+    __device__ __forceinline__ int meta_sub(int i) const { return (quad + 4 * i) / kGroups % kSubs; }
+    __device__ __forceinline__ int meta_group() const { return quad % kGroups < NG ? quad % kGroups : 0; }
 
-    // Scales and zeros lie over the lanes as token col and, along the quads, group (and
-    // subtile, where the groups leave room)
-    static __device__ __forceinline__ int meta_tile(int i, int quad) { return NG <= 2 ? quad / NG : i; }
-    static __device__ __forceinline__ int meta_group(int quad) { return NG <= 2 ? quad % NG : quad < NG ? quad : 0; }
-    static __device__ __forceinline__ bool meta_there(int i, int quad) { return NG <= 2 ? quad / NG < 2 : quad < NG; }
-
-    __device__ __forceinline__ void load_meta(const Where &w, Meta &m) const
+    // All of a tile, nothing under a condition that the lanes do not share: the rows are there
+    // whether their tokens count or not
+    __device__ __forceinline__ void load(const Where &w, Loads &l) const
     {
+        if (a.page_mask >= kTile - 1) {      // the tile's rows follow each other: one base for the wave
+            const int64_t base = w.row[0] * NG;
 #pragma unroll
-        for (int i = 0; i < kMetas; ++i) {
-            const int t = meta_tile(i, quad);
-            // tokens that do not count: 1 / scale and zero of 0, whatever the page holds there
-            m.ks[i] = m.vs[i] = INFINITY;
-            m.kz[i] = m.vz[i] = 0.0f;
-            const bool in = w.whole || (t ? counts(w, 1, col) : counts(w, 0, col));
-            if (meta_there(i, quad) && in) {
-                if (w.joined) {          // the tile's rows follow each other: one base for the wave
-                    const int64_t base = w.row[0] * NG;
-                    const uint32_t from = (16 * t + col) * NG + meta_group(quad);
-                    m.ks[i] = (a.scale[0] + base)[from], m.kz[i] = (a.zero[0] + base)[from];
-                    m.vs[i] = (a.scale[1] + base)[from], m.vz[i] = (a.zero[1] + base)[from];
-                } else {
-                    const int64_t from = ((t ? w.row[1] : w.row[0]) + col) * NG + meta_group(quad);
-                    m.ks[i] = a.scale[0][from], m.kz[i] = a.zero[0][from];
-                    m.vs[i] = a.scale[1][from], m.vz[i] = a.zero[1][from];
-                }
+            for (int i = 0; i < kMetas; ++i) {
+                const uint32_t from = (16 * meta_sub(i) + col) * NG + meta_group();
+                l.ks[i] = (a.scale[0] + base)[from], l.kz[i] = (a.zero[0] + base)[from];
+                l.vs[i] = (a.scale[1] + base)[from], l.vz[i] = (a.zero[1] + base)[from];
             }
+            const uint4v *k = reinterpret_cast<const uint4v *>((const char *)a.packed[0] + w.row[0] * kRowBytes);
+            const uint4v *v = reinterpret_cast<const uint4v *>((const char *)a.packed[1] + w.row[0] * kRowBytes);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                l.k[i] = k[piece(i)];
+                l.v[i] = v[piece(i)];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kMetas; ++i) {
+                const int64_t from = (of_subtile(w.row, meta_sub(i)) + col) * NG + meta_group();
+                l.ks[i] = a.scale[0][from], l.kz[i] = a.zero[0][from];
+                l.vs[i] = a.scale[1][from], l.vz[i] = a.zero[1][from];
+            }
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int t = piece(i) / kRowBytes;
+                const int64_t from = of_subtile(w.row, t) * kRowBytes + (piece(i) - t * kRowBytes) * 16;
+                l.k[i] = *reinterpret_cast<const uint4v *>((const char *)a.packed[0] + from);
+                l.v[i] = *reinterpret_cast<const uint4v *>((const char *)a.packed[1] + from);
+            }
+        }
+    }
+
+    // Rows stand in LDS with their pieces exchanged by the row, or the 16 rows of one access would lie
+    // on 2 to 4 of the banks' 8 pieces
+    static constexpr int kRowPieces = kRowBytes / 16;
+    static constexpr bool kExchange = kRowBytes % 16 == 0 && kRowPieces > 1 && (kRowPieces & (kRowPieces - 1)) == 0;
+    static __device__ __forceinline__ int exchange(int row)
+    {
+        return !kExchange ? 0 : kRowPieces <= 8 ? row / (8 / kRowPieces) & (kRowPieces - 1) : row & 7;
+    }
+
+    static __device__ __forceinline__ int piece_place(int x)
+    {
+        return kExchange ? x ^ exchange(x / kRowPieces) : x;
+    }
+
+    static __device__ __forceinline__ const char *row_byte(const uint4v *rows, int row, int byte)
+    {
+        return (const char *)rows + row * kRowBytes + (byte ^ exchange(row) << 4);
+    }
+
+    // a lane's words of a token's group
+    static __device__ __forceinline__ void read_keys(const uint4v *rows, int row, int byte,
+                                                     uint32_t (&w)[(Keys::kBytes + 3) / 4])
+    {
+        constexpr int kPart = Keys::kBytes < 16 ? Keys::kBytes : 16;
+#pragma unroll
+        for (int i = 0; i < Keys::kBytes / kPart; ++i) {
+            uint32_t part[(kPart + 3) / 4];
+            load_words<kPart>(part, row_byte(rows, row, byte + i * kPart));
+#pragma unroll
+            for (int k = 0; k < (kPart + 3) / 4; ++k)
+                w[i * (kPart / 4) + k] = part[k];
         }
     }
 
     // One segment, from q to the output or the workspace's slot
     __device__ __forceinline__ void segment(Shared &sh, int slot, bool whole_sequence)
     {
-        const int row_tile = blockIdx.x / a.heads;
         const int in_group = row_tile * 16 + col;               // this column's q head within the group
         const bool real = in_group < a.G;
         const int q_head = head * a.G + (real ? in_group : 0);
 
         // ---- the first tile's loads
-        const int at0 = begin + wave * kCacheTile;
-        const int tiles = at0 < end ? (end - at0 + kCacheStep - 1) / kCacheStep : 0;
+        const int at0 = begin + wave * kTile;
+        const int tiles = at0 < end ? (end - at0 + kStep - 1) / kStep : 0;
         int pages = pages_from(at0);
-        KeyWords kw;
-        ValueWords vw;
-        Meta next_meta;
+        Loads l;
         Where next = where(at0, pages, 0);
-        if (tiles > 0) {
-            load_meta(next, next_meta);
-            load_keys(next, kw);
-            load_values(next, vw);
-        }
+        if (tiles > 0)
+            load(next, l);
 
         // ---- q: operands of the first product (in LDS: 16 to 32 registers; every wave writes the
         // same), and each group's sum
@@ -330,7 +414,7 @@ struct CacheAttention {
             for (int g = 0; g < NG; ++g)
 #pragma unroll
                 for (int i = 0; i < GS / 4; i += 8) {
-                    const uint4 raw = *reinterpret_cast<const uint4 *>(src + g * GS + i);
+                    const uint4v raw = *reinterpret_cast<const uint4v *>(src + g * GS + i);
                     uint16_t h[8];
                     __builtin_memcpy(h, &raw, 16);
 #pragma unroll
@@ -354,7 +438,7 @@ struct CacheAttention {
                     uint32_t q16[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float factor = field_factor<NB, true>(Keys::field_of(u, r));
+                        const float factor = key_factor<NB>(Keys::field_of(u, r));
                         const float inv = f / factor;
                         half2v h;
                         h[0] = (_Float16)(q[g][Keys::lo(u, r)] * inv);
@@ -362,134 +446,166 @@ struct CacheAttention {
                         __builtin_memcpy(&q16[r], &h, 4);
                         sum += ((float)h[0] + (float)h[1]) * (factor * 0x1p-24f);
                     }
-                    sh.q[g][u][lane] = uint4{q16[0], q16[1], q16[2], q16[3]};
+                    sh.q[g][u][lane] = uint4v{q16[0], q16[1], q16[2], q16[3]};
                 }
                 q_sum[g] = column_sum(sum);
             }
         }
-        // the zeros' part of the scores, -sum_g (r z)_tg q_sum_g, is a product of depth 4 in fp32,
-        // with a row's groups (NG <= 2: of both subtiles) along its depth
-        float q_zero[2];
+        // the zeros' part of the scores, -sum_g (r z)_tg q_sum_g, is a product of depth 4 in fp32, with the
+        // groups of kPerQuads subtiles along its depth
+        float q_zero[kPerQuads];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int g = NG <= 2 ? quad - t * NG : quad;
+        for (int t = 0; t < kPerQuads; ++t) {
             q_zero[t] = 0.0f;
 #pragma unroll
             for (int i = 0; i < NG; ++i)
-                q_zero[t] = g == i ? -q_sum[i] : q_zero[t];
+                q_zero[t] = quad == t * kGroups + i ? -q_sum[i] : q_zero[t];
         }
 
         // ---- state: per column, but sums of weights and zeros only over this lane's tokens
-        float4v o[NG][kCodes];
+        float4v o[kBlocks][kCodes];
         float z_sum[NG], v_unit[NG];
         float m2 = -INFINITY, total = 0.0f;                     // maximum (exponent of 2), sum of weights
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             z_sum[g] = 0.0f;
             v_unit[g] = 0x1p120f;
+        }
+#pragma unroll
+        for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
             for (int i = 0; i < kCodes; ++i)
-                o[g][i] = float4v{0.f, 0.f, 0.f, 0.f};
-        }
+                o[n][i] = float4v{0.f, 0.f, 0.f, 0.f};
         float lane_unit = v_unit[0];                            // of the group whose scales this lane loads
-        float (*meta)[NG][kCacheTile] = sh.meta[wave];
+        float (*meta)[NG][kTile] = sh.meta[wave];
+        uint4v *k_rows = sh.rows[wave][0], *v_rows = sh.rows[wave][1];
+        // the row that this lane names to the transposing reads: its quad's tokens in their order
+        // (8 bits: 16 dims of each, in two halves; else one block of dims of each and then the next)
+        const int named = NB == 8 ? col / 2 : col % 8;
+        const int v_row = 16 * (named / 4) + 4 * quad + named % 4;
 
-        for (int tile = 0; tile < tiles; ++tile) {
+        // One tile.  The next one's loads leave at its top, when its own are in LDS.  Nothing is loaded
+        // under a condition, which would make the waits for older loads wait for these too.
+        const auto step = [&](int tile, auto more) {
             const Where now = next;
-            const bool more = tile + 1 < tiles;
 
             // ---- scales: reciprocals (to 1 ulp), to the layout of the scores through LDS
             float rz[kMetas];                                   // (r z) of k
             float vr[kMetas];
             float raise = 0.0f;
+            if (!now.whole) {
+                // tokens that do not count: 1 / scale and zero of 0, whatever the page holds there
+#pragma unroll
+                for (int i = 0; i < kMetas; ++i) {
+                    const bool in = counts(now, meta_sub(i), col);
+                    l.ks[i] = in ? l.ks[i] : INFINITY;
+                    l.vs[i] = in ? l.vs[i] : INFINITY;
+                    l.kz[i] = in ? l.kz[i] : 0.0f;
+                    l.vz[i] = in ? l.vz[i] : 0.0f;
+                }
+            }
+            const float factor = token_factor<NB>(col);
 #pragma unroll
             for (int i = 0; i < kMetas; ++i) {
-                const float kr = __builtin_amdgcn_rcpf(next_meta.ks[i]) * 0x1p12f;  // the codes' 2^-24 taken back, half here
-                vr[i] = __builtin_amdgcn_rcpf(next_meta.vs[i]);
-                rz[i] = kr * next_meta.kz[i];
-                if (meta_there(i, quad)) {
-                    float *to = &meta[0][meta_group(quad)][16 * meta_tile(i, quad) + col];
-                    to[0] = kr;
-                    to[2 * NG * kCacheTile] = next_meta.vz[i];
-                }
+                const float kr = __builtin_amdgcn_rcpf(l.ks[i]) * 0x1p12f;  // the codes' 2^-24 taken back, half here
+                vr[i] = __builtin_amdgcn_rcpf(l.vs[i]);
+                rz[i] = kr * l.kz[i];
+                float *to = &meta[0][meta_group()][16 * meta_sub(i) + col];
+                to[0] = kr;
+                to[2 * NG * kTile] = l.vz[i] * factor;
                 raise = fmaxf(raise, vr[i]);
             }
             // a group's r of v beyond the unit that its weights are held in?
             if (__any(!(raise * lane_unit <= 0x1p15f))) {
+                // the largest of each row of lanes, which hold one group each
+                float row_most = raise;
+                row_most = fmaxf(row_most, dpp_float<0x128>(row_most));
+                row_most = fmaxf(row_most, dpp_float<0x124>(row_most));
+                row_most = fmaxf(row_most, dpp_float<0x122>(row_most));
+                row_most = fmaxf(row_most, dpp_float<0x121>(row_most));
+                float unit[NG];
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     float most = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < kMetas; ++i)
-                        most = fmaxf(most, meta_there(i, quad) && meta_group(quad) == g ? vr[i] : 0.0f);
-#pragma unroll
-                    for (int off = 1; off < 64; off *= 2)
-                        most = fmaxf(most, __shfl_xor(most, off));
+                    for (int k = 0; k < 4; ++k)
+                        if (k % kGroups == g)
+                            most = fmaxf(most, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(row_most), 16 * k)));
                     // most * unit in [2^14, 2^15)
                     const int ue = 14 - ((int)(__float_as_uint(most) >> 23) - 127);
-                    const float unit = power_of_two(ue < -120 ? -120 : ue > 120 ? 120 : ue);
-                    if (unit < v_unit[g]) {
-                        const float f = unit / v_unit[g];
-                        v_unit[g] = unit;
-                        z_sum[g] *= f;
-#pragma unroll
-                        for (int i = 0; i < kCodes; ++i)
-                            o[g][i] *= f;
-                    }
+                    unit[g] = fminf(v_unit[g], power_of_two(ue < -120 ? -120 : ue > 120 ? 120 : ue));
+                    z_sum[g] *= unit[g] / v_unit[g];
                 }
-                lane_unit = pick(v_unit, meta_group(quad));
+#pragma unroll
+                for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int i = 0; i < kCodes; ++i)
+                        o[n][i] *= unit[n * kBlockDims / GS] / v_unit[n * kBlockDims / GS];
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    v_unit[g] = unit[g];
+                lane_unit = pick(v_unit, meta_group());
             }
 #pragma unroll
             for (int i = 0; i < kMetas; ++i)
-                if (meta_there(i, quad))
-                    meta[1][meta_group(quad)][16 * meta_tile(i, quad) + col] = vr[i] * lane_unit;
+                meta[1][meta_group()][16 * meta_sub(i) + col] = vr[i] * (lane_unit / factor);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                k_rows[piece_place(piece(i))] = l.k[i];
+                v_rows[piece_place(piece(i))] = l.v[i];
+            }
             wave_lds_fence();
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (more) {
+                if (((tile + 1) * kSubs & 63) == 0)
+                    pages = pages_from(now.at + kStep);
+                next = where(now.at + kStep, pages, tile + 1);
+                load(next, l);
+            }
 
             // ---- scores
-            float4v s[2];
+            float4v s[kSubs];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(rz[NG <= 2 ? 0 : t], q_zero[t], float4v{0.f, 0.f, 0.f, 0.f}, 0,
-                                                            0, 0);
+            for (int t = 0; t < kSubs; ++t)
+                s[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(rz[t / kPerQuads], q_zero[t % kPerQuads],
+                                                            float4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                float4v acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                float4v acc[kSubs];
+                uint32_t kw[kSubs][(Keys::kBytes + 3) / 4];
+#pragma unroll
+                for (int t = 0; t < kSubs; ++t) {
+                    acc[t] = float4v{0.f, 0.f, 0.f, 0.f};
+                    read_keys(k_rows, 16 * t + col, g * (GS * NB / 8) + quad * Keys::kBytes, kw[t]);
+                }
 #pragma unroll
                 for (int u = 0; u < Keys::kUnits; ++u) {
-                    const uint4 q4 = sh.q[g][u][lane];
-                    const uint32_t q16[4] = {q4.x, q4.y, q4.z, q4.w};
+                    const uint4v q4 = sh.q[g][u][lane];
+                    const uint32_t q16[4] = {q4[0], q4[1], q4[2], q4[3]};
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
+                    for (int t = 0; t < kSubs; ++t) {
                         uint32_t regs[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            uint32_t x = kw[t][g][Keys::word_of(u, r)];
+                            uint32_t x = kw[t][Keys::word_of(u, r)];
                             if constexpr (Keys::kHalf)
                                 x = (x & 0xffu) | (x >> 8) << 16;
-                            regs[r] = field<NB, true>(x, Keys::field_of(u, r));
+                            regs[r] = key_field<NB>(x, Keys::field_of(u, r));
                         }
                         acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(q16), acc[t], 0, 0, 0);
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < kSubs; ++t) {
                     const float4v r4 = *reinterpret_cast<const float4v *>(&meta[0][g][16 * t + 4 * quad]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         s[t][r] = fmaf(acc[t][r], r4[r], s[t][r]);
                 }
             }
-            // the keys' registers are free: the next tile's go there while the weights are formed
-            if (more) {
-                if ((tile & 31) == 31)
-                    pages = pages_from(now.at + kCacheStep);
-                next = where(now.at + kCacheStep, pages, tile + 1);
-                load_meta(next, next_meta);
-                load_keys(next, kw);
-            }
             if (!now.whole) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < kSubs; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (!counts(now, t, 4 * quad + r))
@@ -499,7 +615,7 @@ struct CacheAttention {
             // ---- weights
             float top = s[0][0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j)
+            for (int j = 1; j < 4 * kSubs; ++j)
                 top = fmaxf(top, s[j / 4][j % 4]);
             const float m_new = fmaxf(m2, column_max(top) * score_scale);
             const float ref = m_new == -INFINITY ? 0.0f : m_new;
@@ -508,68 +624,67 @@ struct CacheAttention {
             if (__any(alpha != 1.0f)) {
                 total *= alpha;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
+                for (int g = 0; g < NG; ++g)
                     z_sum[g] *= alpha;
 #pragma unroll
-                    for (int i = 0; i < kCodes; ++i)
-                        o[g][i] *= alpha;
-                }
-            }
-            float p[2][4];
+                for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                    for (int i = 0; i < kCodes; ++i)
+                        o[n][i] *= alpha;
+            }
+#pragma unroll
+            for (int t = 0; t < kSubs; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    p[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], score_scale, -ref));
-                    total += p[t][r];
+                    s[t][r] = __builtin_amdgcn_exp2f(fmaf(s[t][r], score_scale, -ref));
+                    total += s[t][r];
                 }
 
             // ---- the second product
+            uint32_t w16[NG][4];                                // weights, paired as value_field pairs tokens
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint32_t w16[4];
+                float4v w[2], z4[2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const float4v r4 = *reinterpret_cast<const float4v *>(&meta[1][g][16 * t + 4 * quad]);
-                    const float4v z4 = *reinterpret_cast<const float4v *>(&meta[2][g][16 * t + 4 * quad]);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const half2v h = __builtin_convertvector(
-                            float2v{p[t][2 * k] * r4[2 * k], p[t][2 * k + 1] * r4[2 * k + 1]}, half2v);
-                        // the zeros go with the rounded weights, as the codes do
-                        z_sum[g] = fmaf((float)h[0], z4[2 * k], z_sum[g]);
-                        z_sum[g] = fmaf((float)h[1], z4[2 * k + 1], z_sum[g]);
-                        __builtin_memcpy(&w16[2 * t + k], &h, 4);
-                    }
+                    w[t] = s[t] * *reinterpret_cast<const float4v *>(&meta[1][g][16 * t + 4 * quad]);
+                    z4[t] = *reinterpret_cast<const float4v *>(&meta[2][g][16 * t + 4 * quad]);
                 }
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    uint32_t x[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t lo = vw[2 * k][g][c / 2], hi = vw[2 * k + 1][g][c / 2];
-                        if constexpr (kValueBits < 32)
-                            x[k] = lo | hi << 16;
-                        else
-                            x[k] = __builtin_amdgcn_perm(hi, lo, c % 2 ? 0x07060302u : 0x05040100u);
-                        if constexpr (kValueBits == 4)
-                            x[k] >>= 4 * (col & 1);
-                    }
-#pragma unroll
-                    for (int f = 0; f < kPerChunk; ++f) {
-                        uint32_t regs[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            regs[k] = field<NB, false>(x[k], f);
-                        float4v &acc = o[g][c * kPerChunk + f];
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(w16), acc, 0, 0, 0);
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    // 8 bits: tokens (0, 2) and (1, 3) of either subtile; else the same one of both
+                    const int t0 = NB == 8 ? r / 2 : 0, t1 = NB == 8 ? r / 2 : 1;
+                    const int r0 = NB == 8 ? r % 2 : r, r1 = NB == 8 ? r % 2 + 2 : r;
+                    const half2v pair = __builtin_convertvector(float2v{w[t0][r0], w[t1][r1]}, half2v);
+                    // the zeros go with the rounded weights, as the codes do
+                    z_sum[g] = fmaf((float)pair[0], z4[t0][r0], z_sum[g]);
+                    z_sum[g] = fmaf((float)pair[1], z4[t1][r1], z_sum[g]);
+                    __builtin_memcpy(&w16[g][r], &pair, 4);
                 }
             }
-            if (more)
-                load_values(next, vw);
-            wave_lds_fence();       // the next tile's scales go where these were
-        }
+#pragma unroll
+            for (int n = 0; n < kBlocks; n += kReadBlocks) {
+                const int block = kReadBlocks == 1 ? n : n + col / 8;       // (96 dims of 2 bits: the last one twice)
+                const int byte = NB == 8 ? 16 * n + 8 * (col & 1) : 8 * (block < kBlocks ? block : kBlocks - 1);
+                const int2v x = read_transposed<NB>(row_byte(v_rows, v_row, byte));
+#pragma unroll
+                for (int h = 0; h < kReadBlocks && n + h < kBlocks; ++h)
+#pragma unroll
+                    for (int i = 0; i < kCodes; ++i) {
+                        uint32_t regs[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            regs[r] = NB == 8 ? value_field<NB>(x[r / 2], r % 2, 0) : value_field<NB>(x[h], r, i);
+                        o[n + h][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            operand(regs), operand(w16[(n + h) * kBlockDims / GS]), o[n + h][i], 0, 0, 0);
+                    }
+            }
+            wave_lds_fence();       // the next tile's rows and scales go where these were
+        };
+        for (int tile = 0; tile + 1 < tiles; ++tile)
+            step(tile, std::true_type{});
+        if (tiles > 0)
+            step(tiles - 1, std::false_type{});
 
         // ---- the four waves' sums joined
         total = column_sum(total);
@@ -578,7 +693,7 @@ struct CacheAttention {
             z_sum[g] = column_sum(z_sum[g]);
         if (quad == 0)
             sh.ml[wave][col] = float2{m2, total};
-        __syncthreads();            // also: no wave reads scales any more, whose place the sums take
+        __syncthreads();            // also: no wave reads rows or scales any more, whose place the sums take
         float m_all = -INFINITY, total_all = 0.0f;
 #pragma unroll
         for (int w = 0; w < kCacheWaves; ++w)
@@ -590,16 +705,15 @@ struct CacheAttention {
         const float own = __builtin_amdgcn_exp2f(m2 - ref);
         if (real) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
+            for (int n = 0; n < kBlocks; ++n) {
+                const int g = n * kBlockDims / GS;
                 const float back = own / v_unit[g];
+                float *to = &sh.sums[wave][col][n * kBlockDims + 4 * quad * kCodes];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int i = 0; i < kCodes; ++i) {
-                        const float unit = 0x1p24f / field_factor<NB, false>(i % kPerChunk);
-                        sh.sums[wave][col][g * GS + (4 * quad + r) * kCodes + i] =
-                            fmaf(o[g][i][r], unit, -z_sum[g]) * back;
-                    }
+                    for (int i = 0; i < kCodes; ++i)
+                        to[r * kCodes + i] = fmaf(o[n][i][r], 0x1p24f / dim_factor<NB>(i), -z_sum[g]) * back;
             }
         }
         __syncthreads();
@@ -631,7 +745,7 @@ struct CacheAttention {
                     a.lse[out_row] = cache_lse(m_row, total_row);
             }
         }
-        __syncthreads();            // the next segment's scales go where the sums were
+        __syncthreads();            // the next segment's rows go where the sums were
     }
 
     static __device__ __forceinline__ float pick(const float (&v)[NG], int g)
@@ -645,13 +759,14 @@ struct CacheAttention {
 
     __device__ __forceinline__ void run(Shared &sh)
     {
-        const int worker = blockIdx.y;
         int at = 0, start = 0, stop;
         bool cross = false;
         CacheSpan s;
         int slot = 0;
         if (a.workers == 0) {        // a sequence each
             b = worker;
+            if (b >= a.batch)
+                return;
             s = cache_span(a, b);
             stop = s.steps;
         } else {
@@ -668,8 +783,8 @@ struct CacheAttention {
         while (b < a.batch) {
             const int next = start + s.steps, upto = stop < next ? stop : next;
             first = s.first;
-            begin = s.base + (at - start) * kCacheStep;
-            end = upto < next ? s.base + (upto - start) * kCacheStep : s.length;
+            begin = s.base + (at - start) * kStep;
+            end = upto < next ? s.base + (upto - start) * kStep : s.length;
             segment(sh, slot, at == start && upto == next);
             if (!cross || upto == stop)
                 return;
@@ -682,7 +797,7 @@ struct CacheAttention {
 };
 
 template <int NB, int GS, int NG>
-__global__ __launch_bounds__(64 * kCacheWaves, cache_resident(GS * NG, GS)) void cache_attention_kernel(CacheAttentionArgs a)
+__global__ __launch_bounds__(64 * kCacheWaves, kCacheResident) void cache_attention_kernel(CacheAttentionArgs a)
 {
     __shared__ typename CacheAttention<NB, GS, NG>::Shared sh;
     CacheAttention<NB, GS, NG> attention(a);
@@ -692,7 +807,7 @@ __global__ __launch_bounds__(64 * kCacheWaves, cache_resident(GS * NG, GS)) void
 template <int NB, int GS, int NG>
 hipError_t launch_attention(const CacheAttentionArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)(a.workers + a.batch));
+    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)((a.workers + a.batch + 7) / 8 * 8));
     hipLaunchKernelGGL((cache_attention_kernel<NB, GS, NG>), grid, dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }

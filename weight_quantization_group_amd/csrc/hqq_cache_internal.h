@@ -43,13 +43,15 @@ struct CacheAttentionArgs {
     int32_t bf16;
 };
 
-// Tokens that a workgroup takes in one step: 4 waves with 32 each.
+// Tokens that a wave takes at a time, and a workgroup in a step of its waves.
 constexpr int kCacheTile = 32;
 constexpr int kCacheWaves = 4;
 constexpr int kCacheStep = kCacheTile * kCacheWaves;
-// Workgroups of the attention kernel that a CU holds at a time: what their registers
-// (which grow with dim and with its groups) leave room for.
-constexpr int cache_resident(int dim, int gs) { return dim <= 128 && dim / gs <= 2 ? 3 : 2; }
+// Workgroups of the attention kernel that a CU holds at a time: two, eight waves with some 5 KB
+// each on their way.  (More in flight is slower, whatever they compute: the loads alone of 64 x
+// 8192 tokens over 8 heads of 128 at 4 bits, 117 us by two, 130 by three, 159 by two with tiles of 64
+// tokens; with the arithmetic 125 by two, 139 by three, 152 by one.)
+constexpr int kCacheResident = 2;
 constexpr int kCus = 256;
 
 // Sequences of at most this many tokens are not split.

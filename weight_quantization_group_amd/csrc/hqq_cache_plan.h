@@ -32,13 +32,26 @@ __device__ __forceinline__ CacheSpan cache_span(const CacheAttentionArgs &a, int
     return CacheSpan{first, base, n, steps < 1 ? 1 : steps};
 }
 
-__device__ __forceinline__ int wave_sum(int v)
+// Adds another lane's value: CTRL as in DPP, into the rows of MASK
+template <int CTRL, int MASK>
+__device__ __forceinline__ int dpp_add(int v)
 {
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2)
-        v += __shfl_xor(v, o);
-    return __builtin_amdgcn_readfirstlane(v);
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, MASK, 0xF, false);
 }
+
+// Sums of lanes 0 to this one (row shifts by 1, 2, 4 and 8, then the rows' last lanes to the
+// rows behind them)
+__device__ __forceinline__ int wave_inclusive_sum(int v)
+{
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);
+    return dpp_add<0x143, 0xC>(v);
+}
+
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_inclusive_sum(v), 63); }
 
 // Runs of more steps than this cross sequences.
 constexpr int kCacheCross = 8;
@@ -91,12 +104,7 @@ struct CachePlan {
             if (b0)
                 s = b0 + lane < a.batch ? cache_span(a, b0 + lane) : CacheSpan{0, 0, 0, 0};
             const int steps = padded(s.steps);
-            int upto = steps;
-#pragma unroll
-            for (int o = 1; o < 64; o *= 2) {
-                const int up = __shfl_up(upto, o);
-                upto += lane >= o ? up : 0;
-            }
+            int upto = wave_inclusive_sum(steps);
             upto += before;
             const uint64_t behind = __ballot(at < upto);
             if (behind) {
