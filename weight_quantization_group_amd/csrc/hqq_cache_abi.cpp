@@ -126,7 +126,8 @@ CacheCodecArgs codec_args(const hqq_cache &c, const int64_t *slots, int64_t toke
     a.slot_count = c.pages * c.page_size;
     a.tokens = (int32_t)tokens;
     a.heads = c.heads;
-    a.rows = (int32_t)(tokens * c.heads);
+    a.rows = (int32_t)((tokens + kCacheCodecTokens - 1) / kCacheCodecTokens * kCacheCodecTokens * c.heads);
+    a.head_factor = ((uint64_t(1) << 36) + (uint64_t)c.heads - 1) / (uint64_t)c.heads;
     a.page_shift = log2_of(c.page_size);
     a.page_mask = c.page_size - 1;
     return a;

@@ -3,6 +3,9 @@
 //
 // A lane takes 8 consecutive values of a row (one 16-byte load or store), so a
 // group is 4 to 32 neighbouring lanes of one wave; blockIdx.y is the side (k, v).
+// Rows go by blocks of 16 tokens, then heads, then the block's tokens: consecutive
+// tokens of a head lie together in a page, so that codes and scales move by whole lines,
+// where token by token they would by pieces of 8 and 64 bytes.
 #include "hqq_cache_internal.h"
 
 namespace hqq {
@@ -43,7 +46,7 @@ struct Place {
     static constexpr int kLanes = D / 8;              // lanes of a row
     static constexpr int kRows = kBlock / kLanes;     // rows of a workgroup
     int chunk;
-    int32_t row, token, head;
+    int32_t token, head;
     int64_t cache_row;
     bool valid;
 
@@ -51,31 +54,83 @@ struct Place {
     {
         const int local = threadIdx.x / kLanes;
         chunk = threadIdx.x - local * kLanes;
-        row = (int32_t)blockIdx.x * kRows + local;
-        valid = local < kRows && row < a.rows;
+        const uint32_t row = blockIdx.x * kRows + local, line = row / kCacheCodecTokens;
+        // line / heads: the factor is rounded up from 2^36 / heads, line * 1023 < 2^36
+        const uint32_t block = (uint32_t)((line * a.head_factor) >> 36);
+        head = (int32_t)(line - block * (uint32_t)a.heads);
+        token = (int32_t)(block * kCacheCodecTokens + row % kCacheCodecTokens);
+        valid = local < kRows && token < a.tokens;
         cache_row = -1;
-        token = head = 0;
         if (!valid)
             return;
-        token = (int32_t)((uint32_t)row / (uint32_t)a.heads);
-        head = row - token * a.heads;
         const int64_t slot = a.slots[token];
         if (slot >= 0 && slot < a.slot_count)
             cache_row = (((slot >> a.page_shift) * a.heads + head) << a.page_shift) + (slot & a.page_mask);
     }
+
+    __device__ __forceinline__ int64_t hat_at(const CacheCodecArgs &a) const
+    {
+        return ((int64_t)token * a.heads + head) * D + chunk * 8;
+    }
 };
 
-// The values (code - zero) / scale in fp32, rounded once
+// Whether the quotients (code - zero) / scale, their remainders and 1 / scale stay clear of
+// the ends of fp32's range
+__device__ __forceinline__ bool moderate(float scale, float zero)
+{
+    return scale > 0x1p-60f && scale < 0x1p60f && fabsf(zero) < 0x1p60f && (zero == 0.0f || fabsf(zero) > 0x1p-60f);
+}
+
+// The values (code - zero) / scale in fp32, rounded once.  Where all the wave's groups are
+// moderate, the division is a product with the correctly rounded 1 / scale and two
+// corrections by the exact remainder: the first makes the quotient faithful, the second
+// correctly rounded (Markstein's theorem), 5 operations for the division's 10.
 template <bool BF>
 __device__ __forceinline__ uint4 values16(const float (&code)[8], float scale, float zero)
 {
     uint16_t v[8];
+    if (__all(moderate(scale, zero))) {
+        const float inv = 1.0f / scale;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = narrow<BF>((code[j] - zero) / scale);
+        for (int j = 0; j < 8; ++j) {
+            const float x = code[j] - zero;
+            float q = x * inv;
+            q = fmaf(fmaf(-scale, q, x), inv, q);
+            q = fmaf(fmaf(-scale, q, x), inv, q);
+            v[j] = narrow<BF>(q);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = narrow<BF>((code[j] - zero) / scale);
+    }
     uint4 r;
     __builtin_memcpy(&r, v, 16);
     return r;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __uint_as_float(__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+
+// The smallest of v over the LANES neighbouring lanes of a group (the largest: of -v): the lanes of
+// a pair, of 4, of 8 and of 16 exchanged or mirrored, then rows of 16 swapped
+template <int LANES>
+__device__ __forceinline__ float group_min(float v)
+{
+    v = fminf(v, dpp<0xB1>(v));
+    v = fminf(v, dpp<0x4E>(v));
+    if constexpr (LANES >= 8)
+        v = fminf(v, dpp<0x141>(v));
+    if constexpr (LANES >= 16)
+        v = fminf(v, dpp<0x140>(v));
+    if constexpr (LANES >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = fminf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    return v;
 }
 
 template <int NB, int D, int GS, bool BF>
@@ -103,14 +158,11 @@ __global__ __launch_bounds__(kBlock) void cache_write_kernel(CacheCodecArgs a)
         lo = fminf(lo, x[j]);
         hi = fmaxf(hi, x[j]);
     }
-#pragma unroll
-    for (int o = 1; o < GS / 8; o *= 2) {
-        lo = fminf(lo, __shfl_xor(lo, o));
-        hi = fmaxf(hi, __shfl_xor(hi, o));
-    }
+    lo = group_min<GS / 8>(lo);
+    hi = -group_min<GS / 8>(-hi);
     if (!p.valid)
         return;
-    uint16_t *hat = a.hat[side] ? a.hat[side] + (int64_t)p.row * D + p.chunk * 8 : nullptr;
+    uint16_t *hat = a.hat[side] ? a.hat[side] + p.hat_at(a) : nullptr;
     if (p.cache_row < 0) {
         if (hat)
             *reinterpret_cast<uint4 *>(hat) = uint4{0, 0, 0, 0};
@@ -151,7 +203,7 @@ __global__ __launch_bounds__(kBlock) void cache_read_kernel(CacheCodecArgs a)
     const Place<D> p(a);
     if (!p.valid)
         return;
-    uint4 *dst = reinterpret_cast<uint4 *>(a.hat[side] + (int64_t)p.row * D + p.chunk * 8);
+    uint4 *dst = reinterpret_cast<uint4 *>(a.hat[side] + p.hat_at(a));
     if (p.cache_row < 0) {
         *dst = uint4{0, 0, 0, 0};
         return;

@@ -9,6 +9,9 @@
 
 namespace hqq {
 
+// Tokens of a block of rows in the write and read kernels.
+constexpr int kCacheCodecTokens = 16;
+
 // Arguments of the write and read kernels, either side's at [0] (k) and [1] (v).
 struct CacheCodecArgs {
     uint32_t *packed[2];
@@ -18,7 +21,9 @@ struct CacheCodecArgs {
     uint16_t *hat[2];                // read's outputs; write: null, or the values written
     const int64_t *slots;
     int64_t slot_count;              // pages * page_size
-    int32_t tokens, heads, rows;     // rows = tokens * heads
+    int32_t tokens, heads;
+    int32_t rows;                    // heads * tokens, the tokens rounded up to whole blocks
+    uint64_t head_factor;            // 2^36 / heads, rounded up
     int32_t page_shift, page_mask;
 };
 
