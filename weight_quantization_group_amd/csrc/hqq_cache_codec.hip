@@ -13,6 +13,8 @@ namespace {
 
 constexpr int kBlock = 256;
 
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+
 template <bool BF>
 __device__ __forceinline__ float widen(uint16_t v)
 {
@@ -50,22 +52,27 @@ struct Place {
     int64_t cache_row;
     bool valid;
 
-    __device__ __forceinline__ explicit Place(const CacheCodecArgs &a)
+    __device__ __forceinline__ Place(const CacheCodecArgs &a, uint32_t group) : Place(a, group, -1)
     {
-        const int local = threadIdx.x / kLanes;
-        chunk = threadIdx.x - local * kLanes;
-        const uint32_t row = blockIdx.x * kRows + local, line = row / kCacheCodecTokens;
-        // line / heads: the factor is rounded up from 2^36 / heads, line * 1023 < 2^36
-        const uint32_t block = (uint32_t)((line * a.head_factor) >> 36);
-        head = (int32_t)(line - block * (uint32_t)a.heads);
-        token = (int32_t)(block * kCacheCodecTokens + row % kCacheCodecTokens);
-        valid = local < kRows && token < a.tokens;
-        cache_row = -1;
         if (!valid)
             return;
         const int64_t slot = a.slots[token];
         if (slot >= 0 && slot < a.slot_count)
             cache_row = (((slot >> a.page_shift) * a.heads + head) << a.page_shift) + (slot & a.page_mask);
+    }
+
+    // the same again, the cache's row known
+    __device__ __forceinline__ Place(const CacheCodecArgs &a, uint32_t group, int64_t known)
+    {
+        const int local = threadIdx.x / kLanes;
+        chunk = threadIdx.x - local * kLanes;
+        const uint32_t row = group * kRows + local, line = row / kCacheCodecTokens;
+        // line / heads: the factor is rounded up from 2^36 / heads, line * 1023 < 2^36
+        const uint32_t block = (uint32_t)((line * a.head_factor) >> 36);
+        head = (int32_t)(line - block * (uint32_t)a.heads);
+        token = (int32_t)(block * kCacheCodecTokens + row % kCacheCodecTokens);
+        valid = local < kRows && token < a.tokens;
+        cache_row = known;
     }
 
     __device__ __forceinline__ int64_t hat_at(const CacheCodecArgs &a) const
@@ -86,7 +93,7 @@ __device__ __forceinline__ bool moderate(float scale, float zero)
 // corrections by the exact remainder: the first makes the quotient faithful, the second
 // correctly rounded (Markstein's theorem), 5 operations for the division's 10.
 template <bool BF>
-__device__ __forceinline__ uint4 values16(const float (&code)[8], float scale, float zero)
+__device__ __forceinline__ uint4v values16(const float (&code)[8], float scale, float zero)
 {
     uint16_t v[8];
     if (__all(moderate(scale, zero))) {
@@ -104,7 +111,7 @@ __device__ __forceinline__ uint4 values16(const float (&code)[8], float scale, f
         for (int j = 0; j < 8; ++j)
             v[j] = narrow<BF>((code[j] - zero) / scale);
     }
-    uint4 r;
+    uint4v r;
     __builtin_memcpy(&r, v, 16);
     return r;
 }
@@ -133,109 +140,142 @@ __device__ __forceinline__ float group_min(float v)
     return v;
 }
 
-template <int NB, int D, int GS, bool BF>
+// ROWS groups of kRows rows per workgroup, whose loads go out together
+template <int NB, int D, int GS, bool BF, int ROWS>
 __global__ __launch_bounds__(kBlock) void cache_write_kernel(CacheCodecArgs a)
 {
     const int side = blockIdx.y;
-    const Place<D> p(a);
-    float x[8];
-    if (p.valid) {
-        const uint16_t *src = a.x[side] + p.token * a.token_stride[side] + p.head * a.head_stride[side] + p.chunk * 8;
-        const uint4 raw = *reinterpret_cast<const uint4 *>(src);
+    uint4 raw[ROWS];
+    int64_t cache_row[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const Place<D> p(a, blockIdx.x * ROWS + i);
+        cache_row[i] = p.cache_row;
+        raw[i] = uint4{0, 0, 0, 0};
+        if (p.valid)
+            raw[i] = *reinterpret_cast<const uint4 *>(a.x[side] + p.token * a.token_stride[side] +
+                                                      p.head * a.head_stride[side] + p.chunk * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const Place<D> p(a, blockIdx.x * ROWS + i, cache_row[i]);
         uint16_t h[8];
-        __builtin_memcpy(h, &raw, 16);
+        __builtin_memcpy(h, &raw[i], 16);
+        float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             x[j] = widen<BF>(h[j]);
-    } else {
+        float lo = x[0], hi = x[0];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = 0.0f;
-    }
-    float lo = x[0], hi = x[0];
+        for (int j = 1; j < 8; ++j) {
+            lo = fminf(lo, x[j]);
+            hi = fmaxf(hi, x[j]);
+        }
+        lo = group_min<GS / 8>(lo);
+        hi = -group_min<GS / 8>(-hi);
+        constexpr float qmax = (float)((1 << NB) - 1);
+        const float range = hi - lo;
+        const float scale = range == 0.0f ? 1.0f : qmax / range;
+        const float zero = -(lo * scale);
+        float code[8];
+        uint64_t bits = 0;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) {
-        lo = fminf(lo, x[j]);
-        hi = fmaxf(hi, x[j]);
+        for (int j = 0; j < 8; ++j) {
+            code[j] = fminf(fmaxf(rintf(fmaf(x[j], scale, zero)), 0.0f), qmax);
+            bits |= (uint64_t)(uint32_t)code[j] << (NB * j);
+        }
+        if (p.cache_row >= 0) {
+            char *dst = (char *)a.packed[side] + p.cache_row * (D * NB / 8) + p.chunk * NB;
+            if constexpr (NB == 8)
+                *reinterpret_cast<uint2 *>(dst) = uint2{(uint32_t)bits, (uint32_t)(bits >> 32)};
+            else if constexpr (NB == 4)
+                *reinterpret_cast<uint32_t *>(dst) = (uint32_t)bits;
+            else
+                *reinterpret_cast<uint16_t *>(dst) = (uint16_t)bits;
+            if (p.chunk % (GS / 8) == 0) {
+                const int64_t g = p.cache_row * (D / GS) + p.chunk / (GS / 8);
+                a.scale[side][g] = scale;
+                a.zero[side][g] = zero;
+            }
+        }
+        if (a.hat[side]) {
+            const uint4v values = values16<BF>(code, scale, zero);
+            if (p.valid)
+                *reinterpret_cast<uint4v *>(a.hat[side] + p.hat_at(a)) = p.cache_row >= 0 ? values : uint4v{0, 0, 0, 0};
+        }
     }
-    lo = group_min<GS / 8>(lo);
-    hi = -group_min<GS / 8>(-hi);
-    if (!p.valid)
-        return;
-    uint16_t *hat = a.hat[side] ? a.hat[side] + p.hat_at(a) : nullptr;
-    if (p.cache_row < 0) {
-        if (hat)
-            *reinterpret_cast<uint4 *>(hat) = uint4{0, 0, 0, 0};
-        return;
-    }
-    constexpr float qmax = (float)((1 << NB) - 1);
-    const float range = hi - lo;
-    const float scale = range == 0.0f ? 1.0f : qmax / range;
-    const float zero = -(lo * scale);
-    float code[8];
-    uint64_t bits = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        code[j] = fminf(fmaxf(rintf(fmaf(x[j], scale, zero)), 0.0f), qmax);
-        bits |= (uint64_t)(uint32_t)code[j] << (NB * j);
-    }
-    constexpr int kRowBytes = D * NB / 8;
-    char *dst = (char *)a.packed[side] + p.cache_row * kRowBytes + p.chunk * NB;
-    if constexpr (NB == 8)
-        *reinterpret_cast<uint2 *>(dst) = uint2{(uint32_t)bits, (uint32_t)(bits >> 32)};
-    else if constexpr (NB == 4)
-        *reinterpret_cast<uint32_t *>(dst) = (uint32_t)bits;
-    else
-        *reinterpret_cast<uint16_t *>(dst) = (uint16_t)bits;
-    if (p.chunk % (GS / 8) == 0) {
-        const int64_t g = p.cache_row * (D / GS) + p.chunk / (GS / 8);
-        a.scale[side][g] = scale;
-        a.zero[side][g] = zero;
-    }
-    if (hat)
-        *reinterpret_cast<uint4 *>(hat) = values16<BF>(code, scale, zero);
 }
 
-template <int NB, int D, int GS, bool BF>
+template <int NB, int D, int GS, bool BF, int ROWS>
 __global__ __launch_bounds__(kBlock) void cache_read_kernel(CacheCodecArgs a)
 {
     const int side = blockIdx.y;
-    const Place<D> p(a);
-    if (!p.valid)
-        return;
-    uint4 *dst = reinterpret_cast<uint4 *>(a.hat[side] + p.hat_at(a));
-    if (p.cache_row < 0) {
-        *dst = uint4{0, 0, 0, 0};
-        return;
-    }
-    constexpr int kRowBytes = D * NB / 8;
-    const char *src = (const char *)a.packed[side] + p.cache_row * kRowBytes + p.chunk * NB;
-    uint64_t bits;
-    if constexpr (NB == 8) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(src);
-        bits = (uint64_t)w.y << 32 | w.x;
-    } else if constexpr (NB == 4) {
-        bits = *reinterpret_cast<const uint32_t *>(src);
-    } else {
-        bits = *reinterpret_cast<const uint16_t *>(src);
-    }
-    const int64_t g = p.cache_row * (D / GS) + p.chunk / (GS / 8);
-    const float scale = a.scale[side][g], zero = a.zero[side][g];
-    float code[8];
+    uint64_t bits[ROWS];
+    float scale[ROWS], zero[ROWS];
+    int64_t cache_row[ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        code[j] = (float)(uint32_t)(bits >> (NB * j) & ((1u << NB) - 1));
-    *dst = values16<BF>(code, scale, zero);
+    for (int i = 0; i < ROWS; ++i) {
+        const Place<D> p(a, blockIdx.x * ROWS + i);
+        cache_row[i] = p.cache_row;
+        bits[i] = 0;
+        scale[i] = 1.0f;
+        zero[i] = 0.0f;
+        if (p.cache_row >= 0) {
+            const char *src = (const char *)a.packed[side] + p.cache_row * (D * NB / 8) + p.chunk * NB;
+            if constexpr (NB == 8) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                bits[i] = (uint64_t)w.y << 32 | w.x;
+            } else if constexpr (NB == 4) {
+                bits[i] = *reinterpret_cast<const uint32_t *>(src);
+            } else {
+                bits[i] = *reinterpret_cast<const uint16_t *>(src);
+            }
+            const int64_t g = p.cache_row * (D / GS) + p.chunk / (GS / 8);
+            scale[i] = a.scale[side][g];
+            zero[i] = a.zero[side][g];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const Place<D> p(a, blockIdx.x * ROWS + i, cache_row[i]);
+        float code[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            code[j] = (float)(uint32_t)(bits[i] >> (NB * j) & ((1u << NB) - 1));
+        const uint4v values = values16<BF>(code, scale[i], zero[i]);
+        uint4v *to = reinterpret_cast<uint4v *>(a.hat[side] + p.hat_at(a));
+        if (p.valid) {
+            if constexpr (ROWS > 1)          // more than the L2s hold: past them
+                __builtin_nontemporal_store(values, to);
+            else
+                *to = values;
+        }
+    }
+}
+
+// Groups of rows per workgroup: the read waits for slots, then codes, and has little to do with
+// either, so large ones take several at a time (32768 tokens of 8 x 128 at 4 bits 43 us by 4, 56 by 1,
+// 29 by 4 with stores past the caches); the write is no faster so.
+constexpr int kReadRows = 4;
+constexpr int64_t kReadLarge = 65536;
+
+template <int D, int ROWS>
+dim3 grid_of(const CacheCodecArgs &a)
+{
+    constexpr int kRows = Place<D>::kRows * ROWS;
+    return dim3((unsigned)((a.rows + kRows - 1) / kRows), 2);
 }
 
 template <int NB, int D, int GS, bool BF>
 hipError_t launch(bool write, const CacheCodecArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.rows + Place<D>::kRows - 1) / Place<D>::kRows), 2);
     if (write)
-        hipLaunchKernelGGL((cache_write_kernel<NB, D, GS, BF>), grid, dim3(kBlock), 0, s, a);
+        hipLaunchKernelGGL((cache_write_kernel<NB, D, GS, BF, 1>), (grid_of<D, 1>(a)), dim3(kBlock), 0, s, a);
+    else if (a.rows >= kReadLarge)
+        hipLaunchKernelGGL((cache_read_kernel<NB, D, GS, BF, kReadRows>), (grid_of<D, kReadRows>(a)), dim3(kBlock),
+                           0, s, a);
     else
-        hipLaunchKernelGGL((cache_read_kernel<NB, D, GS, BF>), grid, dim3(kBlock), 0, s, a);
+        hipLaunchKernelGGL((cache_read_kernel<NB, D, GS, BF, 1>), (grid_of<D, 1>(a)), dim3(kBlock), 0, s, a);
     return hipGetLastError();
 }
 
