@@ -148,12 +148,12 @@ def test_a_call_of_nothing_needs_no_pointers(lib):
 
 
 def test_workspace(w, lib):
-    """None where no sequence can exceed 1024 tokens; else dim sums and two statistics per query head and
+    """None where no sequence can exceed 768 tokens; else dim sums and two statistics per query head and
     segment: as many segments as runs (the chip's workgroups per key-value head) and sequences."""
     def need(batch, q_heads, width, **kw):
         return lib.hqq_cache_attention_workspace(ctypes.byref(cache(**kw)), batch, q_heads, width)
 
-    assert need(3, 4, 64) == 0 and need(3, 4, 65) > 0 and need(0, 4, 65) == 0
+    assert need(3, 4, 48) == 0 and need(3, 4, 49) > 0 and need(0, 4, 49) == 0
     sizes = {need(b, 4, 100) for b in (1, 2, 3)}
     assert len(sizes) == 3 and max(sizes) - min(sizes) <= 2 * (4 * 128 * 4 + 4 * 8) + 512
     segments = (need(3, 4, 100) // (4 * 128 * 4 + 4 * 8))

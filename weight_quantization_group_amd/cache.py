@@ -194,6 +194,11 @@ def _rows(t, name: str, cache: QuantizedCache):
     return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0, shape
 
 
+def _pair(t):
+    # (empty_like costs the host half of what empty does)
+    return t, torch.empty_like(t)
+
+
 def _call(cache: QuantizedCache, f, *args) -> None:
     """Run the library's call f on the cache's device and its current stream."""
     index = cache._index
@@ -223,7 +228,7 @@ def hqq_cache_write(cache: QuantizedCache, K: torch.Tensor, V: torch.Tensor, slo
     at = _tensor(slots, "slots", _I64, (tokens,), cache._index)
     hat = to_k = to_v = None
     if values:
-        hat = (torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device))
+        hat = _pair(torch.empty_like(K, memory_format=torch.contiguous_format))
         to_k, to_v = hat[0].data_ptr(), hat[1].data_ptr()
     _call(cache, cache._lib.hqq_cache_write, pk, k_token, k_head, pv, v_token, v_head, tokens, at, _DT[dtype], to_k, to_v)
     return hat
@@ -236,13 +241,18 @@ def hqq_cache_read(cache: QuantizedCache, slots: torch.Tensor, dtype=torch.float
     at = _tensor(slots, "slots", _I64, (tokens,), cache._index)
     shape = (tokens, cache.heads, cache.dim)
     if out is None:
-        out = (torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device))
-    K, V = out
-    if not isinstance(K, torch.Tensor) or K.dtype not in _DT:
-        raise TypeError("out must be float16 or bfloat16 tensors, dtype one of these")
-    _call(cache, cache._lib.hqq_cache_read, at, tokens, _DT[K.dtype], _tensor(K, "out K", (K.dtype,), shape, cache._index),
-          _tensor(V, "out V", (K.dtype,), shape, cache._index))
-    return K, V
+        if dtype not in _DT:
+            raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+        out = _pair(torch.empty(shape, dtype=dtype, device=cache.device))
+        pk, pv = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        K, V = out
+        dtype = K.dtype if isinstance(K, torch.Tensor) else None
+        if dtype not in _DT:
+            raise TypeError("out must be float16 or bfloat16 tensors")
+        pk, pv = _tensor(K, "out K", (dtype,), shape, cache._index), _tensor(V, "out V", (dtype,), shape, cache._index)
+    _call(cache, cache._lib.hqq_cache_read, at, tokens, _DT[dtype], pk, pv)
+    return tuple(out)
 
 
 def hqq_cache_attention(cache: QuantizedCache, Q: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
@@ -264,7 +274,7 @@ def hqq_cache_attention(cache: QuantizedCache, Q: torch.Tensor, table: torch.Ten
     pl = _tensor(lengths, "lengths", _I32, (batch,), index)
     need = _bytes(cache, (batch, q_heads, width))
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty_like(Q, memory_format=torch.contiguous_format)
         po = out.data_ptr()
     else:
         po = _tensor(out, "out", (dtype,), shape, index)

@@ -104,6 +104,9 @@ __device__ __forceinline__ uint4v values16(const float (&code)[8], float scale, 
             float q = x * inv;
             q = fmaf(fmaf(-scale, q, x), inv, q);
             q = fmaf(fmaf(-scale, q, x), inv, q);
+            // the quotient is rounded to fp32 first, as the division's is: left to itself the compiler
+            // takes the last step and the rounding to fp16 for one operation, with one rounding
+            asm("" : "+v"(q));
             v[j] = narrow<BF>(q);
         }
     } else {

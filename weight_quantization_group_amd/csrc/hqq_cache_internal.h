@@ -59,8 +59,10 @@ constexpr int kCacheStep = kCacheTile * kCacheWaves;
 constexpr int kCacheResident = 2;
 constexpr int kCus = 256;
 
-// Sequences of at most this many tokens are not split.
-constexpr int kCacheWhole = 1024;
+// Sequences of at most this many tokens are not split: a step more costs a workgroup 1 us, the
+// join's launch 2.5 us and the host 4.  (One sequence of 512 tokens 9.1 us whole, 10.6 split, of
+// 1024 13.2 and 10.6.)
+constexpr int kCacheWhole = 768;
 
 hipError_t launch_cache_write(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
 hipError_t launch_cache_read(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
