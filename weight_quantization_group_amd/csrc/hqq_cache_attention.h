@@ -129,11 +129,12 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[(N + 3) / 4], const cha
     }
 }
 
-__device__ __forceinline__ float widen16(uint16_t v, bool bf16)
+template <bool BF>
+__device__ __forceinline__ float widen16(uint16_t v)
 {
     _Float16 h;
     __builtin_memcpy(&h, &v, 2);
-    return bf16 ? __uint_as_float((uint32_t)v << 16) : (float)h;
+    return BF ? __uint_as_float((uint32_t)v << 16) : (float)h;
 }
 
 // the values of the other half of the wave, and of the other row of 16 in the same half, beside
@@ -203,7 +204,7 @@ __device__ __forceinline__ int2v read_transposed(const char *lds)
         return __builtin_amdgcn_ds_read_tr4_b64_v2i32(p);
 }
 
-template <int NB, int GS, int NG>
+template <int NB, int GS, int NG, bool BF>
 struct CacheAttention {
     static constexpr int D = GS * NG;
     static constexpr int kRowBytes = D * NB / 8;
@@ -419,7 +420,7 @@ struct CacheAttention {
                     __builtin_memcpy(h, &raw, 16);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        q[g][i + j] = widen16(h[j], a.bf16);
+                        q[g][i + j] = widen16<BF>(h[j]);
                         top = fmaxf(top, fabsf(q[g][i + j]));
                     }
                 }
@@ -641,7 +642,10 @@ struct CacheAttention {
                 }
 
             // ---- the second product
-            uint32_t w16[NG][4];                                // weights, paired as value_field pairs tokens
+            // Weights, paired as value_field pairs tokens.  11 bits of them make an error of the size of fp16
+            // outputs' own rounding (0.00029 of the result beside 0.00019), so there the rest of each
+            // weight is a second operand (0.00019; 32 ragged 7B sequences 77 -> 81 us); bf16's own drowns it.
+            uint32_t w16[NG][4], rest16[NG][4];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 float4v w[2], z4[2];
@@ -655,11 +659,20 @@ struct CacheAttention {
                     // 8 bits: tokens (0, 2) and (1, 3) of either subtile; else the same one of both
                     const int t0 = NB == 8 ? r / 2 : 0, t1 = NB == 8 ? r / 2 : 1;
                     const int r0 = NB == 8 ? r % 2 : r, r1 = NB == 8 ? r % 2 + 2 : r;
-                    const half2v pair = __builtin_convertvector(float2v{w[t0][r0], w[t1][r1]}, half2v);
-                    // the zeros go with the rounded weights, as the codes do
-                    z_sum[g] = fmaf((float)pair[0], z4[t0][r0], z_sum[g]);
-                    z_sum[g] = fmaf((float)pair[1], z4[t1][r1], z_sum[g]);
+                    const float2v both{w[t0][r0], w[t1][r1]};
+                    const half2v pair = __builtin_convertvector(both, half2v);
                     __builtin_memcpy(&w16[g][r], &pair, 4);
+                    if constexpr (BF) {
+                        // the zeros go with the rounded weights, as the codes do
+                        z_sum[g] = fmaf((float)pair[0], z4[t0][r0], z_sum[g]);
+                        z_sum[g] = fmaf((float)pair[1], z4[t1][r1], z_sum[g]);
+                    } else {
+                        const half2v rest =
+                            __builtin_convertvector(float2v{both[0] - (float)pair[0], both[1] - (float)pair[1]}, half2v);
+                        __builtin_memcpy(&rest16[g][r], &rest, 4);
+                        z_sum[g] = fmaf(both[0], z4[t0][r0], z_sum[g]);
+                        z_sum[g] = fmaf(both[1], z4[t1][r1], z_sum[g]);
+                    }
                 }
             }
 #pragma unroll
@@ -675,8 +688,11 @@ struct CacheAttention {
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             regs[r] = NB == 8 ? value_field<NB>(x[r / 2], r % 2, 0) : value_field<NB>(x[h], r, i);
-                        o[n + h][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            operand(regs), operand(w16[(n + h) * kBlockDims / GS]), o[n + h][i], 0, 0, 0);
+                        const int g = (n + h) * kBlockDims / GS;
+                        float4v &acc = o[n + h][i];
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(w16[g]), acc, 0, 0, 0);
+                        if constexpr (!BF)
+                            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(rest16[g]), acc, 0, 0, 0);
                     }
             }
             wave_lds_fence();       // the next tile's rows and scales go where these were
@@ -734,7 +750,7 @@ struct CacheAttention {
                 for (int w = 0; w < kCacheWaves; ++w)
                     v += *reinterpret_cast<const float4v *>(&sh.sums[w][h][d]);
                 if (whole_sequence)
-                    *reinterpret_cast<uint2 *>(a.out + out_row * D + d) = cache_round4(v * inv, a.bf16);
+                    *reinterpret_cast<uint2 *>(a.out + out_row * D + d) = cache_round4<BF>(v * inv);
                 else
                     *reinterpret_cast<float4v *>(a.part + part_row * D + d) = v;
             }
@@ -796,36 +812,36 @@ struct CacheAttention {
     }
 };
 
-template <int NB, int GS, int NG>
+template <int NB, int GS, int NG, bool BF>
 __global__ __launch_bounds__(64 * kCacheWaves, kCacheResident) void cache_attention_kernel(CacheAttentionArgs a)
 {
-    __shared__ typename CacheAttention<NB, GS, NG>::Shared sh;
-    CacheAttention<NB, GS, NG> attention(a);
+    __shared__ typename CacheAttention<NB, GS, NG, BF>::Shared sh;
+    CacheAttention<NB, GS, NG, BF> attention(a);
     attention.run(sh);
 }
 
-template <int NB, int GS, int NG>
+template <int NB, int GS, int NG, bool BF>
 hipError_t launch_attention(const CacheAttentionArgs &a, hipStream_t s)
 {
     const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)((a.workers + a.batch + 7) / 8 * 8));
-    hipLaunchKernelGGL((cache_attention_kernel<NB, GS, NG>), grid, dim3(64 * kCacheWaves), 0, s, a);
+    hipLaunchKernelGGL((cache_attention_kernel<NB, GS, NG, BF>), grid, dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }
 
-template <int NB>
+template <int NB, bool BF>
 hipError_t launch_cache_attention(int dim, int gs, const CacheAttentionArgs &a, hipStream_t s)
 {
     switch (dim * 1024 + gs) {
-    case 64 * 1024 + 32: return launch_attention<NB, 32, 2>(a, s);
-    case 64 * 1024 + 64: return launch_attention<NB, 64, 1>(a, s);
-    case 96 * 1024 + 32: return launch_attention<NB, 32, 3>(a, s);
-    case 128 * 1024 + 32: return launch_attention<NB, 32, 4>(a, s);
-    case 128 * 1024 + 64: return launch_attention<NB, 64, 2>(a, s);
-    case 128 * 1024 + 128: return launch_attention<NB, 128, 1>(a, s);
-    case 192 * 1024 + 64: return launch_attention<NB, 64, 3>(a, s);
-    case 256 * 1024 + 64: return launch_attention<NB, 64, 4>(a, s);
-    case 256 * 1024 + 128: return launch_attention<NB, 128, 2>(a, s);
-    case 256 * 1024 + 256: return launch_attention<NB, 256, 1>(a, s);
+    case 64 * 1024 + 32: return launch_attention<NB, 32, 2, BF>(a, s);
+    case 64 * 1024 + 64: return launch_attention<NB, 64, 1, BF>(a, s);
+    case 96 * 1024 + 32: return launch_attention<NB, 32, 3, BF>(a, s);
+    case 128 * 1024 + 32: return launch_attention<NB, 32, 4, BF>(a, s);
+    case 128 * 1024 + 64: return launch_attention<NB, 64, 2, BF>(a, s);
+    case 128 * 1024 + 128: return launch_attention<NB, 128, 1, BF>(a, s);
+    case 192 * 1024 + 64: return launch_attention<NB, 64, 3, BF>(a, s);
+    case 256 * 1024 + 64: return launch_attention<NB, 64, 4, BF>(a, s);
+    case 256 * 1024 + 128: return launch_attention<NB, 128, 2, BF>(a, s);
+    case 256 * 1024 + 256: return launch_attention<NB, 256, 1, BF>(a, s);
     }
     return hipErrorInvalidValue;
 }

@@ -5,7 +5,8 @@ namespace hqq {
 
 hipError_t launch_cache_attention_b8(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s)
 {
-    return launch_cache_attention<8>(dim, group_size, a, s);
+    return a.bf16 ? launch_cache_attention<8, true>(dim, group_size, a, s)
+                  : launch_cache_attention<8, false>(dim, group_size, a, s);
 }
 
 }  // namespace hqq

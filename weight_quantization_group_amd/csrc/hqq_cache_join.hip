@@ -63,7 +63,8 @@ __global__ __launch_bounds__(kJoinBlock) void cache_join_kernel(CacheAttentionAr
     for (int i = 1; i < kAtOnce; ++i)
         v += sums[local][i][at];
     const int64_t row = (int64_t)b * a.q_heads + head;
-    *reinterpret_cast<uint2 *>(a.out + row * D + 4 * at) = cache_round4(v * cache_inverse(total), a.bf16);
+    *reinterpret_cast<uint2 *>(a.out + row * D + 4 * at) =
+        a.bf16 ? cache_round4<true>(v * cache_inverse(total)) : cache_round4<false>(v * cache_inverse(total));
     if (at == 0 && a.lse)
         a.lse[row] = cache_lse(m, total);
 }

@@ -124,12 +124,13 @@ struct CachePlan {
     }
 };
 
-__device__ __forceinline__ uint2 cache_round4(float4v v, bool bf16)
+template <bool BF>
+__device__ __forceinline__ uint2 cache_round4(float4v v)
 {
     uint16_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (bf16) {
+        if constexpr (BF) {
             const __bf16 h = (__bf16)v[i];
             __builtin_memcpy(&u[i], &h, 2);
         } else {
