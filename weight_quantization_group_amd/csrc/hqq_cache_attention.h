@@ -211,6 +211,8 @@ struct CacheAttention {
     typedef KeyOrder<NB, GS> Keys;
     static constexpr int kTile = kCacheTile, kStep = kCacheStep;
     static constexpr int kSubs = kTile / 16;                    // subtiles: 16 consecutive rows of a page
+    // rows in LDS an odd number of 16-byte pieces apart: 8 of them, at one place each, cover the banks
+    static constexpr int kRowPitch = kRowBytes % 32 == 0 ? kRowBytes + 16 : kRowBytes;
     static constexpr int kPieces = (kSubs * kRowBytes + 63) / 64;       // 16-byte pieces per lane and tile
     // a tile's scales over the lanes: token col, and 4 of (subtile, group) along the quads
     static constexpr int kGroups = NG == 3 ? 4 : NG;
@@ -227,7 +229,7 @@ struct CacheAttention {
         union {
             struct {
                 uint4v q[NG][Keys::kUnits][64];                 // operands of the first product
-                uint4v rows[kCacheWaves][2][kSubs * kRowBytes]; // a tile's rows of k and of v
+                uint4v rows[kCacheWaves][2][kTile * kRowPitch / 16];    // a tile's rows of k and of v
                 float meta[kCacheWaves][3][NG][kTile];          // r of k, scaled r of v, z of v
             };
             float sums[kCacheWaves][16][kPitch];
@@ -237,9 +239,8 @@ struct CacheAttention {
 
     struct Where {
         int at;
+        int there;                                              // bit t: subtile t's page is there
         int64_t row[kSubs];
-        bool there[kSubs];
-        bool whole;                                             // all the tile's tokens count
     };
     struct Loads {
         uint4v k[kPieces], v[kPieces];
@@ -279,33 +280,30 @@ struct CacheAttention {
     {
         Where w;
         w.at = at;
-        w.whole = at >= first && at + kTile <= end;
+        w.there = 0;
 #pragma unroll
         for (int t = 0; t < kSubs; ++t) {
             const int page = __builtin_amdgcn_readlane(pages, (kSubs * tile + t) & 63);
-            w.there[t] = page >= 0 && page < a.pages;
-            w.whole = w.whole && w.there[t];
-            w.row[t] = (((int64_t)(w.there[t] ? page : 0) * a.heads + head) << a.page_shift) +
-                       ((at + 16 * t) & a.page_mask);
+            const bool there = (uint32_t)page < (uint32_t)a.pages;
+            w.there |= there << t;
+            w.row[t] = (((int64_t)(there ? page : 0) * a.heads + head) << a.page_shift) + ((at + 16 * t) & a.page_mask);
         }
         return w;
     }
 
-    template <typename T>
-    static __device__ __forceinline__ T of_subtile(const T (&v)[kSubs], int t)
+    // whether all the tile's tokens count
+    __device__ __forceinline__ bool whole(int at, int there) const
     {
-        T r = v[0];
-#pragma unroll
-        for (int i = 1; i < kSubs; ++i)
-            r = t == i ? v[i] : r;
-        return r;
+        return there == (1 << kSubs) - 1 && at >= first && at + kTile <= end;
     }
 
-    __device__ __forceinline__ bool counts(const Where &w, int t, int place) const
+    __device__ __forceinline__ bool counts(int at, int there, int t, int place) const
     {
-        const int token = w.at + 16 * t + place;
-        return token >= first && token < end && of_subtile(w.there, t);
+        const int token = at + 16 * t + place;
+        return token >= first && token < end && (there >> t & 1);
     }
+
+    static __device__ __forceinline__ int64_t row_of(const Where &w, int t) { return t ? w.row[1] : w.row[0]; }
 
     // A lane's i-th piece of a tile; the last lanes may come to the last piece again
     __device__ __forceinline__ int piece(int i) const
@@ -339,48 +337,35 @@ struct CacheAttention {
         } else {
 #pragma unroll
             for (int i = 0; i < kMetas; ++i) {
-                const int64_t from = (of_subtile(w.row, meta_sub(i)) + col) * NG + meta_group();
+                const int64_t from = (row_of(w, meta_sub(i)) + col) * NG + meta_group();
                 l.ks[i] = a.scale[0][from], l.kz[i] = a.zero[0][from];
                 l.vs[i] = a.scale[1][from], l.vz[i] = a.zero[1][from];
             }
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int t = piece(i) / kRowBytes;
-                const int64_t from = of_subtile(w.row, t) * kRowBytes + (piece(i) - t * kRowBytes) * 16;
+                const int64_t from = row_of(w, t) * kRowBytes + (piece(i) - t * kRowBytes) * 16;
                 l.k[i] = *reinterpret_cast<const uint4v *>((const char *)a.packed[0] + from);
                 l.v[i] = *reinterpret_cast<const uint4v *>((const char *)a.packed[1] + from);
             }
         }
     }
 
-    // Rows stand in LDS with their pieces exchanged by the row, or the 16 rows of one access would lie
-    // on 2 to 4 of the banks' 8 pieces
-    static constexpr int kRowPieces = kRowBytes / 16;
-    static constexpr bool kExchange = kRowBytes % 16 == 0 && kRowPieces > 1 && (kRowPieces & (kRowPieces - 1)) == 0;
-    static __device__ __forceinline__ int exchange(int row)
-    {
-        return !kExchange ? 0 : kRowPieces <= 8 ? row / (8 / kRowPieces) & (kRowPieces - 1) : row & 7;
-    }
-
+    // A piece's place in LDS
     static __device__ __forceinline__ int piece_place(int x)
     {
-        return kExchange ? x ^ exchange(x / kRowPieces) : x;
-    }
-
-    static __device__ __forceinline__ const char *row_byte(const uint4v *rows, int row, int byte)
-    {
-        return (const char *)rows + row * kRowBytes + (byte ^ exchange(row) << 4);
+        return kRowPitch == kRowBytes ? 16 * x : x / (kRowBytes / 16) * kRowPitch + x % (kRowBytes / 16) * 16;
     }
 
     // a lane's words of a token's group
-    static __device__ __forceinline__ void read_keys(const uint4v *rows, int row, int byte,
+    static __device__ __forceinline__ void read_keys(const char *rows, int row, int byte,
                                                      uint32_t (&w)[(Keys::kBytes + 3) / 4])
     {
         constexpr int kPart = Keys::kBytes < 16 ? Keys::kBytes : 16;
 #pragma unroll
         for (int i = 0; i < Keys::kBytes / kPart; ++i) {
             uint32_t part[(kPart + 3) / 4];
-            load_words<kPart>(part, row_byte(rows, row, byte + i * kPart));
+            load_words<kPart>(part, rows + row * kRowPitch + byte + i * kPart);
 #pragma unroll
             for (int k = 0; k < (kPart + 3) / 4; ++k)
                 w[i * (kPart / 4) + k] = part[k];
@@ -479,7 +464,7 @@ struct CacheAttention {
                 o[n][i] = float4v{0.f, 0.f, 0.f, 0.f};
         float lane_unit = v_unit[0];                            // of the group whose scales this lane loads
         float (*meta)[NG][kTile] = sh.meta[wave];
-        uint4v *k_rows = sh.rows[wave][0], *v_rows = sh.rows[wave][1];
+        char *k_rows = (char *)sh.rows[wave][0], *v_rows = (char *)sh.rows[wave][1];
         // the row that this lane names to the transposing reads: its quad's tokens in their order
         // (8 bits: 16 dims of each, in two halves; else one block of dims of each and then the next)
         const int named = NB == 8 ? col / 2 : col % 8;
@@ -488,17 +473,18 @@ struct CacheAttention {
         // One tile.  The next one's loads leave at its top, when its own are in LDS.  Nothing is loaded
         // under a condition, which would make the waits for older loads wait for these too.
         const auto step = [&](int tile, auto more) {
-            const Where now = next;
+            const int at = next.at, there = next.there;
+            const bool all = whole(at, there);
 
             // ---- scales: reciprocals (to 1 ulp), to the layout of the scores through LDS
             float rz[kMetas];                                   // (r z) of k
             float vr[kMetas];
             float raise = 0.0f;
-            if (!now.whole) {
+            if (!all) {
                 // tokens that do not count: 1 / scale and zero of 0, whatever the page holds there
 #pragma unroll
                 for (int i = 0; i < kMetas; ++i) {
-                    const bool in = counts(now, meta_sub(i), col);
+                    const bool in = counts(at, there, meta_sub(i), col);
                     l.ks[i] = in ? l.ks[i] : INFINITY;
                     l.vs[i] = in ? l.vs[i] : INFINITY;
                     l.kz[i] = in ? l.kz[i] : 0.0f;
@@ -552,15 +538,15 @@ struct CacheAttention {
                 meta[1][meta_group()][16 * meta_sub(i) + col] = vr[i] * (lane_unit / factor);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                k_rows[piece_place(piece(i))] = l.k[i];
-                v_rows[piece_place(piece(i))] = l.v[i];
+                *reinterpret_cast<uint4v *>(k_rows + piece_place(piece(i))) = l.k[i];
+                *reinterpret_cast<uint4v *>(v_rows + piece_place(piece(i))) = l.v[i];
             }
             wave_lds_fence();
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (more) {
                 if (((tile + 1) * kSubs & 63) == 0)
-                    pages = pages_from(now.at + kStep);
-                next = where(now.at + kStep, pages, tile + 1);
+                    pages = pages_from(at + kStep);
+                next = where(at + kStep, pages, tile + 1);
                 load(next, l);
             }
 
@@ -604,12 +590,12 @@ struct CacheAttention {
                         s[t][r] = fmaf(acc[t][r], r4[r], s[t][r]);
                 }
             }
-            if (!now.whole) {
+            if (!all) {
 #pragma unroll
                 for (int t = 0; t < kSubs; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (!counts(now, t, 4 * quad + r))
+                        if (!counts(at, there, t, 4 * quad + r))
                             s[t][r] = -INFINITY;
             }
 
@@ -679,7 +665,7 @@ struct CacheAttention {
             for (int n = 0; n < kBlocks; n += kReadBlocks) {
                 const int block = kReadBlocks == 1 ? n : n + col / 8;       // (96 dims of 2 bits: the last one twice)
                 const int byte = NB == 8 ? 16 * n + 8 * (col & 1) : 8 * (block < kBlocks ? block : kBlocks - 1);
-                const int2v x = read_transposed<NB>(row_byte(v_rows, v_row, byte));
+                const int2v x = read_transposed<NB>(v_rows + v_row * kRowPitch + byte);
 #pragma unroll
                 for (int h = 0; h < kReadBlocks && n + h < kBlocks; ++h)
 #pragma unroll
