@@ -103,8 +103,9 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  *            aligned), or NULL.  A sequence in which no token counts gives 0 and
  *            -infinity.
  * Scores, exponentials' sums and outputs are formed in fp32; besides the
- * output, each weight times its group's 1 / scale is rounded to 11 bits for the
- * second product (with its own exponent, down to 2^-29 of the largest).
+ * output, each weight times its group's 1 / scale is rounded for the second
+ * product, to 11 bits where the output is bf16 and to 22 where it is fp16
+ * (with its own exponent, down to 2^-25 of the largest).
  * softmax_scale is > 0 and at most 2^100, window >= 0 (HQQ_EINVAL_PARAM); batch
  * at most 2^15, q_heads 2^16, batch * q_heads 2^28, table_width * page_size 2^30
  * and batch times that 2^37 (HQQ_EINVAL_SHAPE).

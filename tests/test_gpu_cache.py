@@ -209,8 +209,9 @@ def reference(cache, Q, table, lengths, scale=None, window=0):
     Weights: exp2 and its argument, 2^-22 together; the largest d: D.  Then
         |dlse| <= D + (n + 8) u + 2 u |lse|
         |dout| <= (2 D + 2^-21 + w) sum_t P_t r |c - z|  +  (n + 24) u sum_t P_t r (c + |z|) + half |out| + tiny
-    with P the exact weights and w = 2^-11, the rounding of P r to 11 bits (with its own exponent, to 2^-29 of the
-    largest: 2^-29 of sum_t max(P r) (c + |z|), in `tiny`)."""
+    with P the exact weights and w = 2^-11, the rounding of P r to 11 bits (fp16 outputs have a second operand for
+    the rest, which the bound does not count on), with an exponent of its own down to 2^-25 of the largest or below,
+    then absolute: `tiny` is 2^-29 of sum_t max(P r) (c + |z|)."""
     scale = 1.0 / math.sqrt(cache.dim) if scale is None else scale
     B, H, D = Q.shape
     G, u = H // cache.heads, 2.0 ** -24
@@ -343,6 +344,28 @@ def test_attention_split_over_the_length(hq, batch, length, heads, G):
     check(c, first, *args)
     again = hq.hqq_cache_attention(c, *args)
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("batch,length,heads,G,dtype", [(70, 500, 40, 1, "fp16"), (3, 9000, 40, 2, "bf16"),
+                                                        (200, 900, 16, 17, "bf16"), (1, 30000, 80, 1, "fp16")])
+def test_attention_runs_that_cross_sequences(hq, batch, length, heads, G, dtype):
+    """Many heads leave few runs to each, longer than a few steps: they go on from one sequence to the next,
+    empty ones and single tokens among them."""
+    g = rng(batch + heads)
+    lengths = [max(0, length - (i * 131) % (length + 40)) for i in range(batch)]
+    if batch > 3:
+        lengths[1], lengths[2], lengths[-1] = 0, 1, 0
+    c = filled(hq, g, sum(-(-n // 128) for n in lengths), 128, heads, 64, 4, 64)
+    args = batch_of(c, g, DTYPES[dtype], lengths, G)
+    got = hq.hqq_cache_attention(c, *args)
+    some = torch.randperm(batch, device="cuda", generator=g)[:12].sort().values
+    some = torch.unique(torch.cat([some, torch.tensor([0, min(1, batch - 1), batch - 1], device="cuda")]))
+    rows = [t[some] for t in args]
+    check(c, [t[some] for t in got], *rows)
+    # and alone each sequence gives the same, within the rounding of another order of its sums
+    one = some[0].item()
+    alone = hq.hqq_cache_attention(c, *[t[one:one + 1] for t in args])
+    check(c, alone, *[t[one:one + 1] for t in args])
 
 
 def test_attention_one_long_sequence_among_short_ones(hq):

@@ -66,20 +66,25 @@ constexpr float key_factor(int f)
 
 // The same for a lane's values: word x holds 8 tokens of 4 bits (or 4 of 8), field f is tokens f and
 // f + 4 (f and f + 2) of it, i the code within 4 bits.  They come out times token_factor and
-// dim_factor; weights have 11 bits, so the fields stay low where that saves a shift.
-template <int NB>
+// dim_factor.  FINE (fp16 outputs): in the upper bits too; weights of 11 bits leave the fields low
+// where that saves a shift.
+template <int NB, bool FINE>
 __device__ __forceinline__ uint32_t value_field(uint32_t x, int f, int i)
 {
     if constexpr (NB == 8)
         return (f ? x >> 8 : x) & 0x00ff00ffu;
-    else
+    else if constexpr (!FINE)
         return (f < 2 ? x : x >> 8) & (NB == 4 ? 0x000f000fu : 0x00030003u << (2 * i)) << (4 * (f % 2));
+    else if constexpr (NB == 4)
+        return key_field<4>(x, f);
+    else
+        return key_field<2>(x, 2 * f + i);
 }
 
-template <int NB>
+template <int NB, bool FINE>
 __device__ __forceinline__ float token_factor(int token)
 {
-    return NB == 8 ? 1.0f : token & 1 ? 16.0f : 1.0f;
+    return NB == 8 ? 1.0f : FINE ? (NB == 4 ? 16.0f : 64.0f) : token & 1 ? 16.0f : 1.0f;
 }
 
 template <int NB>
@@ -491,7 +496,7 @@ struct CacheAttention {
                     l.vz[i] = in ? l.vz[i] : 0.0f;
                 }
             }
-            const float factor = token_factor<NB>(col);
+            const float factor = token_factor<NB, !BF>(col);
 #pragma unroll
             for (int i = 0; i < kMetas; ++i) {
                 const float kr = __builtin_amdgcn_rcpf(l.ks[i]) * 0x1p12f;  // the codes' 2^-24 taken back, half here
@@ -673,7 +678,8 @@ struct CacheAttention {
                         uint32_t regs[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            regs[r] = NB == 8 ? value_field<NB>(x[r / 2], r % 2, 0) : value_field<NB>(x[h], r, i);
+                            regs[r] = NB == 8 ? value_field<NB, !BF>(x[r / 2], r % 2, 0)
+                                              : value_field<NB, !BF>(x[h], r, i);
                         const int g = (n + h) * kBlockDims / GS;
                         float4v &acc = o[n + h][i];
                         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(w16[g]), acc, 0, 0, 0);
