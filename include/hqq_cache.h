@@ -112,8 +112,8 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  * The result does not depend on what else runs: sums are added in an order
  * that sizes and lengths set.
  *
- * The workspace holds the parts of sequences that are split over their length;
- * nothing in it has to be set before a call or kept after it.  Calls that may
+ * The workspace holds the parts of sequences that are split over their length
+ * (and how many sequences are shared out); nothing in it has to be set before a call or kept after it.  Calls that may
  * run at the same time (two streams, two captured graphs) need one each. */
 HQQ_API int64_t hqq_cache_attention_workspace(const hqq_cache *cache, int64_t batch, int64_t q_heads,
                                               int64_t table_width);

@@ -368,6 +368,29 @@ def test_attention_runs_that_cross_sequences(hq, batch, length, heads, G, dtype)
     check(c, alone, *[t[one:one + 1] for t in args])
 
 
+@pytest.mark.parametrize("batch,most,heads,G,width", [
+    (64, 40, 1, 1, 0), (65, 40, 1, 1, 0), (65, 900, 40, 1, 0), (128, 2000, 1, 3, 0), (129, 700, 4, 1, 0), (400, 60, 1, 1, 20), (1000, 60, 1, 2, 20),
+    (1023, 200, 2, 1, 20), (1025, 130, 16, 2, 20), (4097, 100, 1, 1, 13), (5000, 33, 40, 1, 13)])
+@pytest.mark.parametrize("long", [0, 9001])
+def test_attention_many_sequences(hq, batch, most, heads, G, width, long):
+    """The plan of more sequences than a wave's lanes, runs within sequences (many of them to a worker) and
+    across: every row is written, and those of the first, the last, the longest and some others are right."""
+    g = rng(batch + heads + long)
+    lengths = torch.randint(0, most + 1, (batch,), generator=torch.Generator().manual_seed(batch)).tolist()
+    lengths[0] = lengths[-1] = 0
+    lengths[batch // 2], lengths[batch // 3] = most, long or most
+    c = filled(hq, g, sum(-(-n // 64) for n in lengths), 64, heads, 64, 4, 32)
+    args = batch_of(c, g, torch.bfloat16, lengths, G, width=max(width, -(-max(lengths) // 64)))
+    got = torch.full_like(args[0], math.nan), torch.full(args[0].shape[:2], math.nan, device="cuda")
+    hq.hqq_cache_attention(c, *args, out=got[0], lse=got[1])
+    assert not got[0].isnan().any() and not got[1].isnan().any()
+    some = torch.randperm(batch, device="cuda", generator=g)[:6].tolist() + [0, batch // 2, batch // 3, batch - 1]
+    some = torch.tensor(sorted(set(some)), device="cuda")
+    check(c, [t[some] for t in got], *[t[some] for t in args])
+    again = hq.hqq_cache_attention(c, *args)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
 def test_attention_one_long_sequence_among_short_ones(hq):
     g = rng(7)
     lengths = [1, 0, 30000, 5, 0, 64, 129]

@@ -162,8 +162,9 @@ class QuantizedCache:
 
 
 def _bytes(cache: QuantizedCache, sizes) -> int:
-    if cache._room[0] == sizes:
-        return cache._room[1]
+    room = cache._room               # (one read: another thread's call may replace it)
+    if room[0] == sizes:
+        return room[1]
     n = cache._lib.hqq_cache_attention_workspace(cache._ptr, *sizes)
     if n < 0:
         raise CacheError("hqq_cache_attention_workspace", n)

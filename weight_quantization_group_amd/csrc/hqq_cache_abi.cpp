@@ -167,6 +167,7 @@ struct AttentionLayout {
     int32_t row_tiles, workers;      // workers: 0 where no sequence is split
     float *part = nullptr;
     float2 *part_ml = nullptr;
+    int32_t *plan = nullptr;
     int64_t bytes = 0;
     AttentionLayout(void *ws, const hqq_cache &c, int64_t batch, int64_t q_heads, int64_t table_width)
     {
@@ -178,10 +179,14 @@ struct AttentionLayout {
         workers = workers_for(c.heads * row_tiles);
         const int64_t segments = workers + batch;
         const int64_t sums = round_up(segments * q_heads * c.dim * 4, 256);
-        bytes = sums + round_up(segments * q_heads * 8, 256);
+        const int64_t meta = round_up(segments * q_heads * 8, 256);
+        const bool planned = batch > kCachePlanned;
+        bytes = sums + meta + (planned ? round_up((kCachePlanHead + batch + 1) * 4, 256) : 0);
         if (ws) {
             part = (float *)ws;
             part_ml = (float2 *)((char *)ws + sums);
+            if (planned)
+                plan = (int32_t *)((char *)ws + sums + meta);
         }
     }
 };
@@ -309,6 +314,7 @@ int hqq_cache_attention(const hqq_cache *cache, const uint16_t *Q, int64_t q_bat
     a.lse = lse;
     a.part = l.part;
     a.part_ml = l.part_ml;
+    a.plan = l.plan;
     a.batch = (int32_t)batch;
     a.q_heads = (int32_t)q_heads;
     a.heads = c.heads;
@@ -323,6 +329,8 @@ int hqq_cache_attention(const hqq_cache *cache, const uint16_t *Q, int64_t q_bat
     a.scale_log2 = softmax_scale * 1.44269504088896340736f;
     a.bf16 = dtype == HQQ_DTYPE_BF16;
     const hipStream_t s = (hipStream_t)stream;
+    if (a.plan && launch_cache_plan(a, s) != hipSuccess)
+        return HQQ_EHIP;
     const hipError_t e = c.nbits == 2   ? launch_cache_attention_b2(c.dim, c.group_size, a, s)
                          : c.nbits == 4 ? launch_cache_attention_b4(c.dim, c.group_size, a, s)
                                         : launch_cache_attention_b8(c.dim, c.group_size, a, s);

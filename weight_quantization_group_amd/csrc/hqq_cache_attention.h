@@ -765,41 +765,48 @@ struct CacheAttention {
         return r;
     }
 
+    // A sequence
+    __device__ __forceinline__ void run_sequence(Shared &sh)
+    {
+        b = worker;
+        if (b >= a.batch)
+            return;
+        const CacheSpan s = cache_span(a, b);
+        first = s.first;
+        begin = s.base;
+        end = s.length;
+        segment(sh, 0, true);
+    }
+
+    // A run of the plan, or some where there are more than workers
     __device__ __forceinline__ void run(Shared &sh)
     {
-        int at = 0, start = 0, stop;
-        bool cross = false;
-        CacheSpan s;
-        int slot = 0;
-        if (a.workers == 0) {        // a sequence each
-            b = worker;
-            if (b >= a.batch)
+        if (a.workers == 0)
+            return run_sequence(sh);
+        if (worker >= a.workers)
+            return;
+        for (;; worker += a.workers) {
+            const CachePlan plan(a, lane);          // (each time anew: its registers are not held over the segments)
+            if (worker >= plan.runs)
                 return;
-            s = cache_span(a, b);
-            stop = s.steps;
-        } else {
-            const CachePlan plan(a, lane);
-            const int64_t from = (int64_t)worker * plan.run;
-            if (from > 1 << 30)          // behind the last step
-                return;
-            at = (int)from;
-            stop = at + plan.run;
-            cross = plan.cross;
+            int at = worker * plan.run, start;      // (below 2^31: of runs that cross there are `workers`)
+            const int stop = at + plan.run;
+            CacheSpan s;
             b = plan.find(a, at, lane, start, s);
-            slot = plan.slot(worker, b);
-        }
-        while (b < a.batch) {
-            const int next = start + s.steps, upto = stop < next ? stop : next;
-            first = s.first;
-            begin = s.base + (at - start) * kStep;
-            end = upto < next ? s.base + (upto - start) * kStep : s.length;
-            segment(sh, slot, at == start && upto == next);
-            if (!cross || upto == stop)
+            while (b < a.batch) {
+                const int next = start + s.steps, upto = stop < next ? stop : next;
+                first = s.first;
+                begin = s.base + (at - start) * kStep;
+                end = upto < next ? s.base + (upto - start) * kStep : s.length;
+                segment(sh, plan.slot(worker, b), at == start && upto == next);
+                if (!plan.cross || upto == stop)
+                    break;
+                at = start = next;
+                if (++b < a.batch)
+                    s = cache_span(a, b);
+            }
+            if (worker + a.workers >= plan.runs)
                 return;
-            at = start = next;
-            ++slot;
-            if (++b < a.batch)
-                s = cache_span(a, b);
         }
     }
 };
@@ -815,7 +822,7 @@ __global__ __launch_bounds__(64 * kCacheWaves, kCacheResident) void cache_attent
 template <int NB, int GS, int NG, bool BF>
 hipError_t launch_attention(const CacheAttentionArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)((a.workers + a.batch + 7) / 8 * 8));
+    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)(((a.workers ? a.workers : a.batch) + 7) / 8 * 8));
     hipLaunchKernelGGL((cache_attention_kernel<NB, GS, NG, BF>), grid, dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }

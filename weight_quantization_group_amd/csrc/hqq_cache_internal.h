@@ -39,6 +39,7 @@ struct CacheAttentionArgs {
     float *lse;                      // may be null
     float *part;                     // [workers + batch, q_heads, dim] sums of split sequences' segments
     float2 *part_ml;                 // [workers + batch, q_heads] their maxima and sums of weights
+    int32_t *plan;                   // null, or the plan: kCachePlanHead numbers, then where each sequence begins
     int32_t batch, q_heads, heads, G;
     int32_t row_tiles;               // blocks of 16 q heads of a key-value head
     int32_t pages, page_shift, page_mask, table_width;
@@ -64,11 +65,23 @@ constexpr int kCus = 256;
 // 1024 13.2 and 10.6.)
 constexpr int kCacheWhole = 768;
 
+// Runs of more steps than this cross sequences.
+constexpr int kCacheCross = 8;
+
+// Of more sequences than this the plan is found once, by a launch of its own that costs 2.5 us, not by
+// every wave, 64 sequences at a time.  (8 heads: 128 sequences of 100, 1024 and 4000 tokens 19.7, 41.7
+// and 135 us by every wave, 22.3, 43.8 and 131 by the launch; 512 sequences 181, 170 and 481, and 68,
+// 156 and 471.)
+constexpr int kCachePlanned = 128;
+constexpr int kCachePlanHead = 3;    // steps per run, runs, whether these cross sequences
+
 hipError_t launch_cache_write(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
 hipError_t launch_cache_read(int nbits, int dim, int group_size, bool bf16, const CacheCodecArgs &a, hipStream_t s);
 hipError_t launch_cache_attention_b2(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
 hipError_t launch_cache_attention_b4(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
 hipError_t launch_cache_attention_b8(int dim, int group_size, const CacheAttentionArgs &a, hipStream_t s);
+// finds the plan of many sequences
+hipError_t launch_cache_plan(const CacheAttentionArgs &a, hipStream_t s);
 // joins the segments of split sequences
 hipError_t launch_cache_join(int dim, const CacheAttentionArgs &a, hipStream_t s);
 

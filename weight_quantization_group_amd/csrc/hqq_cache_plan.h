@@ -5,8 +5,9 @@
 // The tokens of all sequences, in steps of a workgroup and one sequence after the other, are
 // cut into runs of equal length, about `workers` of them; workgroup w of a key-value head
 // takes run w.  Long runs cross from one sequence to the next, so that all of them end
-// together however ragged the batch is; short ones do not, as each segment (a run's part
-// of a sequence) has a prologue and an end of its own that cost as much as some steps.
+// together however ragged the batch is, and so do runs of more sequences than runs; other short
+// ones do not, as each segment (a run's part of a sequence) has a prologue and an end of its own
+// that cost as much as some steps.  (512 sequences of 100 tokens, 64 runs: 54 us across, 68 within.)
 #pragma once
 
 #include "hqq_cache_internal.h"
@@ -53,44 +54,61 @@ __device__ __forceinline__ int wave_inclusive_sum(int v)
 
 __device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_inclusive_sum(v), 63); }
 
-// Runs of more steps than this cross sequences.
-constexpr int kCacheCross = 8;
-
-// Every wave finds the same plan by itself; lane l holds sequence l's span.  All steps number at
-// most 2^30 (batch * table_width * page_size <= 2^37).
+// Every wave finds the same plan by itself, lane l holding sequence l's span, or, of many
+// sequences, reads the one that cache_plan_kernel left in the workspace.  All steps number at most
+// 2^30 + 2^15 (batch * table_width * page_size <= 2^37).  Of runs that cross sequences there are
+// `workers`, of others at most `batch` more.
 struct CachePlan {
     CacheSpan mine;            // of sequence `lane` (steps 0: there is none)
     int run;                   // steps per run
+    int runs;                  // how many there are
     bool cross;
+
+    __device__ __forceinline__ CachePlan() {}
 
     __device__ __forceinline__ CachePlan(const CacheAttentionArgs &a, int lane)
     {
+        if (a.plan) {
+            mine = CacheSpan{0, 0, 0, 0};
+            run = a.plan[0];
+            runs = a.plan[1];
+            cross = a.plan[2] != 0;
+            return;
+        }
         mine = lane < a.batch ? cache_span(a, lane) : CacheSpan{0, 0, 0, 0};
-        const int steps = sum(a, lane, 1);
-        run = (steps + a.workers - 1) / a.workers;
-        cross = run > kCacheCross;
-        // runs that keep to their sequences are more: lengthened until one round holds them
-        if (!cross)
-            for (int i = 0; i < 3 && sum(a, lane, run) > a.workers; ++i)
-                run += (run + 3) / 4;
+        find_runs(a, [&](int size) {
+            int n = runs_of(mine.steps, size);
+            for (int b = lane + 64; b < a.batch; b += 64)
+                n += runs_of(cache_span(a, b).steps, size);
+            return wave_sum(n);
+        });
     }
 
-    // runs of `size` steps that the sequences take
-    __device__ __forceinline__ int sum(const CacheAttentionArgs &a, int lane, int size) const
+    // sum(size): runs of `size` steps that the sequences take
+    template <class Sum>
+    __device__ __forceinline__ void find_runs(const CacheAttentionArgs &a, Sum sum)
     {
-        int n = runs(mine.steps, size);
-        for (int b = lane + 64; b < a.batch; b += 64)
-            n += runs(cache_span(a, b).steps, size);
-        return wave_sum(n);
+        const int steps = sum(1);
+        run = (steps + a.workers - 1) / a.workers;
+        runs = a.workers;
+        cross = run > kCacheCross || a.batch > a.workers;
+        if (cross)
+            return;
+        // runs that keep to their sequences are more: lengthened until one round holds them
+        runs = sum(run);
+        for (int i = 0; i < 3 && runs > a.workers; ++i) {
+            run += (run + 3) / 4;
+            runs = sum(run);
+        }
     }
 
-    static __device__ __forceinline__ int runs(int steps, int size)
+    static __device__ __forceinline__ int runs_of(int steps, int size)
     {
         return size == 1 ? steps : (uint32_t)(steps + size - 1) / (uint32_t)size;
     }
 
     // a sequence's steps in the order of runs
-    __device__ __forceinline__ int padded(int steps) const { return cross ? steps : runs(steps, run) * run; }
+    __device__ __forceinline__ int padded(int steps) const { return cross ? steps : runs_of(steps, run) * run; }
 
     // the workspace's place of segment (w, b): runs and sequences both advance
     __device__ __forceinline__ int slot(int w, int b) const { return cross ? w + b : w; }
@@ -98,6 +116,24 @@ struct CachePlan {
     // The sequence that holds step `at`, its first step and span (batch: behind the last)
     __device__ __forceinline__ int find(const CacheAttentionArgs &a, int at, int lane, int &start, CacheSpan &span) const
     {
+        start = 0;
+        span = CacheSpan{0, 0, 0, 0};
+        if (a.plan) {
+            const int *starts = a.plan + kCachePlanHead;
+            if (at >= starts[a.batch])
+                return a.batch;
+            // the last sequence that begins at `at` or before, among 64 probes at a time
+            int b = 0;
+            for (int count = a.batch; count > 1;) {
+                const int stride = (count + 63) / 64, i = lane * stride;
+                const int n = __popcll(__ballot(i < count && starts[b + (i < count ? i : 0)] <= at)) - 1;
+                b += n * stride;
+                count = count - n * stride < stride ? count - n * stride : stride;
+            }
+            start = starts[b];
+            span = cache_span(a, b);
+            return __builtin_amdgcn_readfirstlane(b);
+        }
         int before = 0;
         CacheSpan s = mine;
         for (int b0 = 0; b0 < a.batch; b0 += 64) {
@@ -118,8 +154,6 @@ struct CachePlan {
             }
             before = __builtin_amdgcn_readlane(upto, 63);
         }
-        start = 0;
-        span = CacheSpan{0, 0, 0, 0};
         return a.batch;
     }
 };
