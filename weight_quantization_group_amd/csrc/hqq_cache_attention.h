@@ -765,48 +765,40 @@ struct CacheAttention {
         return r;
     }
 
-    // A sequence
-    __device__ __forceinline__ void run_sequence(Shared &sh)
-    {
-        b = worker;
-        if (b >= a.batch)
-            return;
-        const CacheSpan s = cache_span(a, b);
-        first = s.first;
-        begin = s.base;
-        end = s.length;
-        segment(sh, 0, true);
-    }
-
-    // A run of the plan, or some where there are more than workers
     __device__ __forceinline__ void run(Shared &sh)
     {
-        if (a.workers == 0)
-            return run_sequence(sh);
-        if (worker >= a.workers)
-            return;
-        for (;; worker += a.workers) {
-            const CachePlan plan(a, lane);          // (each time anew: its registers are not held over the segments)
+        int at = 0, start = 0, stop;
+        bool cross = false;
+        CacheSpan s;
+        int slot = 0;
+        if (a.workers == 0) {        // a sequence each
+            b = worker;
+            if (b >= a.batch)
+                return;
+            s = cache_span(a, b);
+            stop = s.steps;
+        } else {
+            const CachePlan plan(a, lane);
             if (worker >= plan.runs)
                 return;
-            int at = worker * plan.run, start;      // (below 2^31: of runs that cross there are `workers`)
-            const int stop = at + plan.run;
-            CacheSpan s;
+            at = worker * plan.run;  // (below 2^31: of runs that cross there are `workers`)
+            stop = at + plan.run;
+            cross = plan.cross;
             b = plan.find(a, at, lane, start, s);
-            while (b < a.batch) {
-                const int next = start + s.steps, upto = stop < next ? stop : next;
-                first = s.first;
-                begin = s.base + (at - start) * kStep;
-                end = upto < next ? s.base + (upto - start) * kStep : s.length;
-                segment(sh, plan.slot(worker, b), at == start && upto == next);
-                if (!plan.cross || upto == stop)
-                    break;
-                at = start = next;
-                if (++b < a.batch)
-                    s = cache_span(a, b);
-            }
-            if (worker + a.workers >= plan.runs)
+            slot = plan.slot(worker, b);
+        }
+        while (b < a.batch) {
+            const int next = start + s.steps, upto = stop < next ? stop : next;
+            first = s.first;
+            begin = s.base + (at - start) * kStep;
+            end = upto < next ? s.base + (upto - start) * kStep : s.length;
+            segment(sh, slot, at == start && upto == next);
+            if (!cross || upto == stop)
                 return;
+            at = start = next;
+            ++slot;
+            if (++b < a.batch)
+                s = cache_span(a, b);
         }
     }
 };
@@ -822,7 +814,10 @@ __global__ __launch_bounds__(64 * kCacheWaves, kCacheResident) void cache_attent
 template <int NB, int GS, int NG, bool BF>
 hipError_t launch_attention(const CacheAttentionArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)(((a.workers ? a.workers : a.batch) + 7) / 8 * 8));
+    // runs that keep to their sequences number at most one a sequence more than workers; of more sequences
+    // than workers they cross
+    const int runs = a.workers + (a.workers && a.batch > a.workers ? 0 : a.batch);
+    const dim3 grid((unsigned)(a.heads * a.row_tiles), (unsigned)((runs + 7) / 8 * 8));
     hipLaunchKernelGGL((cache_attention_kernel<NB, GS, NG, BF>), grid, dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }
