@@ -106,15 +106,19 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  * output, each weight times its group's 1 / scale is rounded for the second
  * product, to 11 bits where the output is bf16 and to 22 where it is fp16
  * (with its own exponent, down to 2^-25 of the largest).
+ * Keys, values and queries are taken to be of magnitude 2^64 at most, and
+ * softmax_scale times the largest of a query 2^100 (fp16 values are, bf16 ones
+ * need not be): beyond, a finite result can come out infinite or NaN.
  * softmax_scale is > 0 and at most 2^100, window >= 0 (HQQ_EINVAL_PARAM); batch
  * at most 2^15, q_heads 2^16, batch * q_heads 2^28, table_width * page_size 2^30
  * and batch times that 2^37 (HQQ_EINVAL_SHAPE).
  * The result does not depend on what else runs: sums are added in an order
  * that sizes and lengths set.
  *
- * The workspace holds the parts of sequences that are split over their length
- * (and how many sequences are shared out); nothing in it has to be set before a call or kept after it.  Calls that may
- * run at the same time (two streams, two captured graphs) need one each. */
+ * The workspace holds the parts of sequences that are split over their length,
+ * and how many sequences are shared out; nothing in it has to be set before a
+ * call or kept after it.  Calls that may run at the same time (two streams, two
+ * captured graphs) need one each. */
 HQQ_API int64_t hqq_cache_attention_workspace(const hqq_cache *cache, int64_t batch, int64_t q_heads,
                                               int64_t table_width);
 HQQ_API int hqq_cache_attention(const hqq_cache *cache, const uint16_t *Q, int64_t q_batch_stride,

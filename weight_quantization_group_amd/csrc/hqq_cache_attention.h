@@ -20,6 +20,12 @@
 //
 // A wave takes tiles of 32 tokens, its loads whole lines in 16-byte pieces over the lanes, a tile
 // ahead in registers; through LDS they reach the operands' lanes.
+//
+// What bounds it: the bytes of codes and scales where sequences are long (64 sequences of 8192 tokens,
+// 8 heads of 128 dims at 4 bits in groups of 64, 64 q heads: 673 MB in 123 us, 5.5 TB/s, of 6.2 that a
+// read reaches; its loads alone take 117), with some 90 us of vector operations beside them.  A segment
+// (a workgroup's part of a sequence) costs about 3 us beside its tiles, which is what short sequences
+// pay (32 ragged ones, 32 heads: 344 MB in 77 us), and a call has a floor of some 9 us of launches.
 #pragma once
 
 #include "hqq_cache_plan.h"
@@ -635,7 +641,7 @@ struct CacheAttention {
             // ---- the second product
             // Weights, paired as value_field pairs tokens.  11 bits of them make an error of the size of fp16
             // outputs' own rounding (0.00029 of the result beside 0.00019), so there the rest of each
-            // weight is a second operand (0.00019; 32 ragged 7B sequences 77 -> 81 us); bf16's own drowns it.
+            // weight is a second operand (0.00019; 4 us more of 80 for 32 ragged 7B sequences); bf16's own drowns it.
             uint32_t w16[NG][4], rest16[NG][4];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {

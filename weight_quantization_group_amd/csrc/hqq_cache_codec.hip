@@ -6,6 +6,11 @@
 // Rows go by blocks of 16 tokens, then heads, then the block's tokens: consecutive
 // tokens of a head lie together in a page, so that codes and scales move by whole lines,
 // where token by token they would by pieces of 8 and 64 bytes.
+//
+// What bounds them: memory where there are many tokens (write of 4096 tokens of 32 x 128 to 4 bits
+// with the values back, 155 MB in 33 us, 4.7 TB/s of the 4.9 of a copy; by tokens 39; read of 32768
+// tokens of 8 x 128, 176 MB in 30 us, 5.9 TB/s), else the launch: 3 to 5 us in the kernel, the host's
+// side 8 to 9.
 #include "hqq_cache_internal.h"
 
 namespace hqq {
