@@ -614,6 +614,43 @@ def test_graph_and_streams(hq):
             assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1])
 
 
+def test_graph_of_many_sequences(hq):
+    """The plan that a call leaves in its workspace is that call's own: captured once, it is found anew for other
+    lengths at every replay, whatever the workspace holds; two streams with a workspace each."""
+    g = rng(19)
+    c = filled(hq, g, 1200, 16, 3, 64, 8, 32)
+    Q, table, n = batch_of(c, g, torch.bfloat16, [(i * 37) % 100 for i in range(200)], 2, width=50)
+    size = hq.hqq_cache_attention_workspace(c, 200, 6, 50)
+    ws = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    hq.hqq_cache_attention(c, Q, table, n, workspace=ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = hq.hqq_cache_attention(c, Q, table, n, workspace=ws[0])
+    table.copy_(torch.randint(0, c.pages, table.shape, device="cuda", generator=g))
+    for most in (0, 1, 40, 800, 100):
+        n.copy_(torch.randint(0, most + 1, n.shape, device="cuda", generator=g))
+        ws[0].fill_(most % 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        mine = [t.clone() for t in captured]
+        want = hq.hqq_cache_attention(c, Q, table, n)
+        assert torch.equal(mine[0], want[0]) and torch.equal(mine[1], want[1])
+        check(c, [t[::23] for t in mine], Q[::23], table[::23], n[::23])
+    torch.cuda.synchronize()
+    got = []
+    for w, m in zip(ws[1:], (n, n.flip(0).contiguous())):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append((m, [hq.hqq_cache_attention(c, Q, table, m, workspace=w) for _ in range(3)]))
+    torch.cuda.synchronize()
+    for m, runs in got:
+        want = hq.hqq_cache_attention(c, Q, table, m)
+        for r in runs:
+            assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1])
+
+
 def test_outputs_given(hq):
     """Rows beside a given output's keep what they held; the C call may leave out lse."""
     g = rng(18)
