@@ -122,9 +122,7 @@ struct KeyOrder {
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[(N + 3) / 4], const char *p)
 {
-    if constexpr (N == 1) {
-        w[0] = *(const uint8_t *)p;
-    } else if constexpr (N == 2) {
+    if constexpr (N == 2) {
         w[0] = *(const uint16_t *)p;
     } else if constexpr (N == 4) {
         w[0] = *(const uint32_t *)p;

@@ -148,7 +148,8 @@ __device__ __forceinline__ float group_min(float v)
     return v;
 }
 
-// ROWS groups of kRows rows per workgroup, whose loads go out together
+// ROWS groups of kRows rows per workgroup, whose loads go out together.  (One in the write: without the
+// arrays, the row's place found once, the compiler's order of loads took 33 us of 4096 tokens to 37.)
 template <int NB, int D, int GS, bool BF, int ROWS>
 __global__ __launch_bounds__(kBlock) void cache_write_kernel(CacheCodecArgs a)
 {
