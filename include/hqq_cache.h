@@ -103,9 +103,10 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  *            aligned), or NULL.  A sequence in which no token counts gives 0 and
  *            -infinity.
  * Scores, exponentials' sums and outputs are formed in fp32; besides the
- * output, each weight times its group's 1 / scale is rounded for the second
- * product, to 11 bits where the output is bf16 and to 22 where it is fp16
- * (with its own exponent, down to 2^-25 of the largest).
+ * output, each weight exp(s_t - max) times its group's 1 / scale is rounded for
+ * the second product: to 22 bits, and by at most 2^-39 of the largest 1 / scale
+ * that the group has among the sequence's tokens, whatever their weights (22
+ * bits down to 2^-17 of it, then fewer).
  * Keys, values and queries are taken to be of magnitude 2^64 at most, and
  * softmax_scale times the largest of a query 2^100 (fp16 values are, bf16 ones
  * need not be): beyond, a finite result can come out infinite or NaN.

@@ -734,3 +734,79 @@ def test_binding_refuses(hq):
             pytest.fail(f"call {i} was not refused")
     with pytest.raises(AttributeError):
         c.k = c.v
+
+
+# ---------------------------------------------------------------------------
+# whole weights
+# ---------------------------------------------------------------------------
+
+def whole_bound(cache, Q, table, lengths):
+    """(out, bound of its error) in 64 bits where each weight is held in two fp16 operands.
+
+    Beside the terms of reference(): a weight p r times a power of two that brings the largest r of its
+    group to 2^14 or more goes as the fp16 value next to it and that of the rest.  Together they are off by at
+    most 2^-22 of it or, where the rest is subnormal, by 2^-25 with p <= 1, that is 2^-39 of the largest r in the
+    frame of p (P's, the largest P being p = 1).  The zeros meet the unrounded weights.  A code stands in an fp16
+    subnormal whose last place is 2^-24; products that are aligned by its exponent, 2^-14, lose at
+    most u 2^10 / f of a code's unit each, f = 1, 16 or 64 being the place of the codes' last bit:
+        |dout| <= (2 D + 2^-21) sum_t P_t |v_t|  +  2^-22 sum_t P_t r c  +  2^-39 max(P) max(r) sum_t c
+                  +  (n + 24) u sum_t P_t r (c + |z|)  +  u 2^10 / f sum_t P_t r  +  half |out|"""
+    B, H, D = Q.shape
+    G, u = H // cache.heads, 2.0 ** -24
+    f = {8: 1, 4: 16, 2: 64}[cache.nbits]
+    half = torch.finfo(Q.dtype).eps / 2
+    out, tol = (torch.zeros(B, H, D, dtype=torch.float64, device="cuda") for _ in range(2))
+    for b in range(B):
+        t = torch.arange(int(lengths[b]), device="cuda")
+        page, place = table[b].long()[t // cache.page_size], t % cache.page_size
+        for h in range(cache.heads if len(t) else 0):
+            (kc, kz, kr), (vc, vz, vr) = (decode([a[page, h, place] for a in side], cache.nbits, cache.group_size)
+                                          for side in (cache.k, cache.v))
+            rows = slice(h * G, (h + 1) * G)
+            q = Q[b, rows].double() / math.sqrt(D)
+            S = q @ ((kc - kz) * kr).T
+            d = (D + 24) * u * (q.abs() @ (kr * (kc + kz.abs())).T) + 4 * u * S.abs().amax(1, keepdim=True)
+            P = torch.softmax(S, 1)
+            v = (vc - vz) * vr
+            out[b, rows] = P @ v
+            tol[b, rows] = (2 * d.amax(1, keepdim=True) + 2.0 ** -21) * (P @ v.abs()) + 2.0 ** -22 * (P @ (vr * vc)) \
+                + 2.0 ** -39 * P.amax(1, keepdim=True) * vr.amax(0) * vc.sum(0) \
+                + (len(t) + 24) * u * (P @ (vr * (vc + vz.abs()))) + u * 1024 / f * (P @ vr) + half * out[b, rows].abs()
+    smallest = torch.finfo(Q.dtype).smallest_normal * torch.finfo(Q.dtype).eps
+    return out, tol + smallest
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("nbits", NBITS)
+@pytest.mark.parametrize("dim,gs", [(64, 32), (96, 32), (128, 128), (256, 64)])
+def test_attention_weights_are_whole(hq, dim, gs, nbits, dtype):
+    """Few tokens of nearly even weight: some of their values cancel in some dims, where the output's own
+    rounding is far below a weight's rounding to 11 bits (2^-11 of |v| beside a bound of about 2^-18)."""
+    g = rng(dim + gs + 5 * nbits)
+    lengths = [0] + [1, 2, 3, 4, 6, 9] * 5 + [33, 140, 1000]
+    c = filled(hq, g, sum(-(-n // 16) for n in lengths), 16, 2, dim, nbits, gs)
+    args = batch_of(c, g, DTYPES[dtype], lengths, 3, q=1 / 64)
+    got = hq.hqq_cache_attention(c, *args)[0]
+    out, tol = whole_bound(c, *args)
+    err = (got.double() - out).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("nbits", NBITS)
+@pytest.mark.parametrize("place", [0, 40, 199])
+def test_attention_a_wide_token_that_has_no_weight(hq, nbits, dtype, place):
+    """One token with values 2^24 times the others' and a score some 60 below theirs: it takes nothing from
+    the other tokens' weights but what the bound says."""
+    g = rng(nbits + place)
+    c = filled(hq, g, 13, 16, 1, 64, nbits, 32)
+    Q, table, n = batch_of(c, g, DTYPES[dtype], [200], 4, q=1 / 64)
+    page, at = int(table[0, place // 16]), place % 16
+    Q[..., 0] = 8.0                                            # its key: -60 in the first group
+    c.v[1][page, 0, at] *= 2.0 ** -24
+    c.k[0][page, 0, at] = 0
+    c.k[1][page, 0, at, 0], c.k[2][page, 0, at, 0] = 1.0, 60.0
+    out, tol = whole_bound(c, Q, table, n)
+    got = hq.hqq_cache_attention(c, Q, table, n)[0]
+    err = (got.double() - out).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())

@@ -71,32 +71,17 @@ constexpr float key_factor(int f)
 }
 
 // The same for a lane's values: word x holds 8 tokens of 4 bits (or 4 of 8), field f is tokens f and
-// f + 4 (f and f + 2) of it, i the code within 4 bits.  They come out times token_factor and
-// dim_factor.  FINE (fp16 outputs): in the upper bits too; weights of 11 bits leave the fields low
-// where that saves a shift.
-template <int NB, bool FINE>
+// f + 4 (f and f + 2) of it, i the code within 4 bits.  They come out times value_factor.
+template <int NB>
 __device__ __forceinline__ uint32_t value_field(uint32_t x, int f, int i)
 {
-    if constexpr (NB == 8)
-        return (f ? x >> 8 : x) & 0x00ff00ffu;
-    else if constexpr (!FINE)
-        return (f < 2 ? x : x >> 8) & (NB == 4 ? 0x000f000fu : 0x00030003u << (2 * i)) << (4 * (f % 2));
-    else if constexpr (NB == 4)
-        return key_field<4>(x, f);
-    else
-        return key_field<2>(x, 2 * f + i);
-}
-
-template <int NB, bool FINE>
-__device__ __forceinline__ float token_factor(int token)
-{
-    return NB == 8 ? 1.0f : FINE ? (NB == 4 ? 16.0f : 64.0f) : token & 1 ? 16.0f : 1.0f;
+    return key_field<NB>(x, NB == 2 ? 2 * f + i : f);
 }
 
 template <int NB>
-constexpr float dim_factor(int i)
+constexpr float value_factor(int i)
 {
-    return NB == 2 && i ? 4.0f : 1.0f;
+    return key_factor<NB>(NB == 2 ? i : 0);
 }
 
 // How a lane's gs / 4 codes of a token's group stand in the operands of the first
@@ -500,7 +485,6 @@ struct CacheAttention {
                     l.vz[i] = in ? l.vz[i] : 0.0f;
                 }
             }
-            const float factor = token_factor<NB, !BF>(col);
 #pragma unroll
             for (int i = 0; i < kMetas; ++i) {
                 const float kr = __builtin_amdgcn_rcpf(l.ks[i]) * 0x1p12f;  // the codes' 2^-24 taken back, half here
@@ -508,7 +492,7 @@ struct CacheAttention {
                 rz[i] = kr * l.kz[i];
                 float *to = &meta[0][meta_group()][16 * meta_sub(i) + col];
                 to[0] = kr;
-                to[2 * NG * kTile] = l.vz[i] * factor;
+                to[2 * NG * kTile] = l.vz[i];
                 raise = fmaxf(raise, vr[i]);
             }
             // a group's r of v beyond the unit that its weights are held in?
@@ -544,7 +528,7 @@ struct CacheAttention {
             }
 #pragma unroll
             for (int i = 0; i < kMetas; ++i)
-                meta[1][meta_group()][16 * meta_sub(i) + col] = vr[i] * (lane_unit / factor);
+                meta[1][meta_group()][16 * meta_sub(i) + col] = vr[i] * lane_unit;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 *reinterpret_cast<uint4v *>(k_rows + piece_place(piece(i))) = l.k[i];
@@ -637,9 +621,10 @@ struct CacheAttention {
                 }
 
             // ---- the second product
-            // Weights, paired as value_field pairs tokens.  11 bits of them make an error of the size of fp16
-            // outputs' own rounding (0.00029 of the result beside 0.00019), so there the rest of each
-            // weight is a second operand (0.00019; 4 us more of 80 for 32 ragged 7B sequences); bf16's own drowns it.
+            // Weights, paired as value_field pairs tokens.  One operand holds 11 bits of each, a second one the
+            // rest: 22 bits, or what is above 2^-39 of the group's largest r so far.  (Without it bf16's outputs too
+            // are off by more than their own rounding makes them, 0.00187 of the result beside 0.00181 for one
+            // sequence of 131072 tokens; 64 x 8192 tokens 124 us without, 132 with.)
             uint32_t w16[NG][4], rest16[NG][4];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -657,17 +642,11 @@ struct CacheAttention {
                     const float2v both{w[t0][r0], w[t1][r1]};
                     const half2v pair = __builtin_convertvector(both, half2v);
                     __builtin_memcpy(&w16[g][r], &pair, 4);
-                    if constexpr (BF) {
-                        // the zeros go with the rounded weights, as the codes do
-                        z_sum[g] = fmaf((float)pair[0], z4[t0][r0], z_sum[g]);
-                        z_sum[g] = fmaf((float)pair[1], z4[t1][r1], z_sum[g]);
-                    } else {
-                        const half2v rest =
-                            __builtin_convertvector(float2v{both[0] - (float)pair[0], both[1] - (float)pair[1]}, half2v);
-                        __builtin_memcpy(&rest16[g][r], &rest, 4);
-                        z_sum[g] = fmaf(both[0], z4[t0][r0], z_sum[g]);
-                        z_sum[g] = fmaf(both[1], z4[t1][r1], z_sum[g]);
-                    }
+                    const half2v rest =
+                        __builtin_convertvector(float2v{both[0] - (float)pair[0], both[1] - (float)pair[1]}, half2v);
+                    __builtin_memcpy(&rest16[g][r], &rest, 4);
+                    z_sum[g] = fmaf(both[0], z4[t0][r0], z_sum[g]);
+                    z_sum[g] = fmaf(both[1], z4[t1][r1], z_sum[g]);
                 }
             }
 #pragma unroll
@@ -682,13 +661,11 @@ struct CacheAttention {
                         uint32_t regs[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            regs[r] = NB == 8 ? value_field<NB, !BF>(x[r / 2], r % 2, 0)
-                                              : value_field<NB, !BF>(x[h], r, i);
+                            regs[r] = NB == 8 ? value_field<NB>(x[r / 2], r % 2, 0) : value_field<NB>(x[h], r, i);
                         const int g = (n + h) * kBlockDims / GS;
                         float4v &acc = o[n + h][i];
                         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(w16[g]), acc, 0, 0, 0);
-                        if constexpr (!BF)
-                            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(rest16[g]), acc, 0, 0, 0);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(regs), operand(rest16[g]), acc, 0, 0, 0);
                     }
             }
             wave_lds_fence();       // the next tile's rows and scales go where these were
@@ -725,7 +702,7 @@ struct CacheAttention {
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int i = 0; i < kCodes; ++i)
-                        to[r * kCodes + i] = fmaf(o[n][i][r], 0x1p24f / dim_factor<NB>(i), -z_sum[g]) * back;
+                        to[r * kCodes + i] = fmaf(o[n][i][r], 0x1p24f / value_factor<NB>(i), -z_sum[g]) * back;
             }
         }
         __syncthreads();
