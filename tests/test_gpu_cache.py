@@ -810,3 +810,16 @@ def test_attention_a_wide_token_that_has_no_weight(hq, nbits, dtype, place):
     got = hq.hqq_cache_attention(c, Q, table, n)[0]
     err = (got.double() - out).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("q,scale", [(1e-38, 1e-25), (1e-20, 1e-40), (1.0, 1e-45), (0.0, 1e-45), (1e-38, 2.0 ** 100)])
+def test_attention_tiny_scores_beside_tokens_that_do_not_count(hq, q, scale):
+    """softmax_scale times the query far below fp32's range: even weights for the tokens that count, in tiles
+    with others too."""
+    g = rng(20)
+    c = filled(hq, g, 40, 16, 2, 128, 4, 64)
+    Q, table, n = batch_of(c, g, torch.bfloat16, [100, 37, 0, 128, 1], 2)
+    Q = (Q.float() * q).bfloat16()
+    for window in (0, 33):
+        check(c, hq.hqq_cache_attention(c, Q, table, n, softmax_scale=scale, window=window), Q, table, n, scale=scale,
+              window=window)

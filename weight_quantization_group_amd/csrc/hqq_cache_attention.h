@@ -409,7 +409,9 @@ struct CacheAttention {
             int e = top > 0.0f && top < INFINITY ? 14 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
             e = e > 100 ? 100 : e;
             const float f = power_of_two(e);
-            score_scale = a.scale_log2 * 0x1p12f * power_of_two(-e);      // 2^12 of the 2^24, see kr
+            // (2^12 of the 2^24, see kr; below 2^-126 scores of any size are all alike, and 0 times those of
+            // tokens that do not count, -infinity, would be NaN)
+            score_scale = fmaxf(a.scale_log2 * 0x1p12f * power_of_two(-e), 0x1p-126f);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 float sum = 0.0f;
