@@ -107,12 +107,14 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  * the second product: to 22 bits, and by at most 2^-39 of the largest 1 / scale
  * that the group has among the sequence's tokens, whatever their weights (22
  * bits down to 2^-17 of it, then fewer).
- * Keys, values and queries are taken to be of magnitude 2^64 at most, and
- * softmax_scale times the largest of a query 2^100 (fp16 values are, bf16 ones
- * need not be): beyond, a finite result can come out infinite or NaN.
+ * Keys, values and queries are taken to be of magnitude 2^64 at most,
+ * softmax_scale times the largest of a query 2^100 and a score, summed by
+ * magnitudes, 2^120 (with fp16 values and a scale below 2^80 they are; with bf16
+ * ones they need not be): beyond, a finite result can come out infinite or NaN.
  * softmax_scale is > 0 and at most 2^100, window >= 0 (HQQ_EINVAL_PARAM); batch
- * at most 2^15, q_heads 2^16, batch * q_heads 2^28, table_width * page_size 2^30
- * and batch times that 2^37 (HQQ_EINVAL_SHAPE).
+ * at most 2^15, q_heads 2^16, batch * q_heads 2^28, table_width at least 1 (also
+ * where there are no sequences), table_width * page_size at most 2^30 and batch
+ * times that 2^37 (HQQ_EINVAL_SHAPE).
  * The result does not depend on what else runs: sums are added in an order
  * that sizes and lengths set.
  *
