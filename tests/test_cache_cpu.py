@@ -6,6 +6,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -215,3 +216,22 @@ def test_binding_refuses(w):
     for bad in (dict(nbits=3), dict(group_size=0), dict(group_size=-64), dict(group_size=48)):
         with pytest.raises(ValueError):
             w.QuantizedCache.empty(4, 16, 2, 128, **{**dict(nbits=4, group_size=64, device="cpu"), **bad})
+
+
+def test_imports_on_a_torch_without_a_gpu_runtime():
+    """The package, its host-side checks and workspace sizes need none of torch's device functions."""
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith('_cuda_')]:
+    delattr(torch._C, name)
+import weight_quantization_group_amd as w
+for name in w.CACHE_EXPORTS:
+    assert callable(getattr(w, name)), name
+try:
+    w.QuantizedCache.empty(4, 16, 2, 128, 4, 64, device='cpu')
+    raise SystemExit('not refused')
+except TypeError:
+    pass
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0, r.stderr

@@ -74,8 +74,6 @@ def hqq_cache_strerror(status: int) -> str:
 
 _DT = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
 _F32, _I64, _I32 = (torch.float32,), (torch.int64,), (torch.int32,)
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _tensor(t, name: str, dtypes, shape, index: int) -> int:
@@ -203,11 +201,12 @@ def _pair(t):
 def _call(cache: QuantizedCache, f, *args) -> None:
     """Run the library's call f on the cache's device and its current stream."""
     index = cache._index
-    if _current_device() == index:
-        st = f(cache._ptr, *args, _raw_stream(index))
+    # (torch's functions are looked up here: a torch without a GPU runtime imports the package)
+    if torch._C._cuda_getDevice() == index:
+        st = f(cache._ptr, *args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            st = f(cache._ptr, *args, _raw_stream(index))
+            st = f(cache._ptr, *args, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise CacheError(f.__name__, st)
 
