@@ -235,3 +235,22 @@ except TypeError:
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0, r.stderr
+
+
+def test_workspace_of_large_batches(w, lib):
+    """A run has at most two parts of split sequences, however many sequences there are: beyond as many as runs,
+    the workspace grows by the plan's number per sequence alone, and the largest admitted sizes have one that
+    fits the card."""
+    def need(batch, q_heads, width, **kw):
+        return lib.hqq_cache_attention_workspace(ctypes.byref(cache(**kw)), batch, q_heads, width)
+
+    for heads, q_heads, dim in ((8, 64, 128), (32, 32, 128), (1, 1, 64), (40, 680, 64), (2, 8192, 256)):
+        kw = dict(heads=heads, dim=dim, gs=64)
+        rows = q_heads * (dim * 4 + 8)
+        workers = 4 * 256 * 2 // heads                          # more runs per key-value head than there are
+        top = need(1 << 15, q_heads, 100, **kw)
+        assert 2 * rows <= top <= 2 * workers * rows + 4 * (1 << 15) + 2048
+        batch = 1 << 12
+        assert need(2 * batch, q_heads, 100, **kw) - need(batch, q_heads, 100, **kw) == 4 * batch
+    assert need(4096, 64, 100, heads=8) < 5 << 20               # 64 runs of 8 heads
+    assert need(1 << 15, 1 << 13, 1 << 18, heads=1, dim=256) < 64 << 20

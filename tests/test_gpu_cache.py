@@ -823,3 +823,24 @@ def test_attention_tiny_scores_beside_tokens_that_do_not_count(hq, q, scale):
     for window in (0, 33):
         check(c, hq.hqq_cache_attention(c, Q, table, n, softmax_scale=scale, window=window), Q, table, n, scale=scale,
               window=window)
+
+
+@pytest.mark.parametrize("batch,most,heads,G,long", [(3, 9000, 40, 1, 0), (60, 700, 8, 2, 0), (70, 900, 40, 17, 0), (128, 40, 40, 1, 20000),
+                                                     (600, 90, 16, 1, 9001), (3000, 20, 40, 2, 9001)])
+def test_attention_workspace_of_just_its_bytes(hq, batch, most, heads, G, long):
+    """Runs within sequences and across, fewer sequences than runs and more: what lies behind the workspace
+    stays, whatever the workspace held."""
+    g = rng(batch + most)
+    lengths = torch.randint(0, most + 1, (batch,), generator=torch.Generator().manual_seed(batch)).tolist()
+    lengths[batch // 2] = long or most
+    c = filled(hq, g, sum(-(-n // 64) for n in lengths), 64, heads, 64, 4, 32)
+    args = batch_of(c, g, torch.float16, lengths, G, width=max(13, -(-max(lengths) // 64)))
+    size = hq.hqq_cache_attention_workspace(c, batch, heads * G, args[1].shape[1])
+    assert size > 0 and size % 4 == 0
+    room = torch.full((size // 4 + (1 << 20),), math.nan, device="cuda")
+    want = hq.hqq_cache_attention(c, *args)
+    got = hq.hqq_cache_attention(c, *args, workspace=room[:size // 4])
+    assert bool(room[size // 4:].isnan().all())
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    some = sorted({0, batch // 3, batch // 2, batch // 2 + 1, batch - 1} & set(range(batch)))
+    check(c, [t[some] for t in got], *[t[some] for t in args])

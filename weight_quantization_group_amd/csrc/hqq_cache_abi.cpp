@@ -177,7 +177,7 @@ struct AttentionLayout {
         if (batch == 0 || table_width * c.page_size <= kCacheWhole)
             return;
         workers = workers_for(c.heads * row_tiles);
-        const int64_t segments = workers + batch;
+        const int64_t segments = workers + (batch < workers ? batch : workers);
         const int64_t sums = round_up(segments * q_heads * c.dim * 4, 256);
         const int64_t meta = round_up(segments * q_heads * 8, 256);
         const bool planned = batch > kCachePlanned;

@@ -768,7 +768,7 @@ struct CacheAttention {
             stop = at + plan.run;
             cross = plan.cross;
             b = plan.find(a, at, lane, start, s);
-            slot = plan.slot(worker, b);
+            slot = plan.slot(a, worker, b, at == start);
         }
         while (b < a.batch) {
             const int next = start + s.steps, upto = stop < next ? stop : next;
@@ -779,7 +779,7 @@ struct CacheAttention {
             if (!cross || upto == stop)
                 return;
             at = start = next;
-            ++slot;
+            slot = CachePlan::next_slot(a, slot);
             if (++b < a.batch)
                 s = cache_span(a, b);
         }

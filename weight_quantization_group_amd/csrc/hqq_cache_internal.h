@@ -37,8 +37,9 @@ struct CacheAttentionArgs {
     const int32_t *table, *lengths;
     uint16_t *out;
     float *lse;                      // may be null
-    float *part;                     // [workers + batch, q_heads, dim] sums of split sequences' segments
-    float2 *part_ml;                 // [workers + batch, q_heads] their maxima and sums of weights
+    float *part;                     // [segments, q_heads, dim] sums of split sequences' segments, of which
+                                     // there are at most workers + min(workers, batch)
+    float2 *part_ml;                 // [segments, q_heads] their maxima and sums of weights
     int32_t *plan;                   // null, or the plan: kCachePlanHead numbers, then where each sequence begins
     int32_t batch, q_heads, heads, G;
     int32_t row_tiles;               // blocks of 16 q heads of a key-value head

@@ -79,43 +79,46 @@ struct Join {
         const int local = wave / WAVES, thread = threadIdx.x - local * WAVES * 64;
         const int head = blockIdx.x * kHeads + local;
         const bool real = head < a.q_heads;
-        const int64_t row0 = (int64_t)plan.slot(w0, b) * a.q_heads + (real ? head : 0);
+        // Segment i lies `at` places behind these: i or, where a run has two places, the first one's second and
+        // the others' first
+        const int two = a.batch > a.workers, step = 1 + two;
+        const int64_t row0 = (int64_t)(plan.slot(a, w0, b, true) - two) * a.q_heads + (real ? head : 0);
         const float2 *ml = a.part_ml + row0;
         const float *part = a.part + row0 * D;
         float m = -INFINITY;
-        for (int i = lane; i < count; i += 64)
-            m = fmaxf(m, ml[(int64_t)i * a.q_heads].x);
+        for (int i = lane, at = i ? step * i : two; i < count; i += 64, at = step * i)
+            m = fmaxf(m, ml[(int64_t)at * a.q_heads].x);
 #pragma unroll
         for (int o = 1; o < 64; o *= 2)
             m = fmaxf(m, __shfl_xor(m, o));
         const float ref = m == -INFINITY ? 0.0f : m;
         float total = 0.0f;
-        for (int i = lane; i < count; i += 64) {
-            const float2 v = ml[(int64_t)i * a.q_heads];
+        for (int i = lane, at = i ? step * i : two; i < count; i += 64, at = step * i) {
+            const float2 v = ml[(int64_t)at * a.q_heads];
             total += v.y * __builtin_amdgcn_exp2f(v.x - ref);
         }
 #pragma unroll
         for (int o = 1; o < 64; o *= 2)
             total += __shfl_xor(total, o);
-        const int group = thread / kLanes, at = thread % kLanes;
+        const int group = thread / kLanes, dims = thread % kLanes;
         float4v v{0.f, 0.f, 0.f, 0.f};
         if (group < kAtOnce) {
 #pragma unroll 4
-            for (int i = group; i < count; i += kAtOnce) {
-                const float w = __builtin_amdgcn_exp2f(ml[(int64_t)i * a.q_heads].x - ref);
-                v += w * *reinterpret_cast<const float4v *>(part + (int64_t)i * a.q_heads * D + 4 * at);
+            for (int i = group, at = i ? step * i : two; i < count; i += kAtOnce, at = step * i) {
+                const float w = __builtin_amdgcn_exp2f(ml[(int64_t)at * a.q_heads].x - ref);
+                v += w * *reinterpret_cast<const float4v *>(part + (int64_t)at * a.q_heads * D + 4 * dims);
             }
-            sums[local][group][at] = v;
+            sums[local][group][dims] = v;
         }
         __syncthreads();              // (count is one number for all of the workgroup)
         if (group == 0 && real) {
 #pragma unroll
             for (int i = 1; i < kAtOnce; ++i)
-                v += sums[local][i][at];
+                v += sums[local][i][dims];
             const int64_t row = (int64_t)b * a.q_heads + head;
-            *reinterpret_cast<uint2 *>(a.out + row * D + 4 * at) =
+            *reinterpret_cast<uint2 *>(a.out + row * D + 4 * dims) =
                 a.bf16 ? cache_round4<true>(v * cache_inverse(total)) : cache_round4<false>(v * cache_inverse(total));
-            if (at == 0 && a.lse)
+            if (dims == 0 && a.lse)
                 a.lse[row] = cache_lse(m, total);
         }
     }

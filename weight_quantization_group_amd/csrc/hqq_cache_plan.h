@@ -110,8 +110,19 @@ struct CachePlan {
     // a sequence's steps in the order of runs
     __device__ __forceinline__ int padded(int steps) const { return cross ? steps : runs_of(steps, run) * run; }
 
-    // the workspace's place of segment (w, b): runs and sequences both advance
-    __device__ __forceinline__ int slot(int w, int b) const { return cross ? w + b : w; }
+    // The workspace's place of run w's segment of sequence b, which is split.  Runs and sequences both advance;
+    // of more sequences than runs a run has two places, for what goes on from the run before and for what begins
+    // in it and goes on (those between are whole)
+    __device__ __forceinline__ int slot(const CacheAttentionArgs &a, int w, int b, bool begins) const
+    {
+        return a.batch > a.workers ? 2 * w + begins : cross ? w + b : w;
+    }
+
+    // the place of the run's next segment
+    static __device__ __forceinline__ int next_slot(const CacheAttentionArgs &a, int slot)
+    {
+        return a.batch > a.workers ? slot | 1 : slot + 1;
+    }
 
     // The sequence that holds step `at`, its first step and span (batch: behind the last)
     __device__ __forceinline__ int find(const CacheAttentionArgs &a, int at, int lane, int &start, CacheSpan &span) const
