@@ -254,3 +254,15 @@ def test_workspace_of_large_batches(w, lib):
         assert need(2 * batch, q_heads, 100, **kw) - need(batch, q_heads, 100, **kw) == 4 * batch
     assert need(4096, 64, 100, heads=8) < 5 << 20               # 64 runs of 8 heads
     assert need(1 << 15, 1 << 13, 1 << 18, heads=1, dim=256) < 64 << 20
+
+
+def test_runs_are_for_the_workgroups_that_fit(w, lib):
+    """As many runs as the chip holds workgroups at a time: two a CU, but one where a workgroup takes more than
+    half of a CU's shared memory (8 bits of 256 dims in groups of 64)."""
+    def segments(gs, heads, dim=256, nbits=8):
+        n = lib.hqq_cache_attention_workspace(ctypes.byref(cache(heads=heads, dim=dim, gs=gs, nbits=nbits)), 1, heads, 100)
+        return n // (heads * (dim * 4 + 8))
+
+    for heads in (1, 2, 4, 16):
+        assert segments(64, heads) == 256 // heads + 1
+        assert segments(128, heads) == segments(256, heads) == segments(64, heads, nbits=4) == 512 // heads + 1

@@ -151,9 +151,9 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // Runs per key-value head and row tile, `columns` of those: as many workgroups as the chip
 // holds, or some rounds of them where that divides better.
-int32_t workers_for(int64_t columns)
+int32_t workers_for(const hqq_cache &c, int64_t columns)
 {
-    const int64_t slots = (int64_t)kCus * kCacheResident;
+    const int64_t slots = (int64_t)kCus * cache_resident(c.nbits, c.dim, c.group_size);
     int64_t best = slots / columns, rounds = 1;
     for (int64_t r = 2; r <= 4; ++r)
         if (r * slots / columns * rounds > best * r * 11 / 10) {
@@ -176,7 +176,7 @@ struct AttentionLayout {
         workers = 0;
         if (batch == 0 || table_width * c.page_size <= kCacheWhole)
             return;
-        workers = workers_for(c.heads * row_tiles);
+        workers = workers_for(c, c.heads * row_tiles);
         const int64_t segments = workers + (batch < workers ? batch : workers);
         const int64_t sums = round_up(segments * q_heads * c.dim * 4, 256);
         const int64_t meta = round_up(segments * q_heads * 8, 256);

@@ -787,9 +787,11 @@ struct CacheAttention {
 };
 
 template <int NB, int GS, int NG, bool BF>
-__global__ __launch_bounds__(64 * kCacheWaves, kCacheResident) void cache_attention_kernel(CacheAttentionArgs a)
+__global__ __launch_bounds__(64 * kCacheWaves, cache_resident(NB, GS * NG, GS)) void cache_attention_kernel(CacheAttentionArgs a)
 {
-    __shared__ typename CacheAttention<NB, GS, NG, BF>::Shared sh;
+    typedef typename CacheAttention<NB, GS, NG, BF>::Shared Shared;
+    static_assert(cache_resident(NB, GS * NG, GS) * sizeof(Shared) <= kLdsOfCu);
+    __shared__ Shared sh;
     CacheAttention<NB, GS, NG, BF> attention(a);
     attention.run(sh);
 }

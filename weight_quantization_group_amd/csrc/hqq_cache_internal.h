@@ -57,9 +57,16 @@ constexpr int kCacheStep = kCacheTile * kCacheWaves;
 // Workgroups of the attention kernel that a CU holds at a time: two, eight waves with some 5 KB
 // each on their way.  (More in flight is slower, whatever they compute: the loads alone of 64 x
 // 8192 tokens over 8 heads of 128 at 4 bits, 117 us by two, 130 by three, 159 by two with tiles of 64
-// tokens; with the arithmetic 125 by two, 139 by three, 152 by one.)
-constexpr int kCacheResident = 2;
+// tokens; with the arithmetic 125 by two, 139 by three, 152 by one.)  One where 8 bits of 256 dims in groups of
+// 64 take more than half of a CU's LDS: runs for two would go in two rounds.  (16 sequences of 8192 tokens over 4
+// heads 87.5 us by runs for two, 77.5 for one, 16 of 3000 over 16 heads 89.8 and 75, one of 32768 over 4 heads
+// 49.7 and 41; of 4 sequences to 2000 tokens 22.3 and 22.7.)
+constexpr int cache_resident(int nbits, int dim, int group_size)
+{
+    return nbits == 8 && dim == 256 && group_size == 64 ? 1 : 2;
+}
 constexpr int kCus = 256;
+constexpr int kLdsOfCu = 160 * 1024;
 
 // Sequences of at most this many tokens are not split: a step more costs a workgroup 1 us, the
 // join's launch 2.5 us and the host 4.  (One sequence of 512 tokens 9.1 us whole, 10.6 split, of
