@@ -844,3 +844,49 @@ def test_attention_workspace_of_just_its_bytes(hq, batch, most, heads, G, long):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     some = sorted({0, batch // 3, batch // 2, batch // 2 + 1, batch - 1} & set(range(batch)))
     check(c, [t[some] for t in got], *[t[some] for t in args])
+
+
+CROSSING = [(96, 32, 2, "bf16"), (128, 32, 4, "fp16"), (256, 64, 8, "fp16"), (256, 128, 8, "bf16"), (64, 32, 2, "fp16"), (192, 64, 4, "bf16")]
+
+
+@pytest.mark.parametrize("dim,gs,nbits,dtype", CROSSING)
+@pytest.mark.parametrize("batch,most,heads,G,page_size", [(3, 9000, 40, 1, 64), (60, 1200, 20, 3, 16), (150, 500, 24, 1, 32),
+                                                          (300, 700, 2, 17, 128)])
+@pytest.mark.parametrize("window", [0, 333])
+def test_attention_windows_and_formats_across_sequences(hq, dim, gs, nbits, dtype, batch, most, heads, G, page_size, window):
+    """Runs that cross sequences, fewer and more of these than runs, planned by each wave and by a launch: every
+    format's segments one behind the other in a workgroup's shared memory, and windows that begin inside a tile, where
+    table entries before the window name no page."""
+    g = rng(dim + batch + window)
+    lengths = torch.randint(0, most + 1, (batch,), generator=torch.Generator().manual_seed(batch)).tolist()
+    lengths[0], lengths[batch // 2], lengths[-1] = most, 0, most - 1
+    pages = min(700, sum(-(-n // page_size) for n in lengths))
+    c = filled(hq, g, pages, page_size, heads, dim, nbits, gs)
+    width = max(-(-most // page_size), -(-800 // page_size))
+    table = torch.randint(0, pages, (batch, width), device="cuda", generator=g).int()
+    if window:
+        first = (torch.tensor(lengths, device="cuda") - window).clamp(min=0)
+        behind = torch.arange(width, device="cuda")[None] * page_size + page_size <= first[:, None]
+        table[behind] = torch.tensor([-1, pages, 2 ** 31 - 1, -2 ** 31], device="cuda").int()[
+            torch.randint(0, 4, table[behind].shape, device="cuda", generator=g)]
+    Q = torch.randn(batch, heads * G, dim, device="cuda", generator=g).to(DTYPES[dtype])
+    n = torch.tensor(lengths, device="cuda").int()
+    got = torch.full_like(Q, math.nan), torch.full(Q.shape[:2], math.nan, device="cuda")
+    hq.hqq_cache_attention(c, Q, table, n, window=window, out=got[0], lse=got[1])
+    assert not got[0].isnan().any() and not got[1].isnan().any()
+    some = torch.tensor(sorted({0, 1, batch // 2, batch // 2 + 1, batch - 1}), device="cuda")
+    some = some[some < batch]
+    check(c, [t[some] for t in got], Q[some], table[some], n[some], window=window)
+
+
+def test_attention_of_several_new_tokens_of_a_sequence(hq):
+    """One table row named several times with rising lengths: the tokens of a prompt's end, each seeing those
+    before it."""
+    g = rng(21)
+    c = filled(hq, g, 90, 16, 2, 128, 4, 64)
+    _, row, _ = batch_of(c, g, torch.float16, [1400], 4)
+    table = row.repeat(9, 1)
+    n = torch.arange(1392, 1401, device="cuda").int()
+    Q = torch.randn(9, 8, 128, device="cuda", generator=g).half()
+    for window in (0, 200):
+        check(c, hq.hqq_cache_attention(c, Q, table, n, window=window), Q, table, n, window=window)
