@@ -890,3 +890,72 @@ def test_attention_of_several_new_tokens_of_a_sequence(hq):
     Q = torch.randn(9, 8, 128, device="cuda", generator=g).half()
     for window in (0, 200):
         check(c, hq.hqq_cache_attention(c, Q, table, n, window=window), Q, table, n, window=window)
+
+
+# ---------------------------------------------------------------------------
+# the largest calls
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("heads", [1, 3, 1024])
+def test_write_and_read_the_most_tokens(hq, heads):
+    """2^26 rows: nearly all of them skipped, the first, the last and some between written and read back."""
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GB of device memory")
+    g = rng(heads)
+    tokens, dim = (1 << 26) // heads, 64
+    c = hq.QuantizedCache.empty(20, 16, heads, dim, 4, 32)
+    # rows that overlap: 8 values from one token, or head, to the next
+    K, V = (torch.randn((tokens + heads) * 8 + dim, device="cuda", generator=g).half()
+            .as_strided((tokens, heads, dim), (8, 8, 1)) for _ in range(2))
+    some = torch.cat([torch.tensor([0, 1, 15, 16, tokens - 1, tokens - 17], device="cuda"),
+                      torch.randint(20, tokens - 20, (250,), device="cuda", generator=g)]).unique()
+    slots = torch.full((tokens,), -1, device="cuda")
+    slots[some] = torch.randperm(320, device="cuda", generator=g)[:len(some)]
+    hq.hqq_cache_write(c, K, V, slots)
+    check_written(c, K[some], V[some], slots[some])
+    got = hq.hqq_cache_read(c, slots)
+    want = hq.hqq_cache_read(c, slots[some])
+    for a, b in zip(got, want):
+        assert torch.equal(a[some], b)
+        a[some] = 0
+        assert not a.view(torch.int64).any()
+    with pytest.raises(hq.CacheError):
+        more = torch.full((tokens + 1,), -1, device="cuda")
+        hq.hqq_cache_write(c, K[:1].expand(tokens + 1, -1, -1), V[:1].expand(tokens + 1, -1, -1), more)
+
+
+@pytest.mark.parametrize("place", [0, 1 << 19, (1 << 20) - 1])
+def test_attention_of_the_longest_sequence(hq, place):
+    """2^30 tokens, the table's pages all one but for one that takes all the weight: scores 60 or more above the
+    others', whose 2^30 weights come to less than 2^30 e^-60 = 2^-56."""
+    g = rng(22)
+    c = filled(hq, g, 2, 1024, 1, 64, 2, 32)
+    c.k[1].mul_(1e4)                                           # keys near 0, and one page's of 60 or more
+    c.k[2][1, :, :, 0] -= 8.0 * 60 / 32 * c.k[1][1, :, :, 0]
+    Q = torch.full((2, 3, 64), 1.0, device="cuda").bfloat16()
+    table = torch.zeros(2, 1 << 20, dtype=torch.int32, device="cuda")
+    table[0, place] = 1
+    n = torch.tensor([1 << 30, 5], device="cuda").int()
+    got = hq.hqq_cache_attention(c, Q, table, n)
+    only = torch.tensor([[1], [0]], device="cuda").int(), torch.tensor([1024, 5], device="cuda").int()
+    check(c, got, Q, *only)
+
+
+@pytest.mark.parametrize("width", [1, 13])
+def test_attention_of_the_most_sequences(hq, width):
+    """2^15 sequences, whole and planned: empty ones, single tokens and a few long ones among them."""
+    g = rng(23 + width)
+    batch = 1 << 15
+    c = filled(hq, g, 300, 64, 2, 64, 4, 32)
+    n = torch.randint(0, 4, (batch,), device="cuda", generator=g).int()
+    n[::4096] = width * 64
+    n[-1] = width * 64 - 1
+    table = torch.randint(0, 300, (batch, width), device="cuda", generator=g).int()
+    Q = torch.randn(batch, 4, 64, device="cuda", generator=g).half()
+    got = hq.hqq_cache_attention(c, Q, table, n)
+    some = torch.cat([torch.arange(0, batch, 4096, device="cuda"), torch.tensor([1, 2, 4095, batch - 2, batch - 1], device="cuda")])
+    check(c, [t[some] for t in got], Q[some], table[some], n[some])
+    alone = torch.randint(0, batch, (100,), device="cuda", generator=g)
+    parts = hq.hqq_cache_attention(c, Q[alone], table[alone], n[alone])
+    short = n[alone] <= 128                                    # one step: one segment, whatever else runs
+    assert torch.equal(parts[0][short], got[0][alone][short]) and torch.equal(parts[1][short], got[1][alone][short])
