@@ -104,9 +104,9 @@ HQQ_API int hqq_cache_read(const hqq_cache *cache, const int64_t *slots, int64_t
  *            -infinity.
  * Scores, exponentials' sums and outputs are formed in fp32; besides the
  * output, each weight exp(s_t - max) times its group's 1 / scale is rounded for
- * the second product: to 22 bits, and by at most 2^-39 of the largest 1 / scale
+ * the second product: to 22 bits, or by at most 2^-39 of the largest 1 / scale
  * that the group has among the sequence's tokens, whatever their weights (22
- * bits down to 2^-17 of it, then fewer).
+ * bits down to 2^-17 of it, then fewer), or 2^-145 where that is more.
  * Keys, values and queries are taken to be of magnitude 2^64 at most,
  * softmax_scale times the largest of a query 2^100 and a score, summed by
  * magnitudes, 2^120 (with fp16 values and a scale below 2^80 they are; with bf16

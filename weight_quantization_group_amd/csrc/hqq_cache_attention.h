@@ -22,10 +22,10 @@
 // ahead in registers; through LDS they reach the operands' lanes.
 //
 // What bounds it: the bytes of codes and scales where sequences are long (64 sequences of 8192 tokens,
-// 8 heads of 128 dims at 4 bits in groups of 64, 64 q heads: 673 MB in 123 us, 5.5 TB/s, of 6.2 that a
-// read reaches; its loads alone take 117), with some 90 us of vector operations beside them.  A segment
+// 8 heads of 128 dims at 4 bits in groups of 64, 64 q heads: 673 MB in 132 to 137 us, 5 TB/s, of 6.2 that a
+// read reaches; its loads alone take 117), with about as much time of vector operations beside them.  A segment
 // (a workgroup's part of a sequence) costs about 3 us beside its tiles, which is what short sequences
-// pay (32 ragged ones, 32 heads: 344 MB in 77 us), and a call has a floor of some 9 us of launches.
+// pay (32 ragged ones, 32 heads: 344 MB in 78 to 82 us), and a call has a floor of some 9 us of launches.
 #pragma once
 
 #include "hqq_cache_plan.h"

@@ -57,7 +57,7 @@ constexpr int kCacheStep = kCacheTile * kCacheWaves;
 // Workgroups of the attention kernel that a CU holds at a time: two, eight waves with some 5 KB
 // each on their way.  (More in flight is slower, whatever they compute: the loads alone of 64 x
 // 8192 tokens over 8 heads of 128 at 4 bits, 117 us by two, 130 by three, 159 by two with tiles of 64
-// tokens; with the arithmetic 125 by two, 139 by three, 152 by one.)  One where 8 bits of 256 dims in groups of
+// tokens; with the arithmetic, weights still in one operand, 125 by two, 139 by three, 152 by one.)  One where 8 bits of 256 dims in groups of
 // 64 take more than half of a CU's LDS: runs for two would go in two rounds.  (16 sequences of 8192 tokens over 4
 // heads 87.5 us by runs for two, 77.5 for one, 16 of 3000 over 16 heads 89.8 and 75, one of 32768 over 4 heads
 // 49.7 and 41; of 4 sequences to 2000 tokens 22.3 and 22.7.)
@@ -68,9 +68,11 @@ constexpr int cache_resident(int nbits, int dim, int group_size)
 constexpr int kCus = 256;
 constexpr int kLdsOfCu = 160 * 1024;
 
-// Sequences of at most this many tokens are not split: a step more costs a workgroup 1 us, the
-// join's launch 2.5 us and the host 4.  (One sequence of 512 tokens 9.1 us whole, 10.6 split, of
-// 1024 13.2 and 10.6.)
+// Sequences of at most this many tokens are not split: a step more costs a workgroup 1 us, the join's
+// launch, a segment's end and the host's part of them 3 to 6.  (4 bits of 128 dims, fp16, whole and split: one
+// sequence of 512 tokens over 8 heads 9.3 and 13.4 us, of 768 11.5 and 13.2, of 1024 14.2 and 12.9; over 32 heads
+// of 768 12.4 and 13.2, of 1024 14.8 and 13; 64 sequences of 768 over 8 heads 17.7 and 21.4, 200 of 768 over 32
+// 192 and 199.  Large batches gain up to 4 % on beyond it, small ones lose.)
 constexpr int kCacheWhole = 768;
 
 // Runs of more steps than this cross sequences.
